@@ -381,6 +381,70 @@ q_status dq_blockwise(const uint8_t *q, const float *s, int64_t R, int64_t C, q_
 q_status dq_nvfp4(const uint8_t *q, const uint8_t *sb, const float *s_global, int64_t R,
                   int64_t C, q_nvblk blk, q_dtype out, void *y, q_stream_t stream);
 
+/*
+ * Block-scaled FP8 matrix product: the consumer of the blockwise copies
+ * ([MP] "Blockwise scaling": the forward, input-gradient and weight-gradient
+ * products, each reading the copies whose blocks run along its reduction).
+ *   C[m, n] = (C[m, n] +) sum over the 128-element blocks kb of K of
+ *             s_a[m, kb] * s_b[n, kb] * sum_{k in kb} a[m, k] * b[n, k]
+ *   a [M, K], b [N, K]  E4M3 codes, row-major (both operands have their
+ *   reduction along the rows, as the copies of q_blockwise do):
+ *     forward          Y  = X W^T:   a = X.q_row,   b = W.q_row
+ *     input gradient   dX = dY W:    a = dY.q_row,  b = W.q_colT
+ *     weight gradient  dW = dY^T X:  a = dY.q_colT, b = X.q_colT
+ *   s_a: tile_a Q_T1x128: [M, K/128]; Q_T128x128: [M/128, K/128].
+ *   s_b: tile_b Q_T1x128: [N, K/128]; Q_T128x128: [N/128, K/128].
+ *   c [M, N] in `out` (Q_BF16 rounded to nearest even once, or Q_F32);
+ *   accumulate != 0 adds to what c holds (the FP32 main gradient over
+ *   micro-batches), 0 overwrites it without reading.
+ * Sums are held in FP32; the result does not depend on timing (no atomics),
+ * and a row's result does not depend on the values of other rows.  The E4M3
+ * codes 0x7F and 0xFF are NaN and propagate, as do non-finite scales.
+ * Shapes: K % 128 == 0, M % 128 == 0 (N % 128 == 0) for a 128x128 operand;
+ * M, N, K < 2^31.  M == 0 or N == 0 does nothing; K == 0 is a sum over
+ * nothing: c is set to zero, or left as it is when accumulating.
+ * Alignment: a, b, c 16 bytes, s_a, s_b 4 bytes.
+ */
+q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const uint8_t *b, const float *s_b, q_tile tile_b,
+                      int64_t M, int64_t N, int64_t K, void *c, q_dtype out, int accumulate, int32_t *status,
+                      q_stream_t stream);
+
+/*
+ * Dropout with the residual sum, its mask drawn from a counter and never
+ * stored: y = residual + keep * c * x over n elements (residual NULL:
+ * y = keep * c * x; that is also the backward pass on dy).
+ *   T = 65536 * p rounded to the nearest integer (ties to even), 0 <= p <= 1,
+ *   c = 65536 / (65536 - T) (p = 1 drops every element);
+ *   element i draws 16 bits D_i of Philox4x32-10 with key (seed lo, seed hi)
+ *   and counter (g lo, g hi, 2, 0), g = offset + i / 8: half i % 2 (low half
+ *   first) of output word (i % 8) / 2; it is kept iff D_i >= T.
+ * p is thus taken to the nearest 1/65536, and a kept element is scaled by the
+ * inverse of the exact share that is kept.  A dropped element gives the
+ * residual (or +0) whatever x holds there, NaN and infinities included.  A
+ * shard that starts at element i0 of a tensor (i0 % 8 == 0) passes
+ * offset + i0 / 8 and draws what the whole tensor's call draws there.
+ * x, residual and y have the dtype `in`; the sum is formed in FP32 with one
+ * rounding (a fused multiply-add) and rounded to BF16 once.  Any n >= 0.
+ * y may be x or residual themselves (in place); other overlap is not allowed.
+ * Alignment: 16 bytes each.
+ */
+q_status drop_add(const void *x, q_dtype in, int64_t n, const void *residual, double p, uint64_t seed, uint64_t offset,
+                  void *y, q_stream_t stream);
+
+/*
+ * The blockwise copies of a dropped tensor in one read: q_blockwise with
+ * Q_T1x128 tiles of keep * c * x (FP32, keep and c as in drop_add with flat
+ * index i = m*K + k).  For the gradient behind a dropout: the rowwise copy
+ * feeds the input gradient's product and the transposed copy the weight
+ * gradient's, and neither the mask nor the dropped gradient is stored.
+ * Outputs, shapes, alignment and *status are those of q_blockwise, and the
+ * codes and scales are bit for bit what q_blockwise gives for the FP32 tensor
+ * keep * c * x.
+ */
+q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, double p, uint64_t seed, uint64_t offset,
+                          uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT, int32_t *status,
+                          q_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

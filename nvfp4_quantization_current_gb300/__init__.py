@@ -29,6 +29,17 @@ Recipes (each with its dequantizer, rowwise and columnwise outputs):
 * :func:`q_nvfp4_rht_colT` -- the columnwise NVFP4 copy of the random
   Hadamard transform of x, for the weight-gradient GEMM inputs ("From BF16
   to FP8/FP4 ...", sections 2.4 and 5.6).
+
+Operators on the blockwise copies:
+
+* :func:`mm_blockwise` -- the block-scaled FP8 matrix product of a linear
+  layer's forward, input-gradient and weight-gradient passes;
+* :func:`drop_add` -- dropout with the residual sum, its mask drawn from a
+  counter and never stored;
+* :func:`drop_q_blockwise` -- the blockwise copies of a dropped gradient in
+  one read.
+
+``linear.py`` puts them together as a linear layer.
 """
 from __future__ import annotations
 
@@ -58,6 +69,7 @@ STATUS_NAMES = {Q_OK: "Q_OK", Q_ERR_ARG: "Q_ERR_ARG", Q_ERR_SHAPE: "Q_ERR_SHAPE"
 
 # every exported entry point: name -> (restype, argtypes)
 _P, _I64, _I, _U64, _U32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint32
+_F64 = ctypes.c_double
 SIGNATURES = {
     "q_last_error": (ctypes.c_char_p, []),
     "q_abi_version": (_I, []),
@@ -76,6 +88,9 @@ SIGNATURES = {
     "q_nvfp4": (_I, [_P, _I, _I64, _I64, _I, _I, _U64, _U64, _P, _P, _P, _P, _P, _I, _P, _P, _P]),
     "q_nvfp4_rht_amax": (_I, [_P, _I, _I64, _I64, _U32, _P, _P, _P]),
     "q_nvfp4_rht_colT": (_I, [_P, _I, _I64, _I64, _U32, _I, _U64, _U64, _P, _P, _P, _I, _P, _P, _P]),
+    "mm_blockwise": (_I, [_P, _P, _I, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P]),
+    "drop_add": (_I, [_P, _I, _I64, _P, _F64, _U64, _U64, _P, _P]),
+    "drop_q_blockwise": (_I, [_P, _I, _I64, _I64, _F64, _U64, _U64, _P, _P, _P, _P, _P, _P]),
     "dq_current_scaling": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
     "dq_mxfp8": (_I, [_P, _P, _I64, _I64, _I, _I, _I, _P, _P]),
     "dq_blockwise": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
@@ -561,6 +576,93 @@ def dq_nvfp4(q, sb, s_global, blk="1x16", dtype=torch.float32, out=None):
     return y
 
 
-__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "alloc_", "Q_"))] + [
+# ---------------------------------------------------------------------------
+# operators on the blockwise copies
+# ---------------------------------------------------------------------------
+
+_TILE = {"1x128": Q_T1x128, "128x128": Q_T128x128, Q_T1x128: Q_T1x128, Q_T128x128: Q_T128x128}
+
+
+def _operand(name, q, s, tile):
+    """(rows, K) of a blockwise operand, its codes and scales checked against each other."""
+    if not (q.is_cuda and s.is_cuda):
+        raise ValueError(f"{name} must be CUDA tensors (the library has no CPU path)")
+    if q.dtype != torch.uint8 or s.dtype != torch.float32:
+        raise ValueError(f"{name}: codes must be uint8 and scales float32, got {q.dtype} and {s.dtype}")
+    if q.dim() != 2 or not q.is_contiguous() or not s.is_contiguous():
+        raise ValueError(f"{name}: codes must be a contiguous 2-D tensor and scales contiguous")
+    R, K = q.shape
+    want = (R, K // 128) if tile == Q_T1x128 else (R // 128, K // 128)
+    if tuple(s.shape) != want:
+        raise ValueError(f"{name}: scales are {tuple(s.shape)}, codes {R} x {K} need {want}")
+    return R, K
+
+
+def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.Tensor, tile_a="1x128",
+                 tile_b="128x128", dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, accumulate=False,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C [M, N] = A B^T of blockwise FP8 operands: codes ``a`` [M, K] and ``b``
+    [N, K] with the FP32 scales of their 1x128 or 128x128 tiles, as
+    :func:`q_blockwise` makes them.
+
+    forward ``(x.q_row, x.s_row, w.q_row, w.s_row)``, input gradient
+    ``(dy.q_row, dy.s_row, w.q_colT, w.s_colT)``, weight gradient
+    ``(dy.q_colT, dy.s_colT, x.q_colT, x.s_colT, tile_b="1x128")``.
+    ``dtype`` (that of ``out`` when it is given) is bfloat16 or float32;
+    ``accumulate`` adds to ``out`` (e.g. an FP32 main gradient).  One token
+    upward; sums in FP32, results independent of timing."""
+    ta, tb = _TILE[tile_a], _TILE[tile_b]
+    M, K = _operand("a", a, s_a, ta)
+    N, Kb = _operand("b", b, s_b, tb)
+    if K != Kb:
+        raise ValueError(f"a has K = {K}, b has K = {Kb}")
+    if a.device != b.device:
+        raise ValueError(f"a is on {a.device}, b on {b.device}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    elif tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != a.device:
+        raise ValueError(f"out must be a contiguous {M} x {N} tensor on {a.device}")
+    _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
+          _out(out.dtype), int(accumulate), _ptr(status), _stream(a.device))
+    return out
+
+
+def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``residual + dropout(x)`` (or ``dropout(x)``) for a contiguous tensor of
+    any shape.  Which elements are dropped follows from ``seed``, ``offset`` (in
+    counters of 8 elements) and the element's flat index, so the backward pass
+    is ``drop_add(dy, p, seed, offset)`` and no mask is stored.  ``p`` is taken
+    to the nearest 1/65536.  ``out`` may be ``x`` or ``residual``."""
+    if not x.is_cuda or not x.is_contiguous() or x.dtype not in _DTYPES:
+        raise ValueError("x must be a contiguous CUDA tensor of bfloat16 or float32")
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous, with x's shape, dtype and device")
+    out = torch.empty_like(x) if out is None else out
+    _call("drop_add", x.data_ptr(), _DTYPES[x.dtype], x.numel(), _ptr(residual), float(p), int(seed), int(offset),
+          out.data_ptr(), _stream(x.device))
+    return out
+
+
+_DTYPES = {torch.bfloat16: Q_BF16, torch.float32: Q_F32}
+
+
+def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, rowwise=True, colwise=False,
+                     out: Optional[BlockwiseTensor] = None, status: Optional[torch.Tensor] = None) -> BlockwiseTensor:
+    """The 1x128 blockwise copies of ``dropout(x)`` (FP32, the decisions of
+    :func:`drop_add` with the same seed and offset) in one read of x: the
+    gradient behind a dropout, ready for the two gradient products."""
+    dt = _in(x)
+    M, K = x.shape
+    out = alloc_blockwise(M, K, x.device, "1x128", rowwise, colwise) if out is None else out
+    _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
+          _ptr(out.q_colT), _ptr(out.s_colT), _ptr(status), _stream(x.device))
+    return out
+
+
+__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "mm_", "drop_", "alloc_", "Q_"))] + [
     "CurrentScalingTensor", "DelayedScaling", "MXFP8Tensor", "BlockwiseTensor", "BlockwiseMXTensor", "NVFP4Tensor",
     "QuantError", "lib", "SIGNATURES"]

@@ -26,6 +26,15 @@
 // tile being 4 MXFP8 blocks that share one scale): the tile scale is b / 448
 // rounded up to a power of two, stored as its E8M0 code once per 32 elements
 // (e_row [M, K/32], e_colT [K, M/32]), and alpha = 2^(127 - code).
+//
+// With dropout ahead of the cast (Drop = DropArgs, 1x128 tiles; the backward
+// of a dropout that follows the product) the tensor that is cast is
+// y = keep c x in FP32, and neither y nor the mask is stored: a row chunk of
+// the engine lies inside one Philox block, so a thread draws the decisions of
+// its own 8 rows and zeroes dropped elements in its registers.  Rounding is
+// monotonic, so max|y| = RN(c max|kept x|), and the codes are those of
+// RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.
+#include "q_dropout.cuh"
 #include "q_engine.cuh"
 #include "q_internal.h"
 
@@ -83,12 +92,45 @@ template <int DT, bool P2> QD void bw_tile_scale(uint32_t b, const BwScaleTab &t
     }
 }
 
-template <int DT, int TILE, bool P2>
+struct NoDrop {};
+
+// Keeps the elements of a row chunk (flat index i0, a multiple of VEC inside
+// one Philox block) that the draws keep, as packed input elements.
+template <int DT> QD void drop_chunk(uint4 &v, int64_t i0, const DropArgs &d)
+{
+    const uint4 draws = drop_draws((uint64_t)i0 >> 3, d);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (DT == BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            w[j] &= (drop_keep(draws, 2 * j, d.threshold) ? 0x0000FFFFu : 0u) | (drop_keep(draws, 2 * j + 1, d.threshold) ? 0xFFFF0000u : 0u);
+    } else {
+        const bool upper = (i0 & 4) != 0;
+        const uint4 mine = make_uint4(upper ? draws.z : draws.x, upper ? draws.w : draws.y, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < 4; j++) w[j] = drop_keep(mine, j, d.threshold) ? w[j] : 0u;
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT, int TILE, bool P2, class Drop>
 __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K,
                                                               uint8_t *__restrict__ q_row, void *__restrict__ sc_row,
                                                               uint8_t *__restrict__ q_colT, void *__restrict__ sc_colT,
-                                                              int32_t *status)
+                                                              int32_t *status, const Drop drop)
 {
+    constexpr bool DROP = !std::is_same<Drop, NoDrop>::value;
+    constexpr int SDT = DROP ? F32 : DT;   // c b is no BF16 value: its scales take the divisions
+    static_assert(!DROP || (TILE == 0 && !P2), "dropout goes with 1x128 tiles");
+    // the tile maximum of what is cast, from the maximum of the (kept) inputs
+    auto cast_max = [&](uint32_t b) -> uint32_t {
+        if constexpr (DROP) return __float_as_uint(__fmul_rn(__uint_as_float(b), drop.c));
+        else return b;
+    };
+    // f = c f for two elements on their way to the cast
+    auto cast_mul = [&](float &f0, float &f1) {
+        if constexpr (DROP) mul2(f0, f1, drop.c, drop.c);
+    };
     // scales: FP32 [M, K/128] / [K, M/128] (2D: [M/128, K/128] / [K/128, M/128]),
     // or with P2 E8M0 codes [M, K/32] / [K, M/32], one 4-byte word per 128 elements
     float *const s_row = static_cast<float *>(sc_row), *const s_colT = static_cast<float *>(sc_colT);
@@ -100,7 +142,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
     __shared__ __align__(16) float calpha[TC];   // 1x128: column alphas of the tile
     __shared__ uint32_t tred[kEngWarps][NT];   // 128x128: per-warp tile maxima
     __shared__ BwScaleTab tab;
-    if (DT == BF16 && !P2 && threadIdx.x < 128) {
+    if (SDT == BF16 && !P2 && threadIdx.x < 128) {
         const float a = __fdiv_rn(448.0f, 1.0f + (float)threadIdx.x * (1.0f / 128.0f));
         tab.a[threadIdx.x] = a;
         tab.s[threadIdx.x] = __fdiv_rn(1.0f, a);
@@ -116,6 +158,10 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
         uint4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = lds16(st + (8 * warp + j) * kRowBytes + lane * 16);
+        if constexpr (DROP) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) drop_chunk<DT>(v[j], (m0 + j) * K + k, drop);
+        }
         uint32_t code[8][CW];
         uint32_t cc2 = 0;   // 128x128 with P2: this lane's block code
         // 128x128 with P2: the code once per 32 elements, one 4-byte word per
@@ -176,10 +222,10 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
                 kw = hmax_abs2(kw, __shfl_xor_sync(0xFFFFFFFFu, kw, 2));
                 kw = hmax_abs2(kw, __shfl_xor_sync(0xFFFFFFFFu, kw, 1));
                 const int r = (L >> 1) & 7;
-                const uint32_t bm = (b1 ? kw : (kw << 16)) & 0x7FFF0000u;         // FP32 bits of row r's block max
+                const uint32_t bm = cast_max((b1 ? kw : (kw << 16)) & 0x7FFF0000u);   // FP32 bits of row r's block max
                 float alpha_r, s_r;
                 uint32_t c_r;
-                bw_tile_scale<DT, P2>(bm, tab, alpha_r, s_r, c_r);
+                bw_tile_scale<SDT, P2>(bm, tab, alpha_r, s_r, c_r);
                 if ((L & 1) == 0 && r < nrows) {
                     if (P2) stg4(e_row + (m0 + r) * (K / 32) + (k / 128) * 4, c_r * kRep4);
                     else s_row[(m0 + r) * (K / 128) + k / 128] = s_r;
@@ -190,7 +236,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
                 for (int j = 0; j < 8; j++) {
                     const float alpha = __shfl_sync(0xFFFFFFFFu, alpha_r, (lane & 16) + 2 * j);
                     uint32_t o[CW];
-                    chunk_fp8<DT, E4M3>(v[j], alpha, o);
+                    chunk_fp8<DT, E4M3>(v[j], alpha, o, cast_mul);
                     if (j < nrows) {
                         if (CW == 2) stg8(qr + j * K, o[0], o[CW - 1]);
                         else stg4(qr + j * K, o[0]);
@@ -207,11 +253,12 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
                     group_max2<DT, LPB>(bb[0], bb[1]);
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
+                        bb[h] = cast_max(bb[h]);
                         float alpha, sc;
                         uint32_t cc;
-                        bw_tile_scale<DT, P2>(bb[h], tab, alpha, sc, cc);
+                        bw_tile_scale<SDT, P2>(bb[h], tab, alpha, sc, cc);
                         uint32_t o[CW];
-                        chunk_fp8<DT, E4M3>(v[j + h], alpha, o);
+                        chunk_fp8<DT, E4M3>(v[j + h], alpha, o, cast_mul);
                         if (j + h < nrows) {
                             uint8_t *dst = qr + (j + h) * K;
                             if (CW == 2) stg8(dst, o[0], o[CW - 1]);
@@ -241,10 +288,10 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
                 b2 = hmax_abs2(b2, __shfl_xor_sync(0xFFFFFFFFu, b2, 2));
                 if (sub < 2) {
                     const int col = 2 * wp + sub;             // low half: even column
-                    const uint32_t b = (sub ? b2 : (b2 << 16)) & 0x7FFF0000u;
+                    const uint32_t b = cast_max((sub ? b2 : (b2 << 16)) & 0x7FFF0000u);
                     float alpha, sc;
                     uint32_t cc;
-                    bw_tile_scale<DT, P2>(b, tab, alpha, sc, cc);
+                    bw_tile_scale<SDT, P2>(b, tab, alpha, sc, cc);
                     calpha[col] = alpha;
                     if (kb + col < K) {
                         if (P2) stg4(e_colT + (kb + col) * (M / 32) + tm * 4, cc * kRep4);
@@ -261,10 +308,11 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
 #pragma unroll
                     for (int w = half; w < kEngWarps; w += TPC) b = max(b, colmax_bits<DT>(part[w][q], c));
                     if (TPC == 2) b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
+                    b = cast_max(b);
                     if (half == 0) {
                         float alpha, sc;
                         uint32_t cc;
-                        bw_tile_scale<DT, P2>(b, tab, alpha, sc, cc);
+                        bw_tile_scale<SDT, P2>(b, tab, alpha, sc, cc);
                         calpha[col] = alpha;
                         if (kb + col < K) {
                             if (P2) stg4(e_colT + (kb + col) * (M / 32) + tm * 4, cc * kRep4);
@@ -290,7 +338,10 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
 #pragma unroll
                 for (int c = 0; c < VEC; c++) f[c] = elem<DT>(v[j], c);
 #pragma unroll
-                for (int c = 0; c < VEC; c += 2) mul2(f[c], f[c + 1], ca[c], ca[c + 1]);
+                for (int c = 0; c < VEC; c += 2) {
+                    cast_mul(f[c], f[c + 1]);
+                    mul2(f[c], f[c + 1], ca[c], ca[c + 1]);
+                }
 #pragma unroll
                 for (int q = 0; q < CW; q++) code[j][q] = cvt_fp8x4<E4M3>(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
             }
@@ -346,21 +397,21 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
     });
 }
 
-template <int DT, int TILE, bool P2>
+template <int DT, int TILE, bool P2, class Drop = NoDrop>
 static cudaError_t bw_t(const void *x, int64_t M, int64_t K, uint8_t *q_row, void *s_row, uint8_t *q_colT,
-                        void *s_colT, int32_t *status, cudaStream_t st)
+                        void *s_colT, int32_t *status, cudaStream_t st, const Drop &drop = Drop())
 {
     constexpr int TC = 32 * In<DT>::VEC;
     alignas(64) CUtensorMap map;
     cudaError_t e = make_tile_map(&map, x, DT, M, K);
     if (e != cudaSuccess) return e;
     {
-        const cudaError_t ea = engine_smem_ready<k_blockwise<DT, TILE, P2>>();
+        const cudaError_t ea = engine_smem_ready<k_blockwise<DT, TILE, P2, Drop>>();
         if (ea != cudaSuccess) return ea;
     }
     const int64_t tiles = ((M + kTileRowsE - 1) / kTileRowsE) * ((K + TC - 1) / TC);
     const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-    k_blockwise<DT, TILE, P2><<<grid, kEngThreads, kEngSmem, st>>>(map, M, K, q_row, s_row, q_colT, s_colT, status);
+    k_blockwise<DT, TILE, P2, Drop><<<grid, kEngThreads, kEngSmem, st>>>(map, M, K, q_row, s_row, q_colT, s_colT, status, drop);
     return cudaGetLastError();
 }
 
@@ -382,6 +433,15 @@ cudaError_t launch_blockwise_mx(const void *x, int dt, int64_t M, int64_t K, int
                          : bw_t<BF16, 1, true>(x, M, K, q_row, e_row, q_colT, e_colT, status, st);
     return tile == 0 ? bw_t<F32, 0, true>(x, M, K, q_row, e_row, q_colT, e_colT, status, st)
                      : bw_t<F32, 1, true>(x, M, K, q_row, e_row, q_colT, e_colT, status, st);
+}
+
+cudaError_t launch_drop_q_blockwise(const void *x, int dt, int64_t M, int64_t K, uint32_t threshold, float c, uint64_t seed,
+                                    uint64_t offset, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
+                                    int32_t *status, cudaStream_t st)
+{
+    const DropArgs d = {philox_keys(seed), offset, threshold, c};
+    return dt == BF16 ? bw_t<BF16, 0, false, DropArgs>(x, M, K, q_row, s_row, q_colT, s_colT, status, st, d)
+                      : bw_t<F32, 0, false, DropArgs>(x, M, K, q_row, s_row, q_colT, s_colT, status, st, d);
 }
 
 }  // namespace qk

@@ -1,5 +1,6 @@
 // The C ABI (include/q.h): argument validation on the host, then stream-
 // ordered launches.  Nothing here allocates or synchronizes.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -83,6 +84,17 @@ thread_local int g_inject_launch_failures = 0;
         cudaError_t e_ = (expr);                                           \
         if (e_ != cudaSuccess) return cuda_fail(where, e_);                \
     } while (0)
+
+// 65536 p to the nearest integer (ties to even), the drop threshold of 16-bit draws.
+q_status drop_threshold(const char *fn, double p, uint32_t *threshold)
+{
+    if (!(p >= 0.0 && p <= 1.0)) return fail(Q_ERR_ARG, "%s: p = %g is outside [0, 1]", fn, p);
+    *threshold = (uint32_t)std::nearbyint(p * 65536.0);
+    return Q_OK;
+}
+
+// 1 / (share of the draws that keep an element); 0 where none does.
+float drop_scale(uint32_t threshold) { return threshold < 65536u ? (float)(65536.0 / (65536.0 - (double)threshold)) : 0.0f; }
 
 cudaStream_t S(q_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -380,6 +392,76 @@ q_status q_nvfp4_rht_colT(const void *x, q_dtype in, int64_t M, int64_t K, uint3
     TRY(need(fn, "s_global", s_global, 4));
     LAUNCH(fn, qk::launch_nvfp4_rht_colT(x, (int)in, M, K, sign_mask, (int)rnd, seed, offset, amax_mode == Q_AMAX_COMPUTE,
                                          amax, q_colT, sb_colT, s_global, status, S(stream)));
+    return Q_OK;
+}
+
+q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const uint8_t *b, const float *s_b, q_tile tile_b,
+                      int64_t M, int64_t N, int64_t K, void *c, q_dtype out, int accumulate, int32_t *status,
+                      q_stream_t stream)
+{
+    const char *fn = "mm_blockwise";
+    constexpr int64_t kMost = (int64_t)1 << 31;
+    if (M < 0 || N < 0 || K < 0 || M >= kMost || N >= kMost || K >= kMost)
+        return fail(Q_ERR_SHAPE, "%s: shape (%lld, %lld, %lld) is negative or not below 2^31", fn, (long long)M, (long long)N, (long long)K);
+    for (q_tile t : {tile_a, tile_b})
+        if (t != Q_T1x128 && t != Q_T128x128) return fail(Q_ERR_ARG, "%s: tile %d is not Q_T1x128 or Q_T128x128", fn, (int)t);
+    TRY(check_out(fn, out));
+    TRY(multiple(fn, "K", K, 128));
+    if (tile_a == Q_T128x128) TRY(multiple(fn, "M (128x128 tiles of a)", M, 128));
+    if (tile_b == Q_T128x128) TRY(multiple(fn, "N (128x128 tiles of b)", N, 128));
+    if (M == 0 || N == 0) return Q_OK;
+    TRY(need(fn, "c", c, 16));
+    if (K == 0) {   // a sum over nothing
+        if (!accumulate) LAUNCH(fn, cudaMemsetAsync(c, 0, (size_t)M * (size_t)N * (out == Q_BF16 ? 2 : 4), S(stream)));
+        return Q_OK;
+    }
+    TRY(need(fn, "a", a, 16));
+    TRY(need(fn, "s_a", s_a, 4));
+    TRY(need(fn, "b", b, 16));
+    TRY(need(fn, "s_b", s_b, 4));
+    LAUNCH(fn, qk::launch_mm_blockwise(a, s_a, (int)tile_a, b, s_b, (int)tile_b, M, N, K, c, (int)out, accumulate != 0, status,
+                                       S(stream)));
+    return Q_OK;
+}
+
+q_status drop_add(const void *x, q_dtype in, int64_t n, const void *residual, double p, uint64_t seed, uint64_t offset,
+                  void *y, q_stream_t stream)
+{
+    const char *fn = "drop_add";
+    uint32_t threshold;
+    if (n < 0) return fail(Q_ERR_SHAPE, "%s: negative size %lld", fn, (long long)n);
+    TRY(check_in(fn, x, in, n));
+    TRY(drop_threshold(fn, p, &threshold));
+    if (n == 0) return Q_OK;
+    if (residual != nullptr) TRY(need(fn, "residual", residual, 16));
+    TRY(need(fn, "y", y, 16));
+    LAUNCH(fn, qk::launch_drop_add(x, (int)in, n, residual, threshold, drop_scale(threshold), seed, offset, y, S(stream)));
+    return Q_OK;
+}
+
+q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, double p, uint64_t seed, uint64_t offset,
+                          uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT, int32_t *status,
+                          q_stream_t stream)
+{
+    const char *fn = "drop_q_blockwise";
+    uint32_t threshold;
+    TRY(check_dims(fn, M, K));
+    TRY(check_in(fn, x, in, M * K));
+    TRY(drop_threshold(fn, p, &threshold));
+    TRY(multiple(fn, "K", K, 128));
+    if (M * K == 0) return Q_OK;
+    if (q_row == nullptr && q_colT == nullptr) return fail(Q_ERR_ARG, "%s: neither direction requested", fn);
+    if (q_row != nullptr) {
+        TRY(need(fn, "q_row", q_row, 16));
+        TRY(need(fn, "s_row", s_row, 4));
+    }
+    if (q_colT != nullptr) {
+        TRY(need(fn, "q_colT", q_colT, 16));
+        TRY(need(fn, "s_colT", s_colT, 4));
+        TRY(multiple(fn, "M (with q_colT)", M, 128));
+    }
+    LAUNCH(fn, qk::launch_drop_q_blockwise(x, (int)in, M, K, threshold, drop_scale(threshold), seed, offset, q_row, s_row,
+                                           q_colT, s_colT, status, S(stream)));
     return Q_OK;
 }
 

@@ -266,15 +266,21 @@ QD void bfly2(float &a0, float &a1, float &b0, float &b1)
 }
 
 // The VEC elements of a 16-byte row chunk times s, as FP8 codes (VEC/4 words,
-// element 0 in the lowest byte).
-template <int DT, int FMT> QD void chunk_fp8(const uint4 &v, float s, uint32_t *o)
+// element 0 in the lowest byte).  `pre` may change each pair of elements first.
+struct NoChange {
+    QD void operator()(float &, float &) const {}
+};
+template <int DT, int FMT, class Pre = NoChange> QD void chunk_fp8(const uint4 &v, float s, uint32_t *o, const Pre &pre = Pre())
 {
     constexpr int VEC = In<DT>::VEC;
     float f[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; j++) f[j] = elem<DT>(v, j);
 #pragma unroll
-    for (int j = 0; j < VEC; j += 2) mul2(f[j], f[j + 1], s, s);
+    for (int j = 0; j < VEC; j += 2) {
+        pre(f[j], f[j + 1]);
+        mul2(f[j], f[j + 1], s, s);
+    }
 #pragma unroll
     for (int w = 0; w < VEC / 4; w++) o[w] = cvt_fp8x4<FMT>(f[4 * w], f[4 * w + 1], f[4 * w + 2], f[4 * w + 3]);
 }

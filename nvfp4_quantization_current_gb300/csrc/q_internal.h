@@ -43,6 +43,17 @@ cudaError_t make_tile_map(void *map /* CUtensorMap, 64-byte aligned */, const vo
 cudaError_t make_store_map_u8(void *map /* CUtensorMap, 64-byte aligned */, void *base, int64_t row_bytes,
                               int64_t rows, int box_bytes, int box_rows);
 
+// A 2-D TMA tensor map over an operand of a matrix product: row-major FP8
+// codes [rows, K] (K a multiple of 128, base 16-byte aligned), box box_rows
+// rows x 128 bytes written to shared memory in the 128-byte swizzle.
+cudaError_t make_operand_map(void *map /* CUtensorMap, 64-byte aligned */, const void *codes, int64_t rows, int64_t K,
+                             int box_rows);
+
+// A 2-D TMA tensor map for stores into a row-major BF16 / F32 matrix
+// [rows, cols] (row bytes a multiple of 16, base 16-byte aligned), box 32 rows
+// x 128 bytes read from shared memory in the 128-byte swizzle.
+cudaError_t make_result_map(void *map /* CUtensorMap, 64-byte aligned */, void *c, int dt, int64_t rows, int64_t cols);
+
 // current scaling
 cudaError_t launch_amax(const void *x, int dt, int64_t n, float *amax, int32_t *status, cudaStream_t st);
 cudaError_t launch_cs_cast(const void *x, int dt, int64_t M, int64_t K, int fmt, const float *amax,
@@ -85,6 +96,22 @@ cudaError_t launch_blockwise(const void *x, int dt, int64_t M, int64_t K, int ti
                              float *s_row, uint8_t *q_colT, float *s_colT, int32_t *status, cudaStream_t st);
 cudaError_t launch_blockwise_mx(const void *x, int dt, int64_t M, int64_t K, int tile, uint8_t *q_row,
                                 uint8_t *e_row, uint8_t *q_colT, uint8_t *e_colT, int32_t *status, cudaStream_t st);
+
+// blockwise with dropout ahead of it (1x128 tiles): elements whose 16-bit draw
+// is below `threshold` are zeroed, the others multiplied by `c`
+cudaError_t launch_drop_q_blockwise(const void *x, int dt, int64_t M, int64_t K, uint32_t threshold, float c, uint64_t seed,
+                                    uint64_t offset, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
+                                    int32_t *status, cudaStream_t st);
+
+// y = residual + dropout(x) over n elements (residual may be null)
+cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residual, uint32_t threshold, float c,
+                            uint64_t seed, uint64_t offset, void *y, cudaStream_t st);
+
+// block-scaled FP8 product: c [M, N] (+)= a [M, K] b [N, K]^T with the tiles'
+// scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0
+cudaError_t launch_mm_blockwise(const uint8_t *a, const float *s_a, int tile_a, const uint8_t *b, const float *s_b, int tile_b,
+                                int64_t M, int64_t N, int64_t K, void *c, int out, bool accumulate, int32_t *status,
+                                cudaStream_t st);
 
 // NVFP4 (the amax is already in *amax)
 cudaError_t launch_nvfp4(const void *x, int dt, int64_t M, int64_t K, int blk, int rnd, uint64_t seed,

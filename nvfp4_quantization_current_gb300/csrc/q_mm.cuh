@@ -1,0 +1,148 @@
+// What the kernels of the block-scaled product share: their arguments, bounded
+// waits that end when the CTA aborts, and the way out of the accumulators.
+#pragma once
+
+#include "q_tcgen05.cuh"
+
+namespace qk {
+
+constexpr int kMmBlock = 128;   // elements of K per scale, and bytes per operand row of a stage
+
+// How finished sums reach C.
+enum MmStore { kStoreDirect = 0, kStoreBulk = 1, kStoreBulkAdd = 2 };
+
+// C = P Q^T: P's rows lie on tensor memory lanes, Q's rows on its columns.
+struct MmArgs {
+    const float *s_p, *s_q;
+    int64_t rows_p, rows_q, kblocks;
+    int shift_p, shift_q;       // row -> scale row: 0 for 1x128 tiles, 7 for 128x128
+    void *c;
+    int64_t ldc;
+    int32_t *status;
+    bool accumulate;
+    int store;
+};
+
+// Waits for a phase of `bar`; false when the CTA's abort flag is up or the
+// wait ran out (which raises it and reports the timeout).
+template <bool CLUSTER> QD bool mm_wait_t(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    auto test = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (test()) return true;
+    const unsigned long long t0 = globaltimer();
+    while (true) {
+        if (test()) return true;
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            if (status != nullptr) atomicOr(status, kStTimeout);
+            return false;
+        }
+    }
+}
+QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    return mm_wait_t<false>(bar, parity, abort_flag, status);
+}
+// For a barrier that the other CTA of a pair arrives on or signals through.
+QD bool mm_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    return mm_wait_t<true>(bar, parity, abort_flag, status);
+}
+
+template <int OUT> struct OutT;
+template <> struct OutT<BF16> { using T = uint16_t; };
+template <> struct OutT<F32> { using T = float; };
+
+template <int OUT> QD void put_one(typename OutT<OUT>::T *p, float v, bool accumulate)
+{
+    if constexpr (OUT == F32) {
+        *p = accumulate ? *p + v : v;
+    } else {
+        *p = (uint16_t)bf16_bits(accumulate ? __uint_as_float((uint32_t)*p << 16) + v : v);
+    }
+}
+
+QD uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
+}
+
+// One warp's sums, 32 rows (one per lane, from row0) x 128 columns (from
+// col0), to C through its 4 KiB of staging: 32 rows x 128 bytes at a time, the
+// 16-byte piece i of row r at place i ^ (r % 8), which is the 128-byte swizzle
+// of the bulk store and spreads the lanes' rows over the banks.  Rows and
+// columns outside C are cut off by the store.  C's whose rows are no multiple
+// of 16 bytes, and sums onto a BF16 C, are written by the lanes themselves,
+// one row at a time, from FP32 staging (so that a sum is rounded once).
+template <int OUT>
+QD void mm_store_rows(const MmArgs &g, const CUtensorMap *map_c, uint8_t *stg, const uint64_t (&acc)[64], int64_t row0,
+                      int64_t col0, int lane)
+{
+    using T = typename OutT<OUT>::T;
+    const bool bulk = g.store != kStoreDirect;
+    auto slot = [&](int r, int i) { return stg + r * 128 + ((i ^ (r & 7)) << 4); };
+    if (OUT == BF16 && bulk) {
+#pragma unroll
+        for (int pass = 0; pass < 2; pass++) {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    float a, b;
+                    unpack2(acc[pass * 32 + i * 4 + j], a, b);
+                    w[j] = bf16_pair(a, b);
+                }
+                *reinterpret_cast<uint4 *>(slot(lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && row0 < g.rows_p && col0 + pass * 64 < g.rows_q) {
+                tma_store_tile(map_c, stg, (int)(col0 + pass * 64), (int)row0);
+                bulk_commit();
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int pass = 0; pass < 4; pass++) {
+        if (bulk && lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            float a, b, c, d;
+            unpack2(acc[pass * 16 + i * 2], a, b);
+            unpack2(acc[pass * 16 + i * 2 + 1], c, d);
+            *reinterpret_cast<float4 *>(slot(lane, i)) = make_float4(a, b, c, d);
+        }
+        if (bulk) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && row0 < g.rows_p && col0 + pass * 32 < g.rows_q) {
+                if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, stg, (int)(col0 + pass * 32), (int)row0);
+                else tma_store_tile(map_c, stg, (int)(col0 + pass * 32), (int)row0);
+                bulk_commit();
+            }
+        } else {
+            __syncwarp();
+            const int64_t col = col0 + pass * 32 + lane;
+            for (int r = 0; r < 32 && row0 + r < g.rows_p; r++)
+                if (col < g.rows_q)
+                    put_one<OUT>(static_cast<T *>(g.c) + (row0 + r) * g.ldc + col,
+                                 *reinterpret_cast<const float *>(slot(r, lane >> 2) + (lane & 3) * 4), g.accumulate);
+        }
+    }
+}
+
+}  // namespace qk

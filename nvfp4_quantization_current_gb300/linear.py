@@ -1,0 +1,105 @@
+"""A linear layer on the blockwise FP8 copies, with dropout and the residual sum behind it:
+
+    y = residual + dropout(x W^T)
+
+Forward: the activations in 1x128 tiles and the weights in 128x128 tiles
+(:func:`q_blockwise`), their product (:func:`mm_blockwise`), then
+:func:`drop_add`.  Backward: :func:`drop_q_blockwise` draws the dropout's
+decisions again and casts the gradient behind it in one read; the input
+gradient is the product of its rowwise copy with the weights' transposed copy
+and the weight gradient the product of the two transposed copies.  The layer
+keeps FP8 copies for the backward pass, no mask and no BF16 activation.
+
+The recipe is the DeepSeek-V3-like one of "Mixed-precision training: fp16 to
+fp8", "Blockwise scaling".
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import BlockwiseTensor, drop_add, drop_q_blockwise, mm_blockwise, q_blockwise
+
+
+def _cast_rows(x, rowwise, colwise):
+    """1x128 copies of x [M, K].  The transposed copy needs M % 128 == 0: a
+    ragged x is cast with zero rows below it, which add nothing to the weight
+    gradient; the rowwise copy is cut back to M rows."""
+    M = x.shape[0]
+    if not colwise or M % 128 == 0:
+        return q_blockwise(x, "1x128", rowwise, colwise)
+    t = q_blockwise(torch.nn.functional.pad(x, (0, 0, 0, -M % 128)), "1x128", rowwise, True)
+    if rowwise:
+        t.q_row, t.s_row = t.q_row[:M], t.s_row[:M]
+    return t
+
+
+class _BlockwiseLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, w, p, seed, offset, main_grad, train):
+        need_x, need_w = (train and n for n in ctx.needs_input_grad[:2])
+        if need_x and w.q_colT is None:
+            raise ValueError("copies lacks the transposed copy, which the input gradient reads")
+        x2 = x.reshape(-1, x.shape[-1])
+        xq = _cast_rows(x2, True, need_w)
+        y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype)
+        if p > 0 or residual is not None:
+            drop_add(y, p, seed, offset, None if residual is None else residual.reshape(y.shape), out=y)
+        ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
+                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
+        ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, residual is not None)
+        return y.view(*x.shape[:-1], -1)
+
+    @staticmethod
+    def backward(ctx, dy):
+        w_q, w_s, x_q, x_s = ctx.saved_tensors
+        p, seed, offset, main_grad, w_dtype, x_shape, has_residual = ctx.args
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dx = dw = None
+        if need_x or need_w:
+            d = dy.reshape(-1, dy.shape[-1]).contiguous()
+            M = d.shape[0]
+            if need_w and M % 128 != 0:   # zero rows below, as in the forward pass; the draws are by flat index
+                d = torch.nn.functional.pad(d, (0, 0, 0, -M % 128))
+            g = drop_q_blockwise(d, p, seed, offset, need_x, need_w)
+            if need_x:
+                dx = mm_blockwise(g.q_row[:M], g.s_row[:M], w_q, w_s, dtype=dy.dtype).view(x_shape)
+            if need_w:
+                dw = mm_blockwise(g.q_colT, g.s_colT, x_q, x_s, tile_b="1x128", dtype=w_dtype, out=main_grad,
+                                  accumulate=main_grad is not None)
+        return dx, None if main_grad is not None else dw, dy if has_residual else None, None, None, None, None, None, None
+
+
+class BlockwiseLinear(torch.nn.Module):
+    """``y = residual + dropout(x W^T)`` on blockwise FP8 copies.
+
+    ``in_features`` and ``out_features`` are multiples of 128; x is bfloat16 or
+    float32 with any number of rows.  Dropout runs in training mode; its
+    decisions follow from the layer's ``seed`` and the ``offset`` of the call
+    (in counters of 8 elements; give each step its own, e.g. ``step *
+    rows * out_features // 8``).  With ``main_grad`` set (FP32, the weight's
+    shape) the weight gradient is added to it and ``weight.grad`` stays unset.
+    ``copies`` takes the result of :meth:`quantize_weight`, made once for the
+    micro-batches of a step, or once for serving."""
+
+    def __init__(self, in_features: int, out_features: int, p: float = 0.0, seed: int = 0, device="cuda",
+                 dtype=torch.bfloat16):
+        super().__init__()
+        if in_features % 128 or out_features % 128:
+            raise ValueError("in_features and out_features must be multiples of 128")
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=0.02)
+        self.p, self.seed = float(p), int(seed)
+        self.main_grad: Optional[torch.Tensor] = None
+
+    def quantize_weight(self, colwise=True) -> BlockwiseTensor:
+        """The weight's 128x128 copies (``colwise``: also the transposed one, for the input gradient)."""
+        return q_blockwise(self.weight.detach(), "128x128", rowwise=True, colwise=colwise)
+
+    def forward(self, x, residual=None, offset: int = 0, copies: Optional[BlockwiseTensor] = None):
+        train = torch.is_grad_enabled()
+        if copies is None:
+            copies = self.quantize_weight(colwise=train and x.requires_grad)
+        return _BlockwiseLinear.apply(x, self.weight, residual, copies, self.p if self.training else 0.0, self.seed,
+                                      int(offset), self.main_grad, train)
