@@ -23,6 +23,7 @@
 // CTA's abort flag, which ends the other roles' waits, and the copies and MMAs
 // in flight are waited for (bounded again) before shared and tensor memory go
 // away.
+#include "k_mm_pair.cuh"
 #include "q_internal.h"
 #include "q_mm.cuh"
 
@@ -166,9 +167,31 @@ cudaError_t mm_one(const uint8_t *p, const uint8_t *q, const MmArgs &g, cudaStre
     return cudaGetLastError();
 }
 
+// Tiles of 256 x 256 on CTA pairs.
+template <int OUT, bool COLS>
+cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t st)
+{
+    alignas(64) CUtensorMap map_p, map_q, map_c = {};
+    const int64_t K = g.kblocks * kMmBlock;
+    cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K, 128);
+    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K, 128);
+    const bool bulk = g.ldc % (OUT == F32 ? 4 : 8) == 0 && (OUT == F32 || !g.accumulate);
+    g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
+    if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm_pair<OUT, COLS>>(sizeof(PairSmem));
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + kPairN - 1) / kPairN);
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    const int64_t pairs = sm_count() / 2;
+    k_mm_pair<OUT, COLS><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, sizeof(PairSmem), st>>>(map_p, map_q, map_c, g);
+    return cudaGetLastError();
+}
+
 template <int OUT>
 cudaError_t mm_t(const uint8_t *p, const uint8_t *q, const MmArgs &g, cudaStream_t st)
 {
+    if (g.rows_p > 512)
+        return g.shift_q ? mm_pair<OUT, false>(p, q, g, st) : mm_pair<OUT, true>(p, q, g, st);
     return mm_one<OUT>(p, q, g, st);
 }
 

@@ -25,31 +25,25 @@ struct MmArgs {
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the
 // wait ran out (which raises it and reports the timeout).
-template <bool CLUSTER> QD bool mm_wait_t(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
-    auto test = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
-    if (test()) return true;
-    const unsigned long long t0 = globaltimer();
-    while (true) {
-        if (test()) return true;
+    // The timer is read once in many polls: a read takes about as long as a
+    // block's MMAs, and these waits are on the path of every block.
+    unsigned long long t0 = 0;
+    for (uint32_t n = 1;; n++) {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (globaltimer() - t0 > kWaitNs) {
-            *abort_flag = 1;
-            if (status != nullptr) atomicOr(status, kStTimeout);
-            return false;
+        if (n % 1024 == 0) {
+            const unsigned long long now = globaltimer();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitNs) {
+                *abort_flag = 1;
+                if (status != nullptr) atomicOr(status, kStTimeout);
+                return false;
+            }
         }
     }
 }
-QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
-{
-    return mm_wait_t<false>(bar, parity, abort_flag, status);
-}
-// For a barrier that the other CTA of a pair arrives on or signals through.
-QD bool mm_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
-{
-    return mm_wait_t<true>(bar, parity, abort_flag, status);
-}
-
 template <int OUT> struct OutT;
 template <> struct OutT<BF16> { using T = uint16_t; };
 template <> struct OutT<F32> { using T = float; };

@@ -64,9 +64,7 @@ QD void mma_commit(uint64_t *bar)
 }
 
 // ---------------------------------------------------------------------------
-// CTA pairs (clusters of two): one MMA spans both CTAs' tensor memory, each
-// CTA holding its own 128 rows of A and D and half of B's rows.  All tensor
-// memory instructions of such a kernel name the pair.
+// clusters
 // ---------------------------------------------------------------------------
 
 QD uint32_t cluster_rank()
@@ -80,60 +78,20 @@ QD void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Address of `p`'s counterpart in the shared memory of cluster rank `rank`.
-QD uint32_t cluster_addr(const void *p, uint32_t rank)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-QD void mbar_arrive_cluster(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// mbar_try_wait for a barrier that other CTAs of the cluster arrive on.
-QD bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return done != 0;
-}
 
-template <int COLS> QD void tmem_alloc_pair(uint32_t *dst)
+// tma_load_tile into the same place of every CTA in `mask`, counted on the
+// barrier at bar's place in each of them.
+QD void tma_load_tile_multicast(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint16_t mask)
 {
-    static_assert(COLS >= 32 && COLS <= 512 && (COLS & (COLS - 1)) == 0, "column count");
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+                 "[%0], [%1, {%2, %3}], [%4], %5;"
+                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask) : "memory");
 }
-template <int COLS> QD void tmem_free_pair(uint32_t base)
+// mma_commit with one arrival on the barrier at bar's place in every CTA of `mask`.
+QD void mma_commit_multicast(uint64_t *bar, uint16_t mask)
 {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS) : "memory");
-}
-
-// A tile into this CTA's shared memory whose bytes count on a barrier of the
-// pair (bar: a cluster address, this CTA's or its peer's).
-QD void tma_load_tile_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-
-// mma_f8 over the pair: the descriptors give offsets that hold in both CTAs.
-QD void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
-{
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
-}
-// mma_commit with one arrival on the barrier at this offset in both CTAs.
-QD void mma_commit_pair(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"(mask) : "memory");
 }
 
 // Moves registers between warpgroups (all four warps of one; multiples of 8,
@@ -178,6 +136,14 @@ QD void tmem_ld32(uint32_t (&r)[32], uint32_t addr)
                    "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(addr));
 }
+QD void tmem_ld16(uint32_t (&r)[16], uint32_t addr)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
 // Waits for this thread's accumulator loads; r passes through so that no use
 // of the loaded registers is scheduled ahead of the wait.
 QD void tmem_wait_ld(uint32_t (&r)[32])
@@ -187,6 +153,13 @@ QD void tmem_wait_ld(uint32_t (&r)[32])
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
                    "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                    "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) ::"memory");
+}
+
+QD void tmem_wait_ld(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]) ::"memory");
 }
 
 QD void mbar_arrive(uint64_t *bar)
