@@ -129,7 +129,6 @@ k_mm_blockwise(const __grid_constant__ CUtensorMap map_p, const __grid_constant_
                 for (int h = 0; h < kMmN / 32; h++) {
                     uint32_t r[32];
                     tmem_ld32(r, tmem + ((uint32_t)(warp * 32) << 16) + buf * kMmN + h * 32);
-                    tmem_wait_ld(r);
 #pragma unroll
                     for (int j = 0; j < 32; j++)
                         acc[h * 32 + j] = __fmaf_rn(__uint_as_float(r[j]) * col_scale[buf][h * 32 + j], srow, acc[h * 32 + j]);
@@ -179,6 +178,15 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
     g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
     if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
     if (e == cudaSuccess) e = engine_smem_ready<k_mm_pair<OUT, COLS>>(sizeof(PairSmem));
+    if (e == cudaSuccess) {   // the epilogue's registers have to be there to be moved: it would wait for them forever
+        static const cudaError_t enough = [] {
+            cudaFuncAttributes a;
+            const cudaError_t ea = cudaFuncGetAttributes(&a, k_mm_pair<OUT, COLS>);
+            if (ea != cudaSuccess) return ea;
+            return a.numRegs * kPairThreads >= 32 * (kPairEpiWarps * kPairEpiRegs + 4 * kPairRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
+        }();
+        e = enough;
+    }
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + kPairN - 1) / kPairN);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;

@@ -7,18 +7,27 @@
 // 128 x 256 x 128 products.  The block products alternate between two
 // accumulator buffers, which together fill tensor memory.
 //
-// Warp 0 loads operand tiles, one thread of warp 1 issues the MMAs, warp 2
-// fetches the column scales when Q has 1x128 tiles, and the eight warps 4-11
-// keep the FP32 sums of 32 rows x 128 columns each in registers: a block's
-// product is read from tensor memory, multiplied by its scales and added while
-// the next block's runs.  Finished tiles go through shared memory to C as bulk
-// tensor stores (adds, when accumulating in FP32), 32 rows x 128 bytes each.
+// Warp 0 loads operand tiles, warps 1 and 2 issue the MMAs of the even and the
+// odd blocks, warp 3 fetches scales, four blocks at a time, and the eight
+// warps 4-11 keep the FP32 sums of 32 rows x 128 columns each in registers: a
+// block's product is read from tensor memory, multiplied by its scales and
+// added while the next block's runs.  Finished tiles go through shared memory
+// to C as bulk tensor stores (adds, when accumulating in FP32), 32 rows x 128
+// bytes each.
 //
 // The hand-over of the accumulator buffers is what the block rate hangs on:
-// MMAs, commit, read, release and the next MMAs into the same buffer form a
-// chain, of which two are in flight.  It stays inside the CTA (one MMA over
-// both CTAs of a pair would need half the loads of Q, but its chain crosses
-// the pair twice per block and took twice as long).
+// MMAs (512 cycles), commit (207 until a waiting warp sees it), read (about
+// 300), release and the next MMAs into the same buffer form a chain, of which
+// two are in flight.  It stays inside the CTA: one MMA over both CTAs of a
+// pair would need half the loads of Q, but its chain crosses the pair twice
+// per block and took twice as long.  The release is a named barrier (about 20
+// cycles from arrival to wake-up, an mbarrier takes 160 to 200); as a warp's
+// barrier waits for its own commits too, each buffer has an MMA warp of its
+// own.  A named barrier cannot time out, and need not: an MMA warp waits there
+// only for a block k whose MMAs it has issued, with a look at the abort flag
+// between one such wait and the next; those MMAs needed block k - 2 released,
+// so an epilogue warp that has not arrived for k is at k - 1 or k, and one
+// that gives up there raises the flag and arrives for both buffers.
 #pragma once
 
 #include "q_internal.h"
@@ -26,19 +35,40 @@
 
 namespace qk {
 
-constexpr int kPairThreads = 384;
-constexpr int kPairStages = 4;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 32 * (4 + kPairEpiWarps);
+constexpr int kPairStages = 3;
 constexpr int kPairN = 256;       // columns of a CTA's tile
 constexpr int kPairStageBytes = (128 + kPairN) * kMmBlock;
-constexpr int kPairScaleSlots = 2;
-constexpr int kPairEpiWarps = 8;
+constexpr int kPairScaleSlots = 2, kPairScaleBlocks = 4;
 constexpr int kPairGroup = 8;     // tile rows per group of the tile order
+// Named barriers of the accumulator buffers' release (two from kAccFree on):
+// the epilogue's threads arrive, the MMA warp waits.
+constexpr int kAccFree = 1, kAccThreads = 32 * (kPairEpiWarps + 1);
+// Registers per thread of the epilogue's and the other warps; their sum is what
+// the kernel is launched with.
+constexpr int kPairEpiRegs = 200, kPairRegs = 104;
+
+// (Constant barrier numbers: one held in a register claims all sixteen.)
+QD void acc_release(int buf)
+{
+    if (buf == 0) named_barrier_arrive(kAccFree, kAccThreads);
+    else named_barrier_arrive(kAccFree + 1, kAccThreads);
+}
+QD void acc_await(int buf)
+{
+    if (buf == 0) named_barrier(kAccFree, kAccThreads);
+    else named_barrier(kAccFree + 1, kAccThreads);
+}
 
 struct PairSmem {
     uint8_t stage[kPairStages][kPairStageBytes];
-    uint8_t staging[kPairEpiWarps][4096];
-    float col_scale[kPairScaleSlots][kPairN];
-    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], acc_empty[2], drained;
+    uint8_t staging[kPairEpiWarps][2 * 4096];
+    // the blocks' scales: P's rows, and Q's rows (COLS) or two 128-row tiles
+    float row_scale[kPairScaleSlots][kPairScaleBlocks][128];
+    float col_scale[kPairScaleSlots][kPairScaleBlocks][kPairN];
+    uint64_t full[2 * kPairStages], empty[kPairStages],   // full: of the stage's even and odd uses
+        acc_full[2], drained[2];
     uint64_t sc_full[kPairScaleSlots], sc_empty[kPairScaleSlots];
     uint32_t tmem_base;
     int abort_flag;
@@ -57,10 +87,27 @@ QD void pair_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
     q = r / height;
 }
 
+// A walk over the scale slots: par is the parity of the fill that a reader
+// waits for; a writer waits for the release before it (par ^ 1), which the
+// slots' first use does not need.
+struct Slots {
+    int slot = 0;
+    uint32_t par = 0;
+    bool primed = false;
+    QD void next()
+    {
+        if (++slot == kPairScaleSlots) {
+            slot = 0;
+            par ^= 1;
+            primed = true;
+        }
+    }
+};
+
 // Four consecutive block scales from kb on, the last one repeated past the end.
-QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n, bool vec)
+QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n)
 {
-    if (vec) {   // K / 128 a multiple of 4 and 16-byte aligned rows: kb + 3 exists
+    if ((kb_n & 3) == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {   // kb + 3 exists
         const float4 v = __ldg(reinterpret_cast<const float4 *>(row + (kb < kb_n ? kb : 0)));
         s[0] = v.x;
         s[1] = v.y;
@@ -70,6 +117,49 @@ QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n, bool vec
 #pragma unroll
         for (int j = 0; j < 4; j++) s[j] = __ldg(row + (kb + j < kb_n ? kb + j : kb_n - 1));
     }
+}
+
+// A tile's scales (one warp): four rows of P per lane (row, row + 32, ..), and
+// eight rows of Q from col0 on or, from lanes 0 and 1, those of Q's two
+// 128-row tiles.  Rows outside the matrices have zero products: any scale does.
+template <bool COLS>
+QD bool put_scales(PairSmem &sm, Slots &turn, const MmArgs &g, int row, int col0, int lane, volatile int *stop)
+{
+    constexpr int NQ = COLS ? kPairN / 32 : 1;
+    const int rows_p = (int)g.rows_p, rows_q = (int)g.rows_q, kb_n = (int)g.kblocks;
+    float v[4][4], w[NQ][4];
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const int r = row + 32 * j < rows_p ? row + 32 * j : 0;
+            load_scales4(v[j], g.s_p + (int64_t)(r >> g.shift_p) * kb_n, kb, kb_n);
+        }
+#pragma unroll
+        for (int j = 0; j < NQ; j++) {
+            const int c = col0 + (COLS ? 32 * j + lane : 128 * (lane & 1));
+            load_scales4(w[j], g.s_q + (int64_t)((c < rows_q ? c : 0) >> g.shift_q) * kb_n, kb, kb_n);
+        }
+    };
+    load(0);
+    for (int kb = 0; kb < kb_n; kb += kPairScaleBlocks) {
+        const bool got = !turn.primed || mm_wait(&sm.sc_empty[turn.slot], turn.par ^ 1, stop, g.status);
+        if (!__all_sync(0xFFFFFFFFu, got)) return false;
+#pragma unroll
+        for (int i = 0; i < kPairScaleBlocks; i++) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) sm.row_scale[turn.slot][i][32 * j + lane] = v[j][i];
+            if (COLS) {
+#pragma unroll
+                for (int j = 0; j < NQ; j++) sm.col_scale[turn.slot][i][32 * j + lane] = w[j][i];
+            } else if (lane < 2) {
+                sm.col_scale[turn.slot][i][lane] = w[0][i];
+            }
+        }
+        mbar_arrive(&sm.sc_full[turn.slot]);
+        turn.next();
+        load(kb + kPairScaleBlocks);
+    }
+    return true;
 }
 
 // COLS: Q has a scale per row (1x128 tiles); otherwise one per 128 of its rows.
@@ -92,17 +182,17 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; s++) {
             mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[kPairStages + s], 1);
             mbar_init(&sm.empty[s], 2);   // both CTAs have used it
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&sm.acc_full[b], 1);
-            mbar_init(&sm.acc_empty[b], kPairEpiWarps);
+            mbar_init(&sm.drained[b], 1);
         }
         for (int s = 0; s < kPairScaleSlots; s++) {
             mbar_init(&sm.sc_full[s], 32);
             mbar_init(&sm.sc_empty[s], kPairEpiWarps);
         }
-        mbar_init(&sm.drained, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
@@ -114,8 +204,8 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     const uint32_t tmem = sm.tmem_base;
 
     if (warp < 4) {
-        regs_fewer<56>();
-        if (warp == 0 && lane == 0) {
+        regs_fewer<kPairRegs>();
+        if (warp == 0 && elect_one()) {
             bool ok = true;
             uint32_t issued = 0;
             int s = 0;
@@ -130,9 +220,10 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         break;
                     }
                     uint8_t *st = sm.stage[s];
-                    mbar_arrive_expect_tx(&sm.full[s], kPairStageBytes);
-                    tma_load_tile(st, &map_p, kb * kMmBlock, p0, &sm.full[s]);
-                    tma_load_tile_multicast(st + (128 + 128 * rank) * kMmBlock, &map_q, kb * kMmBlock, q0, &sm.full[s], 3);
+                    uint64_t *const bar = &sm.full[issued % (2 * kPairStages)];
+                    mbar_arrive_expect_tx(bar, kPairStageBytes);
+                    tma_load_tile(st, &map_p, kb * kMmBlock, p0, bar);
+                    tma_load_tile_multicast(st + (128 + 128 * rank) * kMmBlock, &map_q, kb * kMmBlock, q0, bar, 3);
                     issued++;
                     if (++s == kPairStages) {
                         s = 0;
@@ -146,161 +237,140 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 ok = mm_wait(&sm.empty[j % kPairStages], (j / kPairStages) & 1, stop, g.status);
             if (!ok)   // copies in flight land before shared memory goes away
                 for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; j++)
-                    (void)mbar_wait_bounded(&sm.full[j % kPairStages], (j / kPairStages) & 1);
-        } else if (warp == 1 && lane == 0) {
-            int s = 0, buf = 0;
-            uint32_t par = 0, acc_use = 1;
-            bool ok = true, primed = false;   // primed: both buffers have been used
-            for (int t = first; t < tiles && ok; t += pairs) {
-                for (int kb = 0; kb < kb_n; kb++) {
-                    if (!mm_wait(&sm.full[s], par, stop, g.status) ||
-                        (primed && !mm_wait(&sm.acc_empty[buf], acc_use, stop, g.status))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t a = smem_desc_k128(sm.stage[s]);
-                    const uint64_t b = smem_desc_k128(sm.stage[s] + 128 * kMmBlock);
+                    (void)mbar_wait_bounded(&sm.full[j % (2 * kPairStages)], (j / (2 * kPairStages)) & 1);
+        } else if (warp < 3 && warp > 0) {
+            // One warp per accumulator buffer: every other block.  (Of three stages it
+            // uses each every other time, so the uses count on six barriers: on three
+            // it could take a phase's parity for that of the phase before.)
+            const int buf = warp - 1;
+            const uint32_t blocks = first < tiles ? (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)kb_n : 0u;
+            const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * kMmBlock);
+            int s = buf, f = buf;
+            uint32_t par = 0;
+            bool aborted = false;
+            for (uint32_t n = buf; n < blocks; n += 2) {
+                // a wait that gives up raises the flag, here or in the epilogue
+                mm_wait<true>(&sm.full[f], par, stop, g.status);
+                aborted = __any_sync(0xFFFFFFFFu, *stop);
+                if (aborted) break;
+                if (n >= 2) acc_await(buf);   // last: it is what the next MMAs wait for
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t at = (uint64_t)(s * (kPairStageBytes >> 4));
 #pragma unroll
                     for (int k = 0; k < kMmBlock / 32; k++)
-                        mma_f8(tmem + buf * kPairN, a + 2 * k, b + 2 * k, idesc_e4m3(128, kPairN), k > 0);
+                        mma_f8(tmem + buf * kPairN, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e4m3(128, kPairN), k > 0);
                     mma_commit(&sm.acc_full[buf]);
                     mma_commit_multicast(&sm.empty[s], 3);
-                    if (++s == kPairStages) {
-                        s = 0;
-                        par ^= 1;
-                    }
-                    buf ^= 1;
-                    if (buf == 0) {
-                        acc_use ^= 1;
-                        primed = true;
-                    }
+                }
+                __syncwarp();
+                s += 2;
+                if (s >= kPairStages) s -= kPairStages;
+                f += 2;
+                if (f >= 2 * kPairStages) {
+                    f -= 2 * kPairStages;
+                    par ^= 1;
                 }
             }
-            if (!ok) {   // MMAs in flight end before their memory goes away
-                mma_commit(&sm.drained);
-                (void)mbar_wait_bounded(&sm.drained, 0);
+            if (aborted && elect_one()) {   // MMAs in flight end before their memory goes away
+                mma_commit(&sm.drained[buf]);
+                (void)mbar_wait_bounded(&sm.drained[buf], 0);
             }
-        } else if (COLS && warp == 2) {
-            // lane l fetches columns l, l + 32, ..: a block's scales are 256 words, 4 K/128 bytes apart
-            int slot = 0;
-            uint32_t use = 1;
-            bool ok = true, primed = false;
+        } else if (warp == 3) {
+            // Lane l fetches rows l, l + 32, .. of both operands.  The next four
+            // blocks' scales are on their way while four wait for a slot.
+            bool ok = true;
+            Slots turn;
             for (int t = first; t < tiles && ok; t += pairs) {
                 int tp, tq;
                 pair_tile(t, tiles_p, tiles_q, tp, tq);
-                uint32_t src[kPairN / 32];   // words from s_q; K rows_q is below 2^39, so they fit
-#pragma unroll
-                for (int j = 0; j < kPairN / 32; j++) {
-                    const int col = tq * kPairN + j * 32 + lane;
-                    src[j] = (uint32_t)((col < rows_q ? col : 0) >> g.shift_q) * (uint32_t)kb_n;   // past the result: any scale
-                }
-                float v[kPairN / 32];
-#pragma unroll
-                for (int j = 0; j < kPairN / 32; j++) v[j] = __ldg(g.s_q + src[j]);
-                for (int kb = 0; kb < kb_n; kb++) {
-                    float next[kPairN / 32];
-                    const int kn = kb + 1 < kb_n ? kb + 1 : kb;
-#pragma unroll
-                    for (int j = 0; j < kPairN / 32; j++) next[j] = __ldg(g.s_q + src[j] + kn);
-                    const bool got = !primed || mm_wait(&sm.sc_empty[slot], use, stop, g.status);
-                    if (!__all_sync(0xFFFFFFFFu, got)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int j = 0; j < kPairN / 32; j++) {
-                        sm.col_scale[slot][j * 32 + lane] = v[j];
-                        v[j] = next[j];
-                    }
-                    mbar_arrive(&sm.sc_full[slot]);
-                    if (++slot == kPairScaleSlots) {
-                        slot = 0;
-                        use ^= 1;
-                        primed = true;
-                    }
-                }
+                ok = put_scales<COLS>(sm, turn, g, tp * 256 + 128 * (int)rank + lane, tq * kPairN, lane, stop);
             }
         }
     } else {
-        regs_more<224>();
+        regs_more<kPairEpiRegs>();
         const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tensor memory lanes, 128 columns
         const uint32_t acc_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
-        const bool vec = (kb_n & 3) == 0 && ((reinterpret_cast<uintptr_t>(g.s_p) | reinterpret_cast<uintptr_t>(g.s_q)) & 15) == 0;
-        int buf = 0, slot = 0;
-        uint32_t par = 0, sc_par = 0;
+        int buf = 0;
+        uint32_t par = 0;
         bool ok = true;
+        Slots turn;
         for (int t = first; t < tiles && ok; t += pairs) {
             int tp, tq;
             pair_tile(t, tiles_p, tiles_q, tp, tq);
-            const int row0 = tp * 256 + 128 * rank + quad * 32, row = row0 + lane, col0 = tq * kPairN + half * 128;
-            // rows and columns outside the result have zero products: any scale in bounds does
-            const float *sp = g.s_p + (int64_t)((row < rows_p ? row : 0) >> g.shift_p) * kb_n;
-            const float *sq = g.s_q + (int64_t)((col0 < rows_q ? col0 : 0) >> g.shift_q) * kb_n;
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; j++) acc[j] = 0ull;
-            float sp_next[4], sq_next[4];
-            load_scales4(sp_next, sp, 0, kb_n, vec);
-            if (!COLS) load_scales4(sq_next, sq, 0, kb_n, vec);
-            float s4[4];   // the scales of blocks kb .. kb | 3, the current one first
+#pragma unroll 1
             for (int kb = 0; kb < kb_n; kb++) {
-                if ((kb & 3) == 0) {
+                const int i = kb % kPairScaleBlocks;
+                bool got = i != 0 || mm_wait(&sm.sc_full[turn.slot], turn.par, stop, g.status);
+                const float *const rs = sm.row_scale[turn.slot][i] + quad * 32;
+                const float *const cs = sm.col_scale[turn.slot][i];
+                // a block's scales: a row's and the column tile's product, or four rows'.
+                // With column scales a thread's 128 sums lie in 4 rows and 32 columns, so
+                // that it needs 32 of them per block and not 128: shared memory returns
+                // 128 bytes a cycle to the whole SM, and 128 took twice as long as the MMAs
+                uint64_t ss[COLS ? 4 : 1];
 #pragma unroll
-                    for (int i = 0; i < 4; i++) s4[i] = COLS ? sp_next[i] : sp_next[i] * sq_next[i];
-                    load_scales4(sp_next, sp, kb + 4, kb_n, vec);   // used four blocks from here
-                    if (!COLS) load_scales4(sq_next, sq, kb + 4, kb_n, vec);
+                for (int k = 0; k < (COLS ? 4 : 1); k++) {
+                    const uint32_t s = __float_as_uint(COLS ? rs[8 * k + (lane >> 2)] : rs[lane] * cs[half]);
+                    ss[k] = pack2(s, s);
                 }
-                bool got = mm_wait(&sm.acc_full[buf], par, stop, g.status);
-                if (COLS) got = got && mm_wait(&sm.sc_full[slot], sc_par, stop, g.status);
+                got = got && mm_wait<true>(&sm.acc_full[buf], par, stop, g.status);
                 if (!__all_sync(0xFFFFFFFFu, got)) {
+                    *stop = 1;
+                    __syncwarp();
+                    acc_release(0);   // the MMA warps may be waiting there
+                    acc_release(1);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ss = pack2(__float_as_uint(s4[0]), __float_as_uint(s4[0]));
-                s4[0] = s4[1];
-                s4[1] = s4[2];
-                s4[2] = s4[3];
-                // the load of 16 columns runs while the 16 before it are added
-                uint32_t r[2][16];
-                tmem_ld16(r[0], acc_addr + buf * kPairN);
-                tmem_wait_ld(r[0]);
+                const uint32_t addr = acc_addr + buf * kPairN;
+                uint32_t r[2][16];   // 16 columns are added while the next 16 are read
+                if constexpr (!COLS) {
+                    tmem_ld16(r[0], addr);
 #pragma unroll
-                for (int h = 0; h < 8; h++) {
-                    const uint32_t(&now)[16] = r[h & 1];
-                    if (h < 7) {
-                        tmem_ld16(r[(h + 1) & 1], acc_addr + buf * kPairN + (h + 1) * 16);
-                    } else {   // all read: the next block may go there
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
-                    }
+                    for (int h = 0; h < 7; h++) tmem_ld16_add(r[(h + 1) & 1], addr + (h + 1) * 16, r[h & 1], acc + h * 8, ss[0]);
+                    tc_fence_before();
+                    acc_release(buf);   // all read: the next block may go there
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        uint64_t v0 = pack2(now[2 * j], now[2 * j + 1]), v1 = pack2(now[2 * j + 2], now[2 * j + 3]);
-                        if (COLS) {
-                            const ulonglong2 cs = *reinterpret_cast<const ulonglong2 *>(&sm.col_scale[slot][half * 128 + h * 16 + 2 * j]);
-                            v0 = fmul2(v0, cs.x);
-                            v1 = fmul2(v1, cs.y);
+                    for (int j = 0; j < 8; j++) acc[56 + j] = ffma2(pack2(r[1][2 * j], r[1][2 * j + 1]), ss[0], acc[56 + j]);
+                } else {
+                    const float *const cl = cs + half * 128 + 2 * (lane & 3);
+                    uint64_t cc[4];
+                    tmem_ld_rows16(r[0], addr);
+#pragma unroll
+                    for (int h = 0; h < 8; h++) {   // 32 columns, rows 0-15 and 16-31 of the 32
+                        if (h % 2 == 0) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) cc[k] = *reinterpret_cast<const uint64_t *>(cl + (h / 2) * 32 + k * 8);
                         }
-                        acc[h * 8 + j] = ffma2(v0, ss, acc[h * 8 + j]);
-                        acc[h * 8 + j + 1] = ffma2(v1, ss, acc[h * 8 + j + 1]);
+                        const uint64_t s0 = ss[2 * (h & 1)], s1 = ss[2 * (h & 1) + 1];
+                        if (h < 7) {
+                            const int n = h + 1;
+                            tmem_ld_rows16_add(r[n & 1], addr + (n / 2) * 32 + ((uint32_t)(16 * (n & 1)) << 16), r[h & 1], acc + h * 8, cc, s0, s1);
+                        } else {
+                            tc_fence_before();
+                            acc_release(buf);   // all read: the next block may go there
+#pragma unroll
+                            for (int j = 0; j < 8; j++)
+                                acc[56 + j] = ffma2(fmul2(pack2(r[1][2 * j], r[1][2 * j + 1]), cc[j >> 1]), j & 1 ? s1 : s0, acc[56 + j]);
+                        }
                     }
-                    if (h < 7) tmem_wait_ld(r[(h + 1) & 1]);
                 }
-                if (COLS) {
+                if (i == kPairScaleBlocks - 1 || kb + 1 == kb_n) {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.sc_empty[slot]);
-                    if (++slot == kPairScaleSlots) {
-                        slot = 0;
-                        sc_par ^= 1;
-                    }
+                    if (lane == 0) mbar_arrive(&sm.sc_empty[turn.slot]);
+                    turn.next();
                 }
                 buf ^= 1;
                 if (buf == 0) par ^= 1;
             }
-            if (ok) mm_store_rows<OUT>(g, &map_c, sm.staging[warp - 4], acc, row0, col0, lane);
+            if (ok)
+                mm_store_tile<OUT, !COLS>(g, &map_c, sm.staging[warp - 4], acc, tp * 256 + 128 * (int)rank + quad * 32,
+                                          tq * kPairN + half * 128, lane);
         }
         if (lane == 0) bulk_wait_all();
     }

@@ -134,6 +134,8 @@ QD void tma_store_tile(const CUtensorMap *map, const void *src, int x, int y)
 QD void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's committed bulk stores have finished reading shared memory.
 QD void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// All but the newest of them have.
+QD void bulk_wait_read_but1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 // This thread's committed bulk stores are complete.
 QD void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Barrier `id` (1..15) among `count` threads (whole warps).

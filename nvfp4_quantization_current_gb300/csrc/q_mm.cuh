@@ -24,16 +24,19 @@ struct MmArgs {
 };
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the
-// wait ran out (which raises it and reports the timeout).
-QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+// wait ran out (which raises it and reports the timeout).  SPIN polls without
+// giving up the issue slot: the waiting warp sees the phase about 130 cycles
+// sooner than one that the hardware wakes, which pays for the two waits in
+// the chain of an accumulator buffer.
+template <bool SPIN = false> QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
     // The timer is read once in many polls: a read takes about as long as a
     // block's MMAs, and these waits are on the path of every block.
     unsigned long long t0 = 0;
     for (uint32_t n = 1;; n++) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
+        if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (n % 1024 == 0) {
+            if (*abort_flag) return false;
             const unsigned long long now = globaltimer();
             if (t0 == 0) t0 = now;
             if (now - t0 > kWaitNs) {
@@ -70,71 +73,91 @@ QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)
                  ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
-// One warp's sums, 32 rows (one per lane, from row0) x 128 columns (from
-// col0), to C through its 4 KiB of staging: 32 rows x 128 bytes at a time, the
-// 16-byte piece i of row r at place i ^ (r % 8), which is the 128-byte swizzle
-// of the bulk store and spreads the lanes' rows over the banks.  Rows and
-// columns outside C are cut off by the store.  C's whose rows are no multiple
-// of 16 bytes, and sums onto a BF16 C, are written by the lanes themselves,
-// one row at a time, from FP32 staging (so that a sum is rounded once).
-template <int OUT>
-QD void mm_store_rows(const MmArgs &g, const CUtensorMap *map_c, uint8_t *stg, const uint64_t (&acc)[64], int64_t row0,
+// One warp's sums, 32 rows (from row0) x 128 columns (from col0), to C in
+// pieces of 32 rows x 128 bytes through its two 4 KiB staging buffers: the
+// 16-byte chunk i of row r at place i ^ (r % 8), which is the 128-byte swizzle
+// of the bulk store and keeps the lanes' accesses off each other's banks.
+// Rows and columns outside C are cut off by the store.  C's whose rows are no
+// multiple of 16 bytes, and sums onto a BF16 C, are written by the lanes
+// themselves, one row at a time, from FP32 staging (so that a sum is rounded
+// once).
+//
+// ROWS: thread t holds row t, acc[j] columns 2j and 2j + 1.  Otherwise
+// acc[16c + 8h + 2i + k] is row 16h + 8k + t / 4, columns 32c + 8i + 2 (t % 4)
+// and the next (tmem_ld_rows16).
+template <int OUT, bool ROWS>
+QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *staging, const uint64_t (&acc)[64], int64_t row0,
                       int64_t col0, int lane)
 {
     using T = typename OutT<OUT>::T;
     const bool bulk = g.store != kStoreDirect;
-    auto slot = [&](int r, int i) { return stg + r * 128 + ((i ^ (r & 7)) << 4); };
+    auto place = [&](uint8_t *buf, int r, int i) { return buf + r * 128 + ((i ^ (r & 7)) << 4); };
+    auto claim = [&](int piece) {   // the piece before the last one has left this buffer
+        if (bulk && lane == 0) bulk_wait_read_but1();
+        __syncwarp();
+        return staging + (piece & 1) * 4096;
+    };
+    auto send = [&](const uint8_t *buf, int64_t col) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0 && row0 < g.rows_p && col < g.rows_q) {
+            if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, buf, (int)col, (int)row0);
+            else tma_store_tile(map_c, buf, (int)col, (int)row0);
+            bulk_commit();
+        }
+    };
     if (OUT == BF16 && bulk) {
 #pragma unroll
-        for (int pass = 0; pass < 2; pass++) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
+        for (int p = 0; p < 2; p++) {
+            uint8_t *buf = claim(p);
+            if constexpr (ROWS) {
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                uint32_t w[4];
+                for (int i = 0; i < 8; i++) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    float a, b;
-                    unpack2(acc[pass * 32 + i * 4 + j], a, b);
-                    w[j] = bf16_pair(a, b);
+                    for (int j = 0; j < 4; j++) {
+                        float a, b;
+                        unpack2(acc[p * 32 + i * 4 + j], a, b);
+                        w[j] = bf16_pair(a, b);
+                    }
+                    *reinterpret_cast<uint4 *>(place(buf, lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *reinterpret_cast<uint4 *>(slot(lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    const int c = j >> 4, h = (j >> 3) & 1, i = (j >> 1) & 3, k = j & 1;
+                    float a, b;
+                    unpack2(acc[p * 32 + j], a, b);
+                    *reinterpret_cast<uint32_t *>(place(buf, 16 * h + 8 * k + (lane >> 2), 4 * c + i) + 4 * (lane & 3)) = bf16_pair(a, b);
+                }
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && row0 < g.rows_p && col0 + pass * 64 < g.rows_q) {
-                tma_store_tile(map_c, stg, (int)(col0 + pass * 64), (int)row0);
-                bulk_commit();
-            }
+            send(buf, col0 + p * 64);
         }
         return;
     }
 #pragma unroll
-    for (int pass = 0; pass < 4; pass++) {
-        if (bulk && lane == 0) bulk_wait_read_all();
-        __syncwarp();
+    for (int p = 0; p < 4; p++) {
+        uint8_t *buf = claim(p);
+        if constexpr (ROWS) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            float a, b, c, d;
-            unpack2(acc[pass * 16 + i * 2], a, b);
-            unpack2(acc[pass * 16 + i * 2 + 1], c, d);
-            *reinterpret_cast<float4 *>(slot(lane, i)) = make_float4(a, b, c, d);
+            for (int i = 0; i < 8; i++)
+                *reinterpret_cast<ulonglong2 *>(place(buf, lane, i)) = make_ulonglong2(acc[p * 16 + i * 2], acc[p * 16 + i * 2 + 1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                const int h = j >> 3, i = (j >> 1) & 3, k = j & 1;
+                *reinterpret_cast<uint64_t *>(place(buf, 16 * h + 8 * k + (lane >> 2), 2 * i + ((lane & 3) >> 1)) + 8 * (lane & 1)) = acc[p * 16 + j];
+            }
         }
         if (bulk) {
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0 && row0 < g.rows_p && col0 + pass * 32 < g.rows_q) {
-                if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, stg, (int)(col0 + pass * 32), (int)row0);
-                else tma_store_tile(map_c, stg, (int)(col0 + pass * 32), (int)row0);
-                bulk_commit();
-            }
+            send(buf, col0 + p * 32);
         } else {
             __syncwarp();
-            const int64_t col = col0 + pass * 32 + lane;
+            const int64_t col = col0 + p * 32 + lane;
             for (int r = 0; r < 32 && row0 + r < g.rows_p; r++)
                 if (col < g.rows_q)
                     put_one<OUT>(static_cast<T *>(g.c) + (row0 + r) * g.ldc + col,
-                                 *reinterpret_cast<const float *>(slot(r, lane >> 2) + (lane & 3) * 4), g.accumulate);
+                                 *reinterpret_cast<const float *>(place(buf, r, lane >> 2) + (lane & 3) * 4), g.accumulate);
         }
     }
 }
