@@ -14,16 +14,18 @@
 // accumulators in registers.  The FP8 products are exact in FP32; a result is
 // rounded once more, to the output type.
 //
-// A CTA owns a 128 x 128 tile of C.  Warp 4 streams operand tiles (128 rows x
-// 128 bytes each, TMA into the 128-byte swizzle, kStages in flight), one
-// thread of warp 5 issues the MMAs of a block into one of two accumulator
-// buffers, and warps 0-3 (one thread per row) scale and add the other.
+// Two kernels: k_mm_pair.cuh for results of many tiles, k_mm_split.cuh for few
+// tokens and for results of few tiles.  In both, one warp streams operand tiles
+// (128 bytes of each row per stage, TMA into the 128-byte swizzle), one thread
+// issues a block's MMAs into one of several accumulator buffers, and other
+// warps scale and add the buffers that are done.
 //
 // Every wait is bounded; a role that gives up reports Q_ST_TIMEOUT, raises the
 // CTA's abort flag, which ends the other roles' waits, and the copies and MMAs
 // in flight are waited for (bounded again) before shared and tensor memory go
 // away.
 #include "k_mm_pair.cuh"
+#include "k_mm_split.cuh"
 #include "q_internal.h"
 #include "q_mm.cuh"
 
@@ -31,139 +33,29 @@ namespace qk {
 
 namespace {
 
-constexpr int kMmThreads = 192, kMmStages = 6, kMmN = 128;
-constexpr int kMmStageBytes = (128 + kMmN) * kMmBlock;
-constexpr int kMmSmem = kMmStages * kMmStageBytes + 1024;
-
-template <int OUT>
-__global__ void __launch_bounds__(kMmThreads, 1)
-k_mm_blockwise(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const MmArgs g)
-{
-    extern __shared__ __align__(1024) uint8_t dsm[];
-    __shared__ __align__(8) uint64_t full[kMmStages], empty[kMmStages], acc_full[2], acc_empty[2], drained;
-    __shared__ __align__(16) float col_scale[2][kMmN];
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag;
-    uint8_t *stages = dsm + ((1024u - (smem_u32(dsm) & 1023u)) & 1023u);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t p0 = (int64_t)blockIdx.x * 128, q0 = (int64_t)blockIdx.y * kMmN;
-    const int kb_n = (int)g.kblocks;
-
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kMmStages; s++) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; b++) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 128);
-        }
-        mbar_init(&drained, 1);
-        abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 5) tmem_alloc<2 * kMmN>(&tmem_base);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base;
-    volatile int *const stop = &abort_flag;
-
-    if (warp == 4) {
-        if (lane == 0) {
-            int kb = 0;
-            for (; kb < kb_n; kb++) {
-                const int s = kb % kMmStages;
-                if (kb >= kMmStages && !mm_wait(&empty[s], ((kb / kMmStages) & 1) ^ 1, stop, g.status)) break;
-                uint8_t *st = stages + s * kMmStageBytes;
-                mbar_arrive_expect_tx(&full[s], kMmStageBytes);
-                tma_load_tile(st, &map_p, kb * kMmBlock, (int)p0, &full[s]);
-                tma_load_tile(st + 128 * kMmBlock, &map_q, kb * kMmBlock, (int)q0, &full[s]);
-            }
-            if (kb < kb_n)   // aborted: the copies in flight land before shared memory goes away
-                for (int j = kb > kMmStages ? kb - kMmStages : 0; j < kb; j++)
-                    (void)mbar_wait_bounded(&full[j % kMmStages], (j / kMmStages) & 1);
-        }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            int kb = 0;
-            for (; kb < kb_n; kb++) {
-                const int s = kb % kMmStages, buf = kb & 1;
-                if (kb >= 2 && !mm_wait(&acc_empty[buf], ((kb >> 1) & 1) ^ 1, stop, g.status)) break;
-                if (!mm_wait(&full[s], (kb / kMmStages) & 1, stop, g.status)) break;
-                tc_fence_after();
-                const uint64_t a = smem_desc_k128(stages + s * kMmStageBytes);
-                const uint64_t b = smem_desc_k128(stages + s * kMmStageBytes + 128 * kMmBlock);
-#pragma unroll
-                for (int k = 0; k < kMmBlock / 32; k++)
-                    mma_f8(tmem + buf * kMmN, a + 2 * k, b + 2 * k, idesc_e4m3(128, kMmN), k > 0);
-                mma_commit(&empty[s]);
-                mma_commit(&acc_full[buf]);
-            }
-            if (kb < kb_n) {   // aborted: the MMAs in flight end before their memory goes away
-                mma_commit(&drained);
-                (void)mbar_wait_bounded(&drained, 0);
-            }
-        }
-    } else {
-        const int64_t row = p0 + threadIdx.x;
-        const bool live = row < g.rows_p;
-        const float *sp = g.s_p + ((live ? row : 0) >> g.shift_p) * g.kblocks;
-        const int64_t col = q0 + threadIdx.x;   // the column whose scale this thread fetches
-        const bool col_live = col < g.rows_q;
-        const float *sq = g.s_q + ((col_live ? col : 0) >> g.shift_q) * g.kblocks;
-        float acc[kMmN];
-#pragma unroll
-        for (int j = 0; j < kMmN; j++) acc[j] = 0.0f;
-        for (int kb = 0; kb < kb_n; kb++) {
-            const int buf = kb & 1;
-            const float srow = sp[kb];
-            col_scale[buf][threadIdx.x] = col_live ? sq[kb] : 0.0f;
-            named_barrier(1, 128);   // also: every thread is done with this buffer's previous scales
-            bool ok = mm_wait(&acc_full[buf], (kb >> 1) & 1, stop, g.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) ok = false;
-            if (ok) {
-                tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < kMmN / 32; h++) {
-                    uint32_t r[32];
-                    tmem_ld32(r, tmem + ((uint32_t)(warp * 32) << 16) + buf * kMmN + h * 32);
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        acc[h * 32 + j] = __fmaf_rn(__uint_as_float(r[j]) * col_scale[buf][h * 32 + j], srow, acc[h * 32 + j]);
-                }
-                tc_fence_before();
-            }
-            mbar_arrive(&acc_empty[buf]);
-        }
-        if (live) {
-            using T = typename OutT<OUT>::T;
-            T *out = static_cast<T *>(g.c) + row * g.ldc + q0;
-#pragma unroll
-            for (int j = 0; j < kMmN; j++)
-                if (q0 + j < g.rows_q) put_one<OUT>(out + j, acc[j], g.accumulate);
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 5) tmem_free<2 * kMmN>(tmem);
-}
-
-// Tiles of 128 x 128, one per CTA.
-template <int OUT>
-cudaError_t mm_one(const uint8_t *p, const uint8_t *q, const MmArgs &g, cudaStream_t st)
+// Tiles of 128 weights x BN tokens, the reduction of each split over a cluster.
+template <int OUT, int BN>
+cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int split, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q;
     const int64_t K = g.kblocks * kMmBlock;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K, 128);
-    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K, kMmN);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm_blockwise<OUT>>(kMmSmem);
+    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K, BN);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm_split<OUT, BN>>(sizeof(SplitSmem<BN>), true);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((g.rows_p + 127) / 128), (unsigned)((g.rows_q + kMmN - 1) / kMmN));
-    k_mm_blockwise<OUT><<<grid, kMmThreads, kMmSmem, st>>>(map_p, map_q, g);
-    return cudaGetLastError();
+    const int64_t ty = (g.rows_p + 127) / 128, tz = (g.rows_q + BN - 1) / BN;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split, (unsigned)ty, (unsigned)tz);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = sizeof(SplitSmem<BN>);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_mm_split<OUT, BN>, map_p, map_q, g);
 }
 
 // Tiles of 256 x 256 on CTA pairs.
@@ -196,11 +88,29 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
 }
 
 template <int OUT>
-cudaError_t mm_t(const uint8_t *p, const uint8_t *q, const MmArgs &g, cudaStream_t st)
+cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream_t st)
 {
-    if (g.rows_p > 512)
-        return g.shift_q ? mm_pair<OUT, false>(p, q, g, st) : mm_pair<OUT, true>(p, q, g, st);
-    return mm_one<OUT>(p, q, g, st);
+    const int64_t M = g.rows_p, N = g.rows_q;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t ty = (N + 127) / 128, tz = (M + bn - 1) / bn;
+    if ((M > 128 && pair_tiles > sm_count() / 2) || ty > 65535 || tz > 65535)
+        return g.shift_q ? mm_pair<OUT, false>(a, b, g, st) : mm_pair<OUT, true>(a, b, g, st);
+    int split = 1;
+    while (split < kSplitMost && 2 * split * ty * tz <= 2 * sm_count() && 4 * split <= g.kblocks) split *= 2;
+    MmArgs w = g;   // the weights on the lanes
+    w.s_p = g.s_q;
+    w.s_q = g.s_p;
+    w.rows_p = N;
+    w.rows_q = M;
+    w.shift_p = g.shift_q;
+    w.shift_q = g.shift_p;
+    switch (bn) {
+    case 16: return mm_split<OUT, 16>(b, a, w, split, st);
+    case 32: return mm_split<OUT, 32>(b, a, w, split, st);
+    case 64: return mm_split<OUT, 64>(b, a, w, split, st);
+    default: return mm_split<OUT, 128>(b, a, w, split, st);
+    }
 }
 
 }  // namespace
