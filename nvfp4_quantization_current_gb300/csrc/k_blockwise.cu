@@ -439,7 +439,7 @@ cudaError_t launch_drop_q_blockwise(const void *x, int dt, int64_t M, int64_t K,
                                     uint64_t offset, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
                                     int32_t *status, cudaStream_t st)
 {
-    const DropArgs d = {philox_keys(seed), offset, threshold, c};
+    const DropArgs d = drop_args(seed, offset, threshold, c);
     return dt == BF16 ? bw_t<BF16, 0, false, DropArgs>(x, M, K, q_row, s_row, q_colT, s_colT, status, st, d)
                       : bw_t<F32, 0, false, DropArgs>(x, M, K, q_row, s_row, q_colT, s_colT, status, st, d);
 }

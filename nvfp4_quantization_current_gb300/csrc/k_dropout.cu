@@ -2,8 +2,13 @@
 // drawn again from the counter (q_dropout.cuh) wherever they are needed.  The
 // backward pass is the same kernel on dy without a residual.
 //
-// One thread takes the eight elements of a Philox block: the sum is formed in
-// FP32 (one fused multiply-add) and rounded once to the output type.
+// Bound by memory (two or three tensors of n elements against ten Philox
+// rounds per eight): a thread takes the eight elements of kDropUnroll Philox
+// blocks, in 16-byte pieces that are all on their way before the first draw is
+// computed.  The sum is formed in FP32 (one fused multiply-add) and rounded
+// once to the output type.
+#include <type_traits>
+
 #include "q_dropout.cuh"
 #include "q_internal.h"
 
@@ -11,41 +16,94 @@ namespace qk {
 
 namespace {
 
-constexpr int kDropThreads = 256;
+constexpr int kDropThreads = 256, kDropUnroll = 4;
 
-template <int DT> QD float load_one(const void *p, int64_t i);
-template <> QD float load_one<BF16>(const void *p, int64_t i)
+// 16 bytes that this thread alone reads, and may overwrite (y may be x).
+QD uint4 load16(const void *p)
 {
-    return __uint_as_float((uint32_t)static_cast<const uint16_t *>(p)[i] << 16);
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
-template <> QD float load_one<F32>(const void *p, int64_t i) { return static_cast<const float *>(p)[i]; }
 
-template <int DT> QD void store_one(void *p, int64_t i, float v);
-template <> QD void store_one<BF16>(void *p, int64_t i, float v) { static_cast<uint16_t *>(p)[i] = (uint16_t)bf16_bits(v); }
-template <> QD void store_one<F32>(void *p, int64_t i, float v) { static_cast<float *>(p)[i] = v; }
+template <bool RES> QD float drop_sum(float x, float r, bool keep, float c)
+{
+    return keep ? (RES ? __fmaf_rn(x, c, r) : __fmul_rn(x, c)) : r;
+}
+
+// Eight elements as 16-byte vectors: one of BF16, two of FP32.
+template <int DT> struct Eight {
+    static constexpr int N = DT == BF16 ? 1 : 2;
+    uint4 v[N];
+    QD void load(const void *p, int64_t block)
+    {
+#pragma unroll
+        for (int i = 0; i < N; i++) v[i] = load16(static_cast<const uint4 *>(p) + block * N + i);
+    }
+    QD void store(void *p, int64_t block) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; i++) stg16(static_cast<uint4 *>(p) + block * N + i, v[i]);
+    }
+    QD float at(int j) const { return DT == BF16 ? elem<BF16>(v[0], j) : elem<F32>(v[(j >> 2) % N], j & 3); }
+};
+
+template <int DT, bool RES> QD Eight<DT> drop_eight(const Eight<DT> &x, const Eight<DT> &r, uint64_t block, const DropArgs &d)
+{
+    const uint4 draws = drop_draws(block, d);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) y[j] = drop_sum<RES>(x.at(j), RES ? r.at(j) : 0.0f, drop_keep(draws, j, d.threshold), d.c);
+    Eight<DT> out;
+    if constexpr (DT == BF16) {
+        out.v[0] = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            out.v[i] = make_uint4(__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                                  __float_as_uint(y[4 * i + 3]));
+    }
+    return out;
+}
 
 template <int DT, bool RES>
 __global__ void __launch_bounds__(kDropThreads)
 k_drop_add(const void *x, const void *residual, void *y, int64_t n, const DropArgs d)
 {
-    const int64_t b = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
-    if (b * 8 >= n) return;
-    const uint4 draws = drop_draws((uint64_t)b, d);
+    const int64_t b0 = (int64_t)blockIdx.x * (kDropThreads * kDropUnroll) + threadIdx.x, blocks = n / 8;
+    Eight<DT> vx[kDropUnroll], vr[kDropUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const int64_t i = b * 8 + j;
-        if (i < n) {
-            const float v = load_one<DT>(x, i), r = RES ? load_one<DT>(residual, i) : 0.0f;
-            const float kept = RES ? __fmaf_rn(v, d.c, r) : __fmul_rn(v, d.c);
-            store_one<DT>(y, i, drop_keep(draws, j, d.threshold) ? kept : r);
+    for (int u = 0; u < kDropUnroll; u++) {
+        const int64_t b = b0 + u * kDropThreads;
+        if (b < blocks) {
+            vx[u].load(x, b);
+            if (RES) vr[u].load(residual, b);
         }
+    }
+#pragma unroll
+    for (int u = 0; u < kDropUnroll; u++) {
+        const int64_t b = b0 + u * kDropThreads;
+        if (b < blocks) drop_eight<DT, RES>(vx[u], vr[u], (uint64_t)b, d).store(y, b);
+    }
+    if (blockIdx.x == 0 && threadIdx.x < (n & 7)) {   // what is left of the last block
+        const int64_t i = blocks * 8 + threadIdx.x;
+        const bool keep = drop_keep(drop_draws((uint64_t)blocks, d), threadIdx.x, d.threshold);
+        using T = typename std::conditional<DT == BF16, uint16_t, float>::type;
+        auto value = [&](const void *p) {
+            if constexpr (DT == BF16) return __uint_as_float((uint32_t) static_cast<const T *>(p)[i] << 16);
+            else return static_cast<const T *>(p)[i];
+        };
+        const float v = drop_sum<RES>(value(x), RES ? value(residual) : 0.0f, keep, d.c);
+        if constexpr (DT == BF16) static_cast<T *>(y)[i] = (T)bf16_bits(v);
+        else static_cast<T *>(y)[i] = v;
     }
 }
 
 template <int DT>
 cudaError_t drop_t(const void *x, int64_t n, const void *residual, const DropArgs &d, void *y, cudaStream_t st)
 {
-    const int64_t grid = ((n + 7) / 8 + kDropThreads - 1) / kDropThreads;
+    const int64_t per = 8 * kDropThreads * kDropUnroll, grid = (n + per - 1) / per;
     if (residual != nullptr) k_drop_add<DT, true><<<(unsigned)grid, kDropThreads, 0, st>>>(x, residual, y, n, d);
     else k_drop_add<DT, false><<<(unsigned)grid, kDropThreads, 0, st>>>(x, nullptr, y, n, d);
     return cudaGetLastError();
@@ -56,7 +114,7 @@ cudaError_t drop_t(const void *x, int64_t n, const void *residual, const DropArg
 cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residual, uint32_t threshold, float c,
                             uint64_t seed, uint64_t offset, void *y, cudaStream_t st)
 {
-    const DropArgs d = {philox_keys(seed), offset, threshold, c};
+    const DropArgs d = drop_args(seed, offset, threshold, c);
     return dt == BF16 ? drop_t<BF16>(x, n, residual, d, y, st) : drop_t<F32>(x, n, residual, d, y, st);
 }
 

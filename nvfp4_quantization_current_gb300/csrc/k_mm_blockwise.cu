@@ -46,7 +46,7 @@ cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int sp
     const int64_t ty = (g.rows_p + 127) / 128, tz = (g.rows_q + BN - 1) / BN;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split, (unsigned)ty, (unsigned)tz);
-    cfg.blockDim = dim3(kSplitThreads);
+    cfg.blockDim = dim3(SplitSmem<BN>::kThreads);
     cfg.dynamicSmemBytes = sizeof(SplitSmem<BN>);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -87,17 +87,43 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
     return cudaGetLastError();
 }
 
+// Which kernel, and how wide and how deep a split: the least estimated time on
+// `sms` SMs, in cycles.  What was measured on a GB300: a CTA's block of 128 x bn
+// results costs what shared memory takes to write and read its operands once,
+// 2 (128 + bn) cycles; a 256 x 256 block of the pair kernel about 1000; and
+// beside its blocks a CTA spends about 6000 on its way in and out, and 1500
+// more where a cluster adds up.
+struct MmPlan {
+    int bn, split;   // bn 0: the pair kernel
+};
+MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, int sms)
+{
+    const int64_t ty = (N + 127) / 128, pairs = sms / 2;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
+    MmPlan best = {0, 1};
+    int64_t cost = 8000 + (pair_tiles + pairs - 1) / pairs * (kblocks * 1000 + 2500);
+    for (int bn : {16, 32, 64, 128, 192, 256}) {
+        const int64_t tz = (M + bn - 1) / bn;
+        if ((bn > 16 && M <= bn / 2) || ty > 65535 || tz > 65535) continue;
+        for (int split = 1; split <= kSplitMost; split *= 2) {
+            if (split > 1 && 2 * split > kblocks) break;
+            const int64_t waves = (ty * tz * split + sms - 1) / sms;
+            const int64_t c = waves * ((kblocks + split - 1) / split * 2 * (128 + bn) + 2000) + 4000 + (split > 1 ? 1500 : 0);
+            if (c < cost) {
+                cost = c;
+                best = {bn, split};
+            }
+        }
+    }
+    return best;
+}
+
 template <int OUT>
 cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream_t st)
 {
     const int64_t M = g.rows_p, N = g.rows_q;
-    const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
-    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    const int64_t ty = (N + 127) / 128, tz = (M + bn - 1) / bn;
-    if ((M > 128 && pair_tiles > sm_count() / 2) || ty > 65535 || tz > 65535)
-        return g.shift_q ? mm_pair<OUT, false>(a, b, g, st) : mm_pair<OUT, true>(a, b, g, st);
-    int split = 1;
-    while (split < kSplitMost && 2 * split * ty * tz <= 2 * sm_count() && 4 * split <= g.kblocks) split *= 2;
+    const MmPlan plan = mm_plan(M, N, g.kblocks, sm_count());
+    const int split = plan.split;
     MmArgs w = g;   // the weights on the lanes
     w.s_p = g.s_q;
     w.s_q = g.s_p;
@@ -105,11 +131,14 @@ cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream
     w.rows_q = M;
     w.shift_p = g.shift_q;
     w.shift_q = g.shift_p;
-    switch (bn) {
+    switch (plan.bn) {
+    case 0: return g.shift_q ? mm_pair<OUT, false>(a, b, g, st) : mm_pair<OUT, true>(a, b, g, st);
     case 16: return mm_split<OUT, 16>(b, a, w, split, st);
     case 32: return mm_split<OUT, 32>(b, a, w, split, st);
     case 64: return mm_split<OUT, 64>(b, a, w, split, st);
-    default: return mm_split<OUT, 128>(b, a, w, split, st);
+    case 128: return mm_split<OUT, 128>(b, a, w, split, st);
+    case 192: return mm_split<OUT, 192>(b, a, w, split, st);
+    default: return mm_split<OUT, 256>(b, a, w, split, st);
     }
 }
 

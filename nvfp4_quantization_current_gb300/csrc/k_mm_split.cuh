@@ -9,9 +9,10 @@
 // memory in rank order, each CTA a slice of the columns.  Nothing is added in
 // an order that depends on timing, and no workspace is needed.
 //
-// Warps 0-3 scale and add (one thread per row), warp 4 loads, warp 5 issues
-// the MMAs.  Two CTAs fit an SM: about 100 KiB of stages each and at most half
-// of tensor memory.
+// The first warps, four or for wide tiles eight, scale and add (one thread per
+// row of their columns), the next loads, the last issues the MMAs.  Up to 128
+// tokens wide, two CTAs fit an SM: about 100 KiB of stages each and at most
+// half of tensor memory.
 #pragma once
 
 #include "q_internal.h"
@@ -19,14 +20,17 @@
 
 namespace qk {
 
-constexpr int kSplitThreads = 192;
 constexpr int kSplitMost = 8;   // CTAs of a cluster
 
 template <int BN> struct SplitSmem {
     static constexpr int kStageBytes = (128 + BN) * kMmBlock;
-    static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 64 ? 4 : 3;
-    static constexpr int kBufs = BN == 128 ? 2 : 4;
-    static constexpr int kCols = BN * kBufs;   // of tensor memory
+    static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 128 ? 3 : 4;
+    static constexpr int kBufs = BN >= 128 ? 2 : 4;
+    static constexpr int kCols = BN == 192 ? 512 : BN * kBufs;   // of tensor memory, a power of two
+    static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
+    static constexpr int kWarpCols = BN / (kEpiWarps / 4);
+    static constexpr int kThreads = 32 * (kEpiWarps + 2);
+    static constexpr int kResident = BN <= 128 ? 2 : 1;         // CTAs of an SM
     uint8_t stage[kStages][kStageBytes];       // afterwards this CTA's sums, [BN][128] FP32
     float col_scale[2][BN];
     uint64_t full[kStages], empty[kStages], acc_full[kBufs], acc_empty[kBufs], drained;
@@ -35,19 +39,25 @@ template <int BN> struct SplitSmem {
     static_assert(kStages * kStageBytes >= BN * 128 * 4, "the sums replace the stages");
 };
 
-QD float ld_cluster(uint32_t addr)
+QD float4 ld_cluster4(uint32_t addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
+}
+QD uint32_t cluster_addr(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
 
 template <int OUT, int BN>
-__global__ void __launch_bounds__(kSplitThreads)
+__global__ void __launch_bounds__(SplitSmem<BN>::kThreads, SplitSmem<BN>::kResident)
 k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const MmArgs g)
 {
     using Smem = SplitSmem<BN>;
-    constexpr int kStages = Smem::kStages, kBufs = Smem::kBufs;
+    constexpr int kStages = Smem::kStages, kBufs = Smem::kBufs, kEpiWarps = Smem::kEpiWarps, kWarpCols = Smem::kWarpCols;
     extern __shared__ __align__(1024) uint8_t dsm[];
     Smem &sm = *reinterpret_cast<Smem *>(dsm);
 
@@ -64,19 +74,19 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         }
         for (int b = 0; b < kBufs; b++) {
             mbar_init(&sm.acc_full[b], 1);
-            mbar_init(&sm.acc_empty[b], 4);
+            mbar_init(&sm.acc_empty[b], kEpiWarps);
         }
         mbar_init(&sm.drained, 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc<Smem::kCols>(&sm.tmem_base);
+    if (warp == kEpiWarps + 1) tmem_alloc<Smem::kCols>(&sm.tmem_base);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    if (warp == 4) {
+    if (warp == kEpiWarps) {
         if (elect_one()) {
             int kb = 0;
             for (; kb < kb_n; kb++) {
@@ -90,7 +100,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                 for (int j = kb > kStages ? kb - kStages : 0; j < kb; j++)
                     (void)mbar_wait_bounded(&sm.full[j % kStages], (j / kStages) & 1);
         }
-    } else if (warp == 5) {
+    } else if (warp == kEpiWarps + 1) {
         bool ok = true;
         for (int kb = 0; kb < kb_n; kb++) {
             const int s = kb % kStages, b = kb % kBufs;
@@ -115,13 +125,14 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         __syncwarp();
     } else {
         const int t = threadIdx.x, kb_all = (int)g.kblocks;
-        const int64_t row = (int64_t)p0 + t, col = (int64_t)q0 + t;
+        const int quad = warp & 3, first = (warp >> 2) * kWarpCols;   // 32 tensor memory lanes, the columns from `first` on
+        const int64_t row = (int64_t)p0 + quad * 32 + lane, col = (int64_t)q0 + t;
         // rows and columns outside the result have zero products: any scale in bounds does
         const float *sp = g.s_p + ((row < g.rows_p ? row : 0) >> g.shift_p) * g.kblocks;
         const float *sq = g.s_q + ((col < g.rows_q ? col : 0) >> g.shift_q) * g.kblocks;
-        float acc[BN];
+        float acc[kWarpCols];
 #pragma unroll
-        for (int j = 0; j < BN; j++) acc[j] = 0.0f;
+        for (int j = 0; j < kWarpCols; j++) acc[j] = 0.0f;
         // a block's scales are fetched four blocks ahead
         float rs[4], cs[4];
         const bool fetches = t < BN;
@@ -146,24 +157,22 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             fetch(rs[3], cs[3], kb + 4);
             ok = ok && mm_wait(&sm.acc_full[b], (kb / kBufs) & 1, stop, g.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            named_barrier(1, 128);   // the scales are there, and every thread is done with the other buffer's
+            named_barrier(1, 32 * kEpiWarps);   // the scales are there, and every thread is done with the other buffer's
             if (ok) {
                 tc_fence_after();
-                constexpr int W = BN < 32 ? 16 : 32;
+                const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + b * BN + first;
 #pragma unroll
-                for (int h = 0; h < BN / W; h++) {
-                    uint32_t r[W];
-                    const uint32_t addr = tmem + ((uint32_t)(warp * 32) << 16) + b * BN + h * W;
-                    if constexpr (W == 16) tmem_ld16(r, addr);
-                    else tmem_ld32(r, addr);
-                    if (h + 1 == BN / W) {   // all read: the next block may go there
+                for (int h = 0; h < kWarpCols / 16; h++) {
+                    uint32_t r[16];
+                    tmem_ld16(r, addr + h * 16);
+                    if (h + 1 == kWarpCols / 16) {   // all read: the next block may go there
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < W; j++)
-                        acc[h * W + j] = __fmaf_rn(__uint_as_float(r[j]) * sm.col_scale[cb][h * W + j], s, acc[h * W + j]);
+                    for (int j = 0; j < 16; j++)
+                        acc[h * 16 + j] = __fmaf_rn(__uint_as_float(r[j]) * sm.col_scale[cb][first + h * 16 + j], s, acc[h * 16 + j]);
                 }
             }
         }
@@ -172,30 +181,54 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         if (ok) {
             float *sums = reinterpret_cast<float *>(dsm);
 #pragma unroll
-            for (int j = 0; j < BN; j++) sums[j * 128 + t] = acc[j];
+            for (int j = 0; j < kWarpCols; j++) sums[(first + j) * 128 + quad * 32 + lane] = acc[j];
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5) tmem_free<Smem::kCols>(tmem);
+    if (warp == kEpiWarps + 1) tmem_free<Smem::kCols>(tmem);
     if (split > 1) cluster_sync();   // the cluster's sums are there
-    if (warp < 4 && sm.abort_flag == 0) {
+    if (warp < kEpiWarps && sm.abort_flag == 0) {
+        // a warp takes two columns at a time, four rows per lane
         using T = typename OutT<OUT>::T;
-        const int t = threadIdx.x;
-        const int64_t row = (int64_t)p0 + t;
-        const uint32_t mine = smem_u32(dsm) + 4 * t;
-        for (int j = BN * rank / split; j < BN * (rank + 1) / split; j++) {
-            const int64_t col = (int64_t)q0 + j;
-            if (col >= g.rows_q) break;
-            float v = 0.0f;
-            for (int r = 0; r < split; r++) {
-                uint32_t at = mine + j * 512;
-                if (split > 1) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine + j * 512), "r"(r));
-                v += ld_cluster(at);
+        const int64_t row = (int64_t)p0 + 4 * lane;
+        const bool vec = (g.ldc & 3) == 0 && row + 4 <= g.rows_p && !g.accumulate;
+        const int j1 = BN * (rank + 1) / split;
+        for (int j0 = BN * rank / split + 2 * warp; j0 < j1; j0 += 2 * kEpiWarps) {
+            float4 part[2][kSplitMost];
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int r = 0; r < kSplitMost; r++) {
+                    const uint32_t at = smem_u32(dsm) + (j0 + u) * 512 + lane * 16;
+                    if (r < split && j0 + u < j1) part[u][r] = ld_cluster4(split > 1 ? cluster_addr(at, r) : at);
+                }
+#pragma unroll
+            for (int u = 0; u < 2; u++) {
+                const int64_t col = (int64_t)q0 + j0 + u;
+                if (j0 + u >= j1 || col >= g.rows_q) break;
+                float4 v = part[u][0];
+#pragma unroll
+                for (int r = 1; r < kSplitMost; r++)
+                    if (r < split) {
+                        v.x += part[u][r].x;
+                        v.y += part[u][r].y;
+                        v.z += part[u][r].z;
+                        v.w += part[u][r].w;
+                    }
+                T *c = static_cast<T *>(g.c) + col * g.ldc + row;
+                if (vec) {
+                    if constexpr (OUT == F32) *reinterpret_cast<float4 *>(c) = v;
+                    else *reinterpret_cast<uint2 *>(c) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+                } else {
+                    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (row + i < g.rows_p) put_one<OUT>(c + i, e[i], g.accumulate);
+                }
             }
-            if (row < g.rows_p) put_one<OUT>(static_cast<T *>(g.c) + col * g.ldc + row, v, g.accumulate);
         }
     }
     if (split > 1) cluster_sync();   // nobody reads this CTA's sums any more

@@ -239,6 +239,14 @@ QD uint32_t bf16_bits(float f)
     return h;
 }
 
+// Two of them in one word, lo in the low half.
+QD uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // a *= s0 and b *= s1: two IEEE round-to-nearest FP32 products in one
 // packed instruction (the same results as two separate multiplies).
 QD void mul2(float &a, float &b, float s0, float s1)

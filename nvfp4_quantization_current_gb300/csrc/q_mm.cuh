@@ -60,13 +60,6 @@ template <int OUT> QD void put_one(typename OutT<OUT>::T *p, float v, bool accum
     }
 }
 
-QD uint32_t bf16_pair(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)
 {
     asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
