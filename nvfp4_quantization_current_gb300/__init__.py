@@ -581,6 +581,7 @@ def dq_nvfp4(q, sb, s_global, blk="1x16", dtype=torch.float32, out=None):
 # operators on the blockwise copies
 # ---------------------------------------------------------------------------
 
+_DTYPES = {torch.bfloat16: Q_BF16, torch.float32: Q_F32}
 _TILE = {"1x128": Q_T1x128, "128x128": Q_T128x128, Q_T1x128: Q_T1x128, Q_T128x128: Q_T128x128}
 
 
@@ -590,11 +591,11 @@ def _operand(name, q, s, tile):
         raise ValueError(f"{name} must be CUDA tensors (the library has no CPU path)")
     if q.dtype != torch.uint8 or s.dtype != torch.float32:
         raise ValueError(f"{name}: codes must be uint8 and scales float32, got {q.dtype} and {s.dtype}")
-    if q.dim() != 2 or not q.is_contiguous() or not s.is_contiguous():
+    if q.dim() != 2 or not (q.is_contiguous() and s.is_contiguous()):
         raise ValueError(f"{name}: codes must be a contiguous 2-D tensor and scales contiguous")
     R, K = q.shape
     want = (R, K // 128) if tile == Q_T1x128 else (R // 128, K // 128)
-    if tuple(s.shape) != want:
+    if s.shape != want:
         raise ValueError(f"{name}: scales are {tuple(s.shape)}, codes {R} x {K} need {want}")
     return R, K
 
@@ -617,17 +618,23 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     N, Kb = _operand("b", b, s_b, tb)
     if K != Kb:
         raise ValueError(f"a has K = {K}, b has K = {Kb}")
-    if a.device != b.device:
-        raise ValueError(f"a is on {a.device}, b on {b.device}")
+    dev = a.device
+    if dev != b.device:
+        raise ValueError(f"a is on {dev}, b on {b.device}")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
-    elif tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != a.device:
-        raise ValueError(f"out must be a contiguous {M} x {N} tensor on {a.device}")
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    elif out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
-          _out(out.dtype), int(accumulate), _ptr(status), _stream(a.device))
+          _DTYPES[out.dtype], int(accumulate), _ptr(status), _stream(dev))
     return out
+
+
+def _alike(name, t, x):
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, with x's shape, dtype and device")
 
 
 def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None,
@@ -637,18 +644,18 @@ def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Op
     counters of 8 elements) and the element's flat index, so the backward pass
     is ``drop_add(dy, p, seed, offset)`` and no mask is stored.  ``p`` is taken
     to the nearest 1/65536.  ``out`` may be ``x`` or ``residual``."""
-    if not x.is_cuda or not x.is_contiguous() or x.dtype not in _DTYPES:
+    dt, dev = _DTYPES.get(x.dtype), x.device
+    if dt is None or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor of bfloat16 or float32")
-    for name, t in (("residual", residual), ("out", out)):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous, with x's shape, dtype and device")
-    out = torch.empty_like(x) if out is None else out
-    _call("drop_add", x.data_ptr(), _DTYPES[x.dtype], x.numel(), _ptr(residual), float(p), int(seed), int(offset),
-          out.data_ptr(), _stream(x.device))
+    if residual is not None:
+        _alike("residual", residual, x)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _alike("out", out, x)
+    _call("drop_add", x.data_ptr(), dt, x.numel(), _ptr(residual), float(p), int(seed), int(offset), out.data_ptr(),
+          _stream(dev))
     return out
-
-
-_DTYPES = {torch.bfloat16: Q_BF16, torch.float32: Q_F32}
 
 
 def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, rowwise=True, colwise=False,

@@ -49,12 +49,14 @@ cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int sp
     cfg.blockDim = dim3(SplitSmem<BN>::kThreads);
     cfg.dynamicSmemBytes = sizeof(SplitSmem<BN>);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits before its first read
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k_mm_split<OUT, BN>, map_p, map_q, g);
 }
 
@@ -87,31 +89,46 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
     return cudaGetLastError();
 }
 
-// Which kernel, and how wide and how deep a split: the least estimated time on
-// `sms` SMs, in cycles.  What was measured on a GB300: a CTA's block of 128 x bn
-// results costs what shared memory takes to write and read its operands once,
-// 2 (128 + bn) cycles; a 256 x 256 block of the pair kernel about 1000; and
-// beside its blocks a CTA spends about 6000 on its way in and out, and 1500
-// more where a cluster adds up.
+// Which kernel, and how wide and how deep a split: the least estimated time.
+// What was measured on a GB300 (graphs of calls, weights from memory): a call
+// takes 4.2 us beside its blocks and 0.7 more where a cluster adds up, 2.2 one of
+// eight; a CTA's
+// block of 128 weights x bn tokens the times below (with 4096 x 4096 weights
+// and 40 tokens 14.8 / 9.9 / 7.6 / 8.7 us at splits of 1 / 2 / 4 / 8, with 333
+// tokens 17.2 at 192 wide against 20.2 at 128, 21.3 at 64 and 21.2 on the pair
+// kernel, with 1024 tokens 23.2 there and 40.8 at 128); two resident CTAs 1.4
+// times one's time; and a CTA that comes after another about 2 us more.  A
+// split has to be resident as a whole: clusters that wait for one another's SMs
+// lose more than the split gains (7168 x 18432 with 128 tokens: 37.5 us split in
+// two, 43.5 in four, 59.1 in eight), and clusters of four and eight leave SMs
+// of a GPC unused.
 struct MmPlan {
     int bn, split;   // bn 0: the pair kernel
 };
-MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, int sms)
+MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool cols, int sms)
 {
+    struct Width {
+        int bn;
+        double block;   // us
+        int resident;
+    };
+    static constexpr Width kWidths[] = {{16, 0.24, 2}, {32, 0.27, 2}, {64, 0.33, 2}, {128, 0.475, 1}, {192, 0.64, 1}};
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
     MmPlan best = {0, 1};
-    int64_t cost = 8000 + (pair_tiles + pairs - 1) / pairs * (kblocks * 1000 + 2500);
-    for (int bn : {16, 32, 64, 128, 192, 256}) {
-        const int64_t tz = (M + bn - 1) / bn;
-        if ((bn > 16 && M <= bn / 2) || ty > 65535 || tz > 65535) continue;
-        for (int split = 1; split <= kSplitMost; split *= 2) {
-            if (split > 1 && 2 * split > kblocks) break;
-            const int64_t waves = (ty * tz * split + sms - 1) / sms;
-            const int64_t c = waves * ((kblocks + split - 1) / split * 2 * (128 + bn) + 2000) + 4000 + (split > 1 ? 1500 : 0);
+    double cost = 4.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.68 : 0.5) + 1.0);
+    for (const Width &w : kWidths) {
+        const int64_t tz = (M + w.bn - 1) / w.bn;
+        if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;
+        for (int split = 1; split <= kSplitMost && (split == 1 || 2 * split <= kblocks); split *= 2) {
+            const int64_t ctas = ty * tz * split, n = (ctas + sms - 1) / sms;   // n: CTAs of an SM
+            if (split > 1 && ctas > (int64_t)w.resident * (split == 8 ? sms * 16 / 19 : split == 4 ? sms * 18 / 19 : sms)) break;
+            const double share = n == 2 && w.resident == 2 ? 1.4 : (double)n;
+            const double c = 4.2 + (split == 8 ? 2.2 : split > 1 ? 0.7 : 0.0) + (double)((kblocks + split - 1) / split) * w.block * share +
+                             2.0 * (double)((n - 1) / w.resident);
             if (c < cost) {
                 cost = c;
-                best = {bn, split};
+                best = {w.bn, split};
             }
         }
     }
@@ -122,7 +139,7 @@ template <int OUT>
 cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream_t st)
 {
     const int64_t M = g.rows_p, N = g.rows_q;
-    const MmPlan plan = mm_plan(M, N, g.kblocks, sm_count());
+    const MmPlan plan = mm_plan(M, N, g.kblocks, g.shift_q == 0, sm_count());
     const int split = plan.split;
     MmArgs w = g;   // the weights on the lanes
     w.s_p = g.s_q;
@@ -137,8 +154,7 @@ cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream
     case 32: return mm_split<OUT, 32>(b, a, w, split, st);
     case 64: return mm_split<OUT, 64>(b, a, w, split, st);
     case 128: return mm_split<OUT, 128>(b, a, w, split, st);
-    case 192: return mm_split<OUT, 192>(b, a, w, split, st);
-    default: return mm_split<OUT, 256>(b, a, w, split, st);
+    default: return mm_split<OUT, 192>(b, a, w, split, st);
     }
 }
 

@@ -10,7 +10,7 @@
 // an order that depends on timing, and no workspace is needed.
 //
 // The first warps, four or for wide tiles eight, scale and add (one thread per
-// row of their columns), the next loads, the last issues the MMAs.  Up to 128
+// row of their columns), the next loads, the last issues the MMAs.  Up to 64
 // tokens wide, two CTAs fit an SM: about 100 KiB of stages each and at most
 // half of tensor memory.
 #pragma once
@@ -24,15 +24,15 @@ constexpr int kSplitMost = 8;   // CTAs of a cluster
 
 template <int BN> struct SplitSmem {
     static constexpr int kStageBytes = (128 + BN) * kMmBlock;
-    static constexpr int kStages = BN == 16 ? 6 : BN == 32 ? 5 : BN == 128 ? 3 : 4;
-    static constexpr int kBufs = BN >= 128 ? 2 : 4;
+    static constexpr int kStages = BN == 16 || BN == 128 ? 6 : BN == 32 ? 5 : 4;
+    static constexpr int kBufs = BN > 128 ? 2 : 4;
     static constexpr int kCols = BN == 192 ? 512 : BN * kBufs;   // of tensor memory, a power of two
     static constexpr int kEpiWarps = BN >= 128 ? 8 : 4;
     static constexpr int kWarpCols = BN / (kEpiWarps / 4);
     static constexpr int kThreads = 32 * (kEpiWarps + 2);
-    static constexpr int kResident = BN <= 128 ? 2 : 1;         // CTAs of an SM
+    static constexpr int kResident = BN <= 64 ? 2 : 1;         // CTAs of an SM
     uint8_t stage[kStages][kStageBytes];       // afterwards this CTA's sums, [BN][128] FP32
-    float col_scale[2][BN];
+    alignas(16) float col_scale[2][BN];
     uint64_t full[kStages], empty[kStages], acc_full[kBufs], acc_empty[kBufs], drained;
     uint32_t tmem_base;
     int abort_flag;
@@ -85,6 +85,9 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    // Launched while the kernel ahead still ran; nothing was read or written so far.
+    griddep_wait();
+    griddep_launch_dependents();
 
     if (warp == kEpiWarps) {
         if (elect_one()) {
@@ -130,9 +133,9 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         // rows and columns outside the result have zero products: any scale in bounds does
         const float *sp = g.s_p + ((row < g.rows_p ? row : 0) >> g.shift_p) * g.kblocks;
         const float *sq = g.s_q + ((col < g.rows_q ? col : 0) >> g.shift_q) * g.kblocks;
-        float acc[kWarpCols];
+        uint64_t acc[kWarpCols / 2];   // two columns each
 #pragma unroll
-        for (int j = 0; j < kWarpCols; j++) acc[j] = 0.0f;
+        for (int j = 0; j < kWarpCols / 2; j++) acc[j] = 0ull;
         // a block's scales are fetched four blocks ahead
         float rs[4], cs[4];
         const bool fetches = t < BN;
@@ -147,7 +150,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
 #pragma unroll 1
         for (int kb = 0; kb < kb_n; kb++) {
             const int b = kb % kBufs, cb = kb & 1;
-            const float s = rs[0];
+            const uint64_t ss = pack2(__float_as_uint(rs[0]), __float_as_uint(rs[0]));
             if (fetches) sm.col_scale[cb][t] = cs[0];
 #pragma unroll
             for (int i = 0; i < 3; i++) {
@@ -171,8 +174,11 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                         if (lane == 0) mbar_arrive(&sm.acc_empty[b]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; j++)
-                        acc[h * 16 + j] = __fmaf_rn(__uint_as_float(r[j]) * sm.col_scale[cb][first + h * 16 + j], s, acc[h * 16 + j]);
+                    for (int j = 0; j < 8; j += 2) {
+                        const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(&sm.col_scale[cb][first + h * 16 + 2 * j]);
+                        acc[h * 8 + j] = ffma2(fmul2(pack2(r[2 * j], r[2 * j + 1]), c.x), ss, acc[h * 8 + j]);
+                        acc[h * 8 + j + 1] = ffma2(fmul2(pack2(r[2 * j + 2], r[2 * j + 3]), c.y), ss, acc[h * 8 + j + 1]);
+                    }
                 }
             }
         }
@@ -181,7 +187,8 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         if (ok) {
             float *sums = reinterpret_cast<float *>(dsm);
 #pragma unroll
-            for (int j = 0; j < kWarpCols; j++) sums[(first + j) * 128 + quad * 32 + lane] = acc[j];
+            for (int j = 0; j < kWarpCols / 2; j++)
+                unpack2(acc[j], sums[(first + 2 * j) * 128 + quad * 32 + lane], sums[(first + 2 * j + 1) * 128 + quad * 32 + lane]);
         }
     }
     __syncwarp();
