@@ -24,10 +24,11 @@
 // cycles from arrival to wake-up, an mbarrier takes 160 to 200); as a warp's
 // barrier waits for its own commits too, each buffer has an MMA warp of its
 // own.  A named barrier cannot time out, and need not: an MMA warp waits there
-// only for a block k whose MMAs it has issued, with a look at the abort flag
-// between one such wait and the next; those MMAs needed block k - 2 released,
-// so an epilogue warp that has not arrived for k is at k - 1 or k, and one
-// that gives up there raises the flag and arrives for both buffers.
+// only for blocks whose MMAs it has issued, after a look at the abort flag, and
+// the epilogue warps arrive for every block of a tile, whether their own waits
+// were served or given up (which takes a thousand polls each, so that they
+// never overtake an MMA warp between its look and its barrier), and at both
+// buffers once more when they leave on the flag.
 #pragma once
 
 #include "q_internal.h"
@@ -191,7 +192,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         }
         for (int s = 0; s < kPairScaleSlots; s++) {
             mbar_init(&sm.sc_full[s], 32);
-            mbar_init(&sm.sc_empty[s], kPairEpiWarps);
+            mbar_init(&sm.sc_empty[s], 1);
         }
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -245,7 +246,12 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             const int buf = warp - 1;
             const uint32_t blocks = first < tiles ? (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)kb_n : 0u;
             const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * kMmBlock);
-            int s = buf, f = buf;
+            const int groups = (kb_n + kPairScaleBlocks - 1) / kPairScaleBlocks;   // of scales, per tile
+            int s = buf, f = buf, kb_r = buf, group_r = 0;   // kb_r, group_r: of the block released next
+            while (kb_r >= kb_n) {
+                kb_r -= kb_n;
+                group_r += groups;
+            }
             uint32_t par = 0;
             bool aborted = false;
             for (uint32_t n = buf; n < blocks; n += 2) {
@@ -262,8 +268,18 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         mma_f8(tmem + buf * kPairN, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e4m3(128, kPairN), k > 0);
                     mma_commit(&sm.acc_full[buf]);
                     mma_commit_multicast(&sm.empty[s], 3);
+                    // block n - 2 was the last to use its group of scales
+                    if (n >= 2 && (kb_r % kPairScaleBlocks == kPairScaleBlocks - 1 || kb_r + 1 == kb_n))
+                        mbar_arrive(&sm.sc_empty[(group_r + kb_r / kPairScaleBlocks) % kPairScaleSlots]);
                 }
                 __syncwarp();
+                if (n >= 2) {
+                    kb_r += 2;
+                    while (kb_r >= kb_n) {
+                        kb_r -= kb_n;
+                        group_r += groups;
+                    }
+                }
                 s += 2;
                 if (s >= kPairStages) s -= kPairStages;
                 f += 2;
@@ -291,22 +307,21 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         regs_more<kPairEpiRegs>();
         const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tensor memory lanes, 128 columns
         const uint32_t acc_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
-        int buf = 0;
-        uint32_t par = 0;
-        bool ok = true;
-        Slots turn;
-        for (int t = first; t < tiles && ok; t += pairs) {
+        uint32_t n = 0, group = 0;   // block and group of scales of this CTA's walk
+        for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs) {
             int tp, tq;
             pair_tile(t, tiles_p, tiles_q, tp, tq);
             uint64_t acc[64];
 #pragma unroll
             for (int j = 0; j < 64; j++) acc[j] = 0ull;
+            // After a wait that gave up the rest of the tile goes by as it is (a vote
+            // per block cost 80 cycles of about 450); it is not stored then.
 #pragma unroll 1
-            for (int kb = 0; kb < kb_n; kb++) {
-                const int i = kb % kPairScaleBlocks;
-                bool got = i != 0 || mm_wait(&sm.sc_full[turn.slot], turn.par, stop, g.status);
-                const float *const rs = sm.row_scale[turn.slot][i] + quad * 32;
-                const float *const cs = sm.col_scale[turn.slot][i];
+            for (int kb = 0; kb < kb_n; kb++, n++) {
+                const int i = kb % kPairScaleBlocks, slot = group % kPairScaleSlots, buf = n & 1;
+                if (i == 0) mm_wait(&sm.sc_full[slot], (group / kPairScaleSlots) & 1, stop, g.status);
+                const float *const rs = sm.row_scale[slot][i] + quad * 32;
+                const float *const cs = sm.col_scale[slot][i];
                 // a block's scales: a row's and the column tile's product, or four rows'.
                 // With column scales a thread's 128 sums lie in 4 rows and 32 columns, so
                 // that it needs 32 of them per block and not 128: shared memory returns
@@ -317,60 +332,54 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                     const uint32_t s = __float_as_uint(COLS ? rs[8 * k + (lane >> 2)] : rs[lane] * cs[half]);
                     ss[k] = pack2(s, s);
                 }
-                got = got && mm_wait<true>(&sm.acc_full[buf], par, stop, g.status);
-                if (!__all_sync(0xFFFFFFFFu, got)) {
-                    *stop = 1;
-                    __syncwarp();
-                    acc_release(0);   // the MMA warps may be waiting there
-                    acc_release(1);
-                    ok = false;
-                    break;
-                }
+                mm_wait<true>(&sm.acc_full[buf], (n >> 1) & 1, stop, g.status);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t addr = acc_addr + buf * kPairN;
-                uint32_t r[2][16];   // 16 columns are added while the next 16 are read
                 if constexpr (!COLS) {
-                    tmem_ld16(r[0], addr);
 #pragma unroll
-                    for (int h = 0; h < 7; h++) tmem_ld16_add(r[(h + 1) & 1], addr + (h + 1) * 16, r[h & 1], acc + h * 8, ss[0]);
-                    tc_fence_before();
-                    acc_release(buf);   // all read: the next block may go there
+                    for (int h = 0; h < 8; h++) {
+                        uint32_t r[16];
+                        tmem_ld16(r, addr + h * 16);
+                        if (h == 7) {   // all read: the next block may go there
+                            tc_fence_before();
+                            acc_release(buf);
+                        }
 #pragma unroll
-                    for (int j = 0; j < 8; j++) acc[56 + j] = ffma2(pack2(r[1][2 * j], r[1][2 * j + 1]), ss[0], acc[56 + j]);
+                        for (int j = 0; j < 8; j++) acc[h * 8 + j] = ffma2(pack2(r[2 * j], r[2 * j + 1]), ss[0], acc[h * 8 + j]);
+                    }
                 } else {
                     const float *const cl = cs + half * 128 + 2 * (lane & 3);
-                    uint64_t cc[4];
-                    tmem_ld_rows16(r[0], addr);
 #pragma unroll
-                    for (int h = 0; h < 8; h++) {   // 32 columns, rows 0-15 and 16-31 of the 32
-                        if (h % 2 == 0) {
+                    for (int c = 0; c < 4; c++) {
+                        uint64_t cc[4];
 #pragma unroll
-                            for (int k = 0; k < 4; k++) cc[k] = *reinterpret_cast<const uint64_t *>(cl + (h / 2) * 32 + k * 8);
-                        }
-                        const uint64_t s0 = ss[2 * (h & 1)], s1 = ss[2 * (h & 1) + 1];
-                        if (h < 7) {
-                            const int n = h + 1;
-                            tmem_ld_rows16_add(r[n & 1], addr + (n / 2) * 32 + ((uint32_t)(16 * (n & 1)) << 16), r[h & 1], acc + h * 8, cc, s0, s1);
-                        } else {
-                            tc_fence_before();
-                            acc_release(buf);   // all read: the next block may go there
+                        for (int k = 0; k < 4; k++) cc[k] = *reinterpret_cast<const uint64_t *>(cl + c * 32 + k * 8);
 #pragma unroll
-                            for (int j = 0; j < 8; j++)
-                                acc[56 + j] = ffma2(fmul2(pack2(r[1][2 * j], r[1][2 * j + 1]), cc[j >> 1]), j & 1 ? s1 : s0, acc[56 + j]);
+                        for (int h = 0; h < 2; h++) {
+                            uint32_t r[16];
+                            tmem_ld_rows16(r, addr + c * 32 + ((uint32_t)(16 * h) << 16));
+                            if (c == 3 && h == 1) {   // all read: the next block may go there
+                                tc_fence_before();
+                                acc_release(buf);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; j++) {
+                                const int a = c * 16 + h * 8 + j;
+                                acc[a] = ffma2(fmul2(pack2(r[2 * j], r[2 * j + 1]), cc[j >> 1]), ss[2 * h + (j & 1)], acc[a]);
+                            }
                         }
                     }
                 }
-                if (i == kPairScaleBlocks - 1 || kb + 1 == kb_n) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.sc_empty[turn.slot]);
-                    turn.next();
-                }
-                buf ^= 1;
-                if (buf == 0) par ^= 1;
+                if (i == kPairScaleBlocks - 1 || kb + 1 == kb_n) group++;
             }
-            if (ok)
+            if (!__any_sync(0xFFFFFFFFu, *stop))
                 mm_store_tile<OUT, !COLS>(g, &map_c, sm.staging[warp - 4], acc, tp * 256 + 128 * (int)rank + quad * 32,
                                           tq * kPairN + half * 128, lane);
+        }
+        if (__any_sync(0xFFFFFFFFu, *stop)) {   // the MMA warps may be up to two blocks ahead
+            acc_release(0);
+            acc_release(1);
         }
         if (lane == 0) bulk_wait_all();
     }
