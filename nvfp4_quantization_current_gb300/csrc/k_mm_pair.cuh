@@ -1,14 +1,16 @@
 // The block-scaled product for results of many tiles.
 //
-// A CTA owns a 128 x 256 tile of C and walks the tiles persistently with the
-// CTA beside it (a cluster of two), which owns the 128 rows below: both need
-// the same 256 rows of Q, so each loads half of them and multicasts it to
-// both.  A stage of 128 elements of K costs a CTA 32 KiB of loads from L2 for
-// 128 x 256 x 128 products.  The block products alternate between two
-// accumulator buffers, which together fill tensor memory.
+// A pair of CTAs (a cluster of two) owns a 256 x 256 tile of C and walks the
+// tiles persistently.  One MMA spans both: each CTA's shared memory holds its
+// own 128 rows of P and half of Q's 256, and its tensor memory receives its
+// 128 rows x 256 columns in FP32.  (With an MMA per CTA and Q multicast to
+// both, a block's operands, 48 KiB written and 48 KiB read per CTA, take the
+// 128 bytes a cycle of shared memory 768 cycles, and the MMAs 512.)  Two
+// accumulator buffers together fill tensor memory.
 //
-// Warp 0 loads operand tiles, warps 1 and 2 issue the MMAs of the even and the
-// odd blocks, warp 3 fetches scales, four blocks at a time, and the eight
+// Warp 0 of each CTA loads its operand tiles, all of whose bytes count on the
+// leader's barriers.  The leader's warps 1 and 2 issue the MMAs of the even and
+// the odd blocks, warp 3 fetches scales, four blocks at a time, and the eight
 // warps 4-11 keep the FP32 sums of 32 rows x 128 columns each in registers: a
 // block's product is read from tensor memory, multiplied by its scales and
 // added while the next block's runs.  Finished tiles go through shared memory
@@ -16,19 +18,19 @@
 // bytes each.
 //
 // The hand-over of the accumulator buffers is what the block rate hangs on:
-// MMAs (512 cycles), commit (207 until a waiting warp sees it), read (about
-// 300), release and the next MMAs into the same buffer form a chain, of which
-// two are in flight.  It stays inside the CTA: one MMA over both CTAs of a
-// pair would need half the loads of Q, but its chain crosses the pair twice
-// per block and took twice as long.  The release is a named barrier (about 20
-// cycles from arrival to wake-up, an mbarrier takes 160 to 200); as a warp's
-// barrier waits for its own commits too, each buffer has an MMA warp of its
-// own.  A named barrier cannot time out, and need not: an MMA warp waits there
-// only for blocks whose MMAs it has issued, after a look at the abort flag, and
-// the epilogue warps arrive for every block of a tile, whether their own waits
-// were served or given up (which takes a thousand polls each, so that they
-// never overtake an MMA warp between its look and its barrier), and at both
-// buffers once more when they leave on the flag.
+// MMAs (512 cycles), commit (207 until a polling warp sees it), read (about
+// 400), release and the next MMAs into the same buffer form a chain, of which
+// two are in flight.  The release is a named barrier (about 20 cycles from
+// arrival to wake-up, an mbarrier takes 160 to 200); as a warp's barrier waits
+// for its own commits too, each buffer has an MMA warp of its own.  In the
+// other CTA those two warps wait at the same barrier and pass the release on to
+// the leader.  A named barrier cannot time out, and need not: these warps wait
+// there only for blocks whose MMAs are issued (the leader's) or that the
+// epilogue is going to read, after a look at the abort flag, and the epilogue
+// warps arrive for every block of a tile, whether their own waits were served
+// or given up (which takes a thousand polls each, so that they never overtake a
+// warp between its look and its barrier), and at both buffers once more when
+// they leave on the flag.
 #pragma once
 
 #include "q_internal.h"
@@ -38,9 +40,9 @@ namespace qk {
 
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 32 * (4 + kPairEpiWarps);
-constexpr int kPairStages = 3;
-constexpr int kPairN = 256;       // columns of a CTA's tile
-constexpr int kPairStageBytes = (128 + kPairN) * kMmBlock;
+constexpr int kPairStages = 4;   // even: each MMA warp uses every other one
+constexpr int kPairN = 256;       // columns of a pair's tile
+constexpr int kPairStageBytes = 2 * 128 * kMmBlock;
 constexpr int kPairScaleSlots = 2, kPairScaleBlocks = 4;
 constexpr int kPairGroup = 8;     // tile rows per group of the tile order
 // Named barriers of the accumulator buffers' release (two from kAccFree on):
@@ -68,8 +70,7 @@ struct PairSmem {
     // the blocks' scales: P's rows, and Q's rows (COLS) or two 128-row tiles
     float row_scale[kPairScaleSlots][kPairScaleBlocks][128];
     float col_scale[kPairScaleSlots][kPairScaleBlocks][kPairN];
-    uint64_t full[2 * kPairStages], empty[kPairStages],   // full: of the stage's even and odd uses
-        acc_full[2], drained[2];
+    uint64_t full[kPairStages], empty[kPairStages], acc_full[2], peer_free[2], drained[2];
     uint64_t sc_full[kPairScaleSlots], sc_empty[kPairScaleSlots];
     uint32_t tmem_base;
     int abort_flag;
@@ -183,11 +184,11 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; s++) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.full[kPairStages + s], 1);
-            mbar_init(&sm.empty[s], 2);   // both CTAs have used it
+            mbar_init(&sm.empty[s], 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&sm.acc_full[b], 1);
+            mbar_init(&sm.peer_free[b], 1);
             mbar_init(&sm.drained[b], 1);
         }
         for (int s = 0; s < kPairScaleSlots; s++) {
@@ -197,7 +198,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         sm.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc<512>(&sm.tmem_base);
+    if (warp == 1) tmem_alloc_pair<512>(&sm.tmem_base);
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // the peer's barriers are ready before anything arrives on them
@@ -221,10 +222,10 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         break;
                     }
                     uint8_t *st = sm.stage[s];
-                    uint64_t *const bar = &sm.full[issued % (2 * kPairStages)];
-                    mbar_arrive_expect_tx(bar, kPairStageBytes);
-                    tma_load_tile(st, &map_p, kb * kMmBlock, p0, bar);
-                    tma_load_tile_multicast(st + (128 + 128 * rank) * kMmBlock, &map_q, kb * kMmBlock, q0, bar, 3);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kPairStageBytes);
+                    const uint32_t bar = cluster_addr(smem_u32(&sm.full[s]), 0);
+                    tma_load_tile_pair(st, &map_p, kb * kMmBlock, p0, bar);
+                    tma_load_tile_pair(st + 128 * kMmBlock, &map_q, kb * kMmBlock, q0, bar);
                     issued++;
                     if (++s == kPairStages) {
                         s = 0;
@@ -232,42 +233,60 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                     }
                 }
             }
-            // every stage is released by both CTAs before this one may leave: the
-            // peer's commits arrive here
+            // every stage is released before this CTA may leave: the leader's commits
+            // arrive here
             for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; ok && j < issued; j++)
                 ok = mm_wait(&sm.empty[j % kPairStages], (j / kPairStages) & 1, stop, g.status);
-            if (!ok)   // copies in flight land before shared memory goes away
-                for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; j++)
-                    (void)mbar_wait_bounded(&sm.full[j % (2 * kPairStages)], (j / (2 * kPairStages)) & 1);
+            if (!ok) {   // copies in flight land before shared memory goes away
+                if (rank == 0) {
+                    for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; j++)
+                        (void)mbar_wait_bounded(&sm.full[j % kPairStages], (j / kPairStages) & 1);
+                } else {   // counted on the leader's barriers: far longer than any copy takes
+                    const unsigned long long t0 = globaltimer();
+                    while (globaltimer() - t0 < 10000000ull) {}
+                }
+            }
         } else if (warp < 3 && warp > 0) {
-            // One warp per accumulator buffer: every other block.  (Of three stages it
-            // uses each every other time, so the uses count on six barriers: on three
-            // it could take a phase's parity for that of the phase before.)
+            // One warp per accumulator buffer: every other block.
             const int buf = warp - 1;
             const uint32_t blocks = first < tiles ? (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)kb_n : 0u;
             const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * kMmBlock);
+            const uint32_t to_leader = cluster_addr(smem_u32(&sm.peer_free[buf]), 0);
             const int groups = (kb_n + kPairScaleBlocks - 1) / kPairScaleBlocks;   // of scales, per tile
-            int s = buf, f = buf, kb_r = buf, group_r = 0;   // kb_r, group_r: of the block released next
+            int s = buf, kb_r = buf, group_r = 0;   // kb_r, group_r: of the block released next
             while (kb_r >= kb_n) {
                 kb_r -= kb_n;
                 group_r += groups;
             }
-            uint32_t par = 0;
+            uint32_t par = 0, freed = 0;
             bool aborted = false;
-            for (uint32_t n = buf; n < blocks; n += 2) {
-                // a wait that gives up raises the flag, here or in the epilogue
-                mm_wait<true>(&sm.full[f], par, stop, g.status);
+            for (uint32_t n = buf; n < blocks + 2; n += 2) {
+                if (rank == 0) {
+                    if (n >= blocks) break;
+                    // a wait that gives up raises the flag, here or in the epilogue
+                    mm_wait<true>(&sm.full[s], par, stop, g.status);
+                }
                 aborted = __any_sync(0xFFFFFFFFu, *stop);
                 if (aborted) break;
-                if (n >= 2) acc_await(buf);   // last: it is what the next MMAs wait for
+                if (n >= 2) {   // block n - 2 has been read, in both CTAs
+                    acc_await(buf);
+                    if (rank == 0) {
+                        mm_wait<true>(&sm.peer_free[buf], freed, stop, g.status);
+                        freed ^= 1;
+                    }
+                }
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint64_t at = (uint64_t)(s * (kPairStageBytes >> 4));
+                    if (rank == 0) {
+                        const uint64_t at = (uint64_t)(s * (kPairStageBytes >> 4));
 #pragma unroll
-                    for (int k = 0; k < kMmBlock / 32; k++)
-                        mma_f8(tmem + buf * kPairN, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e4m3(128, kPairN), k > 0);
-                    mma_commit(&sm.acc_full[buf]);
-                    mma_commit_multicast(&sm.empty[s], 3);
+                        for (int k = 0; k < kMmBlock / 32; k++)
+                            mma_f8_pair(tmem + buf * kPairN, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e4m3(256, kPairN), k > 0);
+                        mma_commit_pair(&sm.acc_full[buf]);
+                        mma_commit_pair(&sm.empty[s]);
+                    } else if (n >= 2) {
+                        mbar_arrive_cluster(to_leader);
+                    }
                     // block n - 2 was the last to use its group of scales
                     if (n >= 2 && (kb_r % kPairScaleBlocks == kPairScaleBlocks - 1 || kb_r + 1 == kb_n))
                         mbar_arrive(&sm.sc_empty[(group_r + kb_r / kPairScaleBlocks) % kPairScaleSlots]);
@@ -281,15 +300,13 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                     }
                 }
                 s += 2;
-                if (s >= kPairStages) s -= kPairStages;
-                f += 2;
-                if (f >= 2 * kPairStages) {
-                    f -= 2 * kPairStages;
+                if (s >= kPairStages) {
+                    s -= kPairStages;
                     par ^= 1;
                 }
             }
-            if (aborted && elect_one()) {   // MMAs in flight end before their memory goes away
-                mma_commit(&sm.drained[buf]);
+            if (aborted && rank == 0 && elect_one()) {   // MMAs in flight end before their memory goes away
+                mma_commit_pair(&sm.drained[buf]);
                 (void)mbar_wait_bounded(&sm.drained[buf], 0);
             }
         } else if (warp == 3) {
@@ -388,7 +405,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     __syncthreads();
     cluster_sync();   // nothing of the peer's arrives here any more
     tc_fence_after();
-    if (warp == 1) tmem_free<512>(tmem);
+    if (warp == 1) tmem_free_pair<512>(tmem);
 }
 
 }  // namespace qk

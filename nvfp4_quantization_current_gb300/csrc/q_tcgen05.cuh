@@ -90,19 +90,55 @@ QD void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// tma_load_tile into the same place of every CTA in `mask`, counted on the
-// barrier at bar's place in each of them.
-QD void tma_load_tile_multicast(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar, uint16_t mask)
+// Address of shared memory address `addr`'s counterpart in cluster rank `rank`.
+QD uint32_t cluster_addr(uint32_t addr, int rank)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-                 "[%0], [%1, {%2, %3}], [%4], %5;"
-                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask) : "memory");
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
-// mma_commit with one arrival on the barrier at bar's place in every CTA of `mask`.
-QD void mma_commit_multicast(uint64_t *bar, uint16_t mask)
+// Arrival on a barrier of the cluster.  No data in generic memory is handed
+// over with it (only tensor memory that has been read, which the tcgen05
+// fences order), so it and the waits for it stay at CTA scope: an acquire at
+// cluster scope drops the L1 on every wait.
+QD void mbar_arrive_cluster(uint32_t addr)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 ::"r"(smem_u32(bar)), "h"(mask) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// CTA pairs (clusters of two): one MMA spans both CTAs' tensor memory, each CTA
+// holding its own 128 rows of A and D and half of B's rows.  All tensor memory
+// instructions of such a kernel name the pair.
+template <int COLS> QD void tmem_alloc_pair(uint32_t *dst)
+{
+    static_assert(COLS >= 32 && COLS <= 512 && (COLS & (COLS - 1)) == 0, "column count");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "n"(COLS) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+template <int COLS> QD void tmem_free_pair(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS) : "memory");
+}
+// A tile into this CTA's shared memory whose bytes count on a barrier of the
+// pair (bar: a cluster address, this CTA's or its peer's).
+QD void tma_load_tile_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// mma_f8 over the pair: the descriptors give offsets that hold in both CTAs.
+QD void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+// mma_commit with one arrival on the barrier at this offset in both CTAs.
+QD void mma_commit_pair(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
 // Moves registers between warpgroups (all four warps of one; multiples of 8,
