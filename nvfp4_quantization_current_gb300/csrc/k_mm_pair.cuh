@@ -43,7 +43,8 @@ constexpr int kPairThreads = 32 * (4 + kPairEpiWarps);
 constexpr int kPairStages = 4;   // even: each MMA warp uses every other one
 constexpr int kPairN = 256;       // columns of a pair's tile
 constexpr int kPairStageBytes = 2 * 128 * kMmBlock;
-constexpr int kPairScaleSlots = 2, kPairScaleBlocks = 4;
+constexpr int kPairScaleSlots = 2;
+constexpr uint32_t kPairScaleBlocks = 4;   // a power of two
 constexpr int kPairGroup = 8;     // tile rows per group of the tile order
 // Named barriers of the accumulator buffers' release (two from kAccFree on):
 // the epilogue's threads arrive, the MMA warp waits.
@@ -324,7 +325,8 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         regs_more<kPairEpiRegs>();
         const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tensor memory lanes, 128 columns
         const uint32_t acc_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
-        uint32_t n = 0, group = 0;   // block and group of scales of this CTA's walk
+        uint32_t n = 0;                   // block of this CTA's walk
+        uint32_t ring = 0, sc_par = 0;    // its place among the slots' blocks, and the slots' fill
         for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs) {
             int tp, tq;
             pair_tile(t, tiles_p, tiles_q, tp, tq);
@@ -335,24 +337,25 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             // per block cost 80 cycles of about 450); it is not stored then.
 #pragma unroll 1
             for (int kb = 0; kb < kb_n; kb++, n++) {
-                const int i = kb % kPairScaleBlocks, slot = group % kPairScaleSlots, buf = n & 1;
-                if (i == 0) mm_wait(&sm.sc_full[slot], (group / kPairScaleSlots) & 1, stop, g.status);
-                const float *const rs = sm.row_scale[slot][i] + quad * 32;
-                const float *const cs = sm.col_scale[slot][i];
-                // a block's scales: a row's and the column tile's product, or four rows'.
-                // With column scales a thread's 128 sums lie in 4 rows and 32 columns, so
-                // that it needs 32 of them per block and not 128: shared memory returns
-                // 128 bytes a cycle to the whole SM, and 128 took twice as long as the MMAs
-                uint64_t ss[COLS ? 4 : 1];
-#pragma unroll
-                for (int k = 0; k < (COLS ? 4 : 1); k++) {
-                    const uint32_t s = __float_as_uint(COLS ? rs[8 * k + (lane >> 2)] : rs[lane] * cs[half]);
-                    ss[k] = pack2(s, s);
-                }
+                const int buf = n & 1;
+                if (ring % kPairScaleBlocks == 0) mm_wait(&sm.sc_full[ring / kPairScaleBlocks], sc_par, stop, g.status);
                 mm_wait<true>(&sm.acc_full[buf], (n >> 1) & 1, stop, g.status);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t addr = acc_addr + buf * kPairN;
+                // A block's scales, which arrive under the first read of tensor memory: a
+                // row's times its column tile's, or four rows'.  With column scales a
+                // thread's 128 sums lie in 4 rows and 32 columns, so that it needs 32 of
+                // them per block and not 128: shared memory returns 128 bytes a cycle to
+                // the whole SM, and 128 took twice as long as the MMAs.
+                const float *const rs = &sm.row_scale[0][0][quad * 32 + (COLS ? lane >> 2 : lane)] + ring * 128;
+                const float *const cs = &sm.col_scale[0][0][COLS ? half * 128 + 2 * (lane & 3) : half] + ring * kPairN;
+                uint64_t ss[COLS ? 4 : 1];
+#pragma unroll
+                for (int k = 0; k < (COLS ? 4 : 1); k++) {
+                    const uint32_t s = __float_as_uint(COLS ? rs[8 * k] : rs[0] * cs[0]);
+                    ss[k] = pack2(s, s);
+                }
                 if constexpr (!COLS) {
 #pragma unroll
                     for (int h = 0; h < 8; h++) {
@@ -366,12 +369,11 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         for (int j = 0; j < 8; j++) acc[h * 8 + j] = ffma2(pack2(r[2 * j], r[2 * j + 1]), ss[0], acc[h * 8 + j]);
                     }
                 } else {
-                    const float *const cl = cs + half * 128 + 2 * (lane & 3);
 #pragma unroll
                     for (int c = 0; c < 4; c++) {
                         uint64_t cc[4];
 #pragma unroll
-                        for (int k = 0; k < 4; k++) cc[k] = *reinterpret_cast<const uint64_t *>(cl + c * 32 + k * 8);
+                        for (int k = 0; k < 4; k++) cc[k] = *reinterpret_cast<const uint64_t *>(cs + c * 32 + k * 8);
 #pragma unroll
                         for (int h = 0; h < 2; h++) {
                             uint32_t r[16];
@@ -388,7 +390,12 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         }
                     }
                 }
-                if (i == kPairScaleBlocks - 1 || kb + 1 == kb_n) group++;
+                ring++;
+                if (kb + 1 == kb_n) ring = (ring + kPairScaleBlocks - 1) & ~(kPairScaleBlocks - 1);   // a tile begins a slot
+                if (ring == kPairScaleSlots * kPairScaleBlocks) {
+                    ring = 0;
+                    sc_par ^= 1;
+                }
             }
             if (!__any_sync(0xFFFFFFFFu, *stop))
                 mm_store_tile<OUT, !COLS>(g, &map_c, sm.staging[warp - 4], acc, tp * 256 + 128 * (int)rank + quad * 32,
