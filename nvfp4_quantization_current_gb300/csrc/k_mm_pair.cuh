@@ -43,7 +43,7 @@ constexpr int kPairThreads = 32 * (4 + kPairEpiWarps);
 constexpr int kPairStages = 4;   // even: each MMA warp uses every other one
 constexpr int kPairN = 256;       // columns of a pair's tile
 constexpr int kPairStageBytes = 2 * 128 * kMmBlock;
-constexpr int kPairScaleSlots = 2;
+constexpr int kPairScaleSlots = 4;   // a tile's first scales take a trip to memory: fetched 3 slots ahead
 constexpr uint32_t kPairScaleBlocks = 4;   // a power of two
 constexpr int kPairGroup = 8;     // tile rows per group of the tile order
 // Named barriers of the accumulator buffers' release (two from kAccFree on):
@@ -90,23 +90,6 @@ QD void pair_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
     q = r / height;
 }
 
-// A walk over the scale slots: par is the parity of the fill that a reader
-// waits for; a writer waits for the release before it (par ^ 1), which the
-// slots' first use does not need.
-struct Slots {
-    int slot = 0;
-    uint32_t par = 0;
-    bool primed = false;
-    QD void next()
-    {
-        if (++slot == kPairScaleSlots) {
-            slot = 0;
-            par ^= 1;
-            primed = true;
-        }
-    }
-};
-
 // Four consecutive block scales from kb on, the last one repeated past the end.
 QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n)
 {
@@ -122,16 +105,20 @@ QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n)
     }
 }
 
-// A tile's scales (one warp): four rows of P per lane (row, row + 32, ..), and
-// eight rows of Q from col0 on or, from lanes 0 and 1, those of Q's two
-// 128-row tiles.  Rows outside the matrices have zero products: any scale does.
+// The scales of all tiles of a CTA's walk (one warp), the next four blocks' on
+// their way while four wait for a slot: four rows of P per lane, and eight rows
+// of Q or, from lanes 0 and 1, those of Q's two 128-row tiles.  Rows outside the
+// matrices have zero products: any scale does.
 template <bool COLS>
-QD bool put_scales(PairSmem &sm, Slots &turn, const MmArgs &g, int row, int col0, int lane, volatile int *stop)
+QD void put_scales(PairSmem &sm, const MmArgs &g, int first, int pairs, int tiles_p, int tiles_q, int rank, int lane,
+                   volatile int *stop)
 {
     constexpr int NQ = COLS ? kPairN / 32 : 1;
-    const int rows_p = (int)g.rows_p, rows_q = (int)g.rows_q, kb_n = (int)g.kblocks;
-    float v[4][4], w[NQ][4];
-    auto load = [&](int kb) {
+    const int rows_p = (int)g.rows_p, rows_q = (int)g.rows_q, kb_n = (int)g.kblocks, tiles = tiles_p * tiles_q;
+    float v[4][kPairScaleBlocks], w[NQ][kPairScaleBlocks];
+    int t = first, kb = 0, tp, tq;
+    auto load = [&] {
+        const int row = tp * 256 + 128 * rank + lane, col = tq * kPairN + (COLS ? lane : 128 * (lane & 1));
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const int r = row + 32 * j < rows_p ? row + 32 * j : 0;
@@ -139,30 +126,44 @@ QD bool put_scales(PairSmem &sm, Slots &turn, const MmArgs &g, int row, int col0
         }
 #pragma unroll
         for (int j = 0; j < NQ; j++) {
-            const int c = col0 + (COLS ? 32 * j + lane : 128 * (lane & 1));
-            load_scales4(w[j], g.s_q + (int64_t)((c < rows_q ? c : 0) >> g.shift_q) * kb_n, kb, kb_n);
+            const int c = col + 32 * j < rows_q ? col + 32 * j : 0;
+            load_scales4(w[j], g.s_q + (int64_t)(c >> g.shift_q) * kb_n, kb, kb_n);
         }
     };
-    load(0);
-    for (int kb = 0; kb < kb_n; kb += kPairScaleBlocks) {
-        const bool got = !turn.primed || mm_wait(&sm.sc_empty[turn.slot], turn.par ^ 1, stop, g.status);
-        if (!__all_sync(0xFFFFFFFFu, got)) return false;
+    if (t >= tiles) return;
+    pair_tile(t, tiles_p, tiles_q, tp, tq);
+    load();
+    uint32_t slot = 0, par = 1;   // par: of the release that the slot's next use waits for
+    bool primed = false;
+    while (true) {
+        const bool got = !primed || mm_wait(&sm.sc_empty[slot], par, stop, g.status);
+        if (!__all_sync(0xFFFFFFFFu, got)) return;
 #pragma unroll
-        for (int i = 0; i < kPairScaleBlocks; i++) {
+        for (int i = 0; i < (int)kPairScaleBlocks; i++) {
 #pragma unroll
-            for (int j = 0; j < 4; j++) sm.row_scale[turn.slot][i][32 * j + lane] = v[j][i];
+            for (int j = 0; j < 4; j++) sm.row_scale[slot][i][32 * j + lane] = v[j][i];
             if (COLS) {
 #pragma unroll
-                for (int j = 0; j < NQ; j++) sm.col_scale[turn.slot][i][32 * j + lane] = w[j][i];
+                for (int j = 0; j < NQ; j++) sm.col_scale[slot][i][32 * j + lane] = w[j][i];
             } else if (lane < 2) {
-                sm.col_scale[turn.slot][i][lane] = w[0][i];
+                sm.col_scale[slot][i][lane] = w[0][i];
             }
         }
-        mbar_arrive(&sm.sc_full[turn.slot]);
-        turn.next();
-        load(kb + kPairScaleBlocks);
+        mbar_arrive(&sm.sc_full[slot]);
+        if (++slot == kPairScaleSlots) {
+            slot = 0;
+            par ^= 1;
+            primed = true;
+        }
+        kb += kPairScaleBlocks;
+        if (kb >= kb_n) {
+            kb = 0;
+            t += pairs;
+            if (t >= tiles) return;
+            pair_tile(t, tiles_p, tiles_q, tp, tq);
+        }
+        load();
     }
-    return true;
 }
 
 // COLS: Q has a scale per row (1x128 tiles); otherwise one per 128 of its rows.
@@ -311,15 +312,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 (void)mbar_wait_bounded(&sm.drained[buf], 0);
             }
         } else if (warp == 3) {
-            // Lane l fetches rows l, l + 32, .. of both operands.  The next four
-            // blocks' scales are on their way while four wait for a slot.
-            bool ok = true;
-            Slots turn;
-            for (int t = first; t < tiles && ok; t += pairs) {
-                int tp, tq;
-                pair_tile(t, tiles_p, tiles_q, tp, tq);
-                ok = put_scales<COLS>(sm, turn, g, tp * 256 + 128 * (int)rank + lane, tq * kPairN, lane, stop);
-            }
+            put_scales<COLS>(sm, g, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
         }
     } else {
         regs_more<kPairEpiRegs>();
