@@ -190,7 +190,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&sm.acc_full[b], 1);
-            mbar_init(&sm.peer_free[b], 1);
+            mbar_init(&sm.peer_free[b], kPairEpiWarps);   // the other CTA's
             mbar_init(&sm.drained[b], 1);
         }
         for (int s = 0; s < kPairScaleSlots; s++) {
@@ -253,7 +253,6 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             const int buf = warp - 1;
             const uint32_t blocks = first < tiles ? (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)kb_n : 0u;
             const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * kMmBlock);
-            const uint32_t to_leader = cluster_addr(smem_u32(&sm.peer_free[buf]), 0);
             const int groups = (kb_n + kPairScaleBlocks - 1) / kPairScaleBlocks;   // of scales, per tile
             int s = buf, kb_r = buf, group_r = 0;   // kb_r, group_r: of the block released next
             while (kb_r >= kb_n) {
@@ -286,8 +285,6 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                             mma_f8_pair(tmem + buf * kPairN, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e4m3(256, kPairN), k > 0);
                         mma_commit_pair(&sm.acc_full[buf]);
                         mma_commit_pair(&sm.empty[s]);
-                    } else if (n >= 2) {
-                        mbar_arrive_cluster(to_leader);
                     }
                     // block n - 2 was the last to use its group of scales
                     if (n >= 2 && (kb_r % kPairScaleBlocks == kPairScaleBlocks - 1 || kb_r + 1 == kb_n))
@@ -318,6 +315,12 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
         regs_more<kPairEpiRegs>();
         const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tensor memory lanes, 128 columns
         const uint32_t acc_addr = tmem + ((uint32_t)(quad * 32) << 16) + half * 128;
+        const uint32_t to_leader = cluster_addr(smem_u32(&sm.peer_free[0]), 0);
+        auto release = [&](int buf) {   // all read: the next block may go there
+            tc_fence_before();
+            acc_release(buf);
+            if (rank != 0 && elect_one()) mbar_arrive_cluster(to_leader + 8 * buf);
+        };
         uint32_t n = 0;                   // block of this CTA's walk
         uint32_t ring = 0, sc_par = 0;    // its place among the slots' blocks, and the slots' fill
         for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs) {
@@ -354,10 +357,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                     for (int h = 0; h < 8; h++) {
                         uint32_t r[16];
                         tmem_ld16(r, addr + h * 16);
-                        if (h == 7) {   // all read: the next block may go there
-                            tc_fence_before();
-                            acc_release(buf);
-                        }
+                        if (h == 7) release(buf);
 #pragma unroll
                         for (int j = 0; j < 8; j++) acc[h * 8 + j] = ffma2(pack2(r[2 * j], r[2 * j + 1]), ss[0], acc[h * 8 + j]);
                     }
@@ -371,10 +371,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                         for (int h = 0; h < 2; h++) {
                             uint32_t r[16];
                             tmem_ld_rows16(r, addr + c * 32 + ((uint32_t)(16 * h) << 16));
-                            if (c == 3 && h == 1) {   // all read: the next block may go there
-                                tc_fence_before();
-                                acc_release(buf);
-                            }
+                            if (c == 3 && h == 1) release(buf);
 #pragma unroll
                             for (int j = 0; j < 8; j++) {
                                 const int a = c * 16 + h * 8 + j;
