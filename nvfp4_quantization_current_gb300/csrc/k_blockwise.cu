@@ -94,23 +94,36 @@ template <int DT, bool P2> QD void bw_tile_scale(uint32_t b, const BwScaleTab &t
 
 struct NoDrop {};
 
-// Keeps the elements of a row chunk (flat index i0, a multiple of VEC inside
-// one Philox block) that the draws keep, as packed input elements.
-template <int DT> QD void drop_chunk(uint4 &v, int64_t i0, const DropArgs &d)
+// Keeps the elements of this lane's chunks of two rows (flat indices i0 and
+// i0 + K) that the draws keep, as packed input elements.  A BF16 chunk is one
+// Philox block.  An FP32 chunk is half of one, whose other half the lane beside
+// holds: the even lane draws the first row's block, the odd lane the second's,
+// and they exchange the halves that are the other's.
+template <int DT> QD void drop_rows(uint4 &v0, uint4 &v1, int64_t i0, int64_t K, int lane, const DropArgs &d)
 {
-    const uint4 draws = drop_draws((uint64_t)i0 >> 3, d);
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (DT == BF16) {
+        uint4 *const v[2] = {&v0, &v1};
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            w[j] &= (drop_keep(draws, 2 * j, d.threshold) ? 0x0000FFFFu : 0u) | (drop_keep(draws, 2 * j + 1, d.threshold) ? 0xFFFF0000u : 0u);
+        for (int r = 0; r < 2; r++) {
+            const uint4 draws = drop_draws((uint64_t)(i0 + r * K) >> 3, d);
+            uint32_t w[4] = {v[r]->x, v[r]->y, v[r]->z, v[r]->w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                if (!drop_keep(draws, 2 * j, d.threshold)) w[j] &= 0xFFFF0000u;
+                if (!drop_keep(draws, 2 * j + 1, d.threshold)) w[j] &= 0x0000FFFFu;
+            }
+            *v[r] = d.all ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(w[0], w[1], w[2], w[3]);
+        }
     } else {
-        const bool upper = (i0 & 4) != 0;
-        const uint4 mine = make_uint4(upper ? draws.z : draws.x, upper ? draws.w : draws.y, 0u, 0u);
-#pragma unroll
-        for (int j = 0; j < 4; j++) w[j] = drop_keep(mine, j, d.threshold) ? w[j] : 0u;
+        const bool odd = lane & 1;
+        const uint4 mine = drop_draws((uint64_t)(i0 + (odd ? K : 0)) >> 3, d);
+        const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, odd ? mine.x : mine.z, 1), y = __shfl_xor_sync(0xFFFFFFFFu, odd ? mine.y : mine.w, 1);
+        const uint4 d0 = odd ? make_uint4(x, y, 0u, 0u) : make_uint4(mine.x, mine.y, 0u, 0u);
+        const uint4 d1 = odd ? make_uint4(mine.z, mine.w, 0u, 0u) : make_uint4(x, y, 0u, 0u);
+        auto keep = [&](const uint4 &draws, int j, uint32_t w) { return !d.all && drop_keep(draws, j, d.threshold) ? w : 0u; };
+        v0 = make_uint4(keep(d0, 0, v0.x), keep(d0, 1, v0.y), keep(d0, 2, v0.z), keep(d0, 3, v0.w));
+        v1 = make_uint4(keep(d1, 0, v1.x), keep(d1, 1, v1.y), keep(d1, 2, v1.z), keep(d1, 3, v1.w));
     }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <int DT, int TILE, bool P2, class Drop>
@@ -160,7 +173,12 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
         for (int j = 0; j < 8; j++) v[j] = lds16(st + (8 * warp + j) * kRowBytes + lane * 16);
         if constexpr (DROP) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) drop_chunk<DT>(v[j], (m0 + j) * K + k, drop);
+            for (int j = 0; j < 8; j += 2) {
+                // Two rows' Philox chains at a time: four warps fill a scheduler with
+                // them, and eight at once cost more registers than there are.
+                asm volatile("" ::: "memory");
+                drop_rows<DT>(v[j], v[j + 1], (m0 + j) * K + k, K, lane, drop);
+            }
         }
         uint32_t code[8][CW];
         uint32_t cc2 = 0;   // 128x128 with P2: this lane's block code

@@ -54,7 +54,7 @@ template <int DT, bool RES> QD Eight<DT> drop_eight(const Eight<DT> &x, const Ei
     const uint4 draws = drop_draws(block, d);
     float y[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) y[j] = drop_sum<RES>(x.at(j), RES ? r.at(j) : 0.0f, drop_keep(draws, j, d.threshold), d.c);
+    for (int j = 0; j < 8; j++) y[j] = drop_sum<RES>(x.at(j), RES ? r.at(j) : 0.0f, !d.all && drop_keep(draws, j, d.threshold), d.c);
     Eight<DT> out;
     if constexpr (DT == BF16) {
         out.v[0] = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
@@ -88,7 +88,7 @@ k_drop_add(const void *x, const void *residual, void *y, int64_t n, const DropAr
     }
     if (blockIdx.x == 0 && threadIdx.x < (n & 7)) {   // what is left of the last block
         const int64_t i = blocks * 8 + threadIdx.x;
-        const bool keep = drop_keep(drop_draws((uint64_t)blocks, d), threadIdx.x, d.threshold);
+        const bool keep = !d.all && drop_keep(drop_draws((uint64_t)blocks, d), threadIdx.x, d.threshold);
         using T = typename std::conditional<DT == BF16, uint16_t, float>::type;
         auto value = [&](const void *p) {
             if constexpr (DT == BF16) return __uint_as_float((uint32_t) static_cast<const T *>(p)[i] << 16);

@@ -19,23 +19,24 @@ constexpr uint32_t kDropStream = 2u;
 struct DropArgs {
     PhiloxKeys keys;
     uint64_t offset;
-    uint32_t threshold;   // T << 16, and all ones for T = 65536 (which no draw reaches)
+    uint32_t threshold;   // T << 16
     float c;
+    bool all;             // T = 65536: nothing is kept
 };
 inline DropArgs drop_args(uint64_t seed, uint64_t offset, uint32_t T, float c)
 {
-    return {philox_keys(seed), offset, T < 65536u ? T << 16 : 0xFFFFFFFFu, c};
+    return {philox_keys(seed), offset, T << 16, c, T == 65536u};
 }
 
 // The eight 16-bit draws of elements 8 b .. 8 b + 7, two per word.
 QD uint4 drop_draws(uint64_t b, const DropArgs &d) { return sr_bits_rk<kDropStream>(d.offset + b, d.keys); }
 
-// Whether element j of the eight is kept: its draw, in the upper half of a
-// word whose lower half is zero, against the threshold in the same place.
+// Whether element j of the eight is kept (not for d.all): its draw in the upper
+// half of a word against T in the same place; what is below does not matter.
 QD bool drop_keep(const uint4 &draws, int j, uint32_t threshold)
 {
     const uint32_t w = word(draws, j >> 1);
-    return ((j & 1) ? (w & 0xFFFF0000u) : (w << 16)) >= threshold;
+    return ((j & 1) ? w : (w << 16)) >= threshold;
 }
 
 }  // namespace qk
