@@ -85,23 +85,22 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
     const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + kPairN - 1) / kPairN);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
     const int64_t pairs = sm_count() / 2;
-    k_mm_pair<OUT, COLS><<<(unsigned)(2 * (tiles < pairs ? tiles : pairs)), kPairThreads, sizeof(PairSmem), st>>>(map_p, map_q, map_c, g);
-    return cudaGetLastError();
+    return launch_k(true, k_mm_pair<OUT, COLS>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads),
+                    sizeof(PairSmem), st, map_p, map_q, map_c, g);
 }
 
 // Which kernel, and how wide and how deep a split: the least estimated time.
 // What was measured on a GB300 (graphs of calls, weights from memory): a call
-// takes 4.2 us beside its blocks and 0.7 more where a cluster adds up, 2.2 one of
-// eight; a CTA's
-// block of 128 weights x bn tokens the times below (with 4096 x 4096 weights
-// and 40 tokens 14.8 / 9.9 / 7.6 / 8.7 us at splits of 1 / 2 / 4 / 8, with 333
-// tokens 17.2 at 192 wide against 20.2 at 128, 21.3 at 64 and 21.2 on the pair
-// kernel, with 1024 tokens 23.2 there and 40.8 at 128); two resident CTAs 1.4
-// times one's time; and a CTA that comes after another about 2 us more.  A
-// split has to be resident as a whole: clusters that wait for one another's SMs
-// lose more than the split gains (7168 x 18432 with 128 tokens: 37.5 us split in
-// two, 43.5 in four, 59.1 in eight), and clusters of four and eight leave SMs
-// of a GPC unused.
+// takes 3.2 us beside its blocks, 0.7 more where a cluster adds up, 2.2 one of
+// eight; a CTA's block of 128 weights x bn tokens the times below (with 4096 x
+// 4096 weights and 40 tokens 14.8 / 9.9 / 7.6 / 8.7 us at splits of 1 / 2 / 4 /
+// 8, with 333 tokens 16.0 at 192 wide and two deep against 19.5 at 128, 20.1 at
+// 64 and 18.2 on the pair kernel, with 1024 tokens 19.0 there and 39.4 at 128);
+// two resident CTAs 1.4 times one's time; and a CTA that comes after another
+// about 2 us more.  A split has to be resident as a whole: clusters that wait
+// for one another's SMs lose more than the split gains (7168 x 18432 with 128
+// tokens: 37.5 us split in two, 43.5 in four, 59.1 in eight), and clusters of
+// four and eight leave SMs of a GPC unused.
 struct MmPlan {
     int bn, split;   // bn 0: the pair kernel
 };
@@ -116,7 +115,7 @@ MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool cols, int sms)
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
     MmPlan best = {0, 1};
-    double cost = 4.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.68 : 0.5) + 1.0);
+    double cost = 2.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.56 : 0.5) + 1.0);
     for (const Width &w : kWidths) {
         const int64_t tz = (M + w.bn - 1) / w.bn;
         if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;
@@ -124,7 +123,7 @@ MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool cols, int sms)
             const int64_t ctas = ty * tz * split, n = (ctas + sms - 1) / sms;   // n: CTAs of an SM
             if (split > 1 && ctas > (int64_t)w.resident * (split == 8 ? sms * 16 / 19 : split == 4 ? sms * 18 / 19 : sms)) break;
             const double share = n == 2 && w.resident == 2 ? 1.4 : (double)n;
-            const double c = 4.2 + (split == 8 ? 2.2 : split > 1 ? 0.7 : 0.0) + (double)((kblocks + split - 1) / split) * w.block * share +
+            const double c = 3.2 + (split == 8 ? 2.2 : split > 1 ? 0.7 : 0.0) + (double)((kblocks + split - 1) / split) * w.block * share +
                              2.0 * (double)((n - 1) / w.resident);
             if (c < cost) {
                 cost = c;

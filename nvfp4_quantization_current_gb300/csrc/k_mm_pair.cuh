@@ -18,19 +18,32 @@
 // bytes each.
 //
 // The hand-over of the accumulator buffers is what the block rate hangs on:
-// MMAs (512 cycles), commit (207 until a polling warp sees it), read (about
-// 400), release and the next MMAs into the same buffer form a chain, of which
-// two are in flight.  The release is a named barrier (about 20 cycles from
-// arrival to wake-up, an mbarrier takes 160 to 200); as a warp's barrier waits
-// for its own commits too, each buffer has an MMA warp of its own.  In the
-// other CTA those two warps wait at the same barrier and pass the release on to
-// the leader.  A named barrier cannot time out, and need not: these warps wait
-// there only for blocks whose MMAs are issued (the leader's) or that the
-// epilogue is going to read, after a look at the abort flag, and the epilogue
-// warps arrive for every block of a tile, whether their own waits were served
-// or given up (which takes a thousand polls each, so that they never overtake a
-// warp between its look and its barrier), and at both buffers once more when
-// they leave on the flag.
+// MMAs (512 cycles), commit (150 and more until a waiting warp sees it), read
+// (about 440), release (some 400 more from the other CTA) and the next MMAs
+// into the same buffer form a chain, of which two are in flight; measured, a
+// block takes about 900 cycles, and a tile's end some 3000 more.  Inside a CTA
+// the release is a named barrier (about 20 cycles from arrival to wake-up, an
+// mbarrier takes 160 to 200); as a warp's barrier waits for its own commits
+// too, each buffer has an MMA warp of its own.  The other CTA's warps arrive on
+// the leader's mbarriers; its warps 1 and 2 wait at the named barriers only to
+// say which scales are done with.  Tried and not faster: an MMA per CTA, a block
+// in two MMAs of 128 columns with a chain each, sixteen epilogue warps, more
+// stages, prefetches into L2.
+//
+// Measured on a GB300 in sustained runs, at its 1.4 kW: 16384 x 18432 x 7168
+// 1.71 ms (2.54 PFLOP/s, clocks at 1.72 of 2.07 GHz), 8192 x 14336 x 4096 390
+// us (2.47), with 1x128 tiles of both and an FP32 C added to 14336 x 4096 x
+// 8192 about 490 us (1.96; its FP32 multiplies and adds take 512 cycles of a
+// block, the other's 256).
+// Without the epilogue's work the loads and MMAs alone reach 3.1 PFLOP/s there.
+//
+// A named barrier cannot time out, and need not: these warps wait there only
+// for blocks whose MMAs are issued (the leader's) or that the epilogue is going
+// to read, after a look at the abort flag, and the epilogue warps arrive for
+// every block of a tile, whether their own waits were served or given up (which
+// takes a thousand tries each, so that they never overtake a warp between its
+// look and its barrier), and at both buffers once more when they leave on the
+// flag.
 #pragma once
 
 #include "q_internal.h"
@@ -178,7 +191,6 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int kb_n = (int)g.kblocks;
-    const int rows_p = (int)g.rows_p, rows_q = (int)g.rows_q;   // below 2^31, and fewer than 2^31 tiles
     const int tiles_p = (int)((g.rows_p + 255) / 256), tiles_q = (int)((g.rows_q + kPairN - 1) / kPairN);
     const int tiles = tiles_p * tiles_q, pairs = gridDim.x / 2, first = blockIdx.x / 2;
     volatile int *const stop = &sm.abort_flag;
@@ -206,6 +218,9 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     cluster_sync();   // the peer's barriers are ready before anything arrives on them
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    // Launched while the kernel ahead still ran; nothing was read or written so far.
+    griddep_wait();
+    griddep_launch_dependents();
 
     if (warp < 4) {
         regs_fewer<kPairRegs>();
@@ -265,14 +280,14 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 if (rank == 0) {
                     if (n >= blocks) break;
                     // a wait that gives up raises the flag, here or in the epilogue
-                    mm_wait<true>(&sm.full[s], par, stop, g.status);
+                    mm_wait(&sm.full[s], par, stop, g.status);
                 }
                 aborted = __any_sync(0xFFFFFFFFu, *stop);
                 if (aborted) break;
                 if (n >= 2) {   // block n - 2 has been read, in both CTAs
                     acc_await(buf);
                     if (rank == 0) {
-                        mm_wait<true>(&sm.peer_free[buf], freed, stop, g.status);
+                        mm_wait(&sm.peer_free[buf], freed, stop, g.status);
                         freed ^= 1;
                     }
                 }
@@ -335,7 +350,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             for (int kb = 0; kb < kb_n; kb++, n++) {
                 const int buf = n & 1;
                 if (ring % kPairScaleBlocks == 0) mm_wait(&sm.sc_full[ring / kPairScaleBlocks], sc_par, stop, g.status);
-                mm_wait<true>(&sm.acc_full[buf], (n >> 1) & 1, stop, g.status);
+                mm_wait(&sm.acc_full[buf], (n >> 1) & 1, stop, g.status);
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t addr = acc_addr + buf * kPairN;

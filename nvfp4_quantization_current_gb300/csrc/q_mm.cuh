@@ -24,18 +24,15 @@ struct MmArgs {
 };
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the
-// wait ran out (which raises it and reports the timeout).  SPIN polls without
-// giving up the issue slot: the waiting warp sees the phase about 130 cycles
-// sooner than one that the hardware wakes, which pays for the two waits in
-// the chain of an accumulator buffer.
-template <bool SPIN = false> QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+// wait ran out (which raises it and reports the timeout).  The hardware wakes
+// the warp: polling sees the phase some 130 cycles sooner, but the polls' power
+// costs the large products 2 to 3%.
+QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
-    // The timer is read once in many polls: a read takes about as long as a
-    // block's MMAs, and these waits are on the path of every block.
     unsigned long long t0 = 0;
     for (uint32_t n = 1;; n++) {
-        if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if (n % 1024 == 0) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (n % 1024 == 0) {   // the timer and the flag are off the way of the waits that are served
             if (*abort_flag) return false;
             const unsigned long long now = globaltimer();
             if (t0 == 0) t0 = now;
@@ -47,6 +44,7 @@ template <bool SPIN = false> QD bool mm_wait(uint64_t *bar, uint32_t parity, vol
         }
     }
 }
+
 template <int OUT> struct OutT;
 template <> struct OutT<BF16> { using T = uint16_t; };
 template <> struct OutT<F32> { using T = float; };

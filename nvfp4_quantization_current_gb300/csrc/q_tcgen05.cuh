@@ -174,19 +174,7 @@ QD uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c)
 // load has yet to write.
 // ---------------------------------------------------------------------------
 
-// Lane l of the warp gets 32 columns of tensor memory lane (address lane + l).
-QD void tmem_ld32(uint32_t (&r)[32], uint32_t addr)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-                 : "r"(addr) : "memory");
-}
+// Lane l of the warp gets 16 columns of tensor memory lane (address lane + l).
 QD void tmem_ld16(uint32_t (&r)[16], uint32_t addr)
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -209,70 +197,6 @@ QD void tmem_ld_rows16(uint32_t (&r)[16], uint32_t addr)
                  : "r"(addr) : "memory");
 }
 
-// tmem_ld16 of the next 16 columns while the present 16, times ss, are added
-// to acc: one statement for the same reason, with the arithmetic inside so that
-// it covers the load's latency.
-QD void tmem_ld16_add(uint32_t (&next)[16], uint32_t addr, const uint32_t (&now)[16], uint64_t *acc, uint64_t ss)
-{
-    asm volatile("{\n\t.reg .b64 v;\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%41];\n\t"
-                 "mov.b64 v, {%24, %25};\n\t" "fma.rn.f32x2 %16, v, %40, %16;\n\t"
-                 "mov.b64 v, {%26, %27};\n\t" "fma.rn.f32x2 %17, v, %40, %17;\n\t"
-                 "mov.b64 v, {%28, %29};\n\t" "fma.rn.f32x2 %18, v, %40, %18;\n\t"
-                 "mov.b64 v, {%30, %31};\n\t" "fma.rn.f32x2 %19, v, %40, %19;\n\t"
-                 "mov.b64 v, {%32, %33};\n\t" "fma.rn.f32x2 %20, v, %40, %20;\n\t"
-                 "mov.b64 v, {%34, %35};\n\t" "fma.rn.f32x2 %21, v, %40, %21;\n\t"
-                 "mov.b64 v, {%36, %37};\n\t" "fma.rn.f32x2 %22, v, %40, %22;\n\t"
-                 "mov.b64 v, {%38, %39};\n\t" "fma.rn.f32x2 %23, v, %40, %23;\n\t"
-                 "tcgen05.wait::ld.sync.aligned;\n\t}"
-                 : "=&r"(next[0]), "=&r"(next[1]), "=&r"(next[2]), "=&r"(next[3]), "=&r"(next[4]),
-                   "=&r"(next[5]), "=&r"(next[6]), "=&r"(next[7]), "=&r"(next[8]), "=&r"(next[9]),
-                   "=&r"(next[10]), "=&r"(next[11]), "=&r"(next[12]), "=&r"(next[13]), "=&r"(next[14]),
-                   "=&r"(next[15]), "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]),
-                   "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7])
-                 : "r"(now[0]), "r"(now[1]), "r"(now[2]), "r"(now[3]), "r"(now[4]), "r"(now[5]), "r"(now[6]),
-                   "r"(now[7]), "r"(now[8]), "r"(now[9]), "r"(now[10]), "r"(now[11]), "r"(now[12]),
-                   "r"(now[13]), "r"(now[14]), "r"(now[15]), "l"(ss), "r"(addr) : "memory");
-}
-// The same with tmem_ld_rows16's layout: columns times cc (four pairs), then
-// rows times s0 (r[4i], r[4i + 1]) and s1.
-QD void tmem_ld_rows16_add(uint32_t (&next)[16], uint32_t addr, const uint32_t (&now)[16], uint64_t *acc, const uint64_t (&cc)[4],
-                           uint64_t s0, uint64_t s1)
-{
-    asm volatile("{\n\t.reg .b64 v;\n\t"
-                 "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%46];\n\t"
-                 "mov.b64 v, {%24, %25};\n\t" "mul.rn.f32x2 v, v, %40;\n\t" "fma.rn.f32x2 %16, v, %44, %16;\n\t"
-                 "mov.b64 v, {%26, %27};\n\t" "mul.rn.f32x2 v, v, %40;\n\t" "fma.rn.f32x2 %17, v, %45, %17;\n\t"
-                 "mov.b64 v, {%28, %29};\n\t" "mul.rn.f32x2 v, v, %41;\n\t" "fma.rn.f32x2 %18, v, %44, %18;\n\t"
-                 "mov.b64 v, {%30, %31};\n\t" "mul.rn.f32x2 v, v, %41;\n\t" "fma.rn.f32x2 %19, v, %45, %19;\n\t"
-                 "mov.b64 v, {%32, %33};\n\t" "mul.rn.f32x2 v, v, %42;\n\t" "fma.rn.f32x2 %20, v, %44, %20;\n\t"
-                 "mov.b64 v, {%34, %35};\n\t" "mul.rn.f32x2 v, v, %42;\n\t" "fma.rn.f32x2 %21, v, %45, %21;\n\t"
-                 "mov.b64 v, {%36, %37};\n\t" "mul.rn.f32x2 v, v, %43;\n\t" "fma.rn.f32x2 %22, v, %44, %22;\n\t"
-                 "mov.b64 v, {%38, %39};\n\t" "mul.rn.f32x2 v, v, %43;\n\t" "fma.rn.f32x2 %23, v, %45, %23;\n\t"
-                 "tcgen05.wait::ld.sync.aligned;\n\t}"
-                 : "=&r"(next[0]), "=&r"(next[1]), "=&r"(next[2]), "=&r"(next[3]), "=&r"(next[4]),
-                   "=&r"(next[5]), "=&r"(next[6]), "=&r"(next[7]), "=&r"(next[8]), "=&r"(next[9]),
-                   "=&r"(next[10]), "=&r"(next[11]), "=&r"(next[12]), "=&r"(next[13]), "=&r"(next[14]),
-                   "=&r"(next[15]), "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]),
-                   "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7])
-                 : "r"(now[0]), "r"(now[1]), "r"(now[2]), "r"(now[3]), "r"(now[4]), "r"(now[5]), "r"(now[6]),
-                   "r"(now[7]), "r"(now[8]), "r"(now[9]), "r"(now[10]), "r"(now[11]), "r"(now[12]),
-                   "r"(now[13]), "r"(now[14]), "r"(now[15]), "l"(cc[0]), "l"(cc[1]), "l"(cc[2]), "l"(cc[3]),
-                   "l"(s0), "l"(s1), "r"(addr) : "memory");
-}
-
-// mbar_try_wait that never suspends the thread.
-QD bool mbar_test_wait(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return done != 0;
-}
 // Arrival at barrier `id` (1..15, `count` threads in all) without waiting.
 QD void named_barrier_arrive(int id, int count) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory"); }
 
