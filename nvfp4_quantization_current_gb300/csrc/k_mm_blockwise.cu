@@ -60,6 +60,20 @@ cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int sp
     return cudaLaunchKernelEx(&cfg, k_mm_split<OUT, BN>, map_p, map_q, g);
 }
 
+// The registers that the pair kernel's epilogue takes over have to be there at
+// its launch: it would wait for them forever.
+template <int OUT, bool COLS> cudaError_t pair_registers_ready()
+{
+    static std::atomic<bool> ready{false};
+    if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm_pair<OUT, COLS>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs * kPairThreads < 32 * (kPairEpiWarps * kPairEpiRegs + 4 * kPairRegs)) return cudaErrorInvalidConfiguration;
+    ready.store(true, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
 // Tiles of 256 x 256 on CTA pairs.
 template <int OUT, bool COLS>
 cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t st)
@@ -72,15 +86,7 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
     g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
     if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
     if (e == cudaSuccess) e = engine_smem_ready<k_mm_pair<OUT, COLS>>(sizeof(PairSmem));
-    if (e == cudaSuccess) {   // the epilogue's registers have to be there to be moved: it would wait for them forever
-        static const cudaError_t enough = [] {
-            cudaFuncAttributes a;
-            const cudaError_t ea = cudaFuncGetAttributes(&a, k_mm_pair<OUT, COLS>);
-            if (ea != cudaSuccess) return ea;
-            return a.numRegs * kPairThreads >= 32 * (kPairEpiWarps * kPairEpiRegs + 4 * kPairRegs) ? cudaSuccess : cudaErrorInvalidConfiguration;
-        }();
-        e = enough;
-    }
+    if (e == cudaSuccess) e = pair_registers_ready<OUT, COLS>();
     if (e != cudaSuccess) return e;
     const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + kPairN - 1) / kPairN);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;

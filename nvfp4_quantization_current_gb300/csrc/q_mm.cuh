@@ -91,10 +91,12 @@ QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *stagin
     auto send = [&](const uint8_t *buf, int64_t col) {
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0 && row0 < g.rows_p && col < g.rows_q) {
-            if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, buf, (int)col, (int)row0);
-            else tma_store_tile(map_c, buf, (int)col, (int)row0);
-            bulk_commit();
+        if (lane == 0) {
+            if (row0 < g.rows_p && col < g.rows_q) {
+                if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, buf, (int)col, (int)row0);
+                else tma_store_tile(map_c, buf, (int)col, (int)row0);
+            }
+            bulk_commit();   // an empty group too, for claim() counts them
         }
     };
     if (OUT == BF16 && bulk) {

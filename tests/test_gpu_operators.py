@@ -137,6 +137,62 @@ def test_mm_many_tiles(M, N, K, tb, dtype, accumulate):
     check_mm(M, N, K, "1x128", tb, dtype, accumulate)
 
 
+# widths of 16 to 192 tokens with splits of 1 to 8, tiles that end inside them, and the pair kernel with reductions of
+# 1, 2, 3, 7 and 9 blocks over more tiles than the machine has pairs
+@pytest.mark.parametrize("M,N,K,tb", [(1, 4096, 4096, "128x128"), (16, 14336, 512, "128x128"), (17, 2048, 2048, "128x128"),
+                                      (40, 4096, 4096, "128x128"), (64, 18432, 896, "128x128"), (100, 1000, 4096, "1x128"),
+                                      (128, 7168, 2304, "128x128"), (200, 4096, 4096, "128x128"), (333, 4096, 4096, "128x128"),
+                                      (350, 4000, 1152, "1x128"), (513, 700, 8192, "1x128"), (1024, 1024, 4096, "1x128"),
+                                      (5000, 5120, 128, "128x128"), (5000, 5120, 128, "1x128"), (2600, 5120, 256, "1x128"),
+                                      (4999, 4991, 384, "1x128"), (2305, 4608, 896, "128x128"), (4600, 2300, 1152, "1x128")])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, True), (torch.bfloat16, True)])
+def test_mm_plans(M, N, K, tb, dtype, accumulate):
+    check_mm(M, N, K, "1x128", tb, dtype, accumulate, seed=M)
+
+
+def test_mm_calls_in_a_row():
+    """Calls that may overlap their neighbours' ends (each result is the next one's input or accumulator)."""
+    a, sa = operand(24, 512, "1x128", 81)
+    b, sb = operand(512, 512, "128x128", 82)
+    big, sbig = operand(700, 512, "1x128", 83)
+    c = torch.zeros((24, 512), device="cuda")
+    d = torch.zeros((700, 512), device="cuda")
+    one, two = Q.mm_blockwise(a, sa, b, sb, dtype=torch.float32), Q.mm_blockwise(big, sbig, b, sb, dtype=torch.float32)
+    torch.cuda.synchronize()
+    for i in range(64):
+        Q.mm_blockwise(a, sa, b, sb, out=c, accumulate=True)
+        Q.mm_blockwise(big, sbig, b, sb, out=d, accumulate=True)
+        x = Q.mm_blockwise(a, sa, b, sb)
+        q = Q.q_blockwise(x)
+        y = Q.mm_blockwise(q.q_row, q.s_row, b, sb)
+    # the sums of 64 equal FP32 terms: each addition rounds once
+    assert bool(((c.double() - 64 * one.double()).abs() <= 64 * 64 * 2.0 ** -24 * one.double().abs()).all())
+    assert bool(((d.double() - 64 * two.double()).abs() <= 64 * 64 * 2.0 ** -24 * two.double().abs()).all())
+    x1 = Q.mm_blockwise(a, sa, b, sb)
+    torch.cuda.synchronize()
+    q1 = Q.q_blockwise(x1)
+    torch.cuda.synchronize()
+    assert torch.equal(y, Q.mm_blockwise(q1.q_row, q1.s_row, b, sb))
+
+
+def test_mm_on_two_streams():
+    a, sa = operand(48, 2048, "1x128", 91)
+    b, sb = operand(2048, 2048, "128x128", 92)
+    big, sbig = operand(3000, 2048, "1x128", 93)
+    want, wide = Q.mm_blockwise(a, sa, b, sb), Q.mm_blockwise(big, sbig, b, sb)
+    torch.cuda.synchronize()
+    s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(s0):
+            x = Q.mm_blockwise(a, sa, b, sb)
+        with torch.cuda.stream(s1):
+            y = Q.mm_blockwise(big, sbig, b, sb)
+        got.append((x, y))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) and torch.equal(y, wide) for x, y in got)
+
+
 def test_mm_random_shapes():
     rng = np.random.default_rng(5)
     for i in range(40):
