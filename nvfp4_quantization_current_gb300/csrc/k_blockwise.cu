@@ -33,7 +33,11 @@
 // the engine lies inside one Philox block, so a thread draws the decisions of
 // its own 8 rows and zeroes dropped elements in its registers.  Rounding is
 // monotonic, so max|y| = RN(c max|kept x|), and the codes are those of
-// RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.
+// RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.  Measured on a
+// GB300, both copies of 8192 x 4096: BF16 39.5 us (26.5 without dropout, 29.9
+// with the draws taken out: ten Philox rounds per eight elements are 9.5 us of
+// integer multiplies), FP32 71.6 us (55.4); two calls, drop_add and q_blockwise,
+// take 49 us for BF16.
 #include "q_dropout.cuh"
 #include "q_engine.cuh"
 #include "q_internal.h"

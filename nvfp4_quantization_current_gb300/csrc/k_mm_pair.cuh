@@ -103,21 +103,6 @@ QD void pair_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
     q = r / height;
 }
 
-// Four consecutive block scales from kb on, the last one repeated past the end.
-QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n)
-{
-    if ((kb_n & 3) == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {   // kb + 3 exists
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(row + (kb < kb_n ? kb : 0)));
-        s[0] = v.x;
-        s[1] = v.y;
-        s[2] = v.z;
-        s[3] = v.w;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) s[j] = __ldg(row + (kb + j < kb_n ? kb + j : kb_n - 1));
-    }
-}
-
 // The scales of all tiles of a CTA's walk (one warp), the next four blocks' on
 // their way while four wait for a slot: four rows of P per lane, and eight rows
 // of Q or, from lanes 0 and 1, those of Q's two 128-row tiles.  Rows outside the

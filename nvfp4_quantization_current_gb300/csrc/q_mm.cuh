@@ -45,6 +45,21 @@ QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_
     }
 }
 
+// Four consecutive block scales from kb on, the last one repeated past the end.
+QD void load_scales4(float (&s)[4], const float *row, int kb, int kb_n)
+{
+    if (((kb_n | kb) & 3) == 0 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {   // kb + 3 exists
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(row + (kb < kb_n ? kb : 0)));
+        s[0] = v.x;
+        s[1] = v.y;
+        s[2] = v.z;
+        s[3] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; j++) s[j] = __ldg(row + (kb + j < kb_n ? kb + j : kb_n - 1));
+    }
+}
+
 template <int OUT> struct OutT;
 template <> struct OutT<BF16> { using T = uint16_t; };
 template <> struct OutT<F32> { using T = float; };
