@@ -34,10 +34,12 @@
 // its own 8 rows and zeroes dropped elements in its registers.  Rounding is
 // monotonic, so max|y| = RN(c max|kept x|), and the codes are those of
 // RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.  Measured on a
-// GB300, both copies of 8192 x 4096: BF16 39.5 us (26.5 without dropout, 29.9
+// GB300, both copies of 8192 x 4096: BF16 39.4 us (26.5 without dropout, 29.9
 // with the draws taken out: ten Philox rounds per eight elements are 9.5 us of
-// integer multiplies), FP32 71.6 us (55.4); two calls, drop_add and q_blockwise,
-// take 49 us for BF16.
+// integer multiplies), FP32 71.6 us (55.6); two calls, drop_add and q_blockwise,
+// take 46.9 us for BF16.  The integer pipes bound it: with the next tile's
+// decisions drawn ahead, one bit each, in the body's waiting phases it took 40.9
+// to 42.1 us.
 #include "q_dropout.cuh"
 #include "q_engine.cuh"
 #include "q_internal.h"

@@ -31,10 +31,10 @@
 // stages, prefetches into L2.
 //
 // Measured on a GB300 in sustained runs, at its 1.4 kW: 16384 x 18432 x 7168
-// 1.71 ms (2.54 PFLOP/s, clocks at 1.72 of 2.07 GHz), 8192 x 14336 x 4096 390
-// us (2.47), with 1x128 tiles of both and an FP32 C added to 14336 x 4096 x
-// 8192 about 490 us (1.96; its FP32 multiplies and adds take 512 cycles of a
-// block, the other's 256).
+// 1.67 to 1.74 ms (2.5 to 2.6 PFLOP/s, clocks at 1.72 of 2.07 GHz), 8192 x
+// 14336 x 4096 384 to 397 us (2.4 to 2.5), with 1x128 tiles of both and an FP32
+// C added to 14336 x 4096 x 8192 494 us (1.95; its FP32 multiplies and adds take
+// 512 cycles of a block, the other's 256).
 // Without the epilogue's work the loads and MMAs alone reach 3.1 PFLOP/s there.
 //
 // A named barrier cannot time out, and need not: these warps wait there only

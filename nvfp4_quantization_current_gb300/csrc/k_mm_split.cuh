@@ -16,7 +16,7 @@
 //
 // Measured on a GB300, in graphs of calls: one token with 4096 x 4096 weights
 // 4.9 us (their 16.8 MB at 3.4 TB/s; the launch and two trips to memory are
-// most of it), 16 tokens with 14336 x 4096 13.2 us (4.5 TB/s), 333 tokens with
+// most of it), 16 tokens with 14336 x 4096 13.1 us (4.5 TB/s), 333 tokens with
 // 4096 x 4096 14.8 us (755 TFLOP/s; a block of 128 x 192 takes 1150 cycles,
 // where shared memory needs 640 and the MMAs 384: the hand-over of two
 // accumulator buffers again).
