@@ -59,13 +59,13 @@ REF_BUDGET_S = 120.0
 RHT_MASK = 0xB4E1   # the 16 random signs of the Hadamard transform (any fixed draw)
 
 # DRAM bytes per launch (dram__bytes_read.sum + dram__bytes_write.sum) from one
-# ncu --set full capture of the kernel on the named call (key "workload.tensor:
+# ncu capture of the kernel on the named call (key "workload.tensor:
 # piece"), with the kernel, the commit the capture measured, and the hash of
 # the kernel's source (file + shared device headers) at capture time;
 # reported as null once the source has changed since.
 TRAFFIC = {
-    "bw3.w:bwmx_128x128_T": {"kernel": "qk::k_blockwise<0, 1, 1>", "capture_commit": "a00210f",
-                             "bytes_per_launch": 485297664, "src_hash": "076d29a3116c64ea"},
+    "bw3.w:bwmx_128x128_T": {"kernel": "qk::k_blockwise<0, 1, 1, NoDrop>", "capture_commit": "7636e68",
+                             "bytes_per_launch": 484877824, "src_hash": "deabcf4aa565bce9"},
 }
 
 
