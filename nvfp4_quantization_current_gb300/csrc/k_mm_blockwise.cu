@@ -101,42 +101,80 @@ cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t s
                     sizeof(PairSmem), st, map_p, map_q, map_c, g);
 }
 
+// CTAs that clusters of `split` keep resident, one per SM: a cluster stays
+// inside a GPC, whose SMs need not be a multiple of it (152 SMs: 144 in
+// clusters of four, 120 in clusters of eight).
+int cluster_ctas(int split)
+{
+    static std::atomic<int> known[64][3];   // of a device's splits 2, 4, 8
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;   // no answer, no clusters
+    std::atomic<int> &k = known[dev][split == 2 ? 0 : split == 4 ? 1 : 2];
+    const int c = k.load(std::memory_order_relaxed);
+    if (c > 0) return c;
+    constexpr auto kernel = k_mm_split<BF16, 128, true>;   // one CTA fills an SM
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(SplitSmem<128>::kThreads);
+    cfg.dynamicSmemBytes = sizeof(SplitSmem<128>);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (engine_smem_ready<k_mm_split<BF16, 128, true>>(sizeof(SplitSmem<128>), true) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+        return 0;
+    k.store(n * split, std::memory_order_relaxed);
+    return n * split;
+}
+
 // Which kernel, and how wide and how deep a split: the least estimated time.
-// What was measured on a GB300 (graphs of calls, weights from memory): a call
-// takes 3.2 us beside its blocks, 0.7 more where a cluster adds up, 2.2 one of
-// eight; a CTA's block of 128 weights x bn tokens the times below (with 4096 x
-// 4096 weights and 40 tokens 13.2 / 8.9 / 6.6 / 7.5 us at splits of 1 / 2 / 4 /
-// 8, with 333 tokens 14.8 at 192 wide and two deep against 17.5 at 128, 18.7 at
-// 64 and 17.6 on the pair kernel, with 700 tokens 18.3 there and 23.1 at 192);
-// two resident CTAs 1.4 times one's time; and a CTA that comes after another
-// about 2 us more.  A split has to be resident as a whole: clusters that wait
-// for one another's SMs lose more than the split gains (7168 x 18432 with 128
-// tokens: 32.4 us split in two, 39.1 in four, 55.5 in eight), and clusters of
-// four and eight leave SMs of a GPC unused.
+// The estimate's terms (us) are a fit to 1500 calls of every plan that 180
+// shapes allow (1 to 1024 tokens, weights from 1024 x 1024 to 18432 x 7168 in
+// both tilings; GB300, graphs of calls); its choices take 0.8% more time than
+// the best plan on the average and 13% at most.  A call has a fixed part, a cluster
+// adds its sum, a CTA takes `block` for each block of 128 weights x bn tokens
+// (`rows` times as long where each weight row has a scale), two CTAs of an SM
+// `share` times one's time, and a CTA that comes after another a start of its
+// own.  Some of what it is drawn from, for 4096 x 4096 weights: 333 tokens 14.5
+// at 192 wide and two deep, 17.4 at 128, 15.7 on the pair kernel; 700 tokens
+// 16.5 there and 23 at 192.  A split has to be resident as a whole: clusters
+// that wait for one another's SMs lose more than the split gains (2048 x 8192
+// with 100 tokens, 128 wide: 10.5 us at a split of four, 17.0 at eight, whose
+// 16 clusters are one more than fit).
 struct MmPlan {
     int bn, split;   // bn 0: the pair kernel
 };
-MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool cols, int sms)
+MmPlan mm_plan(int64_t M, int64_t N, int64_t kblocks, bool rows, int sms)
 {
     struct Width {
         int bn;
-        double block;   // us
+        double fixed, block, rows;
         int resident;
+        double share;
     };
-    static constexpr Width kWidths[] = {{16, 0.21, 2}, {32, 0.245, 2}, {64, 0.32, 2}, {128, 0.41, 1}, {192, 0.55, 1}};
+    static constexpr Width kWidths[] = {{16, 2.7, 0.24, 1.1, 2, 1.24},
+                                        {32, 2.7, 0.253, 1.15, 2, 1.63},
+                                        {64, 4.5, 0.3, 1.17, 2, 1.54},
+                                        {128, 5.0, 0.374, 1.23, 1, 1.0},
+                                        {192, 6.0, 0.511, 1.2, 1, 1.0}};
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + kPairN - 1) / kPairN);
     MmPlan best = {0, 1};
-    double cost = 2.2 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (cols ? 0.57 : 0.47) + 1.0);
+    double cost = 3.25 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * (rows ? 0.589 : 0.407) + 0.75);
     for (const Width &w : kWidths) {
         const int64_t tz = (M + w.bn - 1) / w.bn;
         if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;
         for (int split = 1; split <= kSplitMost && (split == 1 || 2 * split <= kblocks); split *= 2) {
             const int64_t ctas = ty * tz * split, n = (ctas + sms - 1) / sms;   // n: CTAs of an SM
-            if (split > 1 && ctas > (int64_t)w.resident * (split == 8 ? sms * 16 / 19 : split == 4 ? sms * 18 / 19 : sms)) break;
-            const double share = n == 2 && w.resident == 2 ? 1.4 : (double)n;
-            const double c = 3.2 + (split == 8 ? 2.2 : split > 1 ? 0.7 : 0.0) + (double)((kblocks + split - 1) / split) * w.block * share +
-                             2.0 * (double)((n - 1) / w.resident);
+            if (split > 1 && ctas > (int64_t)w.resident * cluster_ctas(split)) break;
+            const double blocks = (double)((kblocks + split - 1) / split) * w.block * (rows ? w.rows : 1.0);
+            const double times = (double)(n / w.resident) * w.share + (double)(n % w.resident);
+            const double c = w.fixed + (split == 8 ? 1.0 : split == 4 ? 0.65 : split == 2 ? 0.43 : 0.0) + blocks * times +
+                             1.6 * (double)((n - 1) / w.resident);
             if (c < cost) {
                 cost = c;
                 best = {w.bn, split};

@@ -150,6 +150,21 @@ def test_mm_plans(M, N, K, tb, dtype, accumulate):
     check_mm(M, N, K, "1x128", tb, dtype, accumulate, seed=M)
 
 
+# each width from its narrowest call on and each depth of split, results that end inside a tile and reductions that the
+# split does not divide
+@pytest.mark.parametrize("M,N,K,tb", [(3, 128, 768, "128x128"), (1, 198, 2816, "1x128"), (1, 128, 3456, "128x128"),
+                                      (19, 10240, 1280, "128x128"), (17, 1933, 5120, "1x128"), (17, 2048, 4736, "128x128"),
+                                      (642, 137, 1920, "1x128"), (81, 12939, 256, "1x128"), (36, 13131, 1536, "1x128"),
+                                      (33, 6656, 2560, "128x128"), (1300, 154, 2432, "1x128"), (33, 3200, 7040, "128x128"),
+                                      (132, 8290, 896, "1x128"), (649, 134, 6272, "1x128"), (163, 896, 5760, "128x128"),
+                                      (524, 12895, 512, "1x128"), (555, 12928, 1024, "128x128"), (171, 6604, 1536, "1x128"),
+                                      (1326, 411, 2432, "1x128"), (146, 3968, 3456, "128x128"), (1324, 155, 5760, "1x128"),
+                                      (138, 1920, 8064, "128x128"), (100, 2048, 8192, "128x128"), (192, 2048, 8192, "1x128")])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, True)])
+def test_mm_widths_and_splits(M, N, K, tb, dtype, accumulate):
+    check_mm(M, N, K, "1x128", tb, dtype, accumulate, seed=N)
+
+
 def test_mm_calls_in_a_row():
     """Calls that may overlap their neighbours' ends (each result is the next one's input or accumulator)."""
     a, sa = operand(24, 512, "1x128", 81)
