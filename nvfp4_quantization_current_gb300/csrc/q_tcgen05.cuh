@@ -106,6 +106,14 @@ QD void mbar_arrive_cluster(uint32_t addr)
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// Ahead of a kernel's loads: its tensor map, and a tile into L2 (coherent: a
+// later write reaches it there).
+QD void prefetch_map(const CUtensorMap *map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
+QD void prefetch_tile(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 // CTA pairs (clusters of two): one MMA spans both CTAs' tensor memory, each CTA
 // holding its own 128 rows of A and D and half of B's rows.  All tensor memory
 // instructions of such a kernel name the pair.
