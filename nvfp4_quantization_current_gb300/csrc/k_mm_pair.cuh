@@ -19,22 +19,23 @@
 //
 // The hand-over of the accumulator buffers is what the block rate hangs on:
 // MMAs (512 cycles), commit (150 and more until a waiting warp sees it), read
-// (about 440), release (some 400 more from the other CTA) and the next MMAs
+// (about 350), release (some 400 more from the other CTA) and the next MMAs
 // into the same buffer form a chain, of which two are in flight; measured, a
-// block takes about 900 cycles, and a tile's end some 3000 more.  Inside a CTA
+// block takes about 800 cycles, and a tile's end some 3000 more.  Inside a CTA
 // the release is a named barrier (about 20 cycles from arrival to wake-up, an
 // mbarrier takes 160 to 200); as a warp's barrier waits for its own commits
 // too, each buffer has an MMA warp of its own.  The other CTA's warps arrive on
 // the leader's mbarriers; its warps 1 and 2 wait at the named barriers only to
 // say which scales are done with.  Tried and not faster: an MMA per CTA, a block
 // in two MMAs of 128 columns with a chain each, sixteen epilogue warps, more
-// stages, prefetches into L2.
+// stages, prefetches into L2, a look at the next block's barriers while one is
+// added, the additions between a load of tensor memory and its wait.
 //
 // Measured on a GB300 in sustained runs, at its 1.4 kW: 16384 x 18432 x 7168
-// 1.67 to 1.74 ms (2.5 to 2.6 PFLOP/s, clocks at 1.72 of 2.07 GHz), 8192 x
-// 14336 x 4096 384 to 397 us (2.4 to 2.5), with 1x128 tiles of both and an FP32
-// C added to 14336 x 4096 x 8192 494 us (1.95; its FP32 multiplies and adds take
-// 512 cycles of a block, the other's 256).
+// 1.63 to 1.65 ms (2.6 to 2.7 PFLOP/s, clocks at 1.58 of 2.07 GHz), 8192 x
+// 14336 x 4096 377 to 383 us (2.5), with 1x128 tiles of both and an FP32 C
+// added to 14336 x 4096 x 8192 494 to 506 us (1.9 to 1.95; its FP32 multiplies
+// and adds take 512 cycles of a block, the other's 256).
 // Without the epilogue's work the loads and MMAs alone reach 3.1 PFLOP/s there.
 //
 // A named barrier cannot time out, and need not: these warps wait there only

@@ -15,11 +15,15 @@
 // half of tensor memory.
 //
 // Measured on a GB300, in graphs of calls: one token with 4096 x 4096 weights
-// 4.9 us (their 16.8 MB at 3.4 TB/s; the launch and two trips to memory are
-// most of it), 16 tokens with 14336 x 4096 13.1 us (4.5 TB/s), 333 tokens with
-// 4096 x 4096 14.8 us (755 TFLOP/s; a block of 128 x 192 takes 1150 cycles,
-// where shared memory needs 640 and the MMAs 384: the hand-over of two
-// accumulator buffers again).
+// 4.8 us (6.3 where the weights come from memory and not from L2; the launch and
+// two trips to memory are most of it), 16 tokens with 14336 x 4096 12.1 to 12.6
+// us (4.7 TB/s), one token with 18432 x 7168 22.4 us (5.9 TB/s), 333 tokens
+// with 4096 x 4096 14.5 us (770 TFLOP/s; a block of 128 x 192 takes 1050
+// cycles, where shared memory needs 640 and the MMAs 384; reading and adding it
+// is what takes longer: without that work the call takes 11.6 us, without its
+// column scales 13.6).  Tried there and not faster: loads of 32 columns, and
+// the 16-lane loads of the pair kernel, which need a quarter of the column
+// scales (15.4 us; 15.2 against 16.4 where each weight row has a scale).
 #pragma once
 
 #include "q_internal.h"
