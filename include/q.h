@@ -397,9 +397,11 @@ q_status dq_nvfp4(const uint8_t *q, const uint8_t *sb, const float *s_global, in
  *   c [M, N] in `out` (Q_BF16 rounded to nearest even once, or Q_F32);
  *   accumulate != 0 adds to what c holds (the FP32 main gradient over
  *   micro-batches), 0 overwrites it without reading.
- * Sums are held in FP32; the result does not depend on timing (no atomics),
+ * Sums are held in FP32; the result does not depend on timing (nothing is added to twice in a call),
  * and a row's result does not depend on the values of other rows.  The E4M3
  * codes 0x7F and 0xFF are NaN and propagate, as do non-finite scales.
+ * Scales are multiplied in FP32, with each other or with a block's sum first:
+ * where such a product leaves FP32's normal range, the result is not accurate.
  * Shapes: K % 128 == 0, M % 128 == 0 (N % 128 == 0) for a 128x128 operand;
  * M, N, K < 2^31.  M == 0 or N == 0 does nothing; K == 0 is a sum over
  * nothing: c is set to zero, or left as it is when accumulating.
