@@ -34,7 +34,7 @@
 // its own 8 rows and zeroes dropped elements in its registers.  Rounding is
 // monotonic, so max|y| = RN(c max|kept x|), and the codes are those of
 // RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.  Measured on a
-// GB300, both copies of 8192 x 4096: BF16 39.4 us (26.5 without dropout, 29.9
+// GB300, both copies of 8192 x 4096: BF16 39.2 us (26.5 without dropout, 29.9
 // with the draws taken out: ten Philox rounds per eight elements are 9.5 us of
 // integer multiplies), FP32 71.6 us (55.6); two calls, drop_add and q_blockwise,
 // take 46.9 us for BF16.  The integer pipes bound it: with the next tile's
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_blockwise(const __grid_const
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t tiles_m = (M + kTileRowsE - 1) / kTileRowsE, tiles_k = (K + TC - 1) / TC;
 
+    if constexpr (DROP) griddep_wait();   // launched while the kernel ahead ends; nothing was read or written so far
     run_tiles(&tmap, tiles_m, tiles_k, TC, false, status, [&](uint8_t *st, int64_t tm, int64_t tk) {
         const int64_t mb = tm * kTileRowsE, kb = tk * TC;
         const int64_t k = kb + lane * VEC, m0 = mb + 8 * warp;
@@ -435,8 +436,11 @@ static cudaError_t bw_t(const void *x, int64_t M, int64_t K, uint8_t *q_row, voi
     }
     const int64_t tiles = ((M + kTileRowsE - 1) / kTileRowsE) * ((K + TC - 1) / TC);
     const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-    k_blockwise<DT, TILE, P2, Drop><<<grid, kEngThreads, kEngSmem, st>>>(map, M, K, q_row, s_row, q_colT, s_colT, status, drop);
-    return cudaGetLastError();
+    // Beside dropout: a call in a stream takes 39.3 us for 42.2 (both copies of 8192 x
+    // 4096); fewer tiles wait for the host, whom this launch costs more.
+    const bool early = !std::is_same<Drop, NoDrop>::value && tiles > sm_count();
+    return launch_k(early, k_blockwise<DT, TILE, P2, Drop>, dim3(grid), dim3(kEngThreads), kEngSmem, st, map, M, K, q_row,
+                    s_row, q_colT, s_colT, status, drop);
 }
 
 cudaError_t launch_blockwise(const void *x, int dt, int64_t M, int64_t K, int tile, uint8_t *q_row, float *s_row,

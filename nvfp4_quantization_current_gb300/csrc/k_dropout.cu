@@ -75,6 +75,7 @@ k_drop_add(const void *x, const void *residual, void *y, int64_t n, const DropAr
 {
     const int64_t b0 = (int64_t)blockIdx.x * (kDropThreads * kDropUnroll) + threadIdx.x, blocks = n / 8;
     Eight<DT> vx[kDropUnroll], vr[kDropUnroll];
+    griddep_wait();   // nothing was read or written so far
 #pragma unroll
     for (int u = 0; u < kDropUnroll; u++) {
         const int64_t b = b0 + u * kDropThreads;
@@ -106,9 +107,11 @@ template <int DT>
 cudaError_t drop_t(const void *x, int64_t n, const void *residual, const DropArgs &d, void *y, cudaStream_t st)
 {
     const int64_t per = 8 * kDropThreads * kDropUnroll, grid = (n + per - 1) / per;
-    if (residual != nullptr) k_drop_add<DT, true><<<(unsigned)grid, kDropThreads, 0, st>>>(x, residual, y, n, d);
-    else k_drop_add<DT, false><<<(unsigned)grid, kDropThreads, 0, st>>>(x, nullptr, y, n, d);
-    return cudaGetLastError();
+    // Launched while the kernel ahead ends (8192 x 4096 29.6 -> 27.5 us a call in a
+    // stream), but not where every block is resident at once: the launch costs the
+    // host more, which calls of that size wait for.
+    return launch_k(grid >= 5 * sm_count(), residual != nullptr ? k_drop_add<DT, true> : k_drop_add<DT, false>,
+                    dim3((unsigned)grid), dim3(kDropThreads), 0, st, x, residual, y, n, d);
 }
 
 }  // namespace

@@ -150,6 +150,27 @@ def test_mm_plans(M, N, K, tb, dtype, accumulate):
     check_mm(M, N, K, "1x128", tb, dtype, accumulate, seed=M)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dropout_calls_in_a_row(dtype):
+    """Calls that may overlap their neighbours' ends, each in place on the last one's result, against the same calls one at
+    a time."""
+    def chain(sync):
+        x = torch.randn((4096, 2048), generator=torch.Generator("cuda").manual_seed(5), device="cuda").to(dtype)
+        r, outs = x.clone(), []
+        for i in range(24):
+            Q.drop_add(x, 0.25, i, residual=r, out=r)
+            sync()
+            outs.append(Q.drop_q_blockwise(r, 0.25, i, colwise=True))
+            sync()
+            Q.drop_add(r, 0.5, 100 + i, out=x)
+            sync()
+        torch.cuda.synchronize()
+        return [r, x] + [t for o in outs for t in (o.q_row, o.s_row, o.q_colT, o.s_colT)]
+
+    for a, b in zip(chain(lambda: None), chain(torch.cuda.synchronize)):
+        assert torch.equal(a, b)
+
+
 # each width from its narrowest call on and each depth of split, results that end inside a tile and reductions that the
 # split does not divide
 @pytest.mark.parametrize("M,N,K,tb", [(3, 128, 768, "128x128"), (1, 198, 2816, "1x128"), (1, 128, 3456, "128x128"),
