@@ -37,7 +37,7 @@
 // GB300, both copies of 8192 x 4096: BF16 39.2 us (26.5 without dropout, 29.9
 // with the draws taken out: ten Philox rounds per eight elements are 9.5 us of
 // integer multiplies), FP32 71.6 us (55.6); two calls, drop_add and q_blockwise,
-// take 46.9 us for BF16.  The integer pipes bound it: with the next tile's
+// take 45.9 us for BF16.  The integer pipes bound it: with the next tile's
 // decisions drawn ahead, one bit each, in the body's waiting phases it took 40.9
 // to 42.1 us.
 #include "q_dropout.cuh"
@@ -437,8 +437,8 @@ static cudaError_t bw_t(const void *x, int64_t M, int64_t K, uint8_t *q_row, voi
     const int64_t tiles = ((M + kTileRowsE - 1) / kTileRowsE) * ((K + TC - 1) / TC);
     const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
     // Beside dropout: a call in a stream takes 39.3 us for 42.2 (both copies of 8192 x
-    // 4096); fewer tiles wait for the host, whom this launch costs more.
-    const bool early = !std::is_same<Drop, NoDrop>::value && tiles > sm_count();
+    // 4096), 256 x 2048 in FP32 5.2 for 5.7.
+    const bool early = !std::is_same<Drop, NoDrop>::value;
     return launch_k(early, k_blockwise<DT, TILE, P2, Drop>, dim3(grid), dim3(kEngThreads), kEngSmem, st, map, M, K, q_row,
                     s_row, q_colT, s_colT, status, drop);
 }

@@ -7,8 +7,8 @@
 // blocks, in 16-byte pieces that are all on their way before the first draw is
 // computed.  The sum is formed in FP32 (one fused multiply-add) and rounded
 // once to the output type.  Measured on a GB300: 8192 x 4096 BF16 with the
-// residual 31.2 us (201 MB at 6.4 TB/s), without it 22.5 us, with one element
-// per load 84 us; 128 x 4096 2.1 us, of which the launch is most.
+// residual 30.7 us (201 MB at 6.6 TB/s), without it 22 us, with one element per
+// load 84 us; 128 x 4096 1.6 us, of which the launch is most.
 #include <type_traits>
 
 #include "q_dropout.cuh"
@@ -107,10 +107,10 @@ template <int DT>
 cudaError_t drop_t(const void *x, int64_t n, const void *residual, const DropArgs &d, void *y, cudaStream_t st)
 {
     const int64_t per = 8 * kDropThreads * kDropUnroll, grid = (n + per - 1) / per;
-    // Launched while the kernel ahead ends (8192 x 4096 29.6 -> 27.5 us a call in a
-    // stream), but not where every block is resident at once: the launch costs the
-    // host more, which calls of that size wait for.
-    return launch_k(grid >= 5 * sm_count(), residual != nullptr ? k_drop_add<DT, true> : k_drop_add<DT, false>,
+    // Launched while the kernel ahead ends: 8192 x 4096 27.5 us a call in a stream, 29.6
+    // otherwise, 128 x 4096 in a graph 1.6 and 1.8.  (A signal of its own that the
+    // kernel behind may start filled the SMs unevenly: 3.3 M elements 7.7 us for 5.1.)
+    return launch_k(true, residual != nullptr ? k_drop_add<DT, true> : k_drop_add<DT, false>,
                     dim3((unsigned)grid), dim3(kDropThreads), 0, st, x, residual, y, n, d);
 }
 

@@ -32,8 +32,8 @@
 // added, the additions between a load of tensor memory and its wait.
 //
 // Measured on a GB300 in sustained runs, at its 1.4 kW: 16384 x 18432 x 7168
-// 1.63 to 1.65 ms (2.6 to 2.7 PFLOP/s, clocks at 1.58 of 2.07 GHz), 8192 x
-// 14336 x 4096 377 to 383 us (2.5), with 1x128 tiles of both and an FP32 C
+// 1.60 to 1.65 ms (2.6 to 2.7 PFLOP/s, clocks at 1.58 of 2.07 GHz), 8192 x
+// 14336 x 4096 370 to 383 us (2.5), with 1x128 tiles of both and an FP32 C
 // added to 14336 x 4096 x 8192 494 to 506 us (1.9 to 1.95; its FP32 multiplies
 // and adds take 512 cycles of a block, the other's 256).
 // Without the epilogue's work the loads and MMAs alone reach 3.1 PFLOP/s there.
