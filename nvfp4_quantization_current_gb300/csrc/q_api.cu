@@ -460,6 +460,11 @@ q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, doubl
         TRY(need(fn, "s_colT", s_colT, 4));
         TRY(multiple(fn, "M (with q_colT)", M, 128));
     }
+    if (q_colT == nullptr) {
+        LAUNCH(fn, qk::launch_drop_q_rows(x, (int)in, M * K, threshold, drop_scale(threshold), seed, offset, q_row, s_row, status,
+                                          S(stream)));
+        return Q_OK;
+    }
     LAUNCH(fn, qk::launch_drop_q_blockwise(x, (int)in, M, K, threshold, drop_scale(threshold), seed, offset, q_row, s_row,
                                            q_colT, s_colT, status, S(stream)));
     return Q_OK;

@@ -103,6 +103,10 @@ cudaError_t launch_drop_q_blockwise(const void *x, int dt, int64_t M, int64_t K,
                                     uint64_t offset, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
                                     int32_t *status, cudaStream_t st);
 
+// the rowwise copy alone (n = M K, K a multiple of 128)
+cudaError_t launch_drop_q_rows(const void *x, int dt, int64_t n, uint32_t threshold, float c, uint64_t seed, uint64_t offset,
+                               uint8_t *q_row, float *s_row, int32_t *status, cudaStream_t st);
+
 // y = residual + dropout(x) over n elements (residual may be null)
 cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residual, uint32_t threshold, float c,
                             uint64_t seed, uint64_t offset, void *y, cudaStream_t st);

@@ -454,6 +454,21 @@ def test_drop_q_blockwise(kind, shape, colwise, p, bf16, rowwise):
     assert status.item() == 0
 
 
+@pytest.mark.parametrize("shape", [(128, 128), (1024, 128), (128, 8064), (1152, 1152), (2944, 640)])
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.75])
+@pytest.mark.parametrize("bf16", [True, False])
+def test_drop_q_blockwise_rowwise_alone(shape, p, bf16):
+    """The rowwise copy by itself is that of both directions, inf and NaN elements and empty blocks included."""
+    x = dev(W.gen("outliers", shape, 63, bf16=bf16))
+    x[5:40, :128] = 0
+    x[41, 3], x[42, 5], x[43, 7], x[43, 8], x[44, -128:] = np.nan, np.inf, -np.inf, np.nan, 2.0 ** -133
+    st = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    both = Q.drop_q_blockwise(x, p, 77, 3, colwise=True, status=st[0])
+    alone = Q.drop_q_blockwise(x, p, 77, 3, status=st[1])
+    assert torch.equal(both.q_row, alone.q_row) and st[0].item() == st[1].item()
+    assert torch.equal(both.s_row.view(torch.int32), alone.s_row.view(torch.int32))
+
+
 def test_drop_q_blockwise_drops_nan_and_reports_what_is_kept():
     x = W.gen("normal", (128, 256), 62, bf16=False)
     keep = (draws(x.size, 3, 0) >= 32768).reshape(x.shape)
