@@ -632,6 +632,16 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     return out
 
 
+def _copies(name, c, M, K, dev):
+    """Refuses copies that are not those of an M x K tensor in 1x128 tiles: the kernel would write past them."""
+    if c.tile != Q_T1x128:
+        raise ValueError(f"{name} must hold 1x128 tiles")
+    for field, t, dtype, shape in (("q_row", c.q_row, torch.uint8, (M, K)), ("s_row", c.s_row, torch.float32, (M, K // 128)),
+                                   ("q_colT", c.q_colT, torch.uint8, (K, M)), ("s_colT", c.s_colT, torch.float32, (K, M // 128))):
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{name}.{field} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
+
+
 def _alike(name, t, x):
     if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, with x's shape, dtype and device")
@@ -662,10 +672,17 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
                      out: Optional[BlockwiseTensor] = None, status: Optional[torch.Tensor] = None) -> BlockwiseTensor:
     """The 1x128 blockwise copies of ``dropout(x)`` (FP32, the decisions of
     :func:`drop_add` with the same seed and offset) in one read of x: the
-    gradient behind a dropout, ready for the two gradient products."""
+    gradient behind a dropout, ready for the two gradient products.  ``out``
+    (1x128 copies of an x of this shape) has the directions that it holds
+    written."""
     dt = _in(x)
     M, K = x.shape
-    out = alloc_blockwise(M, K, x.device, "1x128", rowwise, colwise) if out is None else out
+    if out is None:
+        out = alloc_blockwise(M, K, x.device, "1x128", rowwise, colwise)
+    else:
+        _copies("out", out, M, K, x.device)
+        if colwise and out.q_colT is None:
+            raise ValueError("out has no transposed copy")
     _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
           _ptr(out.q_colT), _ptr(out.s_colT), _ptr(status), _stream(x.device))
     return out

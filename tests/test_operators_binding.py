@@ -1,0 +1,45 @@
+"""What the Python binding of the operators on the blockwise copies lets through to the library, on
+the CPU: tensors that say they are CUDA ones, and a library call that only notes its arguments."""
+import dataclasses
+
+import pytest
+import torch
+
+import nvfp4_quantization_current_gb300 as Q
+from test_operators_abi import fake
+
+U8, F32, BF16 = torch.uint8, torch.float32, torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The names of the library calls that were made."""
+    made = []
+    monkeypatch.setattr(Q, "_call", lambda name, *args: made.append(name))
+    monkeypatch.setattr(Q, "_stream", lambda dev: None)
+    return made
+
+
+def copies(M, K, tile=Q.Q_T1x128, rowwise=True, colwise=True, **change):
+    t = Q.alloc_blockwise(M, K, "cpu", tile, rowwise, colwise)
+    t = Q.BlockwiseTensor(*(v if v is None else fake(v.shape, v.dtype) for v in (t.q_row, t.s_row, t.q_colT, t.s_colT)), t.tile)
+    return dataclasses.replace(t, **change)
+
+
+def test_drop_q_blockwise_writes_only_to_copies_of_its_input(calls):
+    """Scales of 128x128 tiles are 128 times too few, copies of a smaller tensor end before the kernel's last write."""
+    x = fake((256, 384), BF16)
+    for out, text in ((copies(256, 384, Q.Q_T128x128), "1x128"), (copies(128, 384), "q_row"), (copies(256, 256), "q_row"),
+                      (copies(384, 256), "q_row"), (copies(256, 384, s_row=fake((256, 2), F32)), "s_row"),
+                      (copies(256, 384, q_row=fake((256, 384), F32)), "q_row"), (copies(256, 384, s_row=fake((256, 3), BF16)), "s_row"),
+                      (copies(256, 384, q_colT=fake((256, 384), U8).t()), "q_colT"), (copies(256, 384, q_colT=fake((256, 384), U8)), "q_colT"),
+                      (copies(256, 384, s_colT=fake((384, 1), F32)), "s_colT"),
+                      (copies(256, 384, s_colT=torch.empty((384, 2), device="meta")), "s_colT")):
+        with pytest.raises(ValueError, match=text):
+            Q.drop_q_blockwise(x, 0.1, 0, out=out)
+    with pytest.raises(ValueError, match="transposed"):   # asked for, and nowhere to write it
+        Q.drop_q_blockwise(x, 0.1, 0, colwise=True, out=copies(256, 384, colwise=False))
+    assert calls == []
+    for out in (copies(256, 384), copies(256, 384, colwise=False), copies(256, 384, rowwise=False)):   # its directions are written
+        assert Q.drop_q_blockwise(x, 0.1, 0, out=out) is out
+    assert calls == ["drop_q_blockwise"] * 3
