@@ -597,6 +597,8 @@ def _operand(name, q, s, tile):
     want = (R, K // 128) if tile == Q_T1x128 else (R // 128, K // 128)
     if s.shape != want:
         raise ValueError(f"{name}: scales are {tuple(s.shape)}, codes {R} x {K} need {want}")
+    if s.device != q.device:
+        raise ValueError(f"{name}: scales are on {s.device}, codes on {q.device}")
     return R, K
 
 

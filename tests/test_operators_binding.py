@@ -43,3 +43,14 @@ def test_drop_q_blockwise_writes_only_to_copies_of_its_input(calls):
     for out in (copies(256, 384), copies(256, 384, colwise=False), copies(256, 384, rowwise=False)):   # its directions are written
         assert Q.drop_q_blockwise(x, 0.1, 0, out=out) is out
     assert calls == ["drop_q_blockwise"] * 3
+
+
+def test_mm_blockwise_wants_its_operands_on_one_device(calls):
+    a, s_a, b, s_b = fake((4, 256), U8), fake((4, 2), F32), fake((128, 256), U8), fake((1, 2), F32)
+    off = lambda t: torch.empty(t.shape, dtype=t.dtype, device="meta").as_subclass(type(a))
+    for args, text in (((a, off(s_a), b, s_b), "a: scales"), ((a, s_a, b, off(s_b)), "b: scales"), ((a, s_a, off(b), off(s_b)), "a is on")):
+        with pytest.raises(ValueError, match=text):
+            Q.mm_blockwise(*args)
+    assert calls == []
+    Q.mm_blockwise(a, s_a, b, s_b)
+    assert calls == ["mm_blockwise"]
