@@ -602,6 +602,15 @@ def _operand(name, q, s, tile):
     return R, K
 
 
+def _status(status, dev):
+    """The address of a status word on dev (or none)."""
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.numel() == 0 or status.device != dev:
+        raise ValueError(f"status must be an int32 tensor of one element on {dev}")
+    return status.data_ptr()
+
+
 def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch.Tensor, tile_a="1x128",
                  tile_b="128x128", dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, accumulate=False,
                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -630,7 +639,7 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     elif out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
-          _DTYPES[out.dtype], int(accumulate), _ptr(status), _stream(dev))
+          _DTYPES[out.dtype], int(accumulate), _status(status, dev), _stream(dev))
     return out
 
 
@@ -686,7 +695,7 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
         if colwise and out.q_colT is None:
             raise ValueError("out has no transposed copy")
     _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
-          _ptr(out.q_colT), _ptr(out.s_colT), _ptr(status), _stream(x.device))
+          _ptr(out.q_colT), _ptr(out.s_colT), _status(status, x.device), _stream(x.device))
     return out
 
 

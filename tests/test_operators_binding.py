@@ -54,3 +54,17 @@ def test_mm_blockwise_wants_its_operands_on_one_device(calls):
     assert calls == []
     Q.mm_blockwise(a, s_a, b, s_b)
     assert calls == ["mm_blockwise"]
+
+
+def test_status_is_an_int32_on_the_device(calls):
+    """The kernels OR into it: a word of another type or place would be overwritten."""
+    a, s_a, b, s_b, x = fake((4, 256), U8), fake((4, 2), F32), fake((128, 256), U8), fake((1, 2), F32), fake((128, 128), BF16)
+    for call in (lambda status: Q.mm_blockwise(a, s_a, b, s_b, status=status), lambda status: Q.drop_q_blockwise(x, 0.1, 0, status=status)):
+        for status in (fake((1,), U8), fake((1,), torch.int64), fake((0,), torch.int32), torch.zeros(1, dtype=torch.int32, device="meta")):
+            with pytest.raises(ValueError, match="status"):
+                call(status)
+        assert calls == []
+        call(fake((1,), torch.int32))
+        call(None)
+        assert len(calls) == 2
+        calls.clear()
