@@ -405,11 +405,23 @@ q_status dq_nvfp4(const uint8_t *q, const uint8_t *sb, const float *s_global, in
  * Shapes: K % 128 == 0, M % 128 == 0 (N % 128 == 0) for a 128x128 operand;
  * M, N, K < 2^31.  M == 0 or N == 0 does nothing; K == 0 is a sum over
  * nothing: c is set to zero, or left as it is when accumulating.
+ * A wait inside the kernel that runs out (2 s) ends the call: Q_ST_TIMEOUT in
+ * *status, and the part of C that the wait's sums would have gone to is not
+ * written.
  * Alignment: a, b, c 16 bytes, s_a, s_b 4 bytes.
  */
 q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const uint8_t *b, const float *s_b, q_tile tile_b,
                       int64_t M, int64_t N, int64_t K, void *c, q_dtype out, int accumulate, int32_t *status,
                       q_stream_t stream);
+
+/*
+ * Diagnostic of that failure path (a library check): in the calling thread's
+ * next mm_blockwise that launches a kernel, the first CTA of every cluster
+ * takes one of its waits for run out.  *status gets Q_ST_TIMEOUT and C is left
+ * as it is.  For calls of few tokens or few tiles; one that is large enough
+ * for the kernel of many tiles returns Q_ERR_CUDA.  on = 0 clears it.
+ */
+q_status selftest_mm_give_up(int on);
 
 /*
  * Dropout with the residual sum, its mask drawn from a counter and never

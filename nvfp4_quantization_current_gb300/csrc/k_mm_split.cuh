@@ -56,6 +56,20 @@ QD float4 ld_cluster4(uint32_t addr)
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
+QD int ld_cluster1(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+// Whether a CTA of the cluster gave up.
+QD bool cluster_gave_up(const int *abort_flag, int split)
+{
+#pragma unroll 1
+    for (int r = 0; r < split; r++)
+        if (ld_cluster1(cluster_addr(smem_u32(abort_flag), r)) != 0) return true;
+    return false;
+}
 // TILES: the weights have 128x128 tiles, so that a block's row scale is one
 // number and goes into the column scales.
 template <int OUT, int BN, bool TILES>
@@ -84,7 +98,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             mbar_init(&sm.acc_empty[b], kEpiWarps);
         }
         mbar_init(&sm.drained, 1);
-        sm.abort_flag = 0;
+        sm.abort_flag = g.give_up && rank == 0;
         fence_mbar_init();
     }
     if (warp == kEpiWarps && elect_one()) {
@@ -211,7 +225,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             }
         }
         // Every MMA is done, so the stages are free.  (After an abort they may
-        // not be, but neither is the result then: nothing is written.)
+        // not be: then there are no sums, and the cluster writes nothing.)
         if (!__any_sync(0xFFFFFFFFu, *stop)) {
             float *sums = reinterpret_cast<float *>(dsm);
 #pragma unroll
@@ -224,8 +238,17 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     if (warp == kEpiWarps + 1) tmem_free<Smem::kCols>(tmem);
+    // A CTA that gave up has operands where the others look for its sums.  It leaves
+    // NaNs there, and who meets one looks at the flags (looking at every call took 0.2 us of it).
+    const bool gave_up = sm.abort_flag != 0;
+    if (gave_up) {
+        if (g.give_up && threadIdx.x == 0 && g.status != nullptr) atomicOr(g.status, kStTimeout);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < BN * 128; i += Smem::kThreads) reinterpret_cast<uint32_t *>(dsm)[i] = 0x7FFFFFFFu;
+        __syncwarp();
+    }
     if (split > 1) cluster_sync();   // the cluster's sums are there
-    if (warp < kEpiWarps && sm.abort_flag == 0) {
+    if (warp < kEpiWarps && !gave_up) {
         // a warp takes two columns at a time, four rows per lane
         using T = typename OutT<OUT>::T;
         const int64_t row = (int64_t)p0 + 4 * lane;
@@ -253,6 +276,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                         v.z += part[u][r].z;
                         v.w += part[u][r].w;
                     }
+                if (v.x != v.x && split > 1 && cluster_gave_up(&sm.abort_flag, split)) continue;
                 T *c = static_cast<T *>(g.c) + col * g.ldc + row;
                 if (vec) {
                     if constexpr (OUT == F32) *reinterpret_cast<float4 *>(c) = v;

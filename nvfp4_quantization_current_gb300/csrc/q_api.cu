@@ -75,6 +75,9 @@ q_status check_out(const char *fn, q_dtype out)
 // enqueued (the error path of every entry point, exercised without a GPU).
 thread_local int g_inject_launch_failures = 0;
 
+// Whether a wait of this thread's next product gives up (selftest_mm_give_up).
+thread_local bool g_inject_mm_give_up = false;
+
 #define LAUNCH(where, expr)                                                \
     do {                                                                   \
         if (g_inject_launch_failures > 0) {                                \
@@ -419,8 +422,10 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
     TRY(need(fn, "s_a", s_a, 4));
     TRY(need(fn, "b", b, 16));
     TRY(need(fn, "s_b", s_b, 4));
+    const bool give_up = g_inject_mm_give_up;
+    g_inject_mm_give_up = false;
     LAUNCH(fn, qk::launch_mm_blockwise(a, s_a, (int)tile_a, b, s_b, (int)tile_b, M, N, K, c, (int)out, accumulate != 0, status,
-                                       S(stream)));
+                                       give_up, S(stream)));
     return Q_OK;
 }
 
@@ -474,6 +479,12 @@ q_status q_selftest_inject_launch_error(int n)
 {
     if (n < 0) return fail(Q_ERR_ARG, "q_selftest_inject_launch_error: n = %d is negative", n);
     g_inject_launch_failures = n;
+    return Q_OK;
+}
+
+q_status selftest_mm_give_up(int on)
+{
+    g_inject_mm_give_up = on != 0;
     return Q_OK;
 }
 

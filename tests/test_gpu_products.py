@@ -1,0 +1,63 @@
+"""mm_blockwise where it can go wrong beside its sums: waits that run out, and the kernel of many
+tiles in all its forms.  Operands, references and tolerances are those of test_gpu_operators."""
+import pytest
+import torch
+
+import nvfp4_quantization_current_gb300 as Q
+from test_gpu_operators import mm_bound, mm_reference, operand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    Q.lib()
+
+
+def check(a, sa, ta, b, sb, tb, got, c=None):
+    ref, tol = mm_bound(*mm_reference(a, sa, ta, b, sb, tb), a.shape[1] // 128, got.dtype, c)
+    assert bool(((got.double() - ref).abs() <= tol).all())
+
+
+# every width, and splits of 1 to 8
+@pytest.mark.parametrize("M,N,K,tb", [(1, 14336, 512, "128x128"), (1, 128, 512, "128x128"), (1, 128, 1024, "128x128"),
+                                      (1, 128, 2048, "128x128"), (20, 4096, 1024, "128x128"), (20, 2048, 2048, "128x128"),
+                                      (40, 14336, 2048, "128x128"), (40, 7168, 4096, "128x128"), (190, 1024, 8192, "128x128"),
+                                      (300, 4096, 1024, "1x128"), (640, 512, 4096, "128x128"), (300, 512, 8192, "128x128"),
+                                      (300, 4096, 2048, "1x128"), (640, 1024, 2048, "1x128")])
+@pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, True), (torch.bfloat16, True)])
+def test_a_wait_that_runs_out_leaves_c_as_it_is(M, N, K, tb, dtype, accumulate):
+    """One CTA of each cluster gives up: the others' sums have no use, and what lies in its shared memory is no sum."""
+    a, sa = operand(M, K, "1x128", 1)
+    b, sb = operand(N, K, tb, 2)
+    c = torch.randn((M, N), device="cuda").to(dtype)
+    out, status = c.clone(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert Q.lib().selftest_mm_give_up(1) == Q.Q_OK
+    try:
+        Q.mm_blockwise(a, sa, b, sb, tile_b=tb, out=out, accumulate=accumulate, status=status)
+    finally:
+        Q.lib().selftest_mm_give_up(0)
+    assert status.item() == Q.Q_ST_TIMEOUT
+    assert torch.equal(out, c)
+    status.zero_()
+    Q.mm_blockwise(a, sa, b, sb, tile_b=tb, out=out, accumulate=accumulate, status=status)   # the next call is whole
+    assert status.item() == 0
+    check(a, sa, "1x128", b, sb, tb, out, c if accumulate else None)
+
+
+@pytest.mark.parametrize("bits", [0xFFD5A5A5 - (1 << 32), 0x7FFFFFFF, 0x7F800001])
+@pytest.mark.parametrize("K", [512, 2048])
+def test_nan_scales_of_any_payload_reach_c(K, bits):
+    """A NaN that is computed with is a result like another, whatever bits it came from."""
+    a, sa = operand(5, K, "1x128", 1)
+    b, sb = operand(256, K, "128x128", 2)
+    clean = Q.mm_blockwise(a, sa, b, sb, dtype=torch.float32)
+    sa.view(torch.int32)[2] = bits
+    got = Q.mm_blockwise(a, sa, b, sb, dtype=torch.float32)
+    rest = [0, 1, 3, 4]
+    assert bool(got[2].isnan().all()) and torch.equal(got[rest], clean[rest])
+    sb.view(torch.int32)[1] = bits
+    got = Q.mm_blockwise(a, sa, b, sb, dtype=torch.float32)
+    assert bool(got[:, 128:].isnan().all()) and torch.equal(got[rest][:, :128], clean[rest][:, :128])

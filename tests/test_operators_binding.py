@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import nvfp4_quantization_current_gb300 as Q
-from test_operators_abi import fake
+from test_operators_abi import L, fake, mm_args, status_of  # noqa: F401 (L is a fixture)
 
 U8, F32, BF16 = torch.uint8, torch.float32, torch.bfloat16
 
@@ -68,3 +68,16 @@ def test_status_is_an_int32_on_the_device(calls):
         call(None)
         assert len(calls) == 2
         calls.clear()
+
+
+def test_give_up_is_for_one_call_and_clears(L):
+    """The diagnostic is taken by the next call that launches, and not by one that is refused or empty."""
+    try:
+        assert L.selftest_mm_give_up(1) == Q.Q_OK
+        assert status_of(L, "mm_blockwise", *mm_args(M=0, a=None, s_a=None, c=None))[0] == Q.Q_OK
+        assert status_of(L, "mm_blockwise", *mm_args(K=192))[0] == Q.Q_ERR_SHAPE
+        assert L.q_selftest_inject_launch_error(1) == Q.Q_OK   # taken here, where nothing is launched after all
+        assert status_of(L, "mm_blockwise", *mm_args())[0] == Q.Q_ERR_CUDA
+    finally:
+        L.q_selftest_inject_launch_error(0)
+        L.selftest_mm_give_up(0)
