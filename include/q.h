@@ -416,10 +416,8 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
 
 /*
  * Diagnostic of that failure path (a library check): in the calling thread's
- * next mm_blockwise that launches a kernel, the first CTA of every cluster
- * takes one of its waits for run out.  *status gets Q_ST_TIMEOUT and C is left
- * as it is.  For calls of few tokens or few tiles; one that is large enough
- * for the kernel of many tiles returns Q_ERR_CUDA.  on = 0 clears it.
+ * next mm_blockwise that launches a kernel, every cluster takes a wait for run
+ * out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it.
  */
 q_status selftest_mm_give_up(int on);
 

@@ -84,7 +84,6 @@ template <int OUT, bool COLS> cudaError_t pair_registers_ready()
 template <int OUT, bool COLS>
 cudaError_t mm_pair(const uint8_t *p, const uint8_t *q, MmArgs g, cudaStream_t st)
 {
-    if (g.give_up) return cudaErrorNotSupported;
     alignas(64) CUtensorMap map_p, map_q, map_c = {};
     const int64_t K = g.kblocks * kMmBlock;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K, 128);

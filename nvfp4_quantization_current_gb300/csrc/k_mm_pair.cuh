@@ -38,13 +38,13 @@
 // and adds take 512 cycles of a block, the other's 256).
 // Without the epilogue's work the loads and MMAs alone reach 3.1 PFLOP/s there.
 //
-// A named barrier cannot time out, and need not: these warps wait there only
-// for blocks whose MMAs are issued (the leader's) or that the epilogue is going
-// to read, after a look at the abort flag, and the epilogue warps arrive for
-// every block of a tile, whether their own waits were served or given up (which
-// takes a thousand tries each, so that they never overtake a warp between its
-// look and its barrier), and at both buffers once more when they leave on the
-// flag.
+// A named barrier cannot time out, and need not.  The epilogue warps arrive for
+// every block of a tile, whether their own waits were served or given up, so
+// without an abort each wait meets its nine arrivals.  After one the arrivals no
+// longer go by blocks (a warp whose waits are given up runs ahead of the others,
+// and may complete a barrier in their stead): the epilogue warps, which never
+// wait there, then go on arriving until both MMA warps have left.  Sums read
+// from a buffer that was released too early are not stored, as the flag is up.
 #pragma once
 
 #include "q_internal.h"
@@ -88,7 +88,7 @@ struct PairSmem {
     uint64_t full[kPairStages], empty[kPairStages], acc_full[2], peer_free[2], drained[2];
     uint64_t sc_full[kPairScaleSlots], sc_empty[kPairScaleSlots];
     uint32_t tmem_base;
-    int abort_flag;
+    int abort_flag, left[2];   // left: the buffer's MMA warp waits no more
 };
 static_assert(sizeof(PairSmem) <= 232448, "shared memory of a CTA");
 
@@ -195,7 +195,8 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             mbar_init(&sm.sc_full[s], 32);
             mbar_init(&sm.sc_empty[s], 1);
         }
-        sm.abort_flag = 0;
+        sm.abort_flag = g.give_up;
+        sm.left[0] = sm.left[1] = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc_pair<512>(&sm.tmem_base);
@@ -309,6 +310,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 mma_commit_pair(&sm.drained[buf]);
                 (void)mbar_wait_bounded(&sm.drained[buf], 0);
             }
+            if (lane == 0) *static_cast<volatile int *>(&sm.left[buf]) = 1;
         } else if (warp == 3) {
             put_scales<COLS>(sm, g, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
         }
@@ -394,9 +396,12 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 mm_store_tile<OUT, !COLS>(g, &map_c, sm.staging[warp - 4], acc, tp * 256 + 128 * (int)rank + quad * 32,
                                           tq * kPairN + half * 128, lane);
         }
-        if (__any_sync(0xFFFFFFFFu, *stop)) {   // the MMA warps may be up to two blocks ahead
-            acc_release(0);
-            acc_release(1);
+        if (__any_sync(0xFFFFFFFFu, *stop)) {   // nobody keeps an MMA warp waiting
+            volatile int *const left = sm.left;
+            while (__any_sync(0xFFFFFFFFu, left[0] == 0 || left[1] == 0)) {
+                acc_release(0);
+                acc_release(1);
+            }
         }
         if (lane == 0) bulk_wait_all();
     }
@@ -406,6 +411,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     cluster_sync();   // nothing of the peer's arrives here any more
     tc_fence_after();
     if (warp == 1) tmem_free_pair<512>(tmem);
+    if (g.give_up && threadIdx.x == 0 && g.status != nullptr) atomicOr(g.status, kStTimeout);
 }
 
 }  // namespace qk

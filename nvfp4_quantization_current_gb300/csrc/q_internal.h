@@ -112,8 +112,8 @@ cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residu
                             uint64_t seed, uint64_t offset, void *y, cudaStream_t st);
 
 // block-scaled FP8 product: c [M, N] (+)= a [M, K] b [N, K]^T with the tiles'
-// scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0; give_up: a wait of the
-// first CTA of every cluster counts as run out (not supported by the pair kernel)
+// scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0; give_up: a wait of
+// every cluster counts as run out
 cudaError_t launch_mm_blockwise(const uint8_t *a, const float *s_a, int tile_a, const uint8_t *b, const float *s_b, int tile_b,
                                 int64_t M, int64_t N, int64_t K, void *c, int out, bool accumulate, int32_t *status,
                                 bool give_up, cudaStream_t st);

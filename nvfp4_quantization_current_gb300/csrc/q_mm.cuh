@@ -21,7 +21,7 @@ struct MmArgs {
     int32_t *status;
     bool accumulate;
     int store;
-    bool give_up;               // the split kernel's first CTA of every cluster takes a wait for run out (a test)
+    bool give_up;               // every cluster takes a wait for run out: the split kernel's first CTA, both of a pair (a test)
 };
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the

@@ -21,12 +21,13 @@ def check(a, sa, ta, b, sb, tb, got, c=None):
     assert bool(((got.double() - ref).abs() <= tol).all())
 
 
-# every width, and splits of 1 to 8
+# every width, splits of 1 to 8, and the kernel of many tiles with one and with several tiles for a CTA
 @pytest.mark.parametrize("M,N,K,tb", [(1, 14336, 512, "128x128"), (1, 128, 512, "128x128"), (1, 128, 1024, "128x128"),
                                       (1, 128, 2048, "128x128"), (20, 4096, 1024, "128x128"), (20, 2048, 2048, "128x128"),
                                       (40, 14336, 2048, "128x128"), (40, 7168, 4096, "128x128"), (190, 1024, 8192, "128x128"),
                                       (300, 4096, 1024, "1x128"), (640, 512, 4096, "128x128"), (300, 512, 8192, "128x128"),
-                                      (300, 4096, 2048, "1x128"), (640, 1024, 2048, "1x128")])
+                                      (300, 4096, 2048, "1x128"), (640, 1024, 2048, "1x128"),
+                                      (2600, 2048, 1024, "128x128"), (4999, 4991, 384, "1x128")])
 @pytest.mark.parametrize("dtype,accumulate", [(torch.bfloat16, False), (torch.float32, True), (torch.bfloat16, True)])
 def test_a_wait_that_runs_out_leaves_c_as_it_is(M, N, K, tb, dtype, accumulate):
     """One CTA of each cluster gives up: the others' sums have no use, and what lies in its shared memory is no sum."""
