@@ -262,25 +262,24 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 group_r += groups;
             }
             uint32_t par = 0, freed = 0;
-            bool aborted = false;
             for (uint32_t n = buf; n < blocks + 2; n += 2) {
                 if (rank == 0) {
                     if (n >= blocks) break;
                     // a wait that gives up raises the flag, here or in the epilogue
                     mm_wait(&sm.full[s], par, stop, g.status);
                 }
-                aborted = __any_sync(0xFFFFFFFFu, *stop);
-                if (aborted) break;
+                if (__any_sync(0xFFFFFFFFu, *stop)) break;
+                bool freed_too = true;   // by the other CTA; else its warps may still be reading the buffer
                 if (n >= 2) {   // block n - 2 has been read, in both CTAs
                     acc_await(buf);
                     if (rank == 0) {
-                        mm_wait(&sm.peer_free[buf], freed, stop, g.status);
+                        freed_too = mm_wait(&sm.peer_free[buf], freed, stop, g.status);
                         freed ^= 1;
                     }
                 }
                 tc_fence_after();
                 if (elect_one()) {
-                    if (rank == 0) {
+                    if (rank == 0 && freed_too) {
                         const uint64_t at = (uint64_t)(s * (kPairStageBytes >> 4));
 #pragma unroll
                         for (int k = 0; k < kMmBlock / 32; k++)
@@ -306,7 +305,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                     par ^= 1;
                 }
             }
-            if (aborted && rank == 0 && elect_one()) {   // MMAs in flight end before their memory goes away
+            if (__any_sync(0xFFFFFFFFu, *stop) && rank == 0 && elect_one()) {   // MMAs in flight end before their memory goes away
                 mma_commit_pair(&sm.drained[buf]);
                 (void)mbar_wait_bounded(&sm.drained[buf], 0);
             }
