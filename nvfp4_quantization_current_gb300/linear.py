@@ -22,14 +22,14 @@ import torch
 from . import BlockwiseTensor, drop_add, drop_q_blockwise, mm_blockwise, q_blockwise
 
 
-def _cast_rows(x, rowwise, colwise):
+def _cast_rows(x, rowwise, colwise, status):
     """1x128 copies of x [M, K].  The transposed copy needs M % 128 == 0: a
     ragged x is cast with zero rows below it, which add nothing to the weight
     gradient; the rowwise copy is cut back to M rows."""
     M = x.shape[0]
     if not colwise or M % 128 == 0:
-        return q_blockwise(x, "1x128", rowwise, colwise)
-    t = q_blockwise(torch.nn.functional.pad(x, (0, 0, 0, -M % 128)), "1x128", rowwise, True)
+        return q_blockwise(x, "1x128", rowwise, colwise, status=status)
+    t = q_blockwise(torch.nn.functional.pad(x, (0, 0, 0, -M % 128)), "1x128", rowwise, True, status=status)
     if rowwise:
         t.q_row, t.s_row = t.q_row[:M], t.s_row[:M]
     return t
@@ -37,24 +37,24 @@ def _cast_rows(x, rowwise, colwise):
 
 class _BlockwiseLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, residual, w, p, seed, offset, main_grad, train):
+    def forward(ctx, x, weight, residual, w, p, seed, offset, main_grad, train, status):
         need_x, need_w = (train and n for n in ctx.needs_input_grad[:2])
         if need_x and w.q_colT is None:
             raise ValueError("copies lacks the transposed copy, which the input gradient reads")
         x2 = x.reshape(-1, x.shape[-1])
-        xq = _cast_rows(x2, True, need_w)
-        y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype)
+        xq = _cast_rows(x2, True, need_w, status)
+        y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype, status=status)
         if p > 0 or residual is not None:
             drop_add(y, p, seed, offset, None if residual is None else residual.reshape(y.shape), out=y)
         ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
                               *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
-        ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, residual is not None)
+        ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, residual is not None, status)
         return y.view(*x.shape[:-1], -1)
 
     @staticmethod
     def backward(ctx, dy):
         w_q, w_s, x_q, x_s = ctx.saved_tensors
-        p, seed, offset, main_grad, w_dtype, x_shape, has_residual = ctx.args
+        p, seed, offset, main_grad, w_dtype, x_shape, has_residual, status = ctx.args
         need_x, need_w = ctx.needs_input_grad[:2]
         dx = dw = None
         if need_x or need_w:
@@ -62,13 +62,13 @@ class _BlockwiseLinear(torch.autograd.Function):
             M = d.shape[0]
             if need_w and M % 128 != 0:   # zero rows below, as in the forward pass; the draws are by flat index
                 d = torch.nn.functional.pad(d, (0, 0, 0, -M % 128))
-            g = drop_q_blockwise(d, p, seed, offset, need_x, need_w)
+            g = drop_q_blockwise(d, p, seed, offset, need_x, need_w, status=status)
             if need_x:
-                dx = mm_blockwise(g.q_row[:M], g.s_row[:M], w_q, w_s, dtype=dy.dtype).view(x_shape)
+                dx = mm_blockwise(g.q_row[:M], g.s_row[:M], w_q, w_s, dtype=dy.dtype, status=status).view(x_shape)
             if need_w:
                 dw = mm_blockwise(g.q_colT, g.s_colT, x_q, x_s, tile_b="1x128", dtype=w_dtype, out=main_grad,
-                                  accumulate=main_grad is not None)
-        return dx, None if main_grad is not None else dw, dy if has_residual else None, None, None, None, None, None, None
+                                  accumulate=main_grad is not None, status=status)
+        return (dx, None if main_grad is not None else dw, dy if has_residual else None) + (None,) * 7
 
 
 class BlockwiseLinear(torch.nn.Module):
@@ -81,7 +81,13 @@ class BlockwiseLinear(torch.nn.Module):
     rows * out_features // 8``).  With ``main_grad`` set (FP32, the weight's
     shape) the weight gradient is added to it and ``weight.grad`` stays unset.
     ``copies`` takes the result of :meth:`quantize_weight`, made once for the
-    micro-batches of a step, or once for serving."""
+    micro-batches of a step, or once for serving.
+
+    ``status`` (a one-element int32 tensor on the layer's device) collects what
+    the layer's casts and products report: ``Q_ST_NONFINITE`` where x, the
+    weight or a gradient was not finite, ``Q_ST_TIMEOUT`` where a kernel gave up
+    waiting and a result is not whole.  Look at it where the host waits anyway
+    (before the optimizer's step, say) and zero it."""
 
     def __init__(self, in_features: int, out_features: int, p: float = 0.0, seed: int = 0, device="cuda",
                  dtype=torch.bfloat16):
@@ -92,14 +98,21 @@ class BlockwiseLinear(torch.nn.Module):
         torch.nn.init.normal_(self.weight, std=0.02)
         self.p, self.seed = float(p), int(seed)
         self.main_grad: Optional[torch.Tensor] = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _status_on(self, device):
+        if self.status.device != device:   # the layer was moved
+            self.status = torch.zeros_like(self.status, device=device) if self.status.is_meta else self.status.to(device)
+        return self.status
 
     def quantize_weight(self, colwise=True) -> BlockwiseTensor:
         """The weight's 128x128 copies (``colwise``: also the transposed one, for the input gradient)."""
-        return q_blockwise(self.weight.detach(), "128x128", rowwise=True, colwise=colwise)
+        return q_blockwise(self.weight.detach(), "128x128", rowwise=True, colwise=colwise,
+                           status=self._status_on(self.weight.device))
 
     def forward(self, x, residual=None, offset: int = 0, copies: Optional[BlockwiseTensor] = None):
         train = torch.is_grad_enabled()
         if copies is None:
             copies = self.quantize_weight(colwise=train and x.requires_grad)
         return _BlockwiseLinear.apply(x, self.weight, residual, copies, self.p if self.training else 0.0, self.seed,
-                                      int(offset), self.main_grad, train)
+                                      int(offset), self.main_grad, train, self._status_on(x.device))

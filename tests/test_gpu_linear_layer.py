@@ -1,0 +1,37 @@
+"""The linear layer and dropout as a model uses them: reports, gradients, masks, strides and shapes."""
+import pytest
+import torch
+
+import nvfp4_quantization_current_gb300 as Q
+from nvfp4_quantization_current_gb300.linear import BlockwiseLinear
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    Q.lib()
+
+
+def test_layer_status_reports_casts_and_products():
+    layer = BlockwiseLinear(256, 128)
+    x = torch.randn(200, 256, device="cuda", dtype=torch.bfloat16)
+    layer(x)
+    assert layer.status.item() == 0
+    y = layer(x)
+    y.backward(torch.full_like(y, torch.inf))
+    assert layer.status.item() == Q.Q_ST_NONFINITE
+    layer.status.zero_()
+    x[3, 5] = torch.nan
+    layer(x)
+    assert layer.status.item() == Q.Q_ST_NONFINITE
+    layer.status.zero_()
+    x[3, 5] = 0
+    try:
+        assert Q.lib().selftest_mm_give_up(1) == Q.Q_OK
+        layer(x)
+    finally:
+        Q.lib().selftest_mm_give_up(0)
+    assert layer.status.item() == Q.Q_ST_TIMEOUT

@@ -1,0 +1,88 @@
+"""The linear layer's own logic on the CPU: its four operators are replaced by plain ones on the
+oracle's copies, which refuse what the library's refuse."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_quantization_current_gb300 as Q
+import nvfp4_quantization_current_gb300.linear as linear
+import oracle as O
+from test_gpu_operators import draws
+
+TILE = {"1x128": O.T1x128, "128x128": O.T128x128}
+
+
+def contiguous(t):
+    if not t.is_contiguous() or t.data_ptr() % 16:
+        raise ValueError("input must be contiguous and aligned")
+    return t
+
+
+def tensors(t, tile):
+    f = lambda v: None if v is None else torch.from_numpy(v)
+    return Q.BlockwiseTensor(f(t.q_row), f(t.s_row), f(t.q_colT), f(t.s_colT), tile)
+
+
+def decoded(q, s, tile):
+    return torch.from_numpy(O.dq_blockwise(q.numpy(), s.numpy(), TILE[tile])).double() if q.numel() else q.double()
+
+
+class Plain:
+    """The operators on CPU tensors; `status` collects what each call was given for it."""
+
+    def __init__(self):
+        self.status, self.offsets, self.version = [], [], {}
+
+    def q_blockwise(self, x, tile="1x128", rowwise=True, colwise=False, out=None, status=None):
+        self.status.append(status)
+        return tensors(O.blockwise(contiguous(x).numpy(), TILE[tile], rowwise, colwise), TILE[tile])
+
+    def mm_blockwise(self, a, s_a, b, s_b, tile_a="1x128", tile_b="128x128", dtype=torch.bfloat16, out=None, accumulate=False,
+                     status=None):
+        self.status.append(status)
+        y = decoded(a, s_a, tile_a) @ decoded(b, s_b, tile_b).T
+        if out is None:
+            return y.to(dtype)
+        return out.copy_(y + out.double() if accumulate else y)
+
+    def kept(self, x, p, seed, offset):
+        self.offsets.append((seed, offset))
+        T = int(np.rint(p * 65536))
+        keep = torch.from_numpy(draws(x.numel(), seed, offset) >= T).view(x.shape)
+        return torch.where(keep, x * (65536 / (65536 - T) if T < 65536 else 0.0), 0.0)
+
+    def drop_add(self, x, p, seed, offset=0, residual=None, out=None):
+        y = self.kept(contiguous(x), p, seed, offset)
+        if residual is not None:
+            if residual.shape != x.shape or residual.dtype != x.dtype:
+                raise ValueError("residual must have x's shape and dtype")
+            y = y + contiguous(residual)
+        return y if out is None else out.copy_(y)
+
+    def drop_q_blockwise(self, x, p, seed, offset=0, rowwise=True, colwise=False, out=None, status=None):
+        self.status.append(status)
+        y = self.kept(contiguous(x), p, seed, offset)
+        return tensors(O.blockwise(y.numpy(), O.T1x128, rowwise, colwise), O.T1x128)
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    ops = Plain()
+    for name in ("q_blockwise", "mm_blockwise", "drop_add", "drop_q_blockwise"):
+        monkeypatch.setattr(linear, name, getattr(ops, name))
+    return ops
+
+
+def layer_of(p=0.0, **kw):
+    torch.manual_seed(1)
+    return linear.BlockwiseLinear(256, 128, p=p, device="cpu", dtype=torch.float32, **kw)
+
+
+def test_every_cast_and_product_gets_the_layers_status(plain):
+    """A wait that ran out, or a non-finite input, is found in the layer's status word, forward and backward."""
+    layer = layer_of(p=0.5, seed=3)
+    x = torch.randn(256, 256, requires_grad=True)
+    layer(x, offset=0).sum().backward()
+    assert len(plain.status) == 6   # two casts and a product, a cast and two products
+    assert layer.status.dtype == torch.int32 and layer.status.tolist() == [0]
+    assert all(s is layer.status for s in plain.status)
