@@ -35,6 +35,18 @@ def _cast_rows(x, rowwise, colwise, status):
     return t
 
 
+class _Once(torch.autograd.Function):
+    """A gradient as it is.  Its own derivative, which the FP8 casts do not have, raises: a graph of the
+    backward pass that ended here would lose that part without a word (`start` begins one where dy has none)."""
+    @staticmethod
+    def forward(ctx, g, dy, start):
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("BlockwiseLinear has no second derivative")
+
+
 class _BlockwiseLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, w, p, seed, offset, main_grad, train, status):
@@ -53,22 +65,31 @@ class _BlockwiseLinear(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        with torch.no_grad():
+            dx, dw = _BlockwiseLinear.gradients(ctx, dy)
+        if torch.is_grad_enabled():   # create_graph
+            dx, dw = (None if g is None else _Once.apply(g, dy, torch.zeros((), requires_grad=True)) for g in (dx, dw))
+        return (dx, dw, dy if ctx.args[6] else None) + (None,) * 7
+
+    @staticmethod
+    def gradients(ctx, dy):
         w_q, w_s, x_q, x_s = ctx.saved_tensors
-        p, seed, offset, main_grad, w_dtype, x_shape, has_residual, status = ctx.args
+        p, seed, offset, main_grad, w_dtype, x_shape, _, status = ctx.args
         need_x, need_w = ctx.needs_input_grad[:2]
+        if not (need_x or need_w):
+            return None, None
         dx = dw = None
-        if need_x or need_w:
-            d = dy.reshape(-1, dy.shape[-1]).contiguous()
-            M = d.shape[0]
-            if need_w and M % 128 != 0:   # zero rows below, as in the forward pass; the draws are by flat index
-                d = torch.nn.functional.pad(d, (0, 0, 0, -M % 128))
-            g = drop_q_blockwise(d, p, seed, offset, need_x, need_w, status=status)
-            if need_x:
-                dx = mm_blockwise(g.q_row[:M], g.s_row[:M], w_q, w_s, dtype=dy.dtype, status=status).view(x_shape)
-            if need_w:
-                dw = mm_blockwise(g.q_colT, g.s_colT, x_q, x_s, tile_b="1x128", dtype=w_dtype, out=main_grad,
-                                  accumulate=main_grad is not None, status=status)
-        return (dx, None if main_grad is not None else dw, dy if has_residual else None) + (None,) * 7
+        d = dy.reshape(-1, dy.shape[-1]).contiguous()
+        M = d.shape[0]
+        if need_w and M % 128 != 0:   # zero rows below, as in the forward pass; the draws are by flat index
+            d = torch.nn.functional.pad(d, (0, 0, 0, -M % 128))
+        g = drop_q_blockwise(d, p, seed, offset, need_x, need_w, status=status)
+        if need_x:
+            dx = mm_blockwise(g.q_row[:M], g.s_row[:M], w_q, w_s, dtype=dy.dtype, status=status).view(x_shape)
+        if need_w:
+            dw = mm_blockwise(g.q_colT, g.s_colT, x_q, x_s, tile_b="1x128", dtype=w_dtype, out=main_grad,
+                              accumulate=main_grad is not None, status=status)
+        return dx, None if main_grad is not None else dw
 
 
 class BlockwiseLinear(torch.nn.Module):
@@ -78,7 +99,8 @@ class BlockwiseLinear(torch.nn.Module):
     float32 with any number of rows.  Dropout runs in training mode; its
     decisions follow from the layer's ``seed`` and the ``offset`` of the call
     (in counters of 8 elements; give each step its own, e.g. ``step *
-    rows * out_features // 8``).  With ``main_grad`` set (FP32, the weight's
+    rows * out_features // 8``).  There is no second derivative: one that is
+    asked for raises.  With ``main_grad`` set (FP32, the weight's
     shape) the weight gradient is added to it and ``weight.grad`` stays unset.
     ``copies`` takes the result of :meth:`quantize_weight`, made once for the
     micro-batches of a step, or once for serving.

@@ -86,3 +86,25 @@ def test_every_cast_and_product_gets_the_layers_status(plain):
     assert len(plain.status) == 6   # two casts and a product, a cast and two products
     assert layer.status.dtype == torch.int32 and layer.status.tolist() == [0]
     assert all(s is layer.status for s in plain.status)
+
+
+@pytest.mark.parametrize("of_y", [lambda y: y.square().sum(), lambda y: y.sum()])
+def test_a_second_derivative_is_refused_and_not_lost(plain, of_y):
+    """The backward pass has no derivative: a gradient penalty must not train without its part, whether its
+    gradient is one of the incoming gradient or of the weight alone (y's sum: dx is the weight's column sums)."""
+    layer = layer_of()
+    x = torch.randn(128, 256, requires_grad=True)
+    r = torch.randn(128, 128, requires_grad=True)
+    y = layer(x, r)
+    dx, dw = torch.autograd.grad(of_y(y), (x, layer.weight), create_graph=True)
+    for g in (dx, dw):
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            (y.sum() + g.square().sum()).backward(retain_graph=True)
+    dr = torch.autograd.grad(of_y(layer(x, r)), r, create_graph=True)[0]
+    if dr.requires_grad:   # y squared: the residual's gradient is 2 y, whose own derivative the layer has
+        first = torch.autograd.grad(dr.sum(), x, create_graph=True)[0]
+        with pytest.raises(RuntimeError, match="no second derivative"):
+            torch.autograd.grad(first.sum(), r)
+    layer.weight.grad = None
+    of_y(layer(x, r)).backward()   # the first derivative alone is as before
+    assert torch.equal(x.grad, dx) and torch.equal(layer.weight.grad, dw) and not x.grad.requires_grad
