@@ -92,14 +92,24 @@ class _BlockwiseLinear(torch.autograd.Function):
         return dx, None if main_grad is not None else dw
 
 
+def _drawn() -> int:
+    """A number below 2^62 from torch's CPU generator: far from any other one, in counters."""
+    return int(torch.empty((), dtype=torch.int64, device="cpu").random_(0, 1 << 62))
+
+
 class BlockwiseLinear(torch.nn.Module):
     """``y = residual + dropout(x W^T)`` on blockwise FP8 copies.
 
     ``in_features`` and ``out_features`` are multiples of 128; x is bfloat16 or
     float32 with any number of rows.  Dropout runs in training mode; its
     decisions follow from the layer's ``seed`` and the ``offset`` of the call
-    (in counters of 8 elements; give each step its own, e.g. ``step *
-    rows * out_features // 8``).  There is no second derivative: one that is
+    (in counters of 8 elements).  Neither has to be given: a seed is drawn when
+    a layer with dropout is made, an offset at every call, both from torch's CPU
+    generator, so that masks differ from call to call and layer to layer,
+    repeat under ``torch.manual_seed``, and a checkpointed forward pass draws
+    its own again.  A call that is captured into a CUDA graph has to be given its
+    offset (every replay draws what it was captured with); give steps their own,
+    e.g. ``step * rows * out_features // 8``.  There is no second derivative: one that is
     asked for raises.  With ``main_grad`` set (FP32, the weight's
     shape) the weight gradient is added to it and ``weight.grad`` stays unset.
     ``copies`` takes the result of :meth:`quantize_weight`, made once for the
@@ -111,14 +121,15 @@ class BlockwiseLinear(torch.nn.Module):
     waiting and a result is not whole.  Look at it where the host waits anyway
     (before the optimizer's step, say) and zero it."""
 
-    def __init__(self, in_features: int, out_features: int, p: float = 0.0, seed: int = 0, device="cuda",
+    def __init__(self, in_features: int, out_features: int, p: float = 0.0, seed: Optional[int] = None, device="cuda",
                  dtype=torch.bfloat16):
         super().__init__()
         if in_features % 128 or out_features % 128:
             raise ValueError("in_features and out_features must be multiples of 128")
         self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
         torch.nn.init.normal_(self.weight, std=0.02)
-        self.p, self.seed = float(p), int(seed)
+        self.p = float(p)
+        self.seed = int(seed) if seed is not None else _drawn() if p > 0 else 0
         self.main_grad: Optional[torch.Tensor] = None
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
 
@@ -132,9 +143,14 @@ class BlockwiseLinear(torch.nn.Module):
         return q_blockwise(self.weight.detach(), "128x128", rowwise=True, colwise=colwise,
                            status=self._status_on(self.weight.device))
 
-    def forward(self, x, residual=None, offset: int = 0, copies: Optional[BlockwiseTensor] = None):
+    def forward(self, x, residual=None, offset: Optional[int] = None, copies: Optional[BlockwiseTensor] = None):
         train = torch.is_grad_enabled()
+        p = self.p if self.training else 0.0
+        if offset is None:
+            if p > 0 and x.is_cuda and torch.cuda.is_current_stream_capturing():
+                raise ValueError("a captured call with dropout needs its offset: a drawn one would be every replay's")
+            offset = _drawn() if p > 0 else 0
         if copies is None:
             copies = self.quantize_weight(colwise=train and x.requires_grad)
-        return _BlockwiseLinear.apply(x, self.weight, residual, copies, self.p if self.training else 0.0, self.seed,
+        return _BlockwiseLinear.apply(x, self.weight, residual, copies, p, self.seed,
                                       int(offset), self.main_grad, train, self._status_on(x.device))

@@ -35,3 +35,19 @@ def test_layer_status_reports_casts_and_products():
     finally:
         Q.lib().selftest_mm_give_up(0)
     assert layer.status.item() == Q.Q_ST_TIMEOUT
+
+
+def test_captured_training_call_needs_its_offset():
+    layer = BlockwiseLinear(256, 128, p=0.5, seed=4, dtype=torch.float32)
+    x = torch.randn(128, 256, device="cuda")
+    want = layer(x, offset=12)
+    assert not torch.equal(layer(x), layer(x))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.no_grad(), torch.cuda.graph(g):
+        with pytest.raises(ValueError, match="offset"):
+            layer(x)
+        y = layer(x, offset=12)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)

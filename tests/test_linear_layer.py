@@ -108,3 +108,55 @@ def test_a_second_derivative_is_refused_and_not_lost(plain, of_y):
     layer.weight.grad = None
     of_y(layer(x, r)).backward()   # the first derivative alone is as before
     assert torch.equal(x.grad, dx) and torch.equal(layer.weight.grad, dw) and not x.grad.requires_grad
+
+
+def test_calls_without_an_offset_draw_masks_of_their_own(plain):
+    """In training, call by call and layer by layer; the backward pass draws what its forward pass drew."""
+    one, two = layer_of(p=0.5), linear.BlockwiseLinear(256, 128, p=0.5, device="cpu", dtype=torch.float32)
+    x = torch.randn(128, 256, requires_grad=True)
+    masks = [layer(x) != 0 for layer in (one, one, two, two)]
+    for i, a in enumerate(masks):
+        assert 0.45 < float(a.double().mean()) < 0.55
+        assert all(0.4 < float((a == b).double().mean()) < 0.6 for b in masks[:i])
+    assert len(set(plain.offsets)) == 4
+    assert one.seed != two.seed   # the same offset gives layers masks of their own, too
+    assert not torch.equal(one(x, offset=7) != 0, two(x, offset=7) != 0)
+    plain.offsets.clear()
+    y, z = one(x), one(x)
+    y.sum().backward()
+    z.sum().backward()
+    assert plain.offsets[2:] == plain.offsets[:2] and plain.offsets[0] != plain.offsets[1]
+    plain.offsets.clear()
+    one.eval()
+    assert torch.equal(one(x), one(x)) and plain.offsets == []
+
+
+def test_masks_follow_torchs_generator_and_checkpointing(plain):
+    """The same seed of torch's generator gives the same masks, and so does a recomputed forward pass."""
+    from torch.utils.checkpoint import checkpoint
+    layer = layer_of(p=0.5)
+    x = torch.randn(128, 256, requires_grad=True)
+
+    def grads(f):
+        torch.manual_seed(5)
+        layer.weight.grad = x.grad = None
+        y = f(x)
+        y.square().sum().backward()
+        return y.detach(), x.grad, layer.weight.grad
+
+    want = grads(layer)
+    for reentrant in (False, True):
+        assert all(torch.equal(a, b) for a, b in zip(grads(lambda x: checkpoint(layer, x, use_reentrant=reentrant)), want))
+
+
+def test_a_given_offset_and_seed_are_taken_as_they_are(plain):
+    layer = layer_of(p=0.5, seed=9)
+    state = torch.get_rng_state()
+    layer(torch.randn(128, 256, generator=torch.Generator().manual_seed(1)), offset=0)
+    assert plain.offsets == [(9, 0)] and torch.equal(torch.get_rng_state(), state)
+    layer_of()   # without dropout nothing is drawn
+    torch.manual_seed(3)
+    a = torch.rand(1)
+    torch.manual_seed(3)
+    linear.BlockwiseLinear(128, 128, device="meta")
+    assert torch.equal(torch.rand(1), a)
