@@ -654,9 +654,34 @@ def _copies(name, c, M, K, dev):
             raise ValueError(f"{name}.{field} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
 
 
+def _wants_grad(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return True
+    return False
+
+
 def _alike(name, t, x):
     if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, with x's shape, dtype and device")
+
+
+def _ready(t):
+    """t as the kernels read it: contiguous, on a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+class _DropAdd(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, p, seed, offset):
+        ctx.args = (p, seed, offset)
+        return drop_add(x, p, seed, offset, residual)
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx = drop_add(_ready(dy), *ctx.args) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None, None, None
 
 
 def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Optional[torch.Tensor] = None,
@@ -664,13 +689,18 @@ def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Op
     """``residual + dropout(x)`` (or ``dropout(x)``) for a contiguous tensor of
     any shape.  Which elements are dropped follows from ``seed``, ``offset`` (in
     counters of 8 elements) and the element's flat index, so the backward pass
-    is ``drop_add(dy, p, seed, offset)`` and no mask is stored.  ``p`` is taken
-    to the nearest 1/65536.  ``out`` may be ``x`` or ``residual``."""
+    is ``drop_add(dy, p, seed, offset)`` and no mask is stored; autograd takes it
+    where a gradient is wanted.  ``p`` is taken to the nearest 1/65536.  ``out``
+    may be ``x`` or ``residual``; with it no gradient is recorded."""
     dt, dev = _DTYPES.get(x.dtype), x.device
     if dt is None or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor of bfloat16 or float32")
     if residual is not None:
         _alike("residual", residual, x)
+    if torch.is_grad_enabled() and _wants_grad(x, residual, out):
+        if out is not None:
+            raise RuntimeError("drop_add with out= records no gradient, but one of its tensors requires one")
+        return _DropAdd.apply(x, residual, p, seed, offset)
     if out is None:
         out = torch.empty_like(x)
     else:

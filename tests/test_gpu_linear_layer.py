@@ -51,3 +51,25 @@ def test_captured_training_call_needs_its_offset():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape", [(3, 7), (64, 512)])
+def test_drop_add_gradient(dtype, shape):
+    """Of x by the same call, of the residual as it is; strided and unaligned gradients; exactly linear, so by differences too."""
+    x, r, t = (torch.randn(shape, device="cuda", dtype=dtype, requires_grad=True) for _ in range(3))
+    y = Q.drop_add(x, 0.25, 5, 3, residual=r)
+    with torch.no_grad():
+        assert torch.equal(y, Q.drop_add(x, 0.25, 5, 3, residual=r))
+    g = torch.randn(shape[::-1], device="cuda", dtype=dtype).t()
+    dx, dr = torch.autograd.grad(y, (x, r), g)
+    assert torch.equal(dx, Q.drop_add(g.contiguous(), 0.25, 5, 3)) and torch.equal(dr, g)
+    both = torch.cat([t.flatten()[:1], Q.drop_add(x, 0.25, 5, 3).flatten()])   # its gradient begins one element off a boundary
+    h = torch.randn_like(both)
+    (dx,) = torch.autograd.grad(both, x, h)
+    assert torch.equal(dx, Q.drop_add(h[1:].clone().view(shape), 0.25, 5, 3))
+    if dtype == torch.float32:   # c = 4/3 is a double's: each product rounds once, by 2^-24 of it
+        with torch.no_grad():
+            f = Q.drop_add(x + 1, 0.25, 5, 3).double() - Q.drop_add(x, 0.25, 5, 3).double()
+            slope = Q.drop_add(torch.ones_like(x), 0.25, 5, 3).double()
+            assert bool(((f - slope).abs() <= 2.0 ** -22 * (x.double().abs() + 2) * slope).all())

@@ -1,5 +1,6 @@
 """What the Python binding of the operators on the blockwise copies lets through to the library, on
 the CPU: tensors that say they are CUDA ones, and a library call that only notes its arguments."""
+import ctypes
 import dataclasses
 
 import pytest
@@ -81,3 +82,45 @@ def test_give_up_is_for_one_call_and_clears(L):
     finally:
         L.q_selftest_inject_launch_error(0)
         L.selftest_mm_give_up(0)
+
+
+def grad(t):
+    return t.requires_grad_()
+
+
+def test_drop_add_into_a_given_tensor_records_no_gradient_and_says_so(calls):
+    """Written to out, the result has no graph: where a gradient is wanted that is refused, as torch does."""
+    new = lambda: fake((4, 128), F32)
+    for kw in (dict(x=grad(new()), out=new()), dict(x=new(), residual=grad(new()), out=new()), dict(x=new(), out=grad(new()))):
+        with pytest.raises(RuntimeError, match="gradient"):
+            Q.drop_add(p=0.1, seed=0, **kw)
+        assert calls == []
+        with torch.no_grad():
+            assert Q.drop_add(p=0.1, seed=0, **kw) is kw["out"]
+        assert calls.pop() == "drop_add"
+
+
+def test_drop_add_has_a_gradient(monkeypatch):
+    """The library's call is linear in x and the residual, and its backward pass is the same call on the gradient."""
+    made, values = [], {}
+
+    def call(name, x, dt, n, residual, p, seed, offset, y, stream):
+        made.append((name, p, seed, offset, residual is not None))
+        t = lambda a: torch.frombuffer((ctypes.c_float * n).from_address(a), dtype=F32)
+        t(y).copy_(t(x) * 3 + (t(residual) if residual else 0))
+
+    monkeypatch.setattr(Q, "_call", call)
+    monkeypatch.setattr(Q, "_stream", lambda dev: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))   # autograd hands plain tensors on
+    x, r = (torch.randn(4, 24, requires_grad=True) for _ in range(2))
+    g = torch.randn(24, 4).t()   # a gradient that is not contiguous
+    y = Q.drop_add(x, 0.25, 7, 9, residual=r)
+    assert torch.equal(y, x * 3 + r)
+    dx, dr = torch.autograd.grad(y, (x, r), g, create_graph=True)
+    assert torch.equal(dx, g * 3) and torch.equal(dr, g)
+    assert made == [("drop_add", 0.25, 7, 9, True), ("drop_add", 0.25, 7, 9, False)]
+    (z,) = torch.autograd.grad(Q.drop_add(r.detach(), 0.25, 7, residual=r), (r,), g)   # the residual's alone: no call
+    assert torch.equal(z, g) and len(made) == 3
+    w = x * 2
+    (second,) = torch.autograd.grad((torch.autograd.grad(Q.drop_add(w, 0.25, 7) ** 2, w, g, create_graph=True)[0]).sum(), x)
+    assert torch.allclose(second, 36 * g)   # y = 3 w with w = 2 x: the sum of 18 w g, by x
