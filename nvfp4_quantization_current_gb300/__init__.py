@@ -624,7 +624,9 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     ``(dy.q_colT, dy.s_colT, x.q_colT, x.s_colT, tile_b="1x128")``.
     ``dtype`` (that of ``out`` when it is given) is bfloat16 or float32;
     ``accumulate`` adds to ``out`` (e.g. an FP32 main gradient).  One token
-    upward; sums in FP32, results independent of timing."""
+    upward; sums in FP32, results independent of timing.  It records no gradient:
+    scales or an ``out`` that require one are refused (``linear.py`` has the
+    backward pass)."""
     ta, tb = _TILE[tile_a], _TILE[tile_b]
     M, K = _operand("a", a, s_a, ta)
     N, Kb = _operand("b", b, s_b, tb)
@@ -639,6 +641,8 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
         out = torch.empty((M, N), dtype=dtype, device=dev)
     elif out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
+    if torch.is_grad_enabled() and _wants_grad(s_a, s_b, out):
+        raise RuntimeError("mm_blockwise records no gradient, but its scales or out require one")
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
           _DTYPES[out.dtype], int(accumulate), _status(status, dev), _stream(dev))
     return out

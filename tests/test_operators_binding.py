@@ -124,3 +124,14 @@ def test_drop_add_has_a_gradient(monkeypatch):
     w = x * 2
     (second,) = torch.autograd.grad((torch.autograd.grad(Q.drop_add(w, 0.25, 7) ** 2, w, g, create_graph=True)[0]).sum(), x)
     assert torch.allclose(second, 36 * g)   # y = 3 w with w = 2 x: the sum of 18 w g, by x
+
+
+def test_mm_blockwise_has_no_gradient_and_says_so(calls):
+    a, s_a, b, s_b = fake((4, 256), U8), fake((4, 2), F32), fake((128, 256), U8), fake((1, 2), F32)
+    for args, out in (((a, grad(s_a.clone()), b, s_b), None), ((a, s_a, b, grad(s_b.clone())), None), ((a, s_a, b, s_b), grad(fake((4, 128), F32)))):
+        with pytest.raises(RuntimeError, match="gradient"):
+            Q.mm_blockwise(*args, out=out)
+        assert calls == []
+        with torch.no_grad():
+            Q.mm_blockwise(*args, out=out)
+        assert calls.pop() == "mm_blockwise"
