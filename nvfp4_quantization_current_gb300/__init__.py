@@ -641,6 +641,8 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
         out = torch.empty((M, N), dtype=dtype, device=dev)
     elif out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
+    else:
+        _written(out)
     if torch.is_grad_enabled() and _wants_grad(s_a, s_b, out):
         raise RuntimeError("mm_blockwise records no gradient, but its scales or out require one")
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
@@ -656,6 +658,10 @@ def _copies(name, c, M, K, dev):
                                    ("q_colT", c.q_colT, torch.uint8, (K, M)), ("s_colT", c.s_colT, torch.float32, (K, M // 128))):
         if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
             raise ValueError(f"{name}.{field} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
+
+
+# The kernels write through a pointer: this is what autograd's check of the tensors that it saved goes by.
+_written = torch.autograd.graph.increment_version
 
 
 def _wants_grad(*tensors):
@@ -709,6 +715,7 @@ def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Op
         out = torch.empty_like(x)
     else:
         _alike("out", out, x)
+        _written(out)
     _call("drop_add", x.data_ptr(), dt, x.numel(), _ptr(residual), float(p), int(seed), int(offset), out.data_ptr(),
           _stream(dev))
     return out
@@ -729,6 +736,9 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
         _copies("out", out, M, K, x.device)
         if colwise and out.q_colT is None:
             raise ValueError("out has no transposed copy")
+        for t in (out.q_row, out.s_row, out.q_colT, out.s_colT):
+            if t is not None:
+                _written(t)
     _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
           _ptr(out.q_colT), _ptr(out.s_colT), _status(status, x.device), _stream(x.device))
     return out

@@ -135,3 +135,29 @@ def test_mm_blockwise_has_no_gradient_and_says_so(calls):
         with torch.no_grad():
             Q.mm_blockwise(*args, out=out)
         assert calls.pop() == "mm_blockwise"
+
+
+def test_writing_into_a_tensor_counts_as_a_new_version(calls):
+    """What autograd saved and finds overwritten raises there; results that are written in place have to count."""
+    a, s_a, b, s_b, c = fake((4, 256), U8), fake((4, 2), F32), fake((128, 256), U8), fake((1, 2), F32), fake((4, 128), F32)
+    x, r = fake((128, 128), F32), fake((128, 128), F32)
+
+    def versions(f, *tensors):
+        before = [t._version for t in tensors]
+        f()
+        return [t._version > v for t, v in zip(tensors, before)]
+
+    assert versions(lambda: Q.mm_blockwise(a, s_a, b, s_b, out=c, accumulate=True), c, a, s_a, b, s_b) == [True] + [False] * 4
+    assert versions(lambda: Q.drop_add(x, 0.1, 0, residual=r, out=r), r, x) == [True, False]
+    assert versions(lambda: Q.drop_add(x, 0.1, 0, residual=r, out=x), r, x) == [False, True]
+    t = copies(128, 128)
+    assert versions(lambda: Q.drop_q_blockwise(x, 0.1, 0, out=t), t.q_row, t.s_row, t.q_colT, t.s_colT, x) == [True] * 4 + [False]
+    t = copies(128, 128, colwise=False)
+    assert versions(lambda: Q.drop_q_blockwise(x, 0.1, 0, out=t), t.q_row, t.s_row) == [True] * 2
+    w = torch.randn(128, 128, requires_grad=True)
+    y = (w * 2).as_subclass(type(x))
+    z = y.square()
+    with torch.no_grad():
+        Q.drop_add(y.detach(), 0.1, 0, out=y.detach())   # shares y's counter
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.sum().backward()
