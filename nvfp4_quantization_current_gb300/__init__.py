@@ -158,6 +158,16 @@ def _out(dtype):
     return {torch.float32: Q_F32, torch.bfloat16: Q_BF16}[dtype]
 
 
+# The kernels write through a pointer: this is what autograd's check of the tensors that it saved goes by.
+_written = torch.autograd.graph.increment_version
+
+
+def _written_copies(c):
+    for t in (c.q_row, c.s_row, c.q_colT, c.s_colT):
+        if t is not None:
+            _written(t)
+
+
 def _u8(shape, dev):
     return torch.empty(shape, dtype=torch.uint8, device=dev)
 
@@ -385,7 +395,10 @@ def q_blockwise(x: torch.Tensor, tile="1x128", rowwise=True, colwise=False, out:
                 status: Optional[torch.Tensor] = None):
     dt = _in(x)
     M, K = x.shape
-    out = alloc_blockwise(M, K, x.device, tile, rowwise, colwise) if out is None else out
+    if out is None:
+        out = alloc_blockwise(M, K, x.device, tile, rowwise, colwise)
+    else:
+        _written_copies(out)
     _call("q_blockwise", _ptr(x), dt, M, K, out.tile, _ptr(out.q_row), _ptr(out.s_row), _ptr(out.q_colT),
           _ptr(out.s_colT), _ptr(status), _stream(x.device))
     return out
@@ -660,10 +673,6 @@ def _copies(name, c, M, K, dev):
             raise ValueError(f"{name}.{field} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
 
 
-# The kernels write through a pointer: this is what autograd's check of the tensors that it saved goes by.
-_written = torch.autograd.graph.increment_version
-
-
 def _wants_grad(*tensors):
     for t in tensors:
         if t is not None and t.requires_grad:
@@ -736,9 +745,7 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
         _copies("out", out, M, K, x.device)
         if colwise and out.q_colT is None:
             raise ValueError("out has no transposed copy")
-        for t in (out.q_row, out.s_row, out.q_colT, out.s_colT):
-            if t is not None:
-                _written(t)
+        _written_copies(out)
     _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
           _ptr(out.q_colT), _ptr(out.s_colT), _status(status, x.device), _stream(x.device))
     return out

@@ -161,3 +161,12 @@ def test_writing_into_a_tensor_counts_as_a_new_version(calls):
         Q.drop_add(y.detach(), 0.1, 0, out=y.detach())   # shares y's counter
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.sum().backward()
+
+
+def test_casting_into_copies_counts_as_a_new_version(calls):
+    """The linear layer saves the weight's copies for its backward pass: casting another weight into them has to be seen."""
+    for tile in (Q.Q_T1x128, Q.Q_T128x128):
+        t = copies(128, 128, tile)
+        before = [c._version for c in (t.q_row, t.s_row, t.q_colT, t.s_colT)]
+        Q.q_blockwise(fake((128, 128), F32), out=t)
+        assert [c._version > v for c, v in zip((t.q_row, t.s_row, t.q_colT, t.s_colT), before)] == [True] * 4
