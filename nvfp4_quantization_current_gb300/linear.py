@@ -53,14 +53,17 @@ class _BlockwiseLinear(torch.autograd.Function):
         need_x, need_w = (train and n for n in ctx.needs_input_grad[:2])
         if need_x and w.q_colT is None:
             raise ValueError("copies lacks the transposed copy, which the input gradient reads")
+        out_shape = (*x.shape[:-1], weight.shape[0])
         x2 = x.reshape(-1, x.shape[-1])
+        if residual is not None and residual.shape not in (out_shape, (x2.shape[0], weight.shape[0])):
+            raise ValueError(f"residual must have the result's shape {out_shape}, not {tuple(residual.shape)}")
         xq = _cast_rows(x2, True, need_w, status)
         y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype, status=status)
         if p > 0 or residual is not None:
             drop_add(y, p, seed, offset, None if residual is None else residual.reshape(y.shape), out=y)
         ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
                               *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
-        ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, residual is not None, status)
+        ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, None if residual is None else residual.shape, status)
         return y.view(*x.shape[:-1], -1)
 
     @staticmethod
@@ -69,7 +72,7 @@ class _BlockwiseLinear(torch.autograd.Function):
             dx, dw = _BlockwiseLinear.gradients(ctx, dy)
         if torch.is_grad_enabled():   # create_graph
             dx, dw = (None if g is None else _Once.apply(g, dy, torch.zeros((), requires_grad=True)) for g in (dx, dw))
-        return (dx, dw, dy if ctx.args[6] else None) + (None,) * 7
+        return (dx, dw, None if ctx.args[6] is None else dy.reshape(ctx.args[6])) + (None,) * 7
 
     @staticmethod
     def gradients(ctx, dy):

@@ -160,3 +160,20 @@ def test_a_given_offset_and_seed_are_taken_as_they_are(plain):
     torch.manual_seed(3)
     linear.BlockwiseLinear(128, 128, device="meta")
     assert torch.equal(torch.rand(1), a)
+
+
+def test_a_residual_of_another_shape_is_refused_and_not_reinterpreted(plain):
+    """It has y's shape, or y's rows flattened; one with as many elements only is another tensor."""
+    layer = layer_of()
+    x = torch.randn(4, 32, 256)
+    r = torch.randn(4, 32, 128, requires_grad=True)
+    y = layer(x)
+    assert torch.allclose(layer(x, r), y + r)
+    flat = r.detach().reshape(128, 128).requires_grad_()
+    z = layer(x, flat)
+    assert z.shape == (4, 32, 128) and torch.equal(z, layer(x, r))
+    g = torch.randn(4, 32, 128)
+    assert torch.equal(torch.autograd.grad(z, flat, g)[0], g.reshape(128, 128))
+    for shape in ((32, 4, 128), (4, 128, 32), (128 * 128,), (4, 32, 64), (64, 256), (32, 128), (128,)):
+        with torch.no_grad(), pytest.raises(ValueError, match="residual"):
+            layer(x, torch.zeros(shape))
