@@ -19,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from . import BlockwiseTensor, drop_add, drop_q_blockwise, mm_blockwise, q_blockwise
+from . import BlockwiseTensor, _ready, drop_add, drop_q_blockwise, mm_blockwise, q_blockwise
 
 
 def _cast_rows(x, rowwise, colwise, status):
@@ -54,13 +54,13 @@ class _BlockwiseLinear(torch.autograd.Function):
         if need_x and w.q_colT is None:
             raise ValueError("copies lacks the transposed copy, which the input gradient reads")
         out_shape = (*x.shape[:-1], weight.shape[0])
-        x2 = x.reshape(-1, x.shape[-1])
+        x2 = _ready(x.reshape(-1, x.shape[-1]))
         if residual is not None and residual.shape not in (out_shape, (x2.shape[0], weight.shape[0])):
             raise ValueError(f"residual must have the result's shape {out_shape}, not {tuple(residual.shape)}")
         xq = _cast_rows(x2, True, need_w, status)
         y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype, status=status)
         if p > 0 or residual is not None:
-            drop_add(y, p, seed, offset, None if residual is None else residual.reshape(y.shape), out=y)
+            drop_add(y, p, seed, offset, None if residual is None else _ready(residual.reshape(y.shape)), out=y)
         ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
                               *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
         ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, None if residual is None else residual.shape, status)
@@ -82,7 +82,7 @@ class _BlockwiseLinear(torch.autograd.Function):
         if not (need_x or need_w):
             return None, None
         dx = dw = None
-        d = dy.reshape(-1, dy.shape[-1]).contiguous()
+        d = _ready(dy.reshape(-1, dy.shape[-1]))
         M = d.shape[0]
         if need_w and M % 128 != 0:   # zero rows below, as in the forward pass; the draws are by flat index
             d = torch.nn.functional.pad(d, (0, 0, 0, -M % 128))
@@ -104,7 +104,8 @@ class BlockwiseLinear(torch.nn.Module):
     """``y = residual + dropout(x W^T)`` on blockwise FP8 copies.
 
     ``in_features`` and ``out_features`` are multiples of 128; x is bfloat16 or
-    float32 with any number of rows.  Dropout runs in training mode; its
+    float32 with any number of rows and any strides, the residual alike and of
+    x's type.  Dropout runs in training mode; its
     decisions follow from the layer's ``seed`` and the ``offset`` of the call
     (in counters of 8 elements).  Neither has to be given: a seed is drawn when
     a layer with dropout is made, an offset at every call, both from torch's CPU

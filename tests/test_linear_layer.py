@@ -177,3 +177,25 @@ def test_a_residual_of_another_shape_is_refused_and_not_reinterpreted(plain):
     for shape in ((32, 4, 128), (4, 128, 32), (128 * 128,), (4, 32, 64), (64, 256), (32, 128), (128,)):
         with torch.no_grad(), pytest.raises(ValueError, match="residual"):
             layer(x, torch.zeros(shape))
+
+
+def off_by_one(t):
+    """The same values one element off a 16-byte boundary."""
+    return torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
+
+
+@pytest.mark.parametrize("made", [lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), lambda t: t.repeat(1, 1, 2)[..., : t.shape[-1]],
+                                  off_by_one])
+def test_strided_and_unaligned_operands_are_those_they_hold(plain, made):
+    """x, the residual and the incoming gradient, as a slice, a transpose or a view into a buffer gives them."""
+    layer = layer_of(p=0.5, seed=2)
+    x, r, g = torch.randn(4, 40, 256), torch.randn(4, 40, 128), torch.randn(4, 40, 128)
+
+    def run(f):
+        layer.weight.grad = None
+        a, b = x.clone().requires_grad_(), r.clone().requires_grad_()
+        y = layer(f(a), f(b), offset=0)
+        y.backward(f(g))
+        return y.detach(), a.grad, b.grad, layer.weight.grad
+
+    assert all(torch.equal(a, b) for a, b in zip(run(made), run(lambda t: t)))
