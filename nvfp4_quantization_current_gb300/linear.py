@@ -64,7 +64,7 @@ class _BlockwiseLinear(torch.autograd.Function):
         ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
                               *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
         ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, None if residual is None else residual.shape, status)
-        return y.view(*x.shape[:-1], -1)
+        return y.view(out_shape)
 
     @staticmethod
     def backward(ctx, dy):

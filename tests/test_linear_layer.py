@@ -199,3 +199,18 @@ def test_strided_and_unaligned_operands_are_those_they_hold(plain, made):
         return y.detach(), a.grad, b.grad, layer.weight.grad
 
     assert all(torch.equal(a, b) for a, b in zip(run(made), run(lambda t: t)))
+
+
+@pytest.mark.parametrize("shape", [(0, 256), (2, 0, 256)])
+def test_no_rows(plain, shape):
+    """A batch that came out empty: an empty result, and gradients of zero."""
+    layer = layer_of(p=0.5)
+    x, r = torch.zeros(shape, requires_grad=True), torch.zeros((*shape[:-1], 128), requires_grad=True)
+    y = layer(x, r)
+    assert y.shape == r.shape
+    y.sum().backward()
+    assert x.grad.shape == x.shape and r.grad.shape == r.shape
+    assert torch.equal(layer.weight.grad, torch.zeros(128, 256))
+    layer.main_grad = torch.ones(128, 256)
+    layer(x, r).sum().backward()
+    assert torch.equal(layer.main_grad, torch.ones(128, 256))
