@@ -163,9 +163,7 @@ _written = torch.autograd.graph.increment_version
 
 
 def _written_copies(c):
-    for t in (c.q_row, c.s_row, c.q_colT, c.s_colT):
-        if t is not None:
-            _written(t)
+    _written([t for t in (c.q_row, c.s_row, c.q_colT, c.s_colT) if t is not None])
 
 
 def _u8(shape, dev):
@@ -611,15 +609,11 @@ def _operand(name, q, s, tile):
     want = (R, K // 128) if tile == Q_T1x128 else (R // 128, K // 128)
     if s.shape != want:
         raise ValueError(f"{name}: scales are {tuple(s.shape)}, codes {R} x {K} need {want}")
-    if s.device != q.device:
-        raise ValueError(f"{name}: scales are on {s.device}, codes on {q.device}")
     return R, K
 
 
 def _status(status, dev):
-    """The address of a status word on dev (or none)."""
-    if status is None:
-        return None
+    """The address of a status word on dev."""
     if status.dtype != torch.int32 or status.numel() == 0 or status.device != dev:
         raise ValueError(f"status must be an int32 tensor of one element on {dev}")
     return status.data_ptr()
@@ -646,8 +640,13 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     if K != Kb:
         raise ValueError(f"a has K = {K}, b has K = {Kb}")
     dev = a.device
-    if dev != b.device:
+    if s_a.device != dev or b.device != dev or s_b.device != dev:
+        for name, q, s in (("a", a, s_a), ("b", b, s_b)):
+            if s.device != q.device:
+                raise ValueError(f"{name}: scales are on {s.device}, codes on {q.device}")
         raise ValueError(f"a is on {dev}, b on {b.device}")
+    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+        raise RuntimeError("mm_blockwise records no gradient, but its scales or out require one")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -656,28 +655,27 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
         raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
     else:
         _written(out)
-    if torch.is_grad_enabled() and _wants_grad(s_a, s_b, out):
-        raise RuntimeError("mm_blockwise records no gradient, but its scales or out require one")
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
-          _DTYPES[out.dtype], int(accumulate), _status(status, dev), _stream(dev))
+          _DTYPES[out.dtype], int(accumulate), None if status is None else _status(status, dev), _stream(dev))
     return out
+
+
+def _is(t, dtype, shape, dev):
+    return t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous()
 
 
 def _copies(name, c, M, K, dev):
     """Refuses copies that are not those of an M x K tensor in 1x128 tiles: the kernel would write past them."""
+    u8, f32 = torch.uint8, torch.float32
     if c.tile != Q_T1x128:
         raise ValueError(f"{name} must hold 1x128 tiles")
-    for field, t, dtype, shape in (("q_row", c.q_row, torch.uint8, (M, K)), ("s_row", c.s_row, torch.float32, (M, K // 128)),
-                                   ("q_colT", c.q_colT, torch.uint8, (K, M)), ("s_colT", c.s_colT, torch.float32, (K, M // 128))):
-        if t is not None and (t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous()):
+    if (c.q_row is None or _is(c.q_row, u8, (M, K), dev)) and (c.s_row is None or _is(c.s_row, f32, (M, K // 128), dev)) and \
+            (c.q_colT is None or _is(c.q_colT, u8, (K, M), dev)) and (c.s_colT is None or _is(c.s_colT, f32, (K, M // 128), dev)):
+        return
+    for field, dtype, shape in (("q_row", u8, (M, K)), ("s_row", f32, (M, K // 128)), ("q_colT", u8, (K, M)), ("s_colT", f32, (K, M // 128))):
+        t = getattr(c, field)
+        if t is not None and not _is(t, dtype, shape, dev):
             raise ValueError(f"{name}.{field} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
-
-
-def _wants_grad(*tensors):
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return True
-    return False
 
 
 def _alike(name, t, x):
@@ -716,7 +714,8 @@ def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Op
         raise ValueError("x must be a contiguous CUDA tensor of bfloat16 or float32")
     if residual is not None:
         _alike("residual", residual, x)
-    if torch.is_grad_enabled() and _wants_grad(x, residual, out):
+    if (x.requires_grad or residual is not None and residual.requires_grad or out is not None and out.requires_grad) \
+            and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError("drop_add with out= records no gradient, but one of its tensors requires one")
         return _DropAdd.apply(x, residual, p, seed, offset)
@@ -747,7 +746,7 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
             raise ValueError("out has no transposed copy")
         _written_copies(out)
     _call("drop_q_blockwise", _ptr(x), dt, M, K, float(p), int(seed), int(offset), _ptr(out.q_row), _ptr(out.s_row),
-          _ptr(out.q_colT), _ptr(out.s_colT), _status(status, x.device), _stream(x.device))
+          _ptr(out.q_colT), _ptr(out.s_colT), None if status is None else _status(status, x.device), _stream(x.device))
     return out
 
 
