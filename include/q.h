@@ -398,8 +398,10 @@ q_status dq_nvfp4(const uint8_t *q, const uint8_t *sb, const float *s_global, in
  *   accumulate != 0 adds to what c holds (the FP32 main gradient over
  *   micro-batches), 0 overwrites it without reading.
  * Sums are held in FP32; the result does not depend on timing (nothing is added to twice in a call),
- * and a row's result does not depend on the values of other rows.  The E4M3
- * codes 0x7F and 0xFF are NaN and propagate, as do non-finite scales.
+ * and a row's result does not depend on the values of other rows.  How K is
+ * split and in which order a block's sum meets its two scales goes by M, N, K
+ * and the tiles, so the same row may round otherwise in a call of another M.
+ * The E4M3 codes 0x7F and 0xFF are NaN and propagate, as do non-finite scales.
  * Scales are multiplied in FP32, with each other or with a block's sum first:
  * where such a product leaves FP32's normal range, the result is not accurate.
  * Shapes: K % 128 == 0, M % 128 == 0 (N % 128 == 0) for a 128x128 operand;

@@ -34,12 +34,14 @@
 // its own 8 rows and zeroes dropped elements in its registers.  Rounding is
 // monotonic, so max|y| = RN(c max|kept x|), and the codes are those of
 // RN(alpha RN(c x)), as q_blockwise gives them for an FP32 y.  Measured on a
-// GB300, both copies of 8192 x 4096: BF16 39.2 us (26.5 without dropout, 29.9
-// with the draws taken out: ten Philox rounds per eight elements are 9.5 us of
-// integer multiplies), FP32 71.6 us (55.6); two calls, drop_add and q_blockwise,
-// take 45.9 us for BF16.  The integer pipes bound it: with the next tile's
-// decisions drawn ahead, one bit each, in the body's waiting phases it took 40.9
-// to 42.1 us.
+// GB300, both copies of 8192 x 4096: BF16 39.3 us (26.4 without dropout, 29.9
+// with the draws taken out: ten Philox rounds per eight elements are 9.4 us),
+// FP32 71.1 us (55.5); the transposed copy alone 32.1 and 42.8; two calls, drop_add
+// and q_blockwise, take 45.9 us for BF16.  What bounds it: the one CTA of an SM
+// draws, takes row and column maxima, casts and copies out in turn, and the parts
+// add up.  No pipe is full (issue 56 % active; drop_add draws the same for more
+// bytes in 30.7), and drawing the next tile's decisions ahead inside the same CTA,
+// one bit each, in the body's waiting phases, took 40.9 to 42.1 us.
 #include "q_dropout.cuh"
 #include "q_engine.cuh"
 #include "q_internal.h"

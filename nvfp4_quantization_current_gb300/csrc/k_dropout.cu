@@ -6,9 +6,9 @@
 // rounds per eight): a thread takes the eight elements of kDropUnroll Philox
 // blocks, in 16-byte pieces that are all on their way before the first draw is
 // computed.  The sum is formed in FP32 (one fused multiply-add) and rounded
-// once to the output type.  Measured on a GB300: 8192 x 4096 BF16 with the
-// residual 30.7 us (201 MB at 6.6 TB/s), without it 22 us, with one element per
-// load 84 us; 128 x 4096 1.6 us, of which the launch is most.
+// once to the output type.  Measured on a GB300, inputs from memory: 8192 x 4096
+// BF16 with the residual 30.7 us (201 MB at 6.6 TB/s), without it 21.6 us, with
+// one element per load 84 us; 128 x 4096 1.7 us, of which the launch is most.
 #include <type_traits>
 
 #include "q_dropout.cuh"
@@ -138,10 +138,11 @@ k_drop_add(const void *x, const void *residual, void *y, int64_t n, const DropAr
 // halving exchange, after which lane l holds that of pass l / 4 % 4, takes its
 // quotients once, and the alphas go back by index shuffles.
 //
-// Bound by the integer pipes beside memory: ten Philox rounds per eight
-// elements, as in both copies' kernel, whose tiles took 28.2 us for 8192 x 4096
-// in BF16, 54.1 in FP32 and 5.0 for 256 x 2048; this takes 23.0 (100 MB at 4.4
-// TB/s), 26.0 (169 MB at 6.5) and 1.7.
+// FP32 is bound by memory: 8192 x 4096 26.0 us (169 MB at 6.5 TB/s).  BF16 takes
+// 22.9 (101 MB at 4.4 TB/s), and the draws alone do not account for it: k_drop_add
+// without a residual draws the same and moves 134 MB in 21.6.  The draws, the
+// reduction over 16 lanes and the cast of one pass follow each other.  256 x 2048
+// takes 1.7.  Both copies' kernel took 54.1 us, 28.2 and 5.0 for the rowwise copy.
 template <int DT>
 __global__ void __launch_bounds__(kDropThreads)
 k_drop_q_rows(const void *x, uint8_t *q_row, float *s_row, int64_t n, int32_t *status, const DropArgs d)
@@ -187,7 +188,7 @@ cudaError_t drop_t(const void *x, int64_t n, const void *residual, const DropArg
 {
     const int64_t per = 8 * kDropThreads * kDropUnroll, grid = (n + per - 1) / per;
     // Launched while the kernel ahead ends: 8192 x 4096 27.5 us a call in a stream, 29.6
-    // otherwise, 128 x 4096 in a graph 1.6 and 1.8.  (A signal of its own that the
+    // otherwise (the inputs partly in L2), 128 x 4096 in a graph 1.6 and 1.8.  (A signal of its own that the
     // kernel behind may start filled the SMs unevenly: 3.3 M elements 7.7 us for 5.1.)
     return launch_k(true, residual != nullptr ? k_drop_add<DT, true> : k_drop_add<DT, false>,
                     dim3((unsigned)grid), dim3(kDropThreads), 0, st, x, residual, y, n, d);

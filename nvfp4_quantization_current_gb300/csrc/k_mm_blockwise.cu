@@ -20,10 +20,13 @@
 // issues a block's MMAs into one of several accumulator buffers, and other
 // warps scale and add the buffers that are done.
 //
-// Every wait is bounded; a role that gives up reports Q_ST_TIMEOUT, raises the
-// CTA's abort flag, which ends the other roles' waits, and the copies and MMAs
-// in flight are waited for (bounded again) before shared and tensor memory go
-// away.
+// Waits on mbarriers are bounded; a role that gives up reports Q_ST_TIMEOUT,
+// raises the CTA's abort flag, which ends the other roles' waits, and the copies
+// and MMAs in flight are waited for (bounded again) before shared and tensor
+// memory go away.  The other waits end because who they wait for does: cluster
+// barriers and __syncthreads come where every role has ended, tensor memory is
+// allocated when the CTA ahead on the SM, which waits for nothing of this one,
+// frees its own, and the named barriers are told of where they are used.
 #include "k_mm_pair.cuh"
 #include "k_mm_split.cuh"
 #include "q_internal.h"

@@ -15,13 +15,14 @@
 // half of tensor memory.
 //
 // Measured on a GB300, in graphs of calls: one token with 4096 x 4096 weights
-// 4.8 us (6.3 where the weights come from memory and not from L2; the launch and
-// two trips to memory are most of it), 16 tokens with 14336 x 4096 12.1 to 12.6
-// us (4.7 TB/s), one token with 18432 x 7168 22.4 us (5.9 TB/s), 333 tokens
-// with 4096 x 4096 14.5 us (770 TFLOP/s; a block of 128 x 192 takes 1050
-// cycles, where shared memory needs 640 and the MMAs 384; reading and adding it
-// is what takes longer: without that work the call takes 11.6 us, without its
-// column scales 13.6).  Tried there and not faster: loads of 32 columns, and
+// 4.8 us (three sets of inputs in turn, whose weights stay in L2; 6.4 with ten
+// sets, whose weights come from memory; the launch and two trips to memory are
+// most of it), 16 tokens with 14336 x 4096 12.2 to 12.6 us (4.7 TB/s), one token
+// with 18432 x 7168 22.4 us (5.9 TB/s), 333 tokens with 4096 x 4096 14.6 to 14.8
+// us (760 TFLOP/s; a block of 128 x 192 takes 1050 cycles, where shared memory
+// needs 640 and the MMAs 384; without reading and adding it the call took 11.6 us
+// of 14.5, without its column scales 13.6, so that loads and what a call costs
+// whatever its size are the larger part).  Tried there and not faster: loads of 32 columns, and
 // the 16-lane loads of the pair kernel, which need a quarter of the column
 // scales (15.4 us; 15.2 against 16.4 where each weight row has a scale).
 #pragma once
@@ -103,8 +104,9 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     }
     if (warp == kEpiWarps && elect_one()) {
         // The weights of the first stages are on their way from memory while the
-        // kernel ahead still runs (16 tokens with 14336 x 4096 12.8 us, 12.0 so; twice
-        // as many stages are no better).
+        // kernel ahead still runs (16 tokens with 14336 x 4096 12.9 us, 12.2 so; one with
+        // 18432 x 7168 23.9 and 22.4; with 4096 x 4096, where most of a CTA's weights are
+        // its first stages', 6.3 and 6.4; twice as many stages are no better).
         prefetch_map(&map_p);
         prefetch_map(&map_q);
         for (int kb = 0; kb < kStages && kb < kb_n; kb++) prefetch_tile(&map_p, (kb0 + kb) * kMmBlock, p0);
