@@ -105,19 +105,20 @@ class BlockwiseLinear(torch.nn.Module):
 
     ``in_features`` and ``out_features`` are multiples of 128; x is bfloat16 or
     float32 with any number of rows and any strides, the residual alike and of
-    x's type.  Dropout runs in training mode; its
-    decisions follow from the layer's ``seed`` and the ``offset`` of the call
-    (in counters of 8 elements).  Neither has to be given: a seed is drawn when
-    a layer with dropout is made, an offset at every call, both from torch's CPU
-    generator, so that masks differ from call to call and layer to layer,
-    repeat under ``torch.manual_seed``, and a checkpointed forward pass draws
-    its own again.  A call that is captured into a CUDA graph has to be given its
-    offset (every replay draws what it was captured with); give steps their own,
-    e.g. ``step * rows * out_features // 8``.  There is no second derivative: one that is
-    asked for raises.  With ``main_grad`` set (FP32, the weight's
-    shape) the weight gradient is added to it and ``weight.grad`` stays unset.
-    ``copies`` takes the result of :meth:`quantize_weight`, made once for the
-    micro-batches of a step, or once for serving.
+    x's type.  With ``main_grad`` set (FP32, the weight's shape) the weight
+    gradient is added to it and ``weight.grad`` stays unset.  ``copies`` takes the
+    result of :meth:`quantize_weight`, made once for the micro-batches of a step,
+    or once for serving.  There is no second derivative: one that is asked for
+    raises.
+
+    Dropout runs in training mode; its decisions follow from the layer's ``seed``
+    and the ``offset`` of the call (in counters of 8 elements).  Neither has to be
+    given: a seed is drawn when a layer with dropout is made, an offset at every
+    call, both from torch's CPU generator, so that masks differ from call to call
+    and layer to layer, repeat under ``torch.manual_seed``, and a checkpointed
+    forward pass draws its own again.  Who gives offsets gives each step its own,
+    e.g. ``step * rows * out_features // 8``.  A call that is captured into a CUDA
+    graph has to be given one (every replay draws what it was captured with).
 
     ``status`` (a one-element int32 tensor on the layer's device) collects what
     the layer's casts and products report: ``Q_ST_NONFINITE`` where x, the
