@@ -459,6 +459,61 @@ q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, doubl
                           uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT, int32_t *status,
                           q_stream_t stream);
 
+/*
+ * The root-mean-square norm ahead of a linear layer, with the residual's
+ * addition.  Per row m:
+ *   h = x + residual, formed in FP32 and rounded to its type (h = x where
+ *   residual is NULL);  rstd = 1 / sqrt(mean(h^2) + eps);  y = (h rstd) w
+ * The norm is that of h as it is kept, so that norm_grad, which is given h and
+ * rstd, works with the numbers of the forward pass.  Sums are FP32, in an
+ * order that K alone decides; y is rounded once.
+ *   x, residual, h, y  [M, K] of dtype `in`;  weight [K] of dtype wt;
+ *   rstd [M] FP32 (written);  eps >= 0, finite.
+ *   h is written where there is a residual, and has to be NULL without one.
+ *   amax  NULL, or one float: max|y| over the tensor as it is stored, what
+ *   q_amax(y) gives and Q_AMAX_GIVEN takes.  *status (may be NULL): Q_ST_NONFINITE
+ *   where that maximum is inf or NaN; without amax nothing is reported.
+ * A row whose squares leave FP32's range has rstd 0, a row of zeros with
+ * eps = 0 rstd inf.  NaN and inf stay in their rows.
+ * h may be x or residual themselves, and y the other one, or x where there is
+ * no residual (in place); other overlap is not allowed.
+ * Shapes: any M >= 0 (M = 0 writes amax = 0), 0 < K < 2^31.  Alignment: 16
+ * bytes (x, residual, weight, h, y), 4 bytes (rstd, amax).
+ */
+q_status norm_add(const void *x, q_dtype in, int64_t M, int64_t K, const void *residual, const void *weight, q_dtype wt, float eps,
+                  void *h, void *y, float *rstd, float *amax, int32_t *status, q_stream_t stream);
+
+/*
+ * The same norm with its result as blockwise copies: q_blockwise with
+ * Q_T1x128 tiles of y = (h rstd) w in FP32, y itself neither rounded to the
+ * input's type nor stored.  h, rstd and their rules are those of norm_add, the
+ * copies, their shapes and alignment and *status those of q_blockwise (K % 128
+ * == 0; with q_colT also M % 128 == 0).  The rowwise copy is made while h is in
+ * registers; a transposed one takes a second read of h.
+ */
+q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const void *residual, const void *weight, q_dtype wt,
+                          float eps, void *h, float *rstd, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
+                          int32_t *status, q_stream_t stream);
+
+/*
+ * The norm's gradient, from h and rstd of its forward pass: with v = h rstd
+ * and g = dy w, per row
+ *   dx = rstd (g - v mean(g v)) + dh     dw = sum over the rows of dy v
+ * dx is the gradient of x and of residual alike; dh (or NULL) is the gradient
+ * of h from where h is used again (the residual stream).  Sums are FP32, in an
+ * order that M and K decide; dx and dw are rounded once.
+ *   dy, h, dh, dx [M, K] of dtype `in`;  weight, dw [K] of dtype wt.
+ *   dw may be NULL.  Otherwise work is scratch of norm_grad_work(M, K, in)
+ *   floats, whose contents before and after do not matter; calls that may run
+ *   at the same time need one each.
+ * dx may be dy, h or dh themselves.  M = 0 sets dw to zero.
+ * 0 < K < 2^31.  Alignment: 16 bytes (dy, h, dh, weight, dx, work), 4 bytes
+ * (rstd, dw).
+ */
+q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void *h, const float *rstd, const void *weight, q_dtype wt,
+                   const void *dh, void *dx, void *dw, float *work, q_stream_t stream);
+int64_t norm_grad_work(int64_t M, int64_t K, q_dtype in);
+
 #ifdef __cplusplus
 }
 #endif

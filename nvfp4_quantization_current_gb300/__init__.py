@@ -69,7 +69,7 @@ STATUS_NAMES = {Q_OK: "Q_OK", Q_ERR_ARG: "Q_ERR_ARG", Q_ERR_SHAPE: "Q_ERR_SHAPE"
 
 # every exported entry point: name -> (restype, argtypes)
 _P, _I64, _I, _U64, _U32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_uint32
-_F64 = ctypes.c_double
+_F64, _F = ctypes.c_double, ctypes.c_float
 SIGNATURES = {
     "q_last_error": (ctypes.c_char_p, []),
     "q_abi_version": (_I, []),
@@ -92,6 +92,10 @@ SIGNATURES = {
     "mm_blockwise": (_I, [_P, _P, _I, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P]),
     "drop_add": (_I, [_P, _I, _I64, _P, _F64, _U64, _U64, _P, _P]),
     "drop_q_blockwise": (_I, [_P, _I, _I64, _I64, _F64, _U64, _U64, _P, _P, _P, _P, _P, _P]),
+    "norm_add": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P]),
+    "norm_q_blockwise": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "norm_grad": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "norm_grad_work": (_I64, [_I64, _I64, _I]),
     "dq_current_scaling": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
     "dq_mxfp8": (_I, [_P, _P, _I64, _I64, _I, _I, _I, _P, _P]),
     "dq_blockwise": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
@@ -750,6 +754,182 @@ def drop_q_blockwise(x: torch.Tensor, p: float, seed: int, offset: int = 0, roww
     return out
 
 
-__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "mm_", "drop_", "alloc_", "Q_"))] + [
+# ---------------------------------------------------------------------------
+# the norm ahead of a linear layer
+# ---------------------------------------------------------------------------
+
+def _call_on(dev, name, *args):
+    """The call with dev current: a launch goes to the current device, whichever one the stream is of."""
+    if dev.index is None or dev.index == torch._C._cuda_getDevice():
+        _call(name, *args)
+    else:
+        with torch.cuda.device(dev):
+            _call(name, *args)
+
+
+class _OnceMore(torch.autograd.Function):
+    """A gradient as it is, whose own derivative raises (`start` begins a graph where g has none)."""
+    @staticmethod
+    def forward(ctx, g, start, name):
+        ctx.name = name
+        return g.view_as(g)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError(f"{ctx.name} has no second derivative")
+
+
+def _once(name, *grads):
+    """Gradients that autograd computed without their graph; under create_graph they raise where one is asked for."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(None if g is None else _OnceMore.apply(g, torch.zeros((), requires_grad=True), name) for g in grads)
+
+
+def _norm_in(name, x, weight, residual):
+    """(dtype, M, K) of x as rows of its last dimension, the operands checked against each other."""
+    dt = _DTYPES.get(x.dtype)
+    if dt is None or not x.is_cuda or x.dim() == 0 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of bfloat16 or float32, of one dimension or more")
+    K = x.shape[-1]
+    if weight.dim() != 1 or weight.shape[0] != K or weight.dtype not in _DTYPES or weight.device != x.device or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of {K} elements on {x.device}")
+    if residual is not None:
+        _alike("residual", residual, x)
+    return dt, x.numel() // K if K else 0, K
+
+
+def _no_gradient(fn, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{fn} records no gradient, but one of its tensors requires one")
+
+
+def _word(name, t, dev):
+    """The address of a one-element FP32 tensor on dev."""
+    if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
+        raise ValueError(f"{name} must be a float32 tensor of one element on {dev}")
+    return t.data_ptr()
+
+
+class _NormAdd(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps, amax, status):
+        y, h, rstd = norm_add(x, weight, eps, residual, amax=amax, status=status)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(rstd)
+        ctx.save_for_backward(h, rstd, weight)
+        return (y, rstd) if residual is None else (y, rstd, h)
+
+    @staticmethod
+    def backward(ctx, dy, _, dh=None):
+        h, rstd, weight = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dy is None:   # the sum alone was used
+            return dh, None, dh if need[2] else None, None, None, None
+        with torch.no_grad():
+            dx, dw = norm_grad(_ready(dy), h, rstd, weight, None if dh is None else _ready(dh), need_dw=need[1])
+        dx, dw = _once("norm_add", dx, dw)
+        return dx, dw, dx if need[2] else None, None, None, None
+
+
+def norm_add(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             amax: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, h_out: Optional[torch.Tensor] = None,
+             status: Optional[torch.Tensor] = None):
+    """``(y, h, rstd)``: the root-mean-square norm ``y = h rstd weight`` of
+    ``h = x + residual`` (rounded to its type; x itself without a residual) over
+    the last dimension, ``rstd = 1 / sqrt(mean(h^2) + eps)`` in FP32, one number
+    per row.
+
+    ``amax`` (a one-element float32 tensor) receives max|y|, for
+    :func:`q_nvfp4` or :func:`q_current_scaling` to be given; ``status`` then
+    reports a maximum that is not finite.  ``out`` (for y) and ``h_out`` may be
+    x and the residual themselves.  Autograd takes :func:`norm_grad` as the
+    backward pass; with ``out`` or ``h_out`` no gradient is recorded."""
+    dt, M, K = _norm_in("x", x, weight, residual)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad):
+        if out is not None or h_out is not None:
+            raise RuntimeError("norm_add with out= or h_out= records no gradient, but one of its tensors requires one")
+        r = _NormAdd.apply(x, weight, residual, eps, amax, status)
+        return r[0], x if residual is None else r[2], r[1]
+    dev = x.device
+    if residual is None and h_out is not None:
+        raise ValueError("h_out without a residual (the sum would be x)")
+    for name, t in (("out", out), ("h_out", h_out)):
+        if t is not None:
+            _no_gradient("norm_add", t)
+            _alike(name, t, x)
+            _written(t)
+    y = torch.empty_like(x) if out is None else out
+    h = None if residual is None else torch.empty_like(x) if h_out is None else h_out
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    if amax is not None:
+        _written(amax)
+    _call_on(dev, "norm_add", x.data_ptr(), dt, M, K, _ptr(residual), weight.data_ptr(), _DTYPES[weight.dtype], float(eps), _ptr(h),
+             y.data_ptr(), rstd.data_ptr(), None if amax is None else _word("amax", amax, dev),
+             None if status is None else _status(status, dev), _stream(dev))
+    return y, x if h is None else h, rstd
+
+
+def norm_q_blockwise(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None, rowwise=True,
+                     colwise=False, out: Optional[BlockwiseTensor] = None, h_out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None):
+    """``(copies, h, rstd)``: the 1x128 blockwise copies of :func:`norm_add`'s
+    result in FP32, which is not stored, for a 2-D x.  ``out`` (1x128 copies of an x
+    of this shape) has the directions that it holds written; ``h_out`` may be x or
+    the residual.  It records no gradient (``linear.py`` has the backward pass)."""
+    dt, M, K = _norm_in("x", x, weight, residual)
+    _no_gradient("norm_q_blockwise", x, weight, residual, h_out)
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    dev = x.device
+    if out is None:
+        out = alloc_blockwise(M, K, dev, "1x128", rowwise, colwise)
+    else:
+        _copies("out", out, M, K, dev)
+        if colwise and out.q_colT is None:
+            raise ValueError("out has no transposed copy")
+        _written_copies(out)
+    if h_out is not None:
+        if residual is None:
+            raise ValueError("h_out without a residual (the sum would be x)")
+        _alike("h_out", h_out, x)
+        _written(h_out)
+    h = None if residual is None else torch.empty_like(x) if h_out is None else h_out
+    rstd = torch.empty((M,), dtype=torch.float32, device=dev)
+    _call_on(dev, "norm_q_blockwise", x.data_ptr(), dt, M, K, _ptr(residual), weight.data_ptr(), _DTYPES[weight.dtype], float(eps),
+             _ptr(h), rstd.data_ptr(), _ptr(out.q_row), _ptr(out.s_row), _ptr(out.q_colT), _ptr(out.s_colT),
+             None if status is None else _status(status, dev), _stream(dev))
+    return out, x if h is None else h, rstd
+
+
+def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dh: Optional[torch.Tensor] = None,
+              need_dw=True, out: Optional[torch.Tensor] = None):
+    """``(dx, dw)`` of :func:`norm_add` from its ``h`` and ``rstd``: the gradient
+    of x (and of the residual alike), with ``dh``, the gradient of h from where h
+    is used again, added to it, and the weight's gradient in the weight's type
+    (None without ``need_dw``).  ``out`` (for dx) may be dy, h or dh.  It records no
+    gradient itself."""
+    dt, M, K = _norm_in("dy", dy, weight, None)
+    _no_gradient("norm_grad", dy, h, rstd, weight, dh, out)
+    dev = dy.device
+    _alike("h", h, dy)
+    if not _is(rstd, torch.float32, dy.shape[:-1], dev):
+        raise ValueError(f"rstd must be a contiguous float32 tensor of shape {tuple(dy.shape[:-1])} on {dev}")
+    if dh is not None:
+        _alike("dh", dh, dy)
+    if out is None:
+        dx = torch.empty_like(dy)
+    else:
+        _alike("out", out, dy)
+        _written(out)
+        dx = out
+    dw = torch.empty_like(weight) if need_dw else None
+    work = _f32((lib().norm_grad_work(M, K, dt),), dev) if need_dw else None
+    _call_on(dev, "norm_grad", dy.data_ptr(), dt, M, K, h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _DTYPES[weight.dtype], _ptr(dh),
+             dx.data_ptr(), _ptr(dw), _ptr(work), _stream(dev))
+    return dx, dw
+
+
+__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "mm_", "drop_", "norm_", "alloc_", "Q_"))] + [
     "CurrentScalingTensor", "DelayedScaling", "MXFP8Tensor", "BlockwiseTensor", "BlockwiseMXTensor", "NVFP4Tensor",
     "QuantError", "lib", "SIGNATURES"]

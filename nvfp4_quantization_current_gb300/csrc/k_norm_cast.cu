@@ -1,0 +1,106 @@
+// The transposed blockwise copy of the norm's result: 128x1 blocks along M of
+// y = (h s) w in FP32 (k_norm.cu), y itself never stored.
+//
+// On the tile engine: thread (warp w, lane l) holds rows 8w..8w+7 x one 16-byte
+// column chunk of h and multiplies by the rows' factors and the columns'
+// weights as it goes.  Per-warp column maxima meet in shared memory, and the
+// codes are transposed in the consumed stage and written as full 128-byte rows
+// (as in k_blockwise).
+#include "q_engine.cuh"
+#include "q_internal.h"
+
+namespace qk {
+
+namespace {
+
+template <int DT>
+__global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K,
+                                                              const float *__restrict__ rstd, const void *__restrict__ weight,
+                                                              bool wf32, uint8_t *__restrict__ q_colT,
+                                                              float *__restrict__ s_colT, int32_t *status)
+{
+    constexpr int VEC = In<DT>::VEC, TC = 32 * VEC, CW = VEC / 4, TPC = kEngThreads / TC;   // threads per column
+    __shared__ __align__(16) uint32_t part[kEngWarps][TC];   // per-warp column maxima
+    __shared__ __align__(16) float calpha[TC];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int64_t tiles_m = M / kTileRowsE, tiles_k = (K + TC - 1) / TC;
+
+    griddep_wait();   // the rows' factors and sums are the kernel's ahead
+    run_tiles(&tmap, tiles_m, tiles_k, TC, false, status, [&](uint8_t *st, int64_t tm, int64_t tk) {
+        const int64_t mb = tm * kTileRowsE, kb = tk * TC, k = kb + lane * VEC;
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = lds16(st + (8 * warp + j) * kRowBytes + lane * 16);
+        float s[8], w[VEC];
+#pragma unroll
+        for (int j = 0; j < 8; j++) s[j] = __ldg(rstd + mb + 8 * warp + j);
+#pragma unroll
+        for (int c = 0; c < VEC; c++)
+            w[c] = k >= K ? 0.0f : wf32 ? __ldg(static_cast<const float *>(weight) + k + c)
+                                        : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(weight) + k + c) << 16);
+        float top[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; c++) top[c] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+#pragma unroll
+            for (int c = 0; c < VEC; c++) top[c] = fmax_abs(top[c], elem<DT>(v[j], c) * s[j] * w[c]);
+#pragma unroll
+        for (int c = 0; c < VEC; c++) part[warp][lane * VEC + c] = __float_as_uint(top[c]) & 0x7FFFFFFFu;
+        __syncthreads();
+        {
+            const int col = t / TPC, sub = t % TPC;
+            uint32_t b = 0;
+#pragma unroll
+            for (int i = sub; i < kEngWarps; i += TPC) b = max(b, part[i][col]);
+            b = group_max<TPC>(b);
+            if (sub == 0) {
+                const float alpha = alpha_from_amax(448.0f, __uint_as_float(b));
+                calpha[col] = alpha;
+                if (kb + col < K) {
+                    s_colT[(kb + col) * (M / 128) + tm] = __fdiv_rn(1.0f, alpha);
+                    flag_nonfinite(status, b);
+                }
+            }
+        }
+        __syncthreads();
+        uint32_t code[8][CW];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float f[VEC];
+#pragma unroll
+            for (int c = 0; c < VEC; c++) f[c] = elem<DT>(v[j], c) * s[j] * w[c] * calpha[lane * VEC + c];
+#pragma unroll
+            for (int q = 0; q < CW; q++) code[j][q] = cvt_fp8x4<E4M3>(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        }
+        park_fp8T<VEC>(st, code, warp, lane);
+        __syncthreads();
+        copy_out_fp8T<VEC>(st, q_colT, M, K, mb, kb);
+    });
+}
+
+template <int DT>
+cudaError_t cols_t(const void *h, int64_t M, int64_t K, const float *rstd, const void *weight, bool wf32, uint8_t *q_colT,
+                   float *s_colT, int32_t *status, cudaStream_t st)
+{
+    constexpr int TC = 32 * In<DT>::VEC;
+    alignas(64) CUtensorMap map;
+    cudaError_t e = make_tile_map(&map, h, DT, M, K);
+    if (e == cudaSuccess) e = engine_smem_ready<k_norm_cols<DT>>();
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (M / kTileRowsE) * ((K + TC - 1) / TC);
+    const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
+    return launch_k(true, k_norm_cols<DT>, dim3(grid), dim3(kEngThreads), kEngSmem, st, map, M, K, rstd, weight, wf32, q_colT,
+                    s_colT, status);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_cast_cols(const void *h, int dt, int64_t M, int64_t K, const float *rstd, const void *weight, bool wf32,
+                                  uint8_t *q_colT, float *s_colT, int32_t *status, cudaStream_t st)
+{
+    return dt == BF16 ? cols_t<BF16>(h, M, K, rstd, weight, wf32, q_colT, s_colT, status, st)
+                      : cols_t<F32>(h, M, K, rstd, weight, wf32, q_colT, s_colT, status, st);
+}
+
+}  // namespace qk

@@ -475,6 +475,104 @@ q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, doubl
     return Q_OK;
 }
 
+// What the norm and its gradient ask of their sizes, the weight and its type.
+static q_status check_norm(const char *fn, int64_t M, int64_t K, const void *weight, q_dtype wt)
+{
+    TRY(check_dims(fn, M, K));
+    if (K == 0 || K >= (int64_t)1 << 31) return fail(Q_ERR_SHAPE, "%s: K = %lld is not in [1, 2^31)", fn, (long long)K);
+    if (M >= (int64_t)1 << 31) return fail(Q_ERR_SHAPE, "%s: M = %lld is not below 2^31", fn, (long long)M);
+    if (wt != Q_BF16 && wt != Q_F32) return fail(Q_ERR_DTYPE, "%s: weight dtype %d is not Q_BF16 or Q_F32", fn, (int)wt);
+    if (M > 0) TRY(need(fn, "weight", weight, 16));
+    return Q_OK;
+}
+
+static q_status check_norm_sum(const char *fn, int64_t M, const void *residual, const void *h, float eps, const float *rstd)
+{
+    if (!(eps >= 0.0f) || std::isinf(eps)) return fail(Q_ERR_ARG, "%s: eps = %g is not a finite number >= 0", fn, (double)eps);
+    if (residual == nullptr && h != nullptr) return fail(Q_ERR_ARG, "%s: h without a residual (it would be x)", fn);
+    if (M == 0) return Q_OK;
+    if (residual != nullptr) {
+        TRY(need(fn, "residual", residual, 16));
+        TRY(need(fn, "h", h, 16));
+    }
+    return need(fn, "rstd", rstd, 4);
+}
+
+q_status norm_add(const void *x, q_dtype in, int64_t M, int64_t K, const void *residual, const void *weight, q_dtype wt, float eps,
+                  void *h, void *y, float *rstd, float *amax, int32_t *status, q_stream_t stream)
+{
+    const char *fn = "norm_add";
+    TRY(check_norm(fn, M, K, weight, wt));
+    TRY(check_in(fn, x, in, M * K));
+    TRY(check_norm_sum(fn, M, residual, h, eps, rstd));
+    if (amax != nullptr) TRY(need(fn, "amax", amax, 4));
+    if (M == 0) {
+        if (amax != nullptr) LAUNCH(fn, qk::launch_zero_word(amax, S(stream)));
+        return Q_OK;
+    }
+    TRY(need(fn, "y", y, 16));
+    if (y == h) return fail(Q_ERR_ARG, "%s: y and h are the same buffer", fn);
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, h, y, rstd, amax, nullptr, nullptr, status, M, K, 0};
+    LAUNCH(fn, qk::launch_norm_add(a, (int)in, S(stream)));
+    return Q_OK;
+}
+
+q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const void *residual, const void *weight, q_dtype wt,
+                          float eps, void *h, float *rstd, uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT,
+                          int32_t *status, q_stream_t stream)
+{
+    const char *fn = "norm_q_blockwise";
+    TRY(check_norm(fn, M, K, weight, wt));
+    TRY(check_in(fn, x, in, M * K));
+    TRY(check_norm_sum(fn, M, residual, h, eps, rstd));
+    TRY(multiple(fn, "K", K, 128));
+    if (M == 0) return Q_OK;
+    if (q_row == nullptr && q_colT == nullptr) return fail(Q_ERR_ARG, "%s: neither direction requested", fn);
+    if (q_row != nullptr) {
+        TRY(need(fn, "q_row", q_row, 16));
+        TRY(need(fn, "s_row", s_row, 4));
+    }
+    if (q_colT != nullptr) {
+        TRY(need(fn, "q_colT", q_colT, 16));
+        TRY(need(fn, "s_colT", s_colT, 4));
+        TRY(multiple(fn, "M (with q_colT)", M, 128));
+    }
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, h, nullptr, rstd, nullptr, q_row, s_row, status, M, K, 0};
+    LAUNCH(fn, qk::launch_norm_cast_rows(a, (int)in, S(stream)));
+    if (q_colT != nullptr)
+        LAUNCH(fn, qk::launch_norm_cast_cols(residual != nullptr ? h : x, (int)in, M, K, rstd, weight, wt == Q_F32, q_colT, s_colT,
+                                             status, S(stream)));
+    return Q_OK;
+}
+
+int64_t norm_grad_work(int64_t M, int64_t K, q_dtype in)
+{
+    if (M <= 0 || K <= 0 || (in != Q_BF16 && in != Q_F32)) return 0;
+    return qk::norm_grad_rows(M, K, (int)in) * K;
+}
+
+q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void *h, const float *rstd, const void *weight, q_dtype wt,
+                   const void *dh, void *dx, void *dw, float *work, q_stream_t stream)
+{
+    const char *fn = "norm_grad";
+    TRY(check_norm(fn, M, K, weight, wt));
+    if (in != Q_BF16 && in != Q_F32) return fail(Q_ERR_DTYPE, "%s: input dtype %d is not Q_BF16 or Q_F32", fn, (int)in);
+    if (dw != nullptr) TRY(need(fn, "dw", dw, 4));
+    if (M == 0) {
+        if (dw != nullptr) LAUNCH(fn, cudaMemsetAsync(dw, 0, (size_t)K * (wt == Q_BF16 ? 2 : 4), S(stream)));
+        return Q_OK;
+    }
+    TRY(need(fn, "dy", dy, 16));
+    TRY(need(fn, "h", h, 16));
+    TRY(need(fn, "rstd", rstd, 4));
+    if (dh != nullptr) TRY(need(fn, "dh", dh, 16));
+    TRY(need(fn, "dx", dx, 16));
+    if (dw != nullptr) TRY(need(fn, "work", work, 16));
+    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, M, K, 0};
+    LAUNCH(fn, qk::launch_norm_grad(a, (int)in, dw, S(stream)));
+    return Q_OK;
+}
+
 q_status q_selftest_inject_launch_error(int n)
 {
     if (n < 0) return fail(Q_ERR_ARG, "q_selftest_inject_launch_error: n = %d is negative", n);

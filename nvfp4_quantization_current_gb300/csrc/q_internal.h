@@ -111,6 +111,40 @@ cudaError_t launch_drop_q_rows(const void *x, int dt, int64_t n, uint32_t thresh
 cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residual, uint32_t threshold, float c,
                             uint64_t seed, uint64_t offset, void *y, cudaStream_t st);
 
+// RMS norm: h = x + residual (h = x without one), rstd = 1 / sqrt(mean(h^2) + eps),
+// and y = h rstd weight, stored or as the rowwise 1x128 copy (M, K > 0)
+struct NormArgs {
+    const void *x, *residual, *weight;
+    bool wf32;
+    float eps;
+    void *h, *y;
+    float *rstd, *amax;
+    uint8_t *q_row;
+    float *s_row;
+    int32_t *status;
+    int64_t M, K;
+    int gshift;   // set by the launcher
+};
+cudaError_t launch_norm_add(const NormArgs &a, int dt, cudaStream_t st);
+// h and rstd, and the rowwise copy where q_row is given
+cudaError_t launch_norm_cast_rows(const NormArgs &a, int dt, cudaStream_t st);
+// the transposed copy of h rstd weight
+cudaError_t launch_norm_cast_cols(const void *h, int dt, int64_t M, int64_t K, const float *rstd, const void *weight, bool wf32,
+                                  uint8_t *q_colT, float *s_colT, int32_t *status, cudaStream_t st);
+
+// the norm's gradient: dx, and dw (may be null) through the rows of `work`
+struct NormGradArgs {
+    const void *dy, *h, *dh, *weight;
+    bool wf32;
+    const float *rstd;
+    void *dx;
+    float *work;
+    int64_t M, K;
+    int gshift;   // set by the launcher
+};
+int64_t norm_grad_rows(int64_t M, int64_t K, int dt);   // rows of K floats in `work`
+cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st);
+
 // block-scaled FP8 product: c [M, N] (+)= a [M, K] b [N, K]^T with the tiles'
 // scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0; give_up: a wait of
 // every cluster counts as run out
