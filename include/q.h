@@ -418,8 +418,8 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
 
 /*
  * Diagnostic of that failure path (a library check): in the calling thread's
- * next mm_blockwise that launches a kernel, every cluster takes a wait for run
- * out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it.
+ * next mm_blockwise or matmul_nvfp4 that launches a kernel, every cluster takes a
+ * wait for run out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it.
  */
 q_status selftest_mm_give_up(int on);
 
@@ -458,6 +458,40 @@ q_status drop_add(const void *x, q_dtype in, int64_t n, const void *residual, do
 q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, double p, uint64_t seed, uint64_t offset,
                           uint8_t *q_row, float *s_row, uint8_t *q_colT, float *s_colT, int32_t *status,
                           q_stream_t stream);
+
+/*
+ * NVFP4 matrix product: the consumer of the copies of q_nvfp4 and
+ * q_nvfp4_recipe ([LP] 2.4: the forward, input-gradient and weight-gradient
+ * products in four bits).
+ *   C[m, n] = (C[m, n] +) s_a s_b * sum over the 16-element blocks kb of K of
+ *             sb_a[m, kb] * sb_b[n, kb] * sum_{k in kb} a[m, k] * b[n, k]
+ *   a [M, K/2], b [N, K/2]  packed E2M1 codes, row-major (both operands have
+ *   their reduction along the rows):
+ *     forward          Y  = X W^T:   a = X.q_row,   b = W.q_row
+ *     input gradient   dX = dY W:    a = dY.q_row,  b = W.q_colT
+ *     weight gradient  dW = dY^T X:  a = dY.q_colT, b = X.q_colT (both behind
+ *     the random Hadamard transform with one sign mask, or neither)
+ *   sb_a: blk_a Q_B1x16: [M, K/16]; Q_B16x16: [M/16, K/16]; sb_b alike with N:
+ *   E4M3 codes >= 0, as the quantizers write them (the code 0x7F is NaN).
+ *   s_a, s_b: one float each, the tensors' scales (s_global).
+ *   c [M, N] in `out` (Q_BF16 rounded to nearest even once, or Q_F32);
+ *   accumulate != 0 adds to what c holds, 0 overwrites it without reading.
+ * Products of codes and block scales are exact; sums are the tensor core's, in
+ * FP32; s_a and s_b multiply the sum one after the other, in FP32.  The result
+ * does not depend on timing, and a row's result does not depend on the values
+ * of other rows.  How K is split goes by M, N and K, so the same row may round
+ * otherwise in a call of another M.
+ * Shapes: K % 32 == 0, M % 16 == 0 (N % 16 == 0) for a 16x16 operand; M, N, K
+ * < 2^31.  M == 0 or N == 0 does nothing; K == 0 is a sum over nothing: c is
+ * set to zero, or left as it is when accumulating.
+ * A wait inside the kernel that runs out (2 s) ends the call: Q_ST_TIMEOUT in
+ * *status, and the part of C that the wait's sums would have gone to is not
+ * written.
+ * Alignment: a, b, c 16 bytes, s_a, s_b 4 bytes, none for sb_a and sb_b.
+ */
+q_status matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, q_nvblk blk_a, const uint8_t *b, const uint8_t *sb_b,
+                      const float *s_b, q_nvblk blk_b, int64_t M, int64_t N, int64_t K, void *c, q_dtype out, int accumulate,
+                      int32_t *status, q_stream_t stream);
 
 /*
  * The root-mean-square norm ahead of a linear layer, with the residual's

@@ -92,6 +92,7 @@ SIGNATURES = {
     "mm_blockwise": (_I, [_P, _P, _I, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P]),
     "drop_add": (_I, [_P, _I, _I64, _P, _F64, _U64, _U64, _P, _P]),
     "drop_q_blockwise": (_I, [_P, _I, _I64, _I64, _F64, _U64, _U64, _P, _P, _P, _P, _P, _P]),
+    "matmul_nvfp4": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P]),
     "norm_add": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P]),
     "norm_q_blockwise": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P]),
     "norm_grad": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I, _P, _P, _P, _P, _P]),
@@ -930,6 +931,63 @@ def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: tor
     return dx, dw
 
 
-__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "mm_", "drop_", "norm_", "alloc_", "Q_"))] + [
+# ---------------------------------------------------------------------------
+# the product of NVFP4 copies
+# ---------------------------------------------------------------------------
+
+_BLK = {"1x16": Q_B1x16, "16x16": Q_B16x16, Q_B1x16: Q_B1x16, Q_B16x16: Q_B16x16}
+
+
+def _operand4(name, q, sb, s, blk, dev):
+    """(rows, K) of an NVFP4 operand on dev, its codes and scales checked against each other."""
+    if not q.is_cuda or q.device != dev or sb.device != dev or s.device != dev:
+        raise ValueError(f"{name}: codes and scales must be CUDA tensors on one device, that of a (the library has no CPU path)")
+    if q.dtype != torch.uint8 or sb.dtype != torch.uint8 or s.dtype != torch.float32:
+        raise ValueError(f"{name}: codes and block scales must be uint8 and the tensor's scale float32, got {q.dtype}, {sb.dtype} and {s.dtype}")
+    if q.dim() != 2 or not (q.is_contiguous() and sb.is_contiguous()):
+        raise ValueError(f"{name}: codes must be a contiguous 2-D tensor and block scales contiguous")
+    R, K = q.shape[0], q.shape[1] * 2
+    want = (R, K // 16) if blk == Q_B1x16 else (R // 16, K // 16)
+    if sb.shape != want or s.numel() != 1:
+        raise ValueError(f"{name}: block scales are {tuple(sb.shape)} and the tensor's {tuple(s.shape)}, codes of {R} x {K} need {want} and one")
+    return R, K
+
+
+def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, sb_b: torch.Tensor, s_b: torch.Tensor,
+                 blk_a="1x16", blk_b="16x16", dtype=torch.bfloat16, out: Optional[torch.Tensor] = None, accumulate=False,
+                 status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C [M, N] = A B^T of NVFP4 operands: packed codes ``a`` [M, K/2] and ``b``
+    [N, K/2], the E4M3 scales of their 1x16 or 16x16 blocks and the tensors' scales,
+    as :func:`q_nvfp4` and :func:`q_nvfp4_recipe` make them (K a multiple of 32).
+
+    forward ``(x.q_row, x.sb_row, x.s_global, w.q_row, w.sb_row, w.s_global)``,
+    input gradient ``dy`` rows with ``w.q_colT, w.sb_colT``, weight gradient
+    ``(dy.q_colT, dy.sb_colT, dy.s_global, x.q_colT, x.sb_colT, x.s_global,
+    blk_b="1x16")``.  ``dtype`` (that of ``out`` when it is given) is bfloat16 or
+    float32; ``accumulate`` adds to ``out``.  One token upward; sums in FP32, results
+    independent of timing.  It records no gradient: scales or an ``out`` that require
+    one are refused (``linear.py`` has the backward pass)."""
+    ba, bb = _BLK[blk_a], _BLK[blk_b]
+    dev = a.device
+    M, K = _operand4("a", a, sb_a, s_a, ba, dev)
+    N, Kb = _operand4("b", b, sb_b, s_b, bb, dev)
+    if K != Kb:
+        raise ValueError(f"a has K = {K}, b has K = {Kb}")
+    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+        raise RuntimeError("matmul_nvfp4 records no gradient, but its scales or out require one")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    elif out.shape != (M, N) or out.dtype not in _DTYPES or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {M} x {N} tensor of bfloat16 or float32 on {dev}")
+    else:
+        _written(out)
+    _call_on(dev, "matmul_nvfp4", a.data_ptr(), sb_a.data_ptr(), s_a.data_ptr(), ba, b.data_ptr(), sb_b.data_ptr(), s_b.data_ptr(), bb, M, N,
+             K, out.data_ptr(), _DTYPES[out.dtype], int(accumulate), None if status is None else _status(status, dev), _stream(dev))
+    return out
+
+
+__all__ = [n for n in dir() if n.startswith(("q_", "dq_", "mm_", "drop_", "norm_", "matmul_", "alloc_", "Q_"))] + [
     "CurrentScalingTensor", "DelayedScaling", "MXFP8Tensor", "BlockwiseTensor", "BlockwiseMXTensor", "NVFP4Tensor",
     "QuantError", "lib", "SIGNATURES"]

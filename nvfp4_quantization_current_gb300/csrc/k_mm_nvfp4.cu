@@ -1,0 +1,88 @@
+// NVFP4 matrix product: the consumer of the copies of q_nvfp4.
+//
+//   C[m, n] (+)= s_a s_b sum_kb sb_a[m, kb] sb_b[n, kb] P_kb[m, n],
+//   P_kb[m, n] = sum of a[m, k] b[n, k] over the 16 elements k of block kb
+//
+// with a [M, K] and b [N, K] E2M1 codes, two per byte, K contiguous, an E4M3
+// scale per 1x16 or 16x16 block and one FP32 scale per tensor.  The tensor core
+// takes the codes and the block scales (tcgen05 kind mxf4nvf4, a scale per 16
+// elements) and adds in FP32; the tensors' scales are multiplied in at the end.
+#include "k_mm4_split.cuh"
+#include "q_internal.h"
+
+namespace qk {
+
+namespace {
+
+template <int OUT, int BN> cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, int split, cudaStream_t st)
+{
+    alignas(64) CUtensorMap map_p, map_q;
+    cudaError_t e = make_operand_map(&map_p, p, a.store.rows_p, K / 2, 128);
+    if (e == cudaSuccess) e = make_operand_map(&map_q, q, a.store.rows_q, K / 2, BN);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_split<OUT, BN>>(sizeof(Split4Smem<BN>), true);
+    if (e != cudaSuccess) return e;
+    const int64_t ty = (a.store.rows_p + 127) / 128, tz = (a.store.rows_q + BN - 1) / BN;
+    if (ty > 65535 || tz > 65535) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split, (unsigned)ty, (unsigned)tz);
+    cfg.blockDim = dim3(Split4Smem<BN>::kThreads);
+    cfg.dynamicSmemBytes = sizeof(Split4Smem<BN>);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // it waits before its first read
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_mm4_split<OUT, BN>, map_p, map_q, a);
+}
+
+Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K)
+{
+    const int64_t pitch = K / 16;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(at) | (uintptr_t)pitch;
+    return {at, pitch, (int)rows, blk ? 4 : 0, both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1};
+}
+
+template <int OUT>
+cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t K, cudaStream_t st)
+{
+    const int64_t M = g.store.rows_p, N = g.store.rows_q;
+    Mm4Args w = g;   // the weights on the lanes
+    w.p = g.q;
+    w.q = g.p;
+    w.s_p = g.s_q;
+    w.s_q = g.s_p;
+    w.store.rows_p = N;
+    w.store.rows_q = M;
+    const int64_t kb = g.store.kblocks;
+    int split = 1;
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 192;
+    while (split < kSplitMost && 2 * split <= kb && ((N + 127) / 128) * ((M + bn - 1) / bn) * split * 2 <= 144) split *= 2;
+    switch (bn) {
+    case 16: return mm4_split<OUT, 16>(b, a, w, K, split, st);
+    case 32: return mm4_split<OUT, 32>(b, a, w, K, split, st);
+    case 64: return mm4_split<OUT, 64>(b, a, w, K, split, st);
+    case 128: return mm4_split<OUT, 128>(b, a, w, K, split, st);
+    default: return mm4_split<OUT, 192>(b, a, w, K, split, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, int blk_a, const uint8_t *b,
+                                const uint8_t *sb_b, const float *s_b, int blk_b, int64_t M, int64_t N, int64_t K, void *c, int out,
+                                bool accumulate, int32_t *status, bool give_up, cudaStream_t st)
+{
+    Mm4Args g = {};
+    g.store = {nullptr, nullptr, M, N, (K + kMm4Block - 1) / kMm4Block, 0, 0, c, N, status, accumulate, kStoreDirect, give_up};
+    g.p = scales_of(sb_a, blk_a, M, K);
+    g.q = scales_of(sb_b, blk_b, N, K);
+    g.s_p = s_a;
+    g.s_q = s_b;
+    return out == BF16 ? mm4_t<BF16>(a, b, g, K, st) : mm4_t<F32>(a, b, g, K, st);
+}
+
+}  // namespace qk

@@ -475,6 +475,39 @@ q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, doubl
     return Q_OK;
 }
 
+q_status matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, q_nvblk blk_a, const uint8_t *b, const uint8_t *sb_b,
+                      const float *s_b, q_nvblk blk_b, int64_t M, int64_t N, int64_t K, void *c, q_dtype out, int accumulate,
+                      int32_t *status, q_stream_t stream)
+{
+    const char *fn = "matmul_nvfp4";
+    constexpr int64_t kMost = (int64_t)1 << 31;
+    if (M < 0 || N < 0 || K < 0 || M >= kMost || N >= kMost || K >= kMost)
+        return fail(Q_ERR_SHAPE, "%s: shape (%lld, %lld, %lld) is negative or not below 2^31", fn, (long long)M, (long long)N, (long long)K);
+    for (q_nvblk t : {blk_a, blk_b})
+        if (t != Q_B1x16 && t != Q_B16x16) return fail(Q_ERR_ARG, "%s: blk %d is not Q_B1x16 or Q_B16x16", fn, (int)t);
+    TRY(check_out(fn, out));
+    TRY(multiple(fn, "K", K, 32));
+    if (blk_a == Q_B16x16) TRY(multiple(fn, "M (16x16 blocks of a)", M, 16));
+    if (blk_b == Q_B16x16) TRY(multiple(fn, "N (16x16 blocks of b)", N, 16));
+    if (M == 0 || N == 0) return Q_OK;
+    TRY(need(fn, "c", c, 16));
+    if (K == 0) {   // a sum over nothing
+        if (!accumulate) LAUNCH(fn, cudaMemsetAsync(c, 0, (size_t)M * (size_t)N * (out == Q_BF16 ? 2 : 4), S(stream)));
+        return Q_OK;
+    }
+    TRY(need(fn, "a", a, 16));
+    TRY(need(fn, "sb_a", sb_a, 1));
+    TRY(need(fn, "s_a", s_a, 4));
+    TRY(need(fn, "b", b, 16));
+    TRY(need(fn, "sb_b", sb_b, 1));
+    TRY(need(fn, "s_b", s_b, 4));
+    const bool give_up = g_inject_mm_give_up;
+    g_inject_mm_give_up = false;
+    LAUNCH(fn, qk::launch_matmul_nvfp4(a, sb_a, s_a, (int)blk_a, b, sb_b, s_b, (int)blk_b, M, N, K, c, (int)out, accumulate != 0,
+                                       status, give_up, S(stream)));
+    return Q_OK;
+}
+
 // What the norm and its gradient ask of their sizes, the weight and its type.
 static q_status check_norm(const char *fn, int64_t M, int64_t K, const void *weight, q_dtype wt)
 {

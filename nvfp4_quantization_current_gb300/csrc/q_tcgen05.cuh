@@ -75,6 +75,55 @@ QD void mma_commit(uint64_t *bar)
 }
 
 // ---------------------------------------------------------------------------
+// block-scaled FP4
+// ---------------------------------------------------------------------------
+
+// Instruction descriptor: E2M1 x E2M1 -> FP32 with unsigned E4M3 scales, both
+// operands K-major, M x N, 64 elements of K.
+__host__ __device__ constexpr uint32_t idesc_e2m1(int m, int n)
+{
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Scales in tensor memory: the four scales of a row's 64 elements are one
+// 32-bit word, row r's in lane r % 32 (of each of the four quarters) and column
+// r / 32 from the address on.  This descriptor is of a copy's source, 32 lanes x
+// 16 bytes (four columns) in a row: lane l's words at 16 l, so that the 8-lane
+// groups are 128 bytes apart, no swizzle.
+QD uint64_t smem_desc_scales(const void *p)
+{
+    return (uint64_t)((smem_u32(p) >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+}
+// 512 bytes of scales to tensor memory, to all four quarters.  MMAs that the
+// same thread issues afterwards read them, those before have read what was there.
+QD void scales_to_tmem(uint32_t d, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+}
+// The same in both CTAs of a pair, each from its own shared memory at this offset.
+QD void scales_to_tmem_pair(uint32_t d, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+}
+
+// D (+)= A B^T over 64 elements of K, each 16 of a row times their scale; add = 0
+// overwrites D.  sa, sb: the scales' columns.  One thread.
+QD void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add) : "memory");
+}
+QD void mma_f4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %6, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------
 
