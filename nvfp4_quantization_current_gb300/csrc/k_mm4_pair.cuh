@@ -1,0 +1,280 @@
+// The NVFP4 product for results of many tiles.
+//
+// A pair of CTAs (a cluster of two) owns a 256 x 256 tile of C and walks the
+// tiles persistently; one MMA spans both, each CTA holding its own 128 rows of P
+// and half of Q's 256 (as in k_mm_pair.cuh).  The tensor core applies the block
+// scales, so a tile's whole sum is formed in tensor memory: 256 columns, and the
+// scales of a stage take 48 of the 512.  Two tiles' columns overlap by 48, [0, 256)
+// and [208, 464): the next tile's MMAs begin once the epilogue has read what they
+// share, and run while the rest is read, scaled and stored.
+//
+// Warp 0 of each CTA loads its operand tiles, all of whose bytes count on the
+// leader's barriers; the leader's warp 1 issues the copies of scales to tensor
+// memory and the MMAs.  Warps 2 to 7 fetch scales: two each for P's 128 rows and
+// the halves of Q's 256 (every CTA needs all of Q's), two blocks at a time in turn,
+// each row's 16 bytes of a block by one lane, and put them into the stage's place.
+// The eight warps 8-15 read 32 rows x 128 columns each when a tile is done.
+#pragma once
+
+#include "q_internal.h"
+#include "q_mm4.cuh"
+
+namespace qk {
+
+constexpr int kPair4EpiWarps = 8, kPair4ScaleWarps = 6;
+constexpr int kPair4Threads = 32 * (2 + kPair4ScaleWarps + kPair4EpiWarps);
+constexpr int kPair4Stages = 4;
+constexpr int kPair4OperandBytes = 2 * 128 * 128;
+constexpr int kPair4Group = 8;              // tile rows per group of the tile order
+constexpr int kPair4Second = 208;           // first column of the second buffer; the scales' columns begin at 464
+constexpr int kPair4Scales = kPair4Second + 256;
+// Registers per thread of the epilogue's and the other warps; their sum is what
+// the kernel is launched with.
+constexpr int kPair4EpiRegs = 184, kPair4Regs = 72;
+
+struct Pair4Smem {
+    uint8_t stage[kPair4Stages][kPair4OperandBytes];
+    uint8_t staging[kPair4EpiWarps][2 * 4096];
+    uint8_t scales[kPair4Stages][3 * kScaleAtom];   // P's rows, and Q's in halves
+    uint64_t full[kPair4Stages], sc_full[kPair4Stages], empty[kPair4Stages], acc_full[2], acc_free, drained;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Pair4Smem) <= 232448, "shared memory of a CTA");
+
+// Tile t of the walk, in units of 256 x 256: groups of kPair4Group tile rows,
+// each walked column by column, so that the tiles in flight share their
+// operands in L2.
+QD void pair4_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
+{
+    const int per_group = kPair4Group * tiles_q;
+    const int gp = t / per_group * kPair4Group, r = t % per_group;
+    const int height = tiles_p - gp < kPair4Group ? tiles_p - gp : kPair4Group;
+    p = gp + r % height;
+    q = r / height;
+}
+
+// Arrival on a barrier of the cluster that hands over shared memory written before it.
+QD void mbar_arrive_release(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// The scales of 128 rows for all tiles of a CTA's walk (one warp of two: every other two blocks).
+QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, bool of_p, int atom, int turn, int first, int pairs, int tiles_p, int tiles_q,
+                    int rank, int lane, volatile int *stop)
+{
+    const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q;
+    const uint32_t bar = cluster_addr(smem_u32(&sm.sc_full[0]), 0);
+    uint32_t n = 0;   // blocks of the walk before this tile
+    for (int t = first; t < tiles; t += pairs) {
+        int tp, tq;
+        pair4_tile(t, tiles_p, tiles_q, tp, tq);
+        const int64_t row0 = of_p ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1);
+        // the walk's blocks in pairs, which may begin in one tile and end in the next
+        for (int kb = 0; kb < kb_n; ) {
+            const uint32_t b = n + kb;
+            const int here = (b & 1) == 0 && kb + 1 < kb_n ? 2 : 1;
+            if (((b >> 1) & 1) == (uint32_t)turn) {
+                ScaleAtom now[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (i < here) now[i].load(of_p ? a.p : a.q, row0, kb + i, lane);
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    if (i < here) {
+                        const uint32_t s = (b + i) % kPair4Stages, use = (b + i) / kPair4Stages;
+                        const bool got = use == 0 || mm_wait(&sm.empty[s], (use & 1) ^ 1, stop, a.store.status);
+                        if (!__all_sync(0xFFFFFFFFu, got)) return;
+                        now[i].put(sm.scales[s] + atom * kScaleAtom, lane);
+                        fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_release(bar + 8 * s);
+                    }
+            }
+            kb += here;
+        }
+        n += kb_n;
+    }
+}
+
+template <int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair4Threads, 1)
+k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+           const __grid_constant__ CUtensorMap map_c, const Mm4Args a)
+{
+    const MmArgs &g = a.store;
+    extern __shared__ __align__(1024) uint8_t dsm[];
+    Pair4Smem &sm = *reinterpret_cast<Pair4Smem *>(dsm);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int kb_n = (int)g.kblocks;
+    const int tiles_p = (int)((g.rows_p + 255) / 256), tiles_q = (int)((g.rows_q + 255) / 256);
+    const int tiles = tiles_p * tiles_q, pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    volatile int *const stop = &sm.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPair4Stages; s++) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.sc_full[s], 6);   // three atoms, two CTAs
+            mbar_init(&sm.empty[s], 1);
+        }
+        for (int b = 0; b < 2; b++) mbar_init(&sm.acc_full[b], 1);
+        mbar_init(&sm.acc_free, 2 * kPair4EpiWarps);
+        mbar_init(&sm.drained, 1);
+        sm.abort_flag = g.give_up;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc_pair<512>(&sm.tmem_base);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the peer's barriers are ready before anything arrives on them
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    // Launched while the kernel ahead still ran; nothing was read or written so far.
+    griddep_wait();
+    griddep_launch_dependents();
+
+    if (warp < 2 + kPair4ScaleWarps) {
+        regs_fewer<kPair4Regs>();
+        if (warp == 0 && elect_one()) {
+            bool ok = true;
+            uint32_t issued = 0;
+            int s = 0;
+            uint32_t use = 1;   // parity of the release that the stage's next use waits for
+            for (int t = first; t < tiles && ok; t += pairs) {
+                int tp, tq;
+                pair4_tile(t, tiles_p, tiles_q, tp, tq);
+                const int p0 = tp * 256 + 128 * rank, q0 = tq * 256 + 128 * rank;
+                for (int kb = 0; kb < kb_n; kb++) {
+                    if (issued >= kPair4Stages && !mm_wait(&sm.empty[s], use, stop, g.status)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = sm.stage[s];
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kPair4OperandBytes);
+                    const uint32_t bar = cluster_addr(smem_u32(&sm.full[s]), 0);
+                    tma_load_tile_pair(st, &map_p, kb * 128, p0, bar);
+                    tma_load_tile_pair(st + 128 * 128, &map_q, kb * 128, q0, bar);
+                    issued++;
+                    if (++s == kPair4Stages) {
+                        s = 0;
+                        use ^= 1;
+                    }
+                }
+            }
+            // every stage is released before this CTA may leave: the leader's commits
+            // arrive here
+            for (uint32_t j = issued > kPair4Stages ? issued - kPair4Stages : 0; ok && j < issued; j++)
+                ok = mm_wait(&sm.empty[j % kPair4Stages], (j / kPair4Stages) & 1, stop, g.status);
+            if (!ok) {   // copies in flight land before shared memory goes away
+                if (rank == 0) {
+                    for (uint32_t j = issued > kPair4Stages ? issued - kPair4Stages : 0; j < issued; j++)
+                        (void)mbar_wait_bounded(&sm.full[j % kPair4Stages], (j / kPair4Stages) & 1);
+                } else {   // counted on the leader's barriers: far longer than any copy takes
+                    const unsigned long long t0 = globaltimer();
+                    while (globaltimer() - t0 < 10000000ull) {}
+                }
+            }
+        } else if (warp == 1) {
+            if (rank == 0) {
+                const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * 128);
+                const uint64_t src0 = smem_desc_scales(sm.scales[0]);
+                const uint32_t sp = tmem + kPair4Scales, sq = sp + 16;
+                bool ok = true;
+                int s = 0;
+                uint32_t par = 0, tile = 0;
+                for (int t = first; t < tiles && ok; t += pairs, tile++) {
+                    const uint32_t d = tmem + (tile & 1) * kPair4Second;
+                    // the columns that this tile shares with the one before have been read
+                    if (tile > 0) ok = mm_wait(&sm.acc_free, (tile - 1) & 1, stop, g.status);
+                    for (int kb = 0; kb < kb_n; kb++) {
+                        ok = ok && mm_wait(&sm.full[s], par, stop, g.status);
+                        ok = ok && mm_wait(&sm.sc_full[s], par, stop, g.status);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t at = (uint64_t)(s * (kPair4OperandBytes >> 4));
+                            const uint64_t src = src0 + (uint64_t)(s * (3 * kScaleAtom >> 4));
+#pragma unroll
+                            for (int k = 0; k < 4; k++) {
+                                scales_to_tmem_pair(sp + 4 * k, src + 32 * k);
+#pragma unroll
+                                for (int j = 0; j < 2; j++) scales_to_tmem_pair(sq + 8 * k + 4 * j, src + 128 * (1 + j) + 32 * k);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                mma_f4_pair(d, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e2m1(256, 256), sp + 4 * k, sq + 8 * k, kb > 0 || k > 0);
+                            mma_commit_pair(&sm.empty[s]);
+                            if (kb + 1 == kb_n) mma_commit_pair(&sm.acc_full[tile & 1]);
+                        }
+                        __syncwarp();
+                        if (++s == kPair4Stages) {
+                            s = 0;
+                            par ^= 1;
+                        }
+                    }
+                }
+                if (!ok && elect_one()) {   // aborted: MMAs in flight end before their memory goes away
+                    mma_commit_pair(&sm.drained);
+                    (void)mbar_wait_bounded(&sm.drained, 0);
+                }
+            }
+        } else if (warp >= 2) {
+            const int w = warp - 2, atom = w >> 1;
+            put_scales4(sm, a, atom == 0, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
+        }
+    } else {
+        regs_more<kPair4EpiRegs>();
+        const int quad = warp & 3, half = (warp - 2 - kPair4ScaleWarps) >> 2;   // 32 tensor memory lanes, 128 columns
+        const uint32_t to_leader = cluster_addr(smem_u32(&sm.acc_free), 0);
+        const float fp = __ldg(a.s_p), fq = __ldg(a.s_q);
+        const uint64_t sp = pack2(__float_as_uint(fp), __float_as_uint(fp)), sq = pack2(__float_as_uint(fq), __float_as_uint(fq));
+        uint32_t tile = 0;
+        for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs, tile++) {
+            int tp, tq;
+            pair4_tile(t, tiles_p, tiles_q, tp, tq);
+            mm_wait(&sm.acc_full[tile & 1], (tile >> 1) & 1, stop, g.status);
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + (tile & 1) * kPair4Second + half * 128;
+            uint64_t acc[64];
+            // The columns shared with the next tile are the last 48 of the second half, then
+            // the first 48 of the first: each half begins at its end of the tile.
+            auto read = [&](int h) {
+                uint32_t r[64];
+                tmem_ld64(r, addr + h * 64);
+#pragma unroll
+                for (int j = 0; j < 32; j++) acc[h * 32 + j] = fmul2(fmul2(pack2(r[2 * j], r[2 * j + 1]), sp), sq);
+            };
+            auto release = [&] {
+                tc_fence_before();
+                if (elect_one()) mbar_arrive_cluster(to_leader);
+            };
+            if (half == 0) {
+                read(0);
+                release();
+                read(1);
+            } else {
+                read(1);
+                release();
+                read(0);
+            }
+            if (!__any_sync(0xFFFFFFFFu, *stop))
+                mm_store_tile<OUT, true>(g, &map_c, sm.staging[warp - 2 - kPair4ScaleWarps], acc, (int64_t)tp * 256 + 128 * (int)rank + quad * 32,
+                                         (int64_t)tq * 256 + half * 128, lane);
+        }
+        if (lane == 0) bulk_wait_all();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // nothing of the peer's arrives here any more
+    tc_fence_after();
+    if (warp == 1) tmem_free_pair<512>(tmem);
+    if (g.give_up && threadIdx.x == 0 && g.status != nullptr) atomicOr(g.status, kStTimeout);
+}
+
+}  // namespace qk

@@ -7,6 +7,7 @@
 // scale per 1x16 or 16x16 block and one FP32 scale per tensor.  The tensor core
 // takes the codes and the block scales (tcgen05 kind mxf4nvf4, a scale per 16
 // elements) and adds in FP32; the tensors' scales are multiplied in at the end.
+#include "k_mm4_pair.cuh"
 #include "k_mm4_split.cuh"
 #include "q_internal.h"
 
@@ -39,6 +40,39 @@ template <int OUT, int BN> cudaError_t mm4_split(const uint8_t *p, const uint8_t
     return cudaLaunchKernelEx(&cfg, k_mm4_split<OUT, BN>, map_p, map_q, a);
 }
 
+// The registers that the pair kernel's epilogue takes over have to be there at
+// its launch: it would wait for them forever.
+template <int OUT> cudaError_t pair4_registers_ready()
+{
+    static std::atomic<bool> ready{false};
+    if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes a;
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT>);
+    if (e != cudaSuccess) return e;
+    if (a.numRegs * kPair4Threads < 32 * (kPair4EpiWarps * kPair4EpiRegs + (2 + kPair4ScaleWarps) * kPair4Regs)) return cudaErrorInvalidConfiguration;
+    ready.store(true, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// Tiles of 256 x 256 on CTA pairs.
+template <int OUT> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
+{
+    alignas(64) CUtensorMap map_p, map_q, map_c = {};
+    MmArgs &g = a.store;
+    cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K / 2, 128);
+    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, 128);
+    const bool bulk = g.ldc % (OUT == F32 ? 4 : 8) == 0 && (OUT == F32 || !g.accumulate);
+    g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
+    if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT>>(sizeof(Pair4Smem));
+    if (e == cudaSuccess) e = pair4_registers_ready<OUT>();
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + 255) / 256), pairs = sm_count() / 2;
+    if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_k(true, k_mm4_pair<OUT>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
+                    sizeof(Pair4Smem), st, map_p, map_q, map_c, a);
+}
+
 Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K)
 {
     const int64_t pitch = K / 16;
@@ -50,6 +84,7 @@ template <int OUT>
 cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t K, cudaStream_t st)
 {
     const int64_t M = g.store.rows_p, N = g.store.rows_q;
+    if (((M + 255) / 256) * ((N + 255) / 256) >= 40) return mm4_pair<OUT>(a, b, g, K, st);
     Mm4Args w = g;   // the weights on the lanes
     w.p = g.q;
     w.q = g.p;
