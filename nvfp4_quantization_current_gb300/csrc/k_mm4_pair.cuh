@@ -25,18 +25,19 @@ constexpr int kPair4EpiWarps = 8, kPair4ScaleWarps = 6;
 constexpr int kPair4Threads = 32 * (2 + kPair4ScaleWarps + kPair4EpiWarps);
 constexpr int kPair4Stages = 4;
 constexpr int kPair4OperandBytes = 2 * 128 * 128;
+constexpr int kPair4Unit = 4, kPair4Slots = 2;   // blocks whose scales are handed over together, and places for them
 constexpr int kPair4Group = 8;              // tile rows per group of the tile order
 constexpr int kPair4Second = 208;           // first column of the second buffer; the scales' columns begin at 464
 constexpr int kPair4Scales = kPair4Second + 256;
 // Registers per thread of the epilogue's and the other warps; their sum is what
 // the kernel is launched with.
-constexpr int kPair4EpiRegs = 184, kPair4Regs = 72;
+constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
 
 struct Pair4Smem {
     uint8_t stage[kPair4Stages][kPair4OperandBytes];
-    uint8_t staging[kPair4EpiWarps][2 * 4096];
-    uint8_t scales[kPair4Stages][3 * kScaleAtom];   // P's rows, and Q's in halves
-    uint64_t full[kPair4Stages], sc_full[kPair4Stages], empty[kPair4Stages], acc_full[2], acc_free, drained;
+    uint8_t staging[kPair4EpiWarps][4096];
+    uint8_t scales[kPair4Slots][kPair4Unit][3 * kScaleAtom];   // P's rows, and Q's in halves
+    uint64_t full[kPair4Stages], empty[kPair4Stages], sc_full[kPair4Slots], sc_empty[kPair4Slots], acc_full[2], acc_free, drained;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -60,41 +61,56 @@ QD void mbar_arrive_release(uint32_t addr)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-// The scales of 128 rows for all tiles of a CTA's walk (one warp of two: every other two blocks).
-QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, bool of_p, int atom, int turn, int first, int pairs, int tiles_p, int tiles_q,
-                    int rank, int lane, volatile int *stop)
+// The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  A unit's four blocks are 64
+// bytes of a scale row, which four lanes take, so that a load touches 8 lines and
+// not 32.  A lane's four loads of a step are the rows that share a source line of
+// the copies (r, r + 32, r + 64, r + 96).  A unit's loads are issued before the one
+// ahead of it waits for its place: among the operands' copies, which keep memory's
+// queues full, a load takes some 4000 cycles.
+QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int first, int pairs, int tiles_p, int tiles_q, int rank,
+                    int lane, volatile int *stop)
 {
-    const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q;
+    const Mm4Scales &g = atom == 0 ? a.p : a.q;
+    const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q, block = lane >> 3;
     const uint32_t bar = cluster_addr(smem_u32(&sm.sc_full[0]), 0);
-    uint32_t n = 0;   // blocks of the walk before this tile
-    for (int t = first; t < tiles; t += pairs) {
+    ScaleAtom now[2], ahead[2];
+    int t = first, kb = 0;   // of the unit that is loaded next
+    int64_t row0 = 0;
+    auto place = [&] {
         int tp, tq;
         pair4_tile(t, tiles_p, tiles_q, tp, tq);
-        const int64_t row0 = of_p ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1);
-        // the walk's blocks in pairs, which may begin in one tile and end in the next
-        for (int kb = 0; kb < kb_n; ) {
-            const uint32_t b = n + kb;
-            const int here = (b & 1) == 0 && kb + 1 < kb_n ? 2 : 1;
-            if (((b >> 1) & 1) == (uint32_t)turn) {
-                ScaleAtom now[2];
+        row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1)) + 16 * part + (lane & 7);
+    };
+    auto load = [&] {
+        if (t >= tiles) return;
 #pragma unroll
-                for (int i = 0; i < 2; i++)
-                    if (i < here) now[i].load(of_p ? a.p : a.q, row0, kb + i, lane);
+        for (int i = 0; i < 2; i++)
 #pragma unroll
-                for (int i = 0; i < 2; i++)
-                    if (i < here) {
-                        const uint32_t s = (b + i) % kPair4Stages, use = (b + i) / kPair4Stages;
-                        const bool got = use == 0 || mm_wait(&sm.empty[s], (use & 1) ^ 1, stop, a.store.status);
-                        if (!__all_sync(0xFFFFFFFFu, got)) return;
-                        now[i].put(sm.scales[s] + atom * kScaleAtom, lane);
-                        fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_release(bar + 8 * s);
-                    }
-            }
-            kb += here;
+            for (int j = 0; j < 4; j++)
+                ahead[i].r[j] = kb + block < kb_n ? load_scales16(g, row0 + 8 * i + 32 * j, kb + block) : make_uint4(0u, 0u, 0u, 0u);
+        kb += kPair4Unit;
+        if (kb >= kb_n) {
+            kb = 0;
+            t += pairs;
+            if (t < tiles) place();
         }
-        n += kb_n;
+    };
+    if (t >= tiles) return;
+    const uint32_t units = (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)((kb_n + kPair4Unit - 1) / kPair4Unit);
+    place();
+    load();
+    for (uint32_t u = 0; u < units; u++) {
+#pragma unroll
+        for (int i = 0; i < 2; i++) now[i] = ahead[i];
+        load();
+        const uint32_t slot = u % kPair4Slots, use = u / kPair4Slots;
+        const bool got = use == 0 || mm_wait(&sm.sc_empty[slot], (use & 1) ^ 1, stop, a.store.status);
+        if (!__all_sync(0xFFFFFFFFu, got)) return;
+#pragma unroll
+        for (int i = 0; i < 2; i++) now[i].put(sm.scales[slot][block] + atom * kScaleAtom, 16 * part + 8 * i + (lane & 7));
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_release(bar + 8 * slot);
     }
 }
 
@@ -117,8 +133,11 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPair4Stages; s++) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.sc_full[s], 6);   // three atoms, two CTAs
             mbar_init(&sm.empty[s], 1);
+        }
+        for (int s = 0; s < kPair4Slots; s++) {
+            mbar_init(&sm.sc_full[s], 2 * kPair4ScaleWarps);
+            mbar_init(&sm.sc_empty[s], 1);
         }
         for (int b = 0; b < 2; b++) mbar_init(&sm.acc_full[b], 1);
         mbar_init(&sm.acc_free, 2 * kPair4EpiWarps);
@@ -180,24 +199,25 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         } else if (warp == 1) {
             if (rank == 0) {
                 const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * 128);
-                const uint64_t src0 = smem_desc_scales(sm.scales[0]);
+                const uint64_t src0 = smem_desc_scales(sm.scales[0][0]);
                 const uint32_t sp = tmem + kPair4Scales, sq = sp + 16;
                 bool ok = true;
                 int s = 0;
-                uint32_t par = 0, tile = 0;
+                uint32_t par = 0, tile = 0, unit = 0;
                 for (int t = first; t < tiles && ok; t += pairs, tile++) {
                     const uint32_t d = tmem + (tile & 1) * kPair4Second;
                     // the columns that this tile shares with the one before have been read
                     if (tile > 0) ok = mm_wait(&sm.acc_free, (tile - 1) & 1, stop, g.status);
                     for (int kb = 0; kb < kb_n; kb++) {
+                        const uint32_t slot = unit % kPair4Slots;
                         ok = ok && mm_wait(&sm.full[s], par, stop, g.status);
-                        ok = ok && mm_wait(&sm.sc_full[s], par, stop, g.status);
+                        if (kb % kPair4Unit == 0) ok = ok && mm_wait(&sm.sc_full[slot], (unit / kPair4Slots) & 1, stop, g.status);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t at = (uint64_t)(s * (kPair4OperandBytes >> 4));
-                            const uint64_t src = src0 + (uint64_t)(s * (3 * kScaleAtom >> 4));
+                            const uint64_t src = src0 + (uint64_t)((slot * kPair4Unit + kb % kPair4Unit) * (3 * kScaleAtom >> 4));
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 scales_to_tmem_pair(sp + 4 * k, src + 32 * k);
@@ -208,9 +228,11 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                             for (int k = 0; k < 4; k++)
                                 mma_f4_pair(d, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e2m1(256, 256), sp + 4 * k, sq + 8 * k, kb > 0 || k > 0);
                             mma_commit_pair(&sm.empty[s]);
+                            if (kb % kPair4Unit == kPair4Unit - 1 || kb + 1 == kb_n) mma_commit_pair(&sm.sc_empty[slot]);
                             if (kb + 1 == kb_n) mma_commit_pair(&sm.acc_full[tile & 1]);
                         }
                         __syncwarp();
+                        if (kb % kPair4Unit == kPair4Unit - 1 || kb + 1 == kb_n) unit++;
                         if (++s == kPair4Stages) {
                             s = 0;
                             par ^= 1;
@@ -224,7 +246,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             }
         } else if (warp >= 2) {
             const int w = warp - 2, atom = w >> 1;
-            put_scales4(sm, a, atom == 0, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
+            put_scales4(sm, a, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
         }
     } else {
         regs_more<kPair4EpiRegs>();
@@ -240,31 +262,24 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             __syncwarp();
             tc_fence_after();
             const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + (tile & 1) * kPair4Second + half * 128;
-            uint64_t acc[64];
             // The columns shared with the next tile are the last 48 of the second half, then
             // the first 48 of the first: each half begins at its end of the tile.
-            auto read = [&](int h) {
+            auto part = [&](int h, bool shared) {
                 uint32_t r[64];
                 tmem_ld64(r, addr + h * 64);
+                if (shared) {
+                    tc_fence_before();
+                    if (elect_one()) mbar_arrive_cluster(to_leader);
+                }
+                uint64_t acc[32];
 #pragma unroll
-                for (int j = 0; j < 32; j++) acc[h * 32 + j] = fmul2(fmul2(pack2(r[2 * j], r[2 * j + 1]), sp), sq);
+                for (int j = 0; j < 32; j++) acc[j] = fmul2(fmul2(pack2(r[2 * j], r[2 * j + 1]), sp), sq);
+                if (!__any_sync(0xFFFFFFFFu, *stop))
+                    mm_store_tile<OUT, true, 1, 64>(g, &map_c, sm.staging[warp - 2 - kPair4ScaleWarps], acc,
+                                                    (int64_t)tp * 256 + 128 * (int)rank + quad * 32, (int64_t)tq * 256 + half * 128 + h * 64, lane);
             };
-            auto release = [&] {
-                tc_fence_before();
-                if (elect_one()) mbar_arrive_cluster(to_leader);
-            };
-            if (half == 0) {
-                read(0);
-                release();
-                read(1);
-            } else {
-                read(1);
-                release();
-                read(0);
-            }
-            if (!__any_sync(0xFFFFFFFFu, *stop))
-                mm_store_tile<OUT, true>(g, &map_c, sm.staging[warp - 2 - kPair4ScaleWarps], acc, (int64_t)tp * 256 + 128 * (int)rank + quad * 32,
-                                         (int64_t)tq * 256 + half * 128, lane);
+            part(half, true);
+            part(1 - half, false);
         }
         if (lane == 0) bulk_wait_all();
     }
