@@ -55,12 +55,6 @@ QD void pair4_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
     q = r / height;
 }
 
-// Arrival on a barrier of the cluster that hands over shared memory written before it.
-QD void mbar_arrive_release(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
 // The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  A unit's four blocks are 64
 // bytes of a scale row, which four lanes take, so that a load touches 8 lines and
 // not 32.  A lane's four loads of a step are the rows that share a source line of
@@ -73,7 +67,7 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
     const Mm4Scales &g = atom == 0 ? a.p : a.q;
     const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q, block = lane >> 3;
     const uint32_t bar = cluster_addr(smem_u32(&sm.sc_full[0]), 0);
-    ScaleAtom now[2], ahead[2];
+    ScaleAtom held[2][2];    // of two units in turn
     int t = first, kb = 0;   // of the unit that is loaded next
     int64_t row0 = 0;
     auto place = [&] {
@@ -81,13 +75,13 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
         pair4_tile(t, tiles_p, tiles_q, tp, tq);
         row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1)) + 16 * part + (lane & 7);
     };
-    auto load = [&] {
+    auto load = [&](ScaleAtom (&to)[2]) {
         if (t >= tiles) return;
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                ahead[i].r[j] = kb + block < kb_n ? load_scales16(g, row0 + 8 * i + 32 * j, kb + block) : make_uint4(0u, 0u, 0u, 0u);
+                to[i].r[j] = kb + block < kb_n ? load_scales16(g, row0 + 8 * i + 32 * j, kb + block) : make_uint4(0u, 0u, 0u, 0u);
         kb += kPair4Unit;
         if (kb >= kb_n) {
             kb = 0;
@@ -98,19 +92,27 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
     if (t >= tiles) return;
     const uint32_t units = (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)((kb_n + kPair4Unit - 1) / kPair4Unit);
     place();
-    load();
-    for (uint32_t u = 0; u < units; u++) {
+    load(held[0]);
+    load(held[1]);
+    for (uint32_t u = 0; u < units; u += 2) {
 #pragma unroll
-        for (int i = 0; i < 2; i++) now[i] = ahead[i];
-        load();
-        const uint32_t slot = u % kPair4Slots, use = u / kPair4Slots;
-        const bool got = use == 0 || mm_wait(&sm.sc_empty[slot], (use & 1) ^ 1, stop, a.store.status);
-        if (!__all_sync(0xFFFFFFFFu, got)) return;
+        for (uint32_t v = 0; v < 2; v++) {
+            if (u + v >= units) return;
+            const uint32_t slot = v, use = u >> 1;
+            static_assert(kPair4Slots == 2, "a place for each of two units in turn");
+            const bool got = use == 0 || mm_wait(&sm.sc_empty[slot], (use & 1) ^ 1, stop, a.store.status);
+            if (!__all_sync(0xFFFFFFFFu, got)) return;
 #pragma unroll
-        for (int i = 0; i < 2; i++) now[i].put(sm.scales[slot][block] + atom * kScaleAtom, 16 * part + 8 * i + (lane & 7));
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_release(bar + 8 * slot);
+            for (int i = 0; i < 2; i++) held[v][i].put(sm.scales[slot][block] + atom * kScaleAtom, 16 * part + 8 * i + (lane & 7));
+            fence_proxy_async();
+            __syncwarp();
+            // What is handed over is read by this SM's own tensor core, whichever CTA's thread
+            // asks for it: the fence has put it there, and the arrival needs no release to the
+            // cluster, which waited for the loads on their way as well (8192 x 14336 x 4096 213
+            // us with it, 171 without).
+            if (lane == 0) mbar_arrive_cluster(bar + 8 * slot);
+            load(held[v]);
+        }
     }
 }
 
