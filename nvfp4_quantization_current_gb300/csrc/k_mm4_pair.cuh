@@ -25,8 +25,7 @@ constexpr int kPair4EpiWarps = 8, kPair4ScaleWarps = 6;
 constexpr int kPair4Threads = 32 * (2 + kPair4ScaleWarps + kPair4EpiWarps);
 constexpr int kPair4Stages = 4;
 constexpr int kPair4OperandBytes = 2 * 128 * 128;
-constexpr int kPair4Unit = 4, kPair4Slots = 2;   // blocks whose scales are handed over together, and places for them
-constexpr int kPair4Group = 8;              // tile rows per group of the tile order
+constexpr int kPair4Unit = 4, kPair4Slots = 2;   // blocks whose scales are handed over together (ScaleUnit), and places for them
 constexpr int kPair4Second = 208;           // first column of the second buffer; the scales' columns begin at 464
 constexpr int kPair4Scales = kPair4Second + 256;
 // Registers per thread of the epilogue's and the other warps; their sum is what
@@ -43,67 +42,71 @@ struct Pair4Smem {
 };
 static_assert(sizeof(Pair4Smem) <= 232448, "shared memory of a CTA");
 
-// Tile t of the walk, in units of 256 x 256: groups of kPair4Group tile rows,
-// each walked column by column, so that the tiles in flight share their
-// operands in L2.
-QD void pair4_tile(int t, int tiles_p, int tiles_q, int &p, int &q)
+// Tile t of the walk, in units of 256 x 256: groups of `group` tile rows, each
+// walked column by column, so that the tiles in flight share their operands in
+// L2.  The launcher says how many: where there are few tile rows, all of them, up
+// to 32, where there are few columns, two (power is what these calls run into, and
+// it goes by the traffic: 8192 x 14336 x 4096, 32 x 56 tiles, 160 us at 32 rows, 172
+// at 8, 165 at one; 8192 x 4096 x 14336, 32 x 16, 161, 154 and 148, at two 148;
+// 16384 x 18432 x 7168, 64 x 72, 647 at 32, 727 at 64, 679 at 8).
+QD void pair4_tile(int t, int tiles_p, int tiles_q, int group, int &p, int &q)
 {
-    const int per_group = kPair4Group * tiles_q;
-    const int gp = t / per_group * kPair4Group, r = t % per_group;
-    const int height = tiles_p - gp < kPair4Group ? tiles_p - gp : kPair4Group;
+    const int per_group = group * tiles_q;
+    const int gp = t / per_group * group, r = t % per_group;
+    const int height = tiles_p - gp < group ? tiles_p - gp : group;
     p = gp + r % height;
     q = r / height;
 }
 
-// The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  A unit's four blocks are 64
-// bytes of a scale row, which four lanes take, so that a load touches 8 lines and
-// not 32.  A lane's four loads of a step are the rows that share a source line of
-// the copies (r, r + 32, r + 64, r + 96).  A unit's loads are issued before the one
-// ahead of it waits for its place: among the operands' copies, which keep memory's
-// queues full, a load takes some 4000 cycles.
+// The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  A unit's loads are issued
+// behind the fence of the unit ahead, which would wait for them: among the operands'
+// copies, which keep memory's queues full, a load takes some 4000 cycles.
+template <bool WHOLE>
 QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int first, int pairs, int tiles_p, int tiles_q, int rank,
                     int lane, volatile int *stop)
 {
     const Mm4Scales &g = atom == 0 ? a.p : a.q;
-    const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q, block = lane >> 3;
+    const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q;
     const uint32_t bar = cluster_addr(smem_u32(&sm.sc_full[0]), 0);
-    ScaleAtom held[2][2];    // of two units in turn
-    int t = first, kb = 0;   // of the unit that is loaded next
-    int64_t row0 = 0;
-    auto place = [&] {
-        int tp, tq;
-        pair4_tile(t, tiles_p, tiles_q, tp, tq);
-        row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1)) + 16 * part + (lane & 7);
+    // places in the walk: of the unit that is loaded next, and of the one that is handed over
+    struct Place {
+        int t, kb;
+        int64_t row0;
     };
-    auto load = [&](ScaleAtom (&to)[2]) {
-        if (t >= tiles) return;
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                to[i].r[j] = kb + block < kb_n ? load_scales16(g, row0 + 8 * i + 32 * j, kb + block) : make_uint4(0u, 0u, 0u, 0u);
-        kb += kPair4Unit;
-        if (kb >= kb_n) {
-            kb = 0;
-            t += pairs;
-            if (t < tiles) place();
+    auto settle = [&](Place &at) {
+        int tp, tq;
+        pair4_tile(at.t, tiles_p, tiles_q, a.group, tp, tq);
+        at.row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1)) + 16 * part;
+    };
+    auto advance = [&](Place &at) {
+        at.kb += kPair4Unit;
+        if (at.kb >= kb_n) {
+            at.kb = 0;
+            at.t += pairs;
+            if (at.t < tiles) settle(at);
         }
     };
-    if (t >= tiles) return;
-    const uint32_t units = (uint32_t)((tiles - 1 - first) / pairs + 1) * (uint32_t)((kb_n + kPair4Unit - 1) / kPair4Unit);
-    place();
-    load(held[0]);
-    load(held[1]);
-    for (uint32_t u = 0; u < units; u += 2) {
+    // Two units' loads on their way, where registers allow.
+    constexpr uint32_t kSets = WHOLE ? 2 : 1;
+    ScaleUnit<WHOLE> held[kSets];
+    if (first >= tiles) return;
+    Place next = {first, 0, 0};
+    settle(next);
+    Place now = next;
+    auto load = [&](ScaleUnit<WHOLE> &to) {
+        if (next.t >= tiles) return;
+        to.template load<4>(g, next.row0, next.kb, lane);
+        advance(next);
+    };
 #pragma unroll
-        for (uint32_t v = 0; v < 2; v++) {
-            if (u + v >= units) return;
-            const uint32_t slot = v, use = u >> 1;
-            static_assert(kPair4Slots == 2, "a place for each of two units in turn");
+    for (uint32_t i = 0; i < kSets; i++) load(held[i]);
+    for (uint32_t use = 0; now.t < tiles; use++) {
+#pragma unroll
+        for (uint32_t slot = 0; slot < kPair4Slots; slot++) {
+            if (now.t >= tiles) return;
             const bool got = use == 0 || mm_wait(&sm.sc_empty[slot], (use & 1) ^ 1, stop, a.store.status);
             if (!__all_sync(0xFFFFFFFFu, got)) return;
-#pragma unroll
-            for (int i = 0; i < 2; i++) held[v][i].put(sm.scales[slot][block] + atom * kScaleAtom, 16 * part + 8 * i + (lane & 7));
+            held[slot % kSets].template put<4>(g, now.row0, now.kb, sm.scales[slot][lane >> 3] + atom * kScaleAtom, 16 * part + (lane & 7), lane);
             fence_proxy_async();
             __syncwarp();
             // What is handed over is read by this SM's own tensor core, whichever CTA's thread
@@ -111,12 +114,13 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
             // cluster, which waited for the loads on their way as well (8192 x 14336 x 4096 213
             // us with it, 171 without).
             if (lane == 0) mbar_arrive_cluster(bar + 8 * slot);
-            load(held[v]);
+            advance(now);
+            load(held[slot % kSets]);
         }
     }
 }
 
-template <int OUT>
+template <int OUT, bool WHOLE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair4Threads, 1)
 k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
            const __grid_constant__ CUtensorMap map_c, const Mm4Args a)
@@ -166,7 +170,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             uint32_t use = 1;   // parity of the release that the stage's next use waits for
             for (int t = first; t < tiles && ok; t += pairs) {
                 int tp, tq;
-                pair4_tile(t, tiles_p, tiles_q, tp, tq);
+                pair4_tile(t, tiles_p, tiles_q, a.group, tp, tq);
                 const int p0 = tp * 256 + 128 * rank, q0 = tq * 256 + 128 * rank;
                 for (int kb = 0; kb < kb_n; kb++) {
                     if (issued >= kPair4Stages && !mm_wait(&sm.empty[s], use, stop, g.status)) {
@@ -248,7 +252,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             }
         } else if (warp >= 2) {
             const int w = warp - 2, atom = w >> 1;
-            put_scales4(sm, a, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
+            put_scales4<WHOLE>(sm, a, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
         }
     } else {
         regs_more<kPair4EpiRegs>();
@@ -259,7 +263,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         uint32_t tile = 0;
         for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs, tile++) {
             int tp, tq;
-            pair4_tile(t, tiles_p, tiles_q, tp, tq);
+            pair4_tile(t, tiles_p, tiles_q, a.group, tp, tq);
             mm_wait(&sm.acc_full[tile & 1], (tile >> 1) & 1, stop, g.status);
             __syncwarp();
             tc_fence_after();

@@ -7,9 +7,8 @@
 // stays in tensor memory, and is read once.
 //
 // The first four warps fetch scales, two for the weights and two for the
-// tokens, two blocks at a time in turn, and put them where the copies to
-// tensor memory take them from; afterwards they, and four more for wide tiles,
-// read the sums.  The next warp loads operands, the last issues the copies and
+// tokens, four blocks at a time, and put them where the copies to tensor memory
+// take them from; afterwards they, and four more for wide tiles, read the sums.  The next warp loads operands, the last issues the copies and
 // the MMAs.
 #pragma once
 
@@ -19,10 +18,10 @@
 namespace qk {
 
 template <int BN> struct Split4Smem {
-    static constexpr int kAtomsQ = (BN + 127) / 128;
+    static constexpr int kAtomsQ = (BN + 127) / 128, kPartsQ = BN > 16 ? 2 : 1;   // 128s of tokens, and warps for their scales
     static constexpr int kOperandBytes = (128 + BN) * 128;
     static constexpr int kScaleBytes = (1 + kAtomsQ) * kScaleAtom;
-    static constexpr int kStages = BN == 16 ? 5 : BN == 128 ? 6 : 4;
+    static constexpr int kStages = BN == 64 ? 3 : BN == 128 ? 6 : 4;
     static constexpr int kScaleCols = 16 * (1 + kAtomsQ);          // tensor memory columns of a stage's scales
     static constexpr int kUsed = BN + 2 * kScaleCols;
     static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
@@ -31,14 +30,43 @@ template <int BN> struct Split4Smem {
     static constexpr int kThreads = 32 * (kEpiWarps + 2);
     static constexpr int kResident = BN <= 64 ? 2 : 1;             // CTAs of an SM
     uint8_t stage[kStages][kOperandBytes];       // afterwards this CTA's sums, [BN][128] FP32
-    uint8_t scales[kStages][kScaleBytes];
-    uint64_t full[kStages], empty[kStages], sc_full[kStages], done, drained;
+    uint8_t scales[2][4][kScaleBytes];           // of two units of four blocks
+    uint64_t full[kStages], empty[kStages], sc_full[2], sc_empty[2], done, drained;
     uint32_t tmem_base;
     int abort_flag;
     static_assert(kStages * kOperandBytes >= BN * 128 * 4, "the sums replace the stages");
 };
 
-template <int OUT, int BN>
+// Half the scale rows (`part`: lines 16 part to 16 part + 15 of the atoms) of ATOMS times 128 rows from row0 on, 32 LAST
+// of them in the last, for a CTA's blocks; one warp.  A unit's four blocks are 64
+// bytes of a scale row, which four lanes take, so that a load touches 8 lines, and
+// are handed over together: a fence waits for the loads that are on their way, so
+// the next unit's are issued behind it.
+template <int BN, int ATOMS, int LAST, bool WHOLE>
+QD void put_split_scales(Split4Smem<BN> &sm, const Mm4Scales &g, int64_t row0, int part, int atom, int kb0, int kb_n, int lane,
+                         volatile int *stop, int32_t *status)
+{
+    row0 += 16 * part;
+    for (int u = 0; 4 * u < kb_n; u++) {
+        const int slot = u & 1, kb = kb0 + 4 * u;
+        ScaleUnit<WHOLE> held[ATOMS];
+#pragma unroll
+        for (int t = 0; t + 1 < ATOMS; t++) held[t].template load<4>(g, row0 + 128 * t, kb, lane);
+        held[ATOMS - 1].template load<LAST>(g, row0 + 128 * (ATOMS - 1), kb, lane);
+        const bool got = u < 2 || mm_wait(&sm.sc_empty[slot], ((u >> 1) & 1) ^ 1, stop, status);
+        if (!__all_sync(0xFFFFFFFFu, got)) return;
+        uint8_t *const to = sm.scales[slot][lane >> 3] + atom * kScaleAtom;
+        const int line = 16 * part + (lane & 7);
+#pragma unroll
+        for (int t = 0; t + 1 < ATOMS; t++) held[t].template put<4>(g, row0 + 128 * t, kb, to + t * kScaleAtom, line, lane);
+        held[ATOMS - 1].template put<LAST>(g, row0 + 128 * (ATOMS - 1), kb, to + (ATOMS - 1) * kScaleAtom, line, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sc_full[slot]);
+    }
+}
+
+template <int OUT, int BN, bool WHOLE>
 __global__ void __launch_bounds__(Split4Smem<BN>::kThreads, Split4Smem<BN>::kResident)
 k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q, const Mm4Args a)
 {
@@ -58,7 +86,10 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
         for (int s = 0; s < kStages; s++) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
-            mbar_init(&sm.sc_full[s], 2);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&sm.sc_full[s], 2 + Smem::kPartsQ);
+            mbar_init(&sm.sc_empty[s], 1);
         }
         mbar_init(&sm.done, 1);
         mbar_init(&sm.drained, 1);
@@ -66,11 +97,14 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
         fence_mbar_init();
     }
     if (warp == kEpiWarps && elect_one()) {
-        // the weights of the first stages are on their way while the kernel ahead still runs
+        // the weights of the first stages, and their scales, are on their way while the
+        // kernel ahead still runs
         prefetch_map(&map_p);
         prefetch_map(&map_q);
         for (int kb = 0; kb < kStages && kb < kb_n; kb++) prefetch_tile(&map_p, (kb0 + kb) * 128, p0);
     }
+    if (warp < 4 && p0 + 32 * warp + lane < a.p.rows && (lane & ((1 << a.p.shift) - 1)) == 0)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.p.at + ((int64_t)(p0 + 32 * warp + lane) >> a.p.shift) * a.p.pitch + kb0 * 16));
     __syncwarp();
     if (warp == kEpiWarps + 1) tmem_alloc<Smem::kCols>(&sm.tmem_base);
     tc_fence_before();
@@ -97,15 +131,15 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
     } else if (warp == kEpiWarps + 1) {
         bool ok = true;
         for (int kb = 0; kb < kb_n; kb++) {
-            const int s = kb % kStages;
+            const int s = kb % kStages, slot = (kb >> 2) & 1;
             ok = mm_wait(&sm.full[s], (kb / kStages) & 1, stop, g.status);
-            ok = ok && mm_wait(&sm.sc_full[s], (kb / kStages) & 1, stop, g.status);
+            if ((kb & 3) == 0) ok = ok && mm_wait(&sm.sc_full[slot], (kb >> 3) & 1, stop, g.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 const uint64_t p = smem_desc_k128(sm.stage[s]), q = smem_desc_k128(sm.stage[s] + 128 * 128);
-                const uint64_t src = smem_desc_scales(sm.scales[s]);
+                const uint64_t src = smem_desc_scales(sm.scales[slot][kb & 3]);
                 const uint32_t sp = tmem + BN + (kb & 1) * Smem::kScaleCols, sq = sp + 16;
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
@@ -117,6 +151,7 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
                 for (int k = 0; k < 4; k++)
                     mma_f4(tmem, p + 2 * k, q + 2 * k, idesc_e2m1(128, BN), sp + 4 * k, sq + 4 * kAtomsQ * k, kb > 0 || k > 0);
                 mma_commit(&sm.empty[s]);
+                if ((kb & 3) == 3) mma_commit(&sm.sc_empty[slot]);
                 if (kb + 1 == kb_n) mma_commit(&sm.done);
             }
             __syncwarp();
@@ -128,33 +163,9 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
         __syncwarp();
     } else {
         if (warp < 4) {
-            const bool of_p = warp < 2;
-            for (int k0 = 2 * (warp & 1); k0 < kb_n; k0 += 4) {
-                ScaleAtom now[2][kAtomsQ];
-#pragma unroll
-                for (int i = 0; i < 2; i++)
-                    if (k0 + i < kb_n) {
-#pragma unroll
-                        for (int j = 0; j < kAtomsQ; j++)
-                            if (j == 0 || !of_p) now[i][j].load(of_p ? a.p : a.q, (of_p ? p0 : q0) + 128 * j, kb0 + k0 + i, lane);
-                    }
-                bool got = true;
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int kb = k0 + i, s = kb % kStages;
-                    if (kb >= kb_n || !got) break;
-                    got = kb < kStages || mm_wait(&sm.empty[s], ((kb / kStages) & 1) ^ 1, stop, g.status);
-                    got = __all_sync(0xFFFFFFFFu, got);
-                    if (!got) break;
-#pragma unroll
-                    for (int j = 0; j < kAtomsQ; j++)
-                        if (j == 0 || !of_p) now[i][j].put(sm.scales[s] + (of_p ? 0 : 1 + j) * kScaleAtom, lane);
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.sc_full[s]);
-                }
-                if (!got) break;
-            }
+            constexpr int kLast = (BN - 128 * (kAtomsQ - 1) + 31) / 32;   // the last tokens, in 32s
+            if (warp < 2) put_split_scales<BN, 1, 4, WHOLE>(sm, a.p, p0, warp, 0, kb0, kb_n, lane, stop, g.status);
+            else if (warp - 2 < Smem::kPartsQ) put_split_scales<BN, kAtomsQ, kLast, WHOLE>(sm, a.q, q0, warp - 2, 1, kb0, kb_n, lane, stop, g.status);
         }
         __syncwarp();
         const int quad = warp & 3, first = (warp >> 2) * kWarpCols;   // 32 tensor memory lanes, the columns from `first` on

@@ -15,12 +15,12 @@ namespace qk {
 
 namespace {
 
-template <int OUT, int BN> cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, int split, cudaStream_t st)
+template <int OUT, int BN, bool WHOLE> cudaError_t mm4_split_t(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, int split, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q;
     cudaError_t e = make_operand_map(&map_p, p, a.store.rows_p, K / 2, 128);
     if (e == cudaSuccess) e = make_operand_map(&map_q, q, a.store.rows_q, K / 2, BN);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_split<OUT, BN>>(sizeof(Split4Smem<BN>), true);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_split<OUT, BN, WHOLE>>(sizeof(Split4Smem<BN>), true);
     if (e != cudaSuccess) return e;
     const int64_t ty = (a.store.rows_p + 127) / 128, tz = (a.store.rows_q + BN - 1) / BN;
     if (ty > 65535 || tz > 65535) return cudaErrorInvalidValue;
@@ -37,17 +37,23 @@ template <int OUT, int BN> cudaError_t mm4_split(const uint8_t *p, const uint8_t
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_mm4_split<OUT, BN>, map_p, map_q, a);
+    return cudaLaunchKernelEx(&cfg, k_mm4_split<OUT, BN, WHOLE>, map_p, map_q, a);
+}
+
+template <int OUT, int BN>
+cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, bool whole, int split, cudaStream_t st)
+{
+    return whole ? mm4_split_t<OUT, BN, true>(p, q, a, K, split, st) : mm4_split_t<OUT, BN, false>(p, q, a, K, split, st);
 }
 
 // The registers that the pair kernel's epilogue takes over have to be there at
 // its launch: it would wait for them forever.
-template <int OUT> cudaError_t pair4_registers_ready()
+template <int OUT, bool WHOLE> cudaError_t pair4_registers_ready()
 {
     static std::atomic<bool> ready{false};
     if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, WHOLE>);
     if (e != cudaSuccess) return e;
     if (a.numRegs * kPair4Threads < 32 * (kPair4EpiWarps * kPair4EpiRegs + (2 + kPair4ScaleWarps) * kPair4Regs)) return cudaErrorInvalidConfiguration;
     ready.store(true, std::memory_order_relaxed);
@@ -55,7 +61,7 @@ template <int OUT> cudaError_t pair4_registers_ready()
 }
 
 // Tiles of 256 x 256 on CTA pairs.
-template <int OUT> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
+template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q, map_c = {};
     MmArgs &g = a.store;
@@ -64,27 +70,27 @@ template <int OUT> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, Mm4A
     const bool bulk = g.ldc % (OUT == F32 ? 4 : 8) == 0 && (OUT == F32 || !g.accumulate);
     g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
     if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT>>(sizeof(Pair4Smem));
-    if (e == cudaSuccess) e = pair4_registers_ready<OUT>();
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, WHOLE>>(sizeof(Pair4Smem));
+    if (e == cudaSuccess) e = pair4_registers_ready<OUT, WHOLE>();
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ((g.rows_p + 255) / 256) * ((g.rows_q + 255) / 256), pairs = sm_count() / 2;
+    const int64_t tiles_p = (g.rows_p + 255) / 256, tiles_q = (g.rows_q + 255) / 256, tiles = tiles_p * tiles_q, pairs = sm_count() / 2;
+    a.group = tiles_q < tiles_p && tiles_q <= 32 ? 2 : tiles_p < 32 ? (int)tiles_p : 32;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_k(true, k_mm4_pair<OUT>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
+    return launch_k(true, k_mm4_pair<OUT, WHOLE>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
                     sizeof(Pair4Smem), st, map_p, map_q, map_c, a);
 }
 
-Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K)
-{
-    const int64_t pitch = K / 16;
-    const uintptr_t both = reinterpret_cast<uintptr_t>(at) | (uintptr_t)pitch;
-    return {at, pitch, (int)rows, blk ? 4 : 0, both % 16 == 0 ? 16 : both % 4 == 0 ? 4 : 1};
-}
+Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K) { return {at, K / 16, (int)rows, blk ? 4 : 0}; }
+
+// Every row of scales begins on a 16-byte boundary.
+bool whole_rows(const Mm4Scales &s) { return ((reinterpret_cast<uintptr_t>(s.at) | (uintptr_t)s.pitch) & 15) == 0; }
 
 template <int OUT>
 cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t K, cudaStream_t st)
 {
     const int64_t M = g.store.rows_p, N = g.store.rows_q;
-    if (((M + 255) / 256) * ((N + 255) / 256) >= 40) return mm4_pair<OUT>(a, b, g, K, st);
+    const bool whole = whole_rows(g.p) && whole_rows(g.q);
+    if (((M + 255) / 256) * ((N + 255) / 256) >= 40) return whole ? mm4_pair<OUT, true>(a, b, g, K, st) : mm4_pair<OUT, false>(a, b, g, K, st);
     Mm4Args w = g;   // the weights on the lanes
     w.p = g.q;
     w.q = g.p;
@@ -97,11 +103,11 @@ cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t 
     const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 192;
     while (split < kSplitMost && 2 * split <= kb && ((N + 127) / 128) * ((M + bn - 1) / bn) * split * 2 <= 144) split *= 2;
     switch (bn) {
-    case 16: return mm4_split<OUT, 16>(b, a, w, K, split, st);
-    case 32: return mm4_split<OUT, 32>(b, a, w, K, split, st);
-    case 64: return mm4_split<OUT, 64>(b, a, w, K, split, st);
-    case 128: return mm4_split<OUT, 128>(b, a, w, K, split, st);
-    default: return mm4_split<OUT, 192>(b, a, w, K, split, st);
+    case 16: return mm4_split<OUT, 16>(b, a, w, K, whole, split, st);
+    case 32: return mm4_split<OUT, 32>(b, a, w, K, whole, split, st);
+    case 64: return mm4_split<OUT, 64>(b, a, w, K, whole, split, st);
+    case 128: return mm4_split<OUT, 128>(b, a, w, K, whole, split, st);
+    default: return mm4_split<OUT, 192>(b, a, w, K, whole, split, st);
     }
 }
 
