@@ -85,12 +85,91 @@ Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K) { retur
 // Every row of scales begins on a 16-byte boundary.
 bool whole_rows(const Mm4Scales &s) { return ((reinterpret_cast<uintptr_t>(s.at) | (uintptr_t)s.pitch) & 15) == 0; }
 
+// CTAs that clusters of `split` keep resident, one per SM (see the blockwise product's).
+int cluster_ctas4(int split)
+{
+    static std::atomic<int> known[64][3];   // of a device's splits 2, 4, 8
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;   // no answer, no clusters
+    std::atomic<int> &k = known[dev][split == 2 ? 0 : split == 4 ? 1 : 2];
+    const int c = k.load(std::memory_order_relaxed);
+    if (c > 0) return c;
+    constexpr auto kernel = k_mm4_split<BF16, 128, true>;   // one CTA fills an SM
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(Split4Smem<128>::kThreads);
+    cfg.dynamicSmemBytes = sizeof(Split4Smem<128>);
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)split;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (engine_smem_ready<k_mm4_split<BF16, 128, true>>(sizeof(Split4Smem<128>), true) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+        return 0;
+    k.store(n * split, std::memory_order_relaxed);
+    return n * split;
+}
+
+// Which kernel, and how wide and how deep a split: the least estimated time.
+// The estimate's terms (us) are a fit to 1160 calls of every plan that 170 shapes
+// allow (1 to 4096 tokens, weights from 512 x 256 to 18432 x 18432, K of every
+// multiple of 32, weights in either blocks; GB300, graphs of calls); its choices take
+// 0.6% more time than the best plan on the average and 10% at most.  A call has a
+// fixed part, a cluster adds its sum, a CTA takes `block` for each 256 elements of K
+// (`odd` times as long where scale rows begin anywhere), two CTAs of an SM `share`
+// times one's time, and a CTA that comes after another a start of its own.  Some of
+// what it is drawn from: one token with 4096 x 4096 weights 4.9 us at a split of four,
+// 7.8 without, 9.7 on the pair kernel; 333 tokens 10.8 there, 11.3 at 192 wide and two
+// deep, 12.4 at 128; 64 tokens with 4096 x 14336 10.6 at 64 and four, 25.5 on the pair.
+struct Mm4Plan {
+    int bn, split;   // bn 0: the pair kernel
+};
+Mm4Plan mm4_plan(int64_t M, int64_t N, int64_t kblocks, bool whole, int sms)
+{
+    struct Width {
+        int bn;
+        double fixed, block, share, odd, split[3], start;
+        int resident;
+    };
+    static constexpr Width kWidths[] = {{16, 3.57, 0.274, 1.504, 1.203, {0.57, 0.57, 0.69}, 2.88, 2},
+                                        {32, 4.72, 0.296, 1.498, 1.113, {0.06, 0.0, 0.32}, 3.96, 2},
+                                        {64, 6.25, 0.312, 1.609, 1.166, {0.0, 0.0, 0.21}, 5.76, 2},
+                                        {128, 6.96, 0.327, 1.0, 1.187, {0.0, 0.0, 0.0}, 6.89, 1},
+                                        {192, 8.78, 0.357, 1.0, 1.298, {0.0, 0.0, 0.0}, 9.36, 1}};
+    const int64_t ty = (N + 127) / 128, pairs = sms / 2;
+    const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
+    Mm4Plan best = {0, 1};
+    double cost = 3.55 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * 0.363 * (whole ? 1.0 : 1.316) + 1.445 * (whole ? 1.0 : 1.718));
+    for (const Width &w : kWidths) {
+        const int64_t tz = (M + w.bn - 1) / w.bn;
+        if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;
+        for (int i = 0; i <= 3; i++) {
+            const int split = 1 << i;
+            const int64_t ctas = ty * tz * split, n = (ctas + sms - 1) / sms;   // n: CTAs of an SM
+            if (split > 1 && (split > kblocks || ctas > (int64_t)w.resident * cluster_ctas4(split))) break;
+            const double times = (double)(n / w.resident) * w.share + (double)(n % w.resident);
+            const double c = w.fixed + (i > 0 ? w.split[i - 1] : 0.0) + (double)((kblocks + split - 1) / split) * w.block * times * (whole ? 1.0 : w.odd) +
+                             w.start * (double)((n - 1) / w.resident);
+            if (c < cost) {
+                cost = c;
+                best = {w.bn, split};
+            }
+        }
+    }
+    return best;
+}
+
 template <int OUT>
 cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t K, cudaStream_t st)
 {
     const int64_t M = g.store.rows_p, N = g.store.rows_q;
     const bool whole = whole_rows(g.p) && whole_rows(g.q);
-    if (((M + 255) / 256) * ((N + 255) / 256) >= 40) return whole ? mm4_pair<OUT, true>(a, b, g, K, st) : mm4_pair<OUT, false>(a, b, g, K, st);
+    const Mm4Plan plan = mm4_plan(M, N, g.store.kblocks, whole, sm_count());
+    const int split = plan.split;
+    if (plan.bn == 0) return whole ? mm4_pair<OUT, true>(a, b, g, K, st) : mm4_pair<OUT, false>(a, b, g, K, st);
     Mm4Args w = g;   // the weights on the lanes
     w.p = g.q;
     w.q = g.p;
@@ -98,11 +177,7 @@ cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t 
     w.s_q = g.s_p;
     w.store.rows_p = N;
     w.store.rows_q = M;
-    const int64_t kb = g.store.kblocks;
-    int split = 1;
-    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 192;
-    while (split < kSplitMost && 2 * split <= kb && ((N + 127) / 128) * ((M + bn - 1) / bn) * split * 2 <= 144) split *= 2;
-    switch (bn) {
+    switch (plan.bn) {
     case 16: return mm4_split<OUT, 16>(b, a, w, K, whole, split, st);
     case 32: return mm4_split<OUT, 32>(b, a, w, K, whole, split, st);
     case 64: return mm4_split<OUT, 64>(b, a, w, K, whole, split, st);
