@@ -541,11 +541,13 @@ q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const
  *   floats, whose contents before and after do not matter; calls that may run
  *   at the same time need one each.
  * dx may be dy, h or dh themselves.  M = 0 sets dw to zero.
+ * *status (may be NULL): Q_ST_TIMEOUT where a wait for the rows' copies ran out
+ * (2 s); dx and dw are not whole then.
  * 0 < K < 2^31.  Alignment: 16 bytes (dy, h, dh, weight, dx, work), 4 bytes
  * (rstd, dw).
  */
 q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void *h, const float *rstd, const void *weight, q_dtype wt,
-                   const void *dh, void *dx, void *dw, float *work, q_stream_t stream);
+                   const void *dh, void *dx, void *dw, float *work, int32_t *status, q_stream_t stream);
 int64_t norm_grad_work(int64_t M, int64_t K, q_dtype in);
 
 #ifdef __cplusplus

@@ -95,7 +95,7 @@ SIGNATURES = {
     "matmul_nvfp4": (_I, [_P, _P, _P, _I, _P, _P, _P, _I, _I64, _I64, _I64, _P, _I, _I, _P, _P]),
     "norm_add": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P]),
     "norm_q_blockwise": (_I, [_P, _I, _I64, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P, _P, _P]),
-    "norm_grad": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I, _P, _P, _P, _P, _P]),
+    "norm_grad": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
     "norm_grad_work": (_I64, [_I64, _I64, _I]),
     "dq_current_scaling": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _P]),
     "dq_mxfp8": (_I, [_P, _P, _I64, _I64, _I, _I, _I, _P, _P]),
@@ -904,12 +904,12 @@ def norm_q_blockwise(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
 
 
 def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dh: Optional[torch.Tensor] = None,
-              need_dw=True, out: Optional[torch.Tensor] = None):
+              need_dw=True, out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
     """``(dx, dw)`` of :func:`norm_add` from its ``h`` and ``rstd``: the gradient
     of x (and of the residual alike), with ``dh``, the gradient of h from where h
     is used again, added to it, and the weight's gradient in the weight's type
-    (None without ``need_dw``).  ``out`` (for dx) may be dy, h or dh.  It records no
-    gradient itself."""
+    (None without ``need_dw``).  ``out`` (for dx) may be dy, h or dh; ``status``
+    reports a kernel that gave up waiting.  It records no gradient itself."""
     dt, M, K = _norm_in("dy", dy, weight, None)
     _no_gradient("norm_grad", dy, h, rstd, weight, dh, out)
     dev = dy.device
@@ -927,7 +927,7 @@ def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: tor
     dw = torch.empty_like(weight) if need_dw else None
     work = _f32((lib().norm_grad_work(M, K, dt),), dev) if need_dw else None
     _call_on(dev, "norm_grad", dy.data_ptr(), dt, M, K, h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _DTYPES[weight.dtype], _ptr(dh),
-             dx.data_ptr(), _ptr(dw), _ptr(work), _stream(dev))
+             dx.data_ptr(), _ptr(dw), _ptr(work), None if status is None else _status(status, dev), _stream(dev))
     return dx, dw
 
 

@@ -32,6 +32,18 @@ template <int DT, int W> struct Piece {
             w[0] = *reinterpret_cast<const uint16_t *>(at);
         }
     }
+    QD void shared(const uint8_t *p, int i)
+    {
+        const uint8_t *const at = p + i * In<DT>::BYTES;
+        if constexpr (kBytes == 16) {
+            const uint4 v = lds16(at);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t *>(at);
+        } else {
+            w[0] = *reinterpret_cast<const uint16_t *>(at);
+        }
+    }
     QD void store(void *p, int64_t i) const
     {
         char *const at = static_cast<char *>(p) + i * In<DT>::BYTES;
@@ -49,6 +61,20 @@ template <int DT, int W> struct Piece {
         if constexpr (DT == F32) return __uint_as_float(w[j]);
         else if constexpr (W == 1) return __uint_as_float(w[0] << 16);
         else return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+    }
+    // Elements 2j and 2j + 1 as two packed FP32 values.
+    QD uint64_t pair(int j) const
+    {
+        static_assert(W % 2 == 0, "pairs");
+        if constexpr (DT == F32) return pack2(w[2 * j], w[2 * j + 1]);
+        else return pack2(w[j] << 16, w[j] & 0xFFFF0000u);
+    }
+    QD void set_pair(int j, uint64_t v)
+    {
+        float a, b;
+        unpack2(v, a, b);
+        if constexpr (DT == F32) w[2 * j] = __float_as_uint(a), w[2 * j + 1] = __float_as_uint(b);
+        else w[j] = bf16_pair(a, b);
     }
     QD void set(const float (&f)[W])
     {
@@ -121,36 +147,77 @@ QD float row_factor(float sum, int64_t K, float eps) { return __fdiv_rn(1.0f, __
 // What is made of a row: y, its rowwise copy, or nothing (its factor, and its sum with the residual).
 enum { kNormStore = 0, kNormCast = 1, kNormFactor = 2 };
 
-// W elements of y from column k of the row that begins at element `base` (zeros where `in` is false): stored, or cast
-// with the block of 128 that 128 / W lanes hold.  m: the largest |y| stored, where that is asked for.
-template <int DT, int W, int MODE> QD void norm_put(const NormArgs &a, float (&y)[W], bool in, int64_t base, int64_t k, int lane, uint32_t &m)
+// W elements of y to column k of the row that begins at element `base`.  m: the largest |y| stored, where that is asked for.
+template <int DT, int W> QD void norm_put(const NormArgs &a, const float (&y)[W], bool in, int64_t base, int64_t k, uint32_t &m)
 {
-    if constexpr (MODE == kNormStore) {
-        if (a.amax != nullptr) {
-            float b = 0.0f;
-#pragma unroll
-            for (int j = 0; j < W; j++) b = fmax_abs(b, y[j]);
-            m = max(m, __float_as_uint(b) & 0x7FFFFFFFu);
-        }
-        Piece<DT, W> out;
-        out.set(y);
-        if (in) out.store(a.y, base + k);
-    } else if constexpr (MODE == kNormCast) {
-        static_assert(W >= 4, "rows of the copy are multiples of 128 elements");
+    if (a.amax != nullptr) {
         float b = 0.0f;
 #pragma unroll
         for (int j = 0; j < W; j++) b = fmax_abs(b, y[j]);
-        const uint32_t bits = group_max<128 / W>(__float_as_uint(b) & 0x7FFFFFFFu);
-        const float alpha = alpha_from_amax(448.0f, __uint_as_float(bits));
+        if (in) m = max(m, __float_as_uint(b) & 0x7FFFFFFFu);
+    }
+    Piece<DT, W> out;
+    out.set(y);
+    if (in) out.store(a.y, base + k);
+}
+
+// y = (h s) w, zeros where `in` is false.
+template <int DT, int W> QD void norm_y(float (&y)[W], const Piece<DT, W> &h, float s, const float (&w)[W], bool in)
+{
+    if constexpr (W > 1) {
+        const uint64_t ss = pack2(__float_as_uint(s), __float_as_uint(s));
 #pragma unroll
-        for (int j = 0; j < W; j++) y[j] = y[j] * alpha;
-        if (!in) return;
-        uint8_t *const q = a.q_row + base + k;
-        if constexpr (W == 8) stg8(q, cvt_fp8x4<E4M3>(y[0], y[1], y[2], y[3]), cvt_fp8x4<E4M3>(y[4], y[5], y[6], y[7]));
-        else stg4(q, cvt_fp8x4<E4M3>(y[0], y[1], y[2], y[3]));
-        if (lane % (128 / W) == 0) {
-            a.s_row[(base + k) / 128] = __fdiv_rn(1.0f, alpha);
-            flag_nonfinite(a.status, bits);
+        for (int j = 0; j < W; j += 2) {
+            unpack2(fmul2(fmul2(h.pair(j / 2), ss), pack2(__float_as_uint(w[j]), __float_as_uint(w[j + 1]))), y[j], y[j + 1]);
+            if (!in) y[j] = y[j + 1] = 0.0f;
+        }
+    } else {
+        y[0] = in ? h.at(0) * s * w[0] : 0.0f;
+    }
+}
+
+// The rowwise copy of N pieces of W elements of y from the columns k0 + i step on (zeros outside the row), N blocks of 128
+// that LPB = 128 / W lanes share.  The N maxima are reduced over the lanes by a
+// halving exchange, after which each lane holds one block's, takes its quotients
+// once, and the alphas go back by index shuffles.
+template <int W, int N> QD void norm_cast(const NormArgs &a, float (&y)[N][W], int64_t base, int64_t k0, int64_t step, int lane)
+{
+    static_assert(W >= 4, "rows of the copy are multiples of 128 elements");
+    constexpr int LPB = 128 / W;
+    static_assert(N <= LPB, "a lane holds one block at most");
+    uint32_t m[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        float b = fmax_abs(fmax_abs(y[i][0], y[i][1]), fmax_abs(y[i][2], y[i][3]));
+        if constexpr (W == 8) b = fmax_abs(b, fmax_abs(fmax_abs(y[i][4], y[i][5]), fmax_abs(y[i][6], y[i][7])));
+        m[i] = __float_as_uint(b) & 0x7FFFFFFFu;
+    }
+    int o = LPB / 2;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2, o /= 2)
+#pragma unroll
+        for (int i = 0; i < n / 2; i++) {
+            const bool up = lane & o;
+            const uint32_t mine = up ? m[i + n / 2] : m[i], other = up ? m[i] : m[i + n / 2];
+            m[i] = max(mine, __shfl_xor_sync(0xFFFFFFFFu, other, o));
+        }
+#pragma unroll
+    for (; o > 0; o /= 2) m[0] = max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], o));
+    const float alpha = alpha_from_amax(448.0f, __uint_as_float(m[0]));
+    const int64_t k = k0 + (lane % LPB) / (LPB / N) * step;   // of the piece in this lane's block
+    if (lane % (LPB / N) == 0 && k < a.K) {
+        a.s_row[(base + k) / 128] = __fdiv_rn(1.0f, alpha);
+        flag_nonfinite(a.status, m[0]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const float f = N == 1 ? alpha : __shfl_sync(0xFFFFFFFFu, alpha, (lane & ~(LPB - 1)) + i * (LPB / N));
+#pragma unroll
+        for (int j = 0; j < W; j += 2) mul2(y[i][j], y[i][j + 1], f, f);
+        if (k0 + i * step < a.K) {
+            uint8_t *const q = a.q_row + base + k0 + i * step;
+            if constexpr (W == 8) stg8(q, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]), cvt_fp8x4<E4M3>(y[i][4], y[i][5], y[i][6], y[i][7]));
+            else stg4(q, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]));
         }
     }
 }
@@ -200,33 +267,54 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
 #pragma unroll
             for (int i = 0; i < VPT; i++) {
                 const int k = (t + i * g) * W;
-                float f[W];
+                if constexpr (W > 1) {
 #pragma unroll
-                for (int j = 0; j < W; j++) f[j] = h[i].at(j) + r[i].at(j);
-                h[i].set(f);
+                    for (int j = 0; j < W / 2; j++) h[i].set_pair(j, fadd2(h[i].pair(j), r[i].pair(j)));
+                } else {
+                    const float f[1] = {h[i].at(0) + r[i].at(0)};
+                    h[i].set(f);
+                }
                 if (live && k < K) h[i].store(a.h, base + k);
             }
         }
     }
     float sum = 0.0f;
+    if constexpr (W > 1) {
+        uint64_t two = 0;
 #pragma unroll
-    for (int i = 0; i < VPT; i++)
+        for (int i = 0; i < VPT; i++)
 #pragma unroll
-        for (int j = 0; j < W; j++) sum = __fmaf_rn(h[i].at(j), h[i].at(j), sum);
+            for (int j = 0; j < W / 2; j++) two = ffma2(h[i].pair(j), h[i].pair(j), two);
+        float odd;
+        unpack2(two, sum, odd);
+        sum += odd;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPT; i++) sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
+    }
     const float s = row_factor(row_sum(sum, part, a.gshift), K, a.eps);
     if (live && t == 0) a.rstd[row] = s;
     if constexpr (MODE == kNormFactor) return;
+    if constexpr (MODE == kNormCast && kAhead) {
+        float y[VPT][W];
+#pragma unroll
+        for (int i = 0; i < VPT; i++) {
+            const bool in = live && (t + i * g) * W < K;
+            norm_y<DT, W>(y[i], h[i], s, w[i], in);
+        }
+        if (live) norm_cast<W, VPT>(a, y, base, t * W, (int64_t)g * W, lane);   // a warp's rows are live together
+        return;
+    }
     uint32_t m = 0;   // largest |y| of this thread
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
         const int k = (t + i * g) * W;
         const bool in = live && k < K;
-        float *const wi = w[kAhead ? i : 0];
         if (!kAhead && in) load_weights<W>(w[0], a.weight, a.wf32, k);
-        float y[W];
-#pragma unroll
-        for (int j = 0; j < W; j++) y[j] = in ? h[i].at(j) * s * wi[j] : 0.0f;
-        norm_put<DT, W, MODE>(a, y, in, base, k, lane, m);
+        float y[1][W];
+        norm_y<DT, W>(y[0], h[i], s, w[kAhead ? i : 0], in);
+        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, base, in ? k : (int64_t)K, 0, lane);
+        else norm_put<DT, W>(a, y[0], in, base, k, m);
     }
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
@@ -264,92 +352,274 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
         const int64_t k = k0 + threadIdx.x * W;
         const bool in = k < a.K;
         Piece<DT, W> h;
-        float w[W], y[W];
+        float w[W], y[1][W];
         h.zero();
         if (in) {
             h.load(from, base + k);
             load_weights<W>(w, a.weight, a.wf32, k);
         }
-#pragma unroll
-        for (int j = 0; j < W; j++) y[j] = in ? h.at(j) * s * w[j] : 0.0f;
-        norm_put<DT, W, MODE>(a, y, in, base, k, lane, m);
+        norm_y<DT, W>(y[0], h, s, w, in);
+        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, base, k, 0, lane);
+        else norm_put<DT, W>(a, y[0], in, base, k, m);
     }
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
 
-// The gradient.  A row to 2^gshift threads as above; a thread keeps its columns over all rows of its walk, and with them
-// its part of dw in registers, which it leaves as one row of `work`.
-template <int DT, int W, int VPT, bool DH>
-__global__ void __launch_bounds__(512) k_norm_grad(const NormGradArgs a)
+// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.
+QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
-    __shared__ float part[2][32];
-    const int g = 1 << a.gshift, t = threadIdx.x & (g - 1), rows = blockDim.x >> a.gshift;
-    const int K = (int)a.K;
-    float w[VPT][W], dw[VPT][W];
-    griddep_wait();   // nothing was read or written so far
-#pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int k = (t + i * g) * W;
-#pragma unroll
-        for (int j = 0; j < W; j++) w[i][j] = dw[i][j] = 0.0f;
-        if (k < K) load_weights<W>(w[i], a.weight, a.wf32, k);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Many rows that begin between 16-byte boundaries (k_norm_rows reads them an element
+// at a time: 3001 x 1111 in FP32 11.1 us): by bulk copies into a ring of shared
+// memory, with the bytes around them, as the gradient does, one row a step.
+template <int DT, int E, bool RES>
+__global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int stages, int stage_bytes)
+{
+    constexpr int kMostStages = 8, ES = In<DT>::BYTES, kTensors = RES ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t dsm[];
+    __shared__ float part[2][16];
+    __shared__ __align__(8) uint64_t full[kMostStages];
+    const int t = threadIdx.x, lane = t & 31, T = blockDim.x, K = (int)a.K, tensor_bytes = stage_bytes / kTensors;
+    const int64_t steps = a.M > blockIdx.x ? (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    auto skew = [&](int64_t row) { return (int)((row * K * ES) & 15); };
+    auto issue = [&](int64_t i) {
+        const int64_t row = blockIdx.x + i * gridDim.x;
+        const int off = skew(row), s = (int)(i % stages);
+        const uint32_t bytes = (uint32_t)(off + K * ES + 15) & ~15u;
+        uint8_t *const st = dsm + (int64_t)s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], bytes * kTensors);
+        bulk_load(st, static_cast<const char *>(a.x) + row * K * ES - off, bytes, &full[s]);
+        if constexpr (RES) bulk_load(st + tensor_bytes, static_cast<const char *>(a.residual) + row * K * ES - off, bytes, &full[s]);
+    };
+    if (t == 0) {
+        for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);
+        fence_mbar_init();
     }
-    int flip = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < a.M; row0 += (int64_t)gridDim.x * rows, flip ^= 1) {
-        const int64_t row = row0 + (threadIdx.x >> a.gshift), base = row * a.K;
-        const bool live = row < a.M;
-        const float s = live ? a.rstd[row] : 0.0f;
-        Piece<DT, W> h[VPT], dy[VPT], dh[DH ? VPT : 1];
+    __syncthreads();
+    griddep_wait();   // nothing was read or written so far
+    if (t == 0)
+        for (int64_t i = 0; i < steps && i < stages; i++) issue(i);
+    float w[E][1];
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const int k = (t + i * g) * W;
-            h[i].zero();
-            dy[i].zero();
-            if (live && k < K) {
-                dy[i].load(a.dy, base + k);
-                h[i].load(a.h, base + k);
-                if constexpr (DH) dh[i].load(a.dh, base + k);
-            }
-        }
+    for (int i = 0; i < E; i++)
+        if (t + i * T < K) load_weights<1>(w[i], a.weight, a.wf32, t + i * T);
+    uint32_t m = 0;
+    int s = 0;
+    uint32_t parity = 0;
+    for (int64_t n = 0; n < steps; n++) {
+        const int64_t row = blockIdx.x + n * gridDim.x;
+        const uint8_t *const st = dsm + (int64_t)s * stage_bytes + skew(row);
+        const bool ok = mbar_wait_bounded(&full[s], parity);
+        Piece<DT, 1> h[E];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < VPT; i++)
-#pragma unroll
-            for (int j = 0; j < W; j++) {
-                const float v = h[i].at(j) * s, d = dy[i].at(j);
-                dw[i][j] = __fmaf_rn(d, v, dw[i][j]);
-                sum = __fmaf_rn(d * w[i][j], v, sum);
+        for (int i = 0; i < E; i++) {
+            const int k = t + i * T;
+            h[i].zero();
+            if (k < K) {
+                h[i].shared(st, k);
+                if constexpr (RES) {
+                    Piece<DT, 1> r;
+                    r.shared(st + tensor_bytes, k);
+                    const float f[1] = {h[i].at(0) + r.at(0)};
+                    h[i].set(f);
+                }
             }
-        const float c = __fdiv_rn(row_sum(sum, part[flip], a.gshift), (float)K);
+            sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) part[n & 1][t >> 5] = sum;
+        if (__syncthreads_or(!ok)) {   // the copies in flight land before shared memory goes away
+            if (t == 0) {
+                for (int64_t j = n; j < steps && j < n + stages; j++) (void)mbar_wait_bounded(&full[j % stages], (uint32_t)((j / stages) & 1));
+                if (a.status != nullptr) atomicOr(a.status, kStTimeout);
+            }
+            break;
+        }
+        if (t == 0 && n + stages < steps) {   // every thread has the stage in its registers
+            fence_proxy_async();
+            issue(n + stages);
+        }
+        const float f = row_factor(warp_sum(lane < (T >> 5) ? part[n & 1][lane] : 0.0f), K, a.eps);
+        if (t == 0) a.rstd[row] = f;
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const int k = (t + i * g) * W;
-            if (live && k < K) {
-                float f[W];
+        for (int i = 0; i < E; i++) {
+            const int k = t + i * T;
+            if (k < K) {
+                if constexpr (RES) h[i].store(a.h, row * K + k);
+                float y[1] = {h[i].at(0) * f * w[i][0]};
+                norm_put<DT, 1>(a, y, true, row * K, k, m);
+            }
+        }
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+    if (a.amax != nullptr) norm_amax<DT>(a, m);
+}
+
+// The gradient.  The rows of dy, h and dh come by bulk copies into a ring of
+// shared memory, so that memory stays busy while rows are summed: a step is R rows,
+// each over all threads of the CTA, or 8 R short ones, R for a warp (where E is 8), E
+// elements per thread in pieces of W.  A thread keeps its columns over all steps, and with them its part of
+// dw in registers, which it leaves as one row of `work`.  Rows that begin between
+// 16-byte boundaries are copied with the bytes around them (a 16-byte piece that holds
+// one of the row's bytes is the allocation's) and read an element at a time.
+template <int DT, int W, int E, int R, bool DH>
+__global__ void __launch_bounds__(512) k_norm_grad(const NormGradArgs a, int stages, int stage_bytes)
+{
+    constexpr bool kWarpRows = E == 8;
+    constexpr int VPT = E / W, kMostStages = 8, ES = In<DT>::BYTES, kTensors = DH ? 3 : 2;
+    extern __shared__ __align__(128) uint8_t dsm[];
+    __shared__ float part[2][R][16];
+    __shared__ __align__(8) uint64_t full[kMostStages];
+    const int lane = threadIdx.x & 31, rows = kWarpRows ? 8 * R : R;
+    const int T = kWarpRows ? 32 : blockDim.x, t = kWarpRows ? lane : threadIdx.x, mine = kWarpRows ? (threadIdx.x >> 5) * R : 0;   // the first row
+    const int K = (int)a.K, tensor_bytes = stage_bytes / kTensors;
+    const int64_t steps_all = (a.M + rows - 1) / rows;
+    const int64_t steps = steps_all > blockIdx.x ? (steps_all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    // step i of this CTA: rows from row0(i) on, whose bytes begin `skew` into their copies
+    auto row0 = [&](int64_t i) { return ((int64_t)blockIdx.x + i * gridDim.x) * rows; };
+    auto skew = [&](int64_t row) { return W > 1 ? 0 : (int)((row * K * ES) & 15); };
+    auto issue = [&](int64_t i) {
+        const int64_t r0 = row0(i), n = a.M - r0 < rows ? a.M - r0 : rows;
+        const int off = skew(r0);
+        const uint32_t bytes = (uint32_t)(off + n * K * ES + 15) & ~15u;
+        const int s = (int)(i % stages);
+        uint8_t *const st = dsm + (int64_t)s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], bytes * kTensors);
+        const int64_t from = r0 * K * ES - off;
+        bulk_load(st, static_cast<const char *>(a.dy) + from, bytes, &full[s]);
+        bulk_load(st + tensor_bytes, static_cast<const char *>(a.h) + from, bytes, &full[s]);
+        if constexpr (DH) bulk_load(st + 2 * tensor_bytes, static_cast<const char *>(a.dh) + from, bytes, &full[s]);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();   // nothing was read or written so far
+    if (threadIdx.x == 0)
+        for (int64_t i = 0; i < steps && i < stages; i++) issue(i);
+    // The weights too, where registers allow; else they are loaded (from L1) where they are used.
+    constexpr bool kHeld = E <= 16;
+    float w[kHeld ? VPT : 1][W], dw[VPT][W];
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const int k = (t + i * T) * W;
+#pragma unroll
+        for (int j = 0; j < W; j++) w[kHeld ? i : 0][j] = dw[i][j] = 0.0f;
+        if (kHeld && k < K) load_weights<W>(w[kHeld ? i : 0], a.weight, a.wf32, k);
+    }
+    const float inv = __fdiv_rn(1.0f, (float)K);
+    int s = 0;
+    uint32_t parity = 0;
+    for (int64_t n = 0; n < steps; n++) {
+        const int64_t r0 = row0(n) + mine;
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) f[r] = r0 + r < a.M ? __ldg(a.rstd + r0 + r) : 0.0f;
+        const uint8_t *const st = dsm + (int64_t)s * stage_bytes + skew(row0(n)) + (int64_t)mine * K * ES;
+        const bool ok = mbar_wait_bounded(&full[s], parity);
+        Piece<DT, W> h[R][VPT], dy[R][VPT], dh[DH ? R : 1][DH ? VPT : 1];
+        float c[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const uint8_t *const at = st + r * K * ES;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                const int k = (t + i * T) * W;
+                h[r][i].zero();
+                dy[r][i].zero();
+                if (r0 + r < a.M && k < K) {
+                    dy[r][i].shared(at, k);
+                    h[r][i].shared(at + tensor_bytes, k);
+                    if constexpr (DH) dh[r][i].shared(at + 2 * tensor_bytes, k);
+                    if (!kHeld) load_weights<W>(w[0], a.weight, a.wf32, k);
+                }
 #pragma unroll
                 for (int j = 0; j < W; j++) {
-                    const float v = h[i].at(j) * s, e = __fmaf_rn(-v, c, dy[i].at(j) * w[i][j]);
-                    f[j] = DH ? __fmaf_rn(e, s, dh[DH ? i : 0].at(j)) : e * s;
+                    const float v = h[r][i].at(j) * f[r], d = dy[r][i].at(j);
+                    dw[i][j] = __fmaf_rn(d, v, dw[i][j]);
+                    sum = __fmaf_rn(d * w[kHeld ? i : 0][j], v, sum);
+                }
+            }
+            c[r] = sum;
+        }
+        // the rows' sums, and word that a wait ran out (no thread waits for another step then)
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            c[r] = warp_sum(c[r]);
+            if (!kWarpRows && lane == 0) part[n & 1][r][threadIdx.x >> 5] = c[r];
+        }
+        const bool stop = __syncthreads_or(!ok);
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            if (!kWarpRows) c[r] = warp_sum(lane < (int)(blockDim.x >> 5) ? part[n & 1][r][lane] : 0.0f);
+            c[r] *= inv;
+        }
+        if (stop) {   // the copies in flight land before shared memory goes away
+            if (threadIdx.x == 0) {
+                for (int64_t j = n; j < steps && j < n + stages; j++) (void)mbar_wait_bounded(&full[j % stages], (uint32_t)((j / stages) & 1));
+                if (a.status != nullptr) atomicOr(a.status, kStTimeout);
+            }
+            break;
+        }
+        if (threadIdx.x == 0 && n + stages < steps) {   // every thread has the stage in its registers
+            fence_proxy_async();
+            issue(n + stages);
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                const int k = (t + i * T) * W;
+                if (r0 + r >= a.M || k >= K) continue;
+                float o[W];
+                if (!kHeld) load_weights<W>(w[0], a.weight, a.wf32, k);
+#pragma unroll
+                for (int j = 0; j < W; j++) {
+                    const float v = h[r][i].at(j) * f[r], e = __fmaf_rn(-v, c[r], dy[r][i].at(j) * w[kHeld ? i : 0][j]);
+                    o[j] = DH ? __fmaf_rn(e, f[r], dh[DH ? r : 0][DH ? i : 0].at(j)) : e * f[r];
                 }
                 Piece<DT, W> out;
-                out.set(f);
-                out.store(a.dx, base + k);
+                out.set(o);
+                out.store(a.dx, (r0 + r) * K + k);
             }
+        }
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
         }
     }
     if (a.work == nullptr) return;
-    float *const mine = a.work + ((int64_t)blockIdx.x * rows + (threadIdx.x >> a.gshift)) * a.K;
+    // one row of `work`: the CTA's only part, or the sum of eight, which meet where the rows were
+    float *const to = !kWarpRows ? a.work + (int64_t)blockIdx.x * K : reinterpret_cast<float *>(dsm) + (threadIdx.x >> 5) * K;
+    if (kWarpRows) __syncthreads();
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
-        const int k = (t + i * g) * W;
+        const int k = (t + i * T) * W;
         if (k < K) {
             if constexpr (W % 4 == 0) {
 #pragma unroll
-                for (int j = 0; j < W; j += 4) *reinterpret_cast<float4 *>(mine + k + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+                for (int j = 0; j < W; j += 4) *reinterpret_cast<float4 *>(to + k + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
             } else {
 #pragma unroll
-                for (int j = 0; j < W; j++) mine[k + j] = dw[i][j];
+                for (int j = 0; j < W; j++) to[k + j] = dw[i][j];
             }
+        }
+    }
+    if (kWarpRows) {
+        __syncthreads();
+        for (int k = threadIdx.x; k < K; k += blockDim.x) {
+            float sum = reinterpret_cast<const float *>(dsm)[k];
+            for (int r = 1; r < 8; r++) sum += reinterpret_cast<const float *>(dsm)[r * K + k];
+            a.work[(int64_t)blockIdx.x * K + k] = sum;
         }
     }
 }
@@ -395,29 +665,34 @@ __global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a)
     }
 }
 
-// dw: the rows of `work`, added in the same order every time (eight walks of every eighth row, then the walks).
-__global__ void __launch_bounds__(256) k_norm_dw(const float *work, int64_t parts, int64_t K, void *dw, bool f32)
+// dw: the rows of `work`, added in the same order every time: 64 walks of every 64th row, then the walks.
+__global__ void __launch_bounds__(1024) k_norm_dw(const float *work, int64_t parts, int64_t K, void *dw, bool f32)
 {
-    __shared__ float sums[8][32];
-    const int c = threadIdx.x & 31, walk = threadIdx.x >> 5;
-    const int64_t k = (int64_t)blockIdx.x * 32 + c;
+    __shared__ float sums[64][17];
+    const int c = threadIdx.x & 15, walk = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t k = (int64_t)blockIdx.x * 16 + c;
     griddep_wait();
     float sum = 0.0f;
-    if (k < K)
-        for (int64_t p = walk; p < parts; p += 8) sum += work[p * K + k];
+    if (k < K) {
+#pragma unroll 8
+        for (int64_t p = walk; p < parts; p += 64) sum += work[p * K + k];
+    }
     sums[walk][c] = sum;
     __syncthreads();
-    if (walk == 0 && k < K) {
-#pragma unroll
-        for (int i = 1; i < 8; i++) sum += sums[i][c];
-        if (f32) static_cast<float *>(dw)[k] = sum;
-        else static_cast<uint16_t *>(dw)[k] = (uint16_t)bf16_bits(sum);
+    if (warp >= 16) return;
+    sum = warp_sum(sums[lane][warp] + sums[lane + 32][warp]);   // the walks of column `warp`
+    const int64_t at = (int64_t)blockIdx.x * 16 + warp;
+    if (lane == 0 && at < K) {
+        if (f32) static_cast<float *>(dw)[at] = sum;
+        else static_cast<uint16_t *>(dw)[at] = (uint16_t)bf16_bits(sum);
     }
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
+
+constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM's CTAs for rows on their way
 
 int log2_up(int64_t n)
 {
@@ -450,52 +725,103 @@ template <int DT, int W, int MODE> cudaError_t norm_w(const NormArgs &a, cudaStr
                     dim3((unsigned)a.M), dim3(1024), 0, st, a);
 }
 
+template <int DT, int E, bool RES> cudaError_t norm_ring_t(const NormArgs &a, int threads, int per_sm, cudaStream_t st)
+{
+    const int bytes = (RES ? 2 : 1) * (int)((a.K * In<DT>::BYTES + 15) / 16 * 16 + 16), fit = kRingBytes / per_sm / bytes;
+    const cudaError_t e = engine_smem_ready<k_norm_ring<DT, E, RES>>(kRingBytes, true);
+    if (e != cudaSuccess) return e;
+    const int stages = fit < 8 ? fit : 8;
+    const int64_t most = (int64_t)per_sm * sm_count();
+    return launch_k(true, k_norm_ring<DT, E, RES>, dim3((unsigned)(a.M < most ? a.M : most)), dim3(threads), (size_t)stages * bytes, st,
+                    a, stages, bytes);
+}
+
+// Odd rows of 256 to 8192 elements, enough of them to keep every CTA's ring busy.
+template <int DT> bool norm_ring(const NormArgs &a, cudaStream_t st, cudaError_t &e)
+{
+    if (a.K <= 256 || a.K > 8192) return false;
+    constexpr int E = 16;
+    const int threads = (int)((a.K + 32 * E - 1) / (32 * E)) * 32, per_sm = 512 / threads < 8 ? 512 / threads : 8;
+    if (a.M < 2 * per_sm * sm_count()) return false;
+    e = a.residual != nullptr ? norm_ring_t<DT, E, true>(a, threads, per_sm, st) : norm_ring_t<DT, E, false>(a, threads, per_sm, st);
+    return true;
+}
+
 template <int DT, int MODE> cudaError_t norm_t(const NormArgs &a, cudaStream_t st)
 {
+    if constexpr (MODE == kNormStore) {
+        cudaError_t e;
+        if (a.K % In<DT>::VEC != 0 && norm_ring<DT>(a, st, e)) return e;
+    }
     if constexpr (MODE != kNormCast) {
         if (a.K % In<DT>::VEC != 0) return norm_w<DT, 1, MODE>(a, st);
     }
     return norm_w<DT, In<DT>::VEC, MODE>(a, st);
 }
 
-// How a gradient's rows are laid out: threads of a row (2^gshift; 0: the loop over long rows), CTAs, and rows of `work`.
+// How a gradient's rows are laid out: rows of a step, elements of a thread (0: the loop over long rows), threads, CTAs,
+// and the ring.  Two rows a step share a reduction (8192 x 4096 BF16 without dh 41.8 us
+// at one, 37.8 at two), unless they spill (with dh 46.4 and 52.3, and dw's 3 in each);
+// 16 elements a thread beat 8 on twice the threads (46.8 and 56.7).
 struct GradPlan {
-    int gshift, vpt, threads, ctas, parts;
+    int rows, elements, threads, ctas, stages, stage_bytes;
 };
-GradPlan grad_plan(int64_t M, int64_t K, int dt)
+GradPlan grad_plan(int64_t M, int64_t K, int dt, bool dh)
 {
-    const int vec = dt == BF16 ? 8 : 4, W = K % vec == 0 ? vec : 1;
-    const int64_t pieces = (K + W - 1) / W;
-    GradPlan p = {};
-    // elements of a thread: 4 or 16 single ones, 8 or 16 in pieces
-    for (const int E : {W == 1 ? 4 : 8, 16}) {
-        const int s = log2_up((pieces + E / W - 1) / (E / W));
-        if (s > (E == 16 ? 9 : 8)) continue;
-        p.gshift = s < 5 ? 5 : s;
-        p.vpt = E / W;
-        break;
+    const int es = dt == BF16 ? 2 : 4, tensors = dh ? 3 : 2;
+    GradPlan p = {1, 0, 1024, 0, 0, 0};
+    // The shared memory of an SM holds the rings of all CTAs, two steps in each at least.
+    auto copy_bytes = [&](int rows) { return (rows * K * es + 15) / 16 * 16 + (K * es % 16 != 0 ? 16 : 0); };   // and what lies around the rows
+    int per_sm = 1;
+    if (K <= 256) {
+        p.rows = 32;
+        p.elements = 8;
+        p.threads = 256;
+        per_sm = 2;
+    } else if (K <= 16384 && 2 * tensors * copy_bytes(1) <= kRingBytes) {
+        p.elements = K <= 8192 ? 16 : 32;
+        p.threads = (int)((K + 32 * p.elements - 1) / (32 * p.elements)) * 32;
+        p.rows = p.elements == 16 && !dh && K * es % 16 == 0 && 4 * tensors * copy_bytes(2) <= kRingBytes ? 2 : 1;
+        per_sm = 512 / p.threads < 8 ? 512 / p.threads : 8;
     }
-    p.threads = p.gshift == 0 ? 1024 : p.gshift < 8 ? 256 : 1 << p.gshift;
-    const int rows = p.gshift == 0 ? 1 : p.threads >> p.gshift;
-    const int64_t most = p.threads == 256 ? 608 : p.threads == 512 ? 304 : 152, need = (M + rows - 1) / rows;
+    if (p.elements != 0) {
+        p.stage_bytes = tensors * (int)copy_bytes(p.rows);
+        const int fits = kRingBytes / (2 * p.stage_bytes);
+        per_sm = per_sm > fits ? fits : per_sm;
+        p.stages = kRingBytes / per_sm / p.stage_bytes;
+        if (p.stages > 8) p.stages = 8;
+    }
+    const int64_t most = (int64_t)per_sm * 152, need = (M + p.rows - 1) / p.rows;
     p.ctas = (int)(need < most ? need : most);
-    p.parts = p.ctas * rows;
     return p;
 }
 
-template <int DT, int W, int VPT> cudaError_t grad_rows(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
+template <int DT, int W, int E, int R, bool DH> cudaError_t grad_rows(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
 {
-    return launch_k(true, a.dh != nullptr ? k_norm_grad<DT, W, VPT, true> : k_norm_grad<DT, W, VPT, false>, dim3(p.ctas),
-                    dim3(p.threads), 0, st, a);
+    const cudaError_t e = engine_smem_ready<k_norm_grad<DT, W, E, R, DH>>(kRingBytes, true);
+    if (e != cudaSuccess) return e;
+    return launch_k(true, k_norm_grad<DT, W, E, R, DH>, dim3(p.ctas), dim3(p.threads), (size_t)p.stages * p.stage_bytes, st, a,
+                    p.stages, p.stage_bytes);
 }
 
-template <int DT, int W> cudaError_t grad_w(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
+template <int DT, int W, bool DH> cudaError_t grad_w(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
 {
-    constexpr int V = W == 1 ? 4 : 8 / W;
-    if (p.gshift == 0)
-        return launch_k(true, a.dh != nullptr ? k_norm_grad_long<DT, W, true> : k_norm_grad_long<DT, W, false>, dim3(p.ctas),
-                        dim3(p.threads), 0, st, a);
-    return p.vpt == V ? grad_rows<DT, W, V>(a, p, st) : grad_rows<DT, W, 16 / W>(a, p, st);
+    switch (p.elements) {
+    case 8: return grad_rows<DT, W, 8, 4, DH>(a, p, st);
+    case 16:
+        if constexpr (!DH && W > 1)
+            if (p.rows == 2) return grad_rows<DT, W, 16, 2, DH>(a, p, st);
+        return grad_rows<DT, W, 16, 1, DH>(a, p, st);
+    case 32: return grad_rows<DT, W, 32, 1, DH>(a, p, st);
+    default: return launch_k(true, k_norm_grad_long<DT, W, DH>, dim3(p.ctas), dim3(p.threads), 0, st, a);
+    }
+}
+
+template <int DT> cudaError_t grad_t(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
+{
+    constexpr int VEC = In<DT>::VEC;
+    if (a.K % VEC != 0) return a.dh != nullptr ? grad_w<DT, 1, true>(a, p, st) : grad_w<DT, 1, false>(a, p, st);
+    return a.dh != nullptr ? grad_w<DT, VEC, true>(a, p, st) : grad_w<DT, VEC, false>(a, p, st);
 }
 
 }  // namespace
@@ -515,19 +841,21 @@ cudaError_t launch_norm_cast_rows(const NormArgs &a, int dt, cudaStream_t st)
     return dt == BF16 ? norm_t<BF16, kNormCast>(a, st) : norm_t<F32, kNormCast>(a, st);
 }
 
-int64_t norm_grad_rows(int64_t M, int64_t K, int dt) { return grad_plan(M, K, dt).parts; }
+int64_t norm_grad_rows(int64_t M, int64_t K, int dt)
+{
+    // enough with dh and without it
+    const GradPlan p = grad_plan(M, K, dt, false), q = grad_plan(M, K, dt, true);
+    return p.ctas > q.ctas ? p.ctas : q.ctas;
+}
 
 cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st)
 {
-    const GradPlan p = grad_plan(a.M, a.K, dt);
-    a.gshift = p.gshift;
+    const GradPlan p = grad_plan(a.M, a.K, dt, a.dh != nullptr);
     if (dw == nullptr) a.work = nullptr;
-    const bool vec = a.K % (dt == BF16 ? 8 : 4) == 0;
-    cudaError_t e = dt == BF16 ? (vec ? grad_w<BF16, 8>(a, p, st) : grad_w<BF16, 1>(a, p, st))
-                               : (vec ? grad_w<F32, 4>(a, p, st) : grad_w<F32, 1>(a, p, st));
+    const cudaError_t e = dt == BF16 ? grad_t<BF16>(a, p, st) : grad_t<F32>(a, p, st);
     if (e != cudaSuccess || dw == nullptr) return e;
-    return launch_k(true, k_norm_dw, dim3((unsigned)((a.K + 31) / 32)), dim3(256), 0, st, (const float *)a.work, (int64_t)p.parts,
-                    a.K, dw, a.wf32);
+    return launch_k(true, k_norm_dw, dim3((unsigned)((a.K + 15) / 16)), dim3(1024), 0, st, (const float *)a.work,
+                    (int64_t)p.ctas, a.K, dw, a.wf32);
 }
 
 }  // namespace qk

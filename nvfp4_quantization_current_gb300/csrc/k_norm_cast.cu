@@ -13,6 +13,23 @@ namespace qk {
 
 namespace {
 
+// N weights from column k on; zeros where `in` is false.
+template <int N> QD void col_weights(float (&w)[N], const void *weight, bool f32, int64_t k, bool in)
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+        float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (in && f32) {
+            f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(weight) + k + c));
+        } else if (in) {
+            const uint2 b = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(weight) + k + c));
+            f = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
+                            __uint_as_float(b.y & 0xFFFF0000u));
+        }
+        w[c] = f.x, w[c + 1] = f.y, w[c + 2] = f.z, w[c + 3] = f.w;
+    }
+}
+
 template <int DT>
 __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K,
                                                               const float *__restrict__ rstd, const void *__restrict__ weight,
@@ -20,7 +37,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
                                                               float *__restrict__ s_colT, int32_t *status)
 {
     constexpr int VEC = In<DT>::VEC, TC = 32 * VEC, CW = VEC / 4, TPC = kEngThreads / TC;   // threads per column
-    __shared__ __align__(16) uint32_t part[kEngWarps][TC];   // per-warp column maxima
+    __shared__ __align__(16) float part[kEngWarps][CW][32][4];   // per-warp column maxima, of four columns of each lane in turn
     __shared__ __align__(16) float calpha[TC];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int64_t tiles_m = M / kTileRowsE, tiles_k = (K + TC - 1) / TC;
@@ -34,42 +51,58 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
         float s[8], w[VEC];
 #pragma unroll
         for (int j = 0; j < 8; j++) s[j] = __ldg(rstd + mb + 8 * warp + j);
-#pragma unroll
-        for (int c = 0; c < VEC; c++)
-            w[c] = k >= K ? 0.0f : wf32 ? __ldg(static_cast<const float *>(weight) + k + c)
-                                        : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(weight) + k + c) << 16);
+        col_weights<VEC>(w, weight, wf32, k, k < K);
+        // y = (h s) w for a pair of a row's elements
+        auto y2 = [&](int j, int c, float &y0, float &y1) {
+            y0 = elem<DT>(v[j], c);
+            y1 = elem<DT>(v[j], c + 1);
+            mul2(y0, y1, s[j], s[j]);
+            mul2(y0, y1, w[c], w[c + 1]);
+        };
         float top[VEC];
 #pragma unroll
         for (int c = 0; c < VEC; c++) top[c] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j++)
 #pragma unroll
-            for (int c = 0; c < VEC; c++) top[c] = fmax_abs(top[c], elem<DT>(v[j], c) * s[j] * w[c]);
+            for (int c = 0; c < VEC; c += 2) {
+                float y0, y1;
+                y2(j, c, y0, y1);
+                top[c] = fmax_abs(top[c], y0);
+                top[c + 1] = fmax_abs(top[c + 1], y1);
+            }
 #pragma unroll
-        for (int c = 0; c < VEC; c++) part[warp][lane * VEC + c] = __float_as_uint(top[c]) & 0x7FFFFFFFu;
+        for (int c = 0; c < VEC; c += 4)   // four columns at a time, a quarter warp's 128 bytes: no two lanes on one bank
+            *reinterpret_cast<float4 *>(&part[warp][c / 4][lane][0]) = make_float4(top[c], top[c + 1], top[c + 2], top[c + 3]);
         __syncthreads();
         {
-            const int col = t / TPC, sub = t % TPC;
-            uint32_t b = 0;
+            const int col = t / TPC, sub = t % TPC, l = col / VEC, q = col % VEC;   // lane l's column q
+            float b = 0.0f;
 #pragma unroll
-            for (int i = sub; i < kEngWarps; i += TPC) b = max(b, part[i][col]);
-            b = group_max<TPC>(b);
+            for (int i = sub; i < kEngWarps; i += TPC) b = fmax_abs(b, part[i][q / 4][l][q % 4]);
+            const uint32_t bits = group_max<TPC>(__float_as_uint(b) & 0x7FFFFFFFu);
             if (sub == 0) {
-                const float alpha = alpha_from_amax(448.0f, __uint_as_float(b));
+                const float alpha = alpha_from_amax(448.0f, __uint_as_float(bits));
                 calpha[col] = alpha;
                 if (kb + col < K) {
                     s_colT[(kb + col) * (M / 128) + tm] = __fdiv_rn(1.0f, alpha);
-                    flag_nonfinite(status, b);
+                    flag_nonfinite(status, bits);
                 }
             }
         }
         __syncthreads();
+        float ca[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; c += 4) *reinterpret_cast<float4 *>(ca + c) = *reinterpret_cast<const float4 *>(&calpha[lane * VEC + c]);
         uint32_t code[8][CW];
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             float f[VEC];
 #pragma unroll
-            for (int c = 0; c < VEC; c++) f[c] = elem<DT>(v[j], c) * s[j] * w[c] * calpha[lane * VEC + c];
+            for (int c = 0; c < VEC; c += 2) {
+                y2(j, c, f[c], f[c + 1]);
+                mul2(f[c], f[c + 1], ca[c], ca[c + 1]);
+            }
 #pragma unroll
             for (int q = 0; q < CW; q++) code[j][q] = cvt_fp8x4<E4M3>(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
         }

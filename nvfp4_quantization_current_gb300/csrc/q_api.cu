@@ -585,7 +585,7 @@ int64_t norm_grad_work(int64_t M, int64_t K, q_dtype in)
 }
 
 q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void *h, const float *rstd, const void *weight, q_dtype wt,
-                   const void *dh, void *dx, void *dw, float *work, q_stream_t stream)
+                   const void *dh, void *dx, void *dw, float *work, int32_t *status, q_stream_t stream)
 {
     const char *fn = "norm_grad";
     TRY(check_norm(fn, M, K, weight, wt));
@@ -601,7 +601,7 @@ q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void 
     if (dh != nullptr) TRY(need(fn, "dh", dh, 16));
     TRY(need(fn, "dx", dx, 16));
     if (dw != nullptr) TRY(need(fn, "work", work, 16));
-    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, M, K, 0};
+    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, status, M, K};
     LAUNCH(fn, qk::launch_norm_grad(a, (int)in, dw, S(stream)));
     return Q_OK;
 }

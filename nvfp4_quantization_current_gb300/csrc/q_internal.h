@@ -139,8 +139,8 @@ struct NormGradArgs {
     const float *rstd;
     void *dx;
     float *work;
+    int32_t *status;
     int64_t M, K;
-    int gshift;   // set by the launcher
 };
 int64_t norm_grad_rows(int64_t M, int64_t K, int dt);   // rows of K floats in `work`
 cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st);

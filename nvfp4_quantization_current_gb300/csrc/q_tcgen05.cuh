@@ -203,28 +203,6 @@ QD void mma_commit_pair(uint64_t *bar)
 template <int N> QD void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> QD void regs_fewer() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Two FP32 values in a 64-bit register, and packed FP32 arithmetic on them
-// (each half rounded as the scalar instruction rounds it).
-QD uint64_t pack2(uint32_t a, uint32_t b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-QD void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-QD uint64_t fmul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-QD uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // ---------------------------------------------------------------------------
 // accumulator loads, complete when they return.  A load and its wait are one
 // statement: between two, the compiler may use (it moves) registers that the

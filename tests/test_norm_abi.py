@@ -22,7 +22,7 @@ def cast_args(x=A, dt=Q.Q_BF16, M=128, K=256, r=A, w=A, wt=Q.Q_F32, eps=1e-6, h=
 
 
 def grad_args(dy=A, dt=Q.Q_F32, M=4, K=250, h=A, s=A, w=A, wt=Q.Q_F32, dh=A, dx=A, dw=A, work=A):
-    return dy, dt, M, K, h, s, w, wt, dh, dx, dw, work, None
+    return dy, dt, M, K, h, s, w, wt, dh, dx, dw, work, None, None
 
 
 ARGS = {"norm_add": add_args, "norm_q_blockwise": cast_args, "norm_grad": grad_args}
@@ -110,7 +110,7 @@ def test_binding_refusals(calls):
     with pytest.raises(ValueError, match="h_out without"):
         Q.norm_q_blockwise(x, w, h_out=x)
     for kw, text in ((dict(h=fake((4, 255), bf)), "h must"), (dict(rstd=fake((5,), f32)), "rstd must"), (dict(dh=fake((4, 256), f32)), "dh must"),
-                     (dict(out=fake((3, 256), bf)), "out must")):
+                     (dict(out=fake((3, 256), bf)), "out must"), (dict(status=s), "status must")):
         with pytest.raises(ValueError, match=text):
             Q.norm_grad(**{**dict(dy=x, h=x, rstd=s, weight=w), **kw})
     assert calls == []
