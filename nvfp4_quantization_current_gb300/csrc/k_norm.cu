@@ -76,6 +76,16 @@ template <int DT, int W> struct Piece {
         if constexpr (DT == F32) w[2 * j] = __float_as_uint(a), w[2 * j + 1] = __float_as_uint(b);
         else w[j] = bf16_pair(a, b);
     }
+    QD void add(const Piece &p)
+    {
+        if constexpr (W > 1) {
+#pragma unroll
+            for (int j = 0; j < W / 2; j++) set_pair(j, fadd2(pair(j), p.pair(j)));
+        } else {
+            const float f[1] = {at(0) + p.at(0)};
+            set(f);
+        }
+    }
     QD void set(const float (&f)[W])
     {
         if constexpr (DT == F32) {
@@ -129,6 +139,26 @@ QD float warp_sum(float v)
     return v;
 }
 
+// The sum of squares of a thread's pieces.
+template <int DT, int W, int N> QD float squares(const Piece<DT, W> (&h)[N])
+{
+    float sum = 0.0f;
+    if constexpr (W > 1) {
+        uint64_t two = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+#pragma unroll
+            for (int j = 0; j < W / 2; j++) two = ffma2(h[i].pair(j), h[i].pair(j), two);
+        float odd;
+        unpack2(two, sum, odd);
+        sum += odd;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
+    }
+    return sum;
+}
+
 // Sum over the 2^gshift consecutive threads (gshift >= 5) that share a row, to
 // all of them; part: a word per warp, used by no other call that is in flight.
 // Every thread of the CTA calls it.
@@ -142,7 +172,16 @@ QD float row_sum(float v, float *part, int gshift)
     return warp_sum(lane < n ? part[(warp & ~(n - 1)) + lane] : 0.0f);
 }
 
-QD float row_factor(float sum, int64_t K, float eps) { return __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(sum, (float)K) + eps)); }
+// 1 / sqrt(sum / K + eps): the approximate root's reciprocal (two units in the last place) after one step of Newton's
+// iteration, which squares its error; every thread of a row takes it, and a division, a
+// root and a division are some 60 instructions.  A v of zero, infinity or NaN goes
+// as it is (the step would make NaNs of the first two).
+QD float row_factor(float sum, float inv, float eps)
+{
+    const float v = __fmaf_rn(sum, inv, eps), y = rsqrtf(v);
+    const float e = __fmaf_rn(-(v * y), y, 1.0f);
+    return v > 0.0f && v < __int_as_float(0x7F800000) ? __fmaf_rn(0.5f * y, e, y) : y;
+}
 
 // What is made of a row: y, its rowwise copy, or nothing (its factor, and its sum with the residual).
 enum { kNormStore = 0, kNormCast = 1, kNormFactor = 2 };
@@ -161,26 +200,24 @@ template <int DT, int W> QD void norm_put(const NormArgs &a, const float (&y)[W]
     if (in) out.store(a.y, base + k);
 }
 
-// y = (h s) w, zeros where `in` is false.
-template <int DT, int W> QD void norm_y(float (&y)[W], const Piece<DT, W> &h, float s, const float (&w)[W], bool in)
+// y = (h s) w.
+template <int DT, int W> QD void norm_y(float (&y)[W], const Piece<DT, W> &h, float s, const float (&w)[W])
 {
     if constexpr (W > 1) {
         const uint64_t ss = pack2(__float_as_uint(s), __float_as_uint(s));
 #pragma unroll
-        for (int j = 0; j < W; j += 2) {
+        for (int j = 0; j < W; j += 2)
             unpack2(fmul2(fmul2(h.pair(j / 2), ss), pack2(__float_as_uint(w[j]), __float_as_uint(w[j + 1]))), y[j], y[j + 1]);
-            if (!in) y[j] = y[j + 1] = 0.0f;
-        }
     } else {
-        y[0] = in ? h.at(0) * s * w[0] : 0.0f;
+        y[0] = h.at(0) * s * w[0];
     }
 }
 
-// The rowwise copy of N pieces of W elements of y from the columns k0 + i step on (zeros outside the row), N blocks of 128
-// that LPB = 128 / W lanes share.  The N maxima are reduced over the lanes by a
-// halving exchange, after which each lane holds one block's, takes its quotients
-// once, and the alphas go back by index shuffles.
-template <int W, int N> QD void norm_cast(const NormArgs &a, float (&y)[N][W], int64_t base, int64_t k0, int64_t step, int lane)
+// The rowwise copy of N pieces of W elements of y, from column k0 + i step on each, to the row's codes and scales: N blocks
+// of 128, each of which LPB = 128 / W lanes share (and lie in the row, or outside it, together).  The N maxima are reduced
+// over the lanes by a halving exchange, after which each lane holds one block's, takes its quotients once, and the alphas go
+// back by index shuffles.
+template <int W, int N> QD void norm_cast(const NormArgs &a, float (&y)[N][W], uint8_t *q, float *s, int k0, int step, int lane)
 {
     static_assert(W >= 4, "rows of the copy are multiples of 128 elements");
     constexpr int LPB = 128 / W;
@@ -204,9 +241,9 @@ template <int W, int N> QD void norm_cast(const NormArgs &a, float (&y)[N][W], i
 #pragma unroll
     for (; o > 0; o /= 2) m[0] = max(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], o));
     const float alpha = alpha_from_amax(448.0f, __uint_as_float(m[0]));
-    const int64_t k = k0 + (lane % LPB) / (LPB / N) * step;   // of the piece in this lane's block
-    if (lane % (LPB / N) == 0 && k < a.K) {
-        a.s_row[(base + k) / 128] = __fdiv_rn(1.0f, alpha);
+    const int k = k0 + (lane % LPB) / (LPB / N) * step, K = (int)a.K;   // of the piece in this lane's block
+    if (lane % (LPB / N) == 0 && k < K) {
+        s[k / 128] = __fdiv_rn(1.0f, alpha);
         flag_nonfinite(a.status, m[0]);
     }
 #pragma unroll
@@ -214,10 +251,10 @@ template <int W, int N> QD void norm_cast(const NormArgs &a, float (&y)[N][W], i
         const float f = N == 1 ? alpha : __shfl_sync(0xFFFFFFFFu, alpha, (lane & ~(LPB - 1)) + i * (LPB / N));
 #pragma unroll
         for (int j = 0; j < W; j += 2) mul2(y[i][j], y[i][j + 1], f, f);
-        if (k0 + i * step < a.K) {
-            uint8_t *const q = a.q_row + base + k0 + i * step;
-            if constexpr (W == 8) stg8(q, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]), cvt_fp8x4<E4M3>(y[i][4], y[i][5], y[i][6], y[i][7]));
-            else stg4(q, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]));
+        if (k0 + i * step < K) {
+            uint8_t *const to = q + k0 + i * step;
+            if constexpr (W == 8) stg8(to, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]), cvt_fp8x4<E4M3>(y[i][4], y[i][5], y[i][6], y[i][7]));
+            else stg4(to, cvt_fp8x4<E4M3>(y[i][0], y[i][1], y[i][2], y[i][3]));
         }
     }
 }
@@ -267,42 +304,19 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
 #pragma unroll
             for (int i = 0; i < VPT; i++) {
                 const int k = (t + i * g) * W;
-                if constexpr (W > 1) {
-#pragma unroll
-                    for (int j = 0; j < W / 2; j++) h[i].set_pair(j, fadd2(h[i].pair(j), r[i].pair(j)));
-                } else {
-                    const float f[1] = {h[i].at(0) + r[i].at(0)};
-                    h[i].set(f);
-                }
+                h[i].add(r[i]);
                 if (live && k < K) h[i].store(a.h, base + k);
             }
         }
     }
-    float sum = 0.0f;
-    if constexpr (W > 1) {
-        uint64_t two = 0;
-#pragma unroll
-        for (int i = 0; i < VPT; i++)
-#pragma unroll
-            for (int j = 0; j < W / 2; j++) two = ffma2(h[i].pair(j), h[i].pair(j), two);
-        float odd;
-        unpack2(two, sum, odd);
-        sum += odd;
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPT; i++) sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
-    }
-    const float s = row_factor(row_sum(sum, part, a.gshift), K, a.eps);
+    const float s = row_factor(row_sum(squares<DT, W, VPT>(h), part, a.gshift), a.inv, a.eps);
     if (live && t == 0) a.rstd[row] = s;
     if constexpr (MODE == kNormFactor) return;
     if constexpr (MODE == kNormCast && kAhead) {
         float y[VPT][W];
 #pragma unroll
-        for (int i = 0; i < VPT; i++) {
-            const bool in = live && (t + i * g) * W < K;
-            norm_y<DT, W>(y[i], h[i], s, w[i], in);
-        }
-        if (live) norm_cast<W, VPT>(a, y, base, t * W, (int64_t)g * W, lane);   // a warp's rows are live together
+        for (int i = 0; i < VPT; i++) norm_y<DT, W>(y[i], h[i], s, w[i]);
+        if (live) norm_cast<W, VPT>(a, y, a.q_row + base, a.s_row + row * (K / 128), t * W, g * W, lane);   // a warp's rows are live together
         return;
     }
     uint32_t m = 0;   // largest |y| of this thread
@@ -312,8 +326,8 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
         const bool in = live && k < K;
         if (!kAhead && in) load_weights<W>(w[0], a.weight, a.wf32, k);
         float y[1][W];
-        norm_y<DT, W>(y[0], h[i], s, w[kAhead ? i : 0], in);
-        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, base, in ? k : (int64_t)K, 0, lane);
+        norm_y<DT, W>(y[0], h[i], s, w[kAhead ? i : 0]);
+        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, a.q_row + base, a.s_row + row * (K / 128), in ? k : K, 0, lane);
         else norm_put<DT, W>(a, y[0], in, base, k, m);
     }
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
 #pragma unroll
         for (int j = 0; j < W; j++) sum = __fmaf_rn(h.at(j), h.at(j), sum);
     }
-    const float s = row_factor(row_sum(sum, part, 10), a.K, a.eps);
+    const float s = row_factor(row_sum(sum, part, 10), a.inv, a.eps);
     if (threadIdx.x == 0) a.rstd[blockIdx.x] = s;
     if constexpr (MODE == kNormFactor) return;
     const void *const from = RES ? a.h : a.x;
@@ -358,8 +372,8 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
             h.load(from, base + k);
             load_weights<W>(w, a.weight, a.wf32, k);
         }
-        norm_y<DT, W>(y[0], h, s, w, in);
-        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, base, k, 0, lane);
+        norm_y<DT, W>(y[0], h, s, w);
+        if constexpr (MODE == kNormCast) norm_cast<W, 1>(a, y, a.q_row + base, a.s_row + blockIdx.x * (a.K / 128), (int)(in ? k : a.K), 0, lane);
         else norm_put<DT, W>(a, y[0], in, base, k, m);
     }
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
@@ -372,86 +386,109 @@ QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
                  ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-// Many rows that begin between 16-byte boundaries (k_norm_rows reads them an element
-// at a time: 3001 x 1111 in FP32 11.1 us): by bulk copies into a ring of shared
-// memory, with the bytes around them, as the gradient does, one row a step.
-template <int DT, int E, bool RES>
-__global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int stages, int stage_bytes)
+// Many rows.  They come by bulk copies into a ring of shared memory, so that
+// memory stays busy while rows are summed and written: a step is one row, 16 elements
+// per thread in pieces of W (WIDE: rows longer than 512 threads' are).  Rows that begin between 16-byte boundaries are copied with
+// the bytes around them (a 16-byte piece that holds one of the row's bytes is the
+// allocation's) and read an element at a time.
+template <int DT, int W, bool WIDE, int MODE, bool RES>
+__global__ void __launch_bounds__(WIDE ? 1024 : 512, RES || WIDE ? 1 : 2) k_norm_ring(const NormArgs a, int stages, int stage_bytes)
 {
-    constexpr int kMostStages = 8, ES = In<DT>::BYTES, kTensors = RES ? 2 : 1;
+    constexpr int E = 16, VPT = E / W, kMostStages = 8, ES = In<DT>::BYTES, kTensors = RES ? 2 : 1;
     extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ float part[2][16];
+    __shared__ float part[2][32];
     __shared__ __align__(8) uint64_t full[kMostStages];
-    const int t = threadIdx.x, lane = t & 31, T = blockDim.x, K = (int)a.K, tensor_bytes = stage_bytes / kTensors;
-    const int64_t steps = a.M > blockIdx.x ? (a.M - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    auto skew = [&](int64_t row) { return (int)((row * K * ES) & 15); };
-    auto issue = [&](int64_t i) {
-        const int64_t row = blockIdx.x + i * gridDim.x;
-        const int off = skew(row), s = (int)(i % stages);
+    const int lane = threadIdx.x & 31, K = (int)a.K, tensor_bytes = stage_bytes / kTensors;
+    const int T = blockDim.x, t = threadIdx.x;
+    const int steps = (int)a.M > (int)blockIdx.x ? ((int)a.M - (int)blockIdx.x - 1) / (int)gridDim.x + 1 : 0;
+    auto skew = [&](int64_t row) { return W > 1 ? 0 : (int)((row * K * ES) & 15); };
+    int64_t next = blockIdx.x;   // the row whose copies are issued next (thread 0's)
+    auto issue = [&](int s) {
+        const int off = skew(next);
         const uint32_t bytes = (uint32_t)(off + K * ES + 15) & ~15u;
-        uint8_t *const st = dsm + (int64_t)s * stage_bytes;
+        uint8_t *const st = dsm + s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], bytes * kTensors);
-        bulk_load(st, static_cast<const char *>(a.x) + row * K * ES - off, bytes, &full[s]);
-        if constexpr (RES) bulk_load(st + tensor_bytes, static_cast<const char *>(a.residual) + row * K * ES - off, bytes, &full[s]);
+        bulk_load(st, static_cast<const char *>(a.x) + next * K * ES - off, bytes, &full[s]);
+        if constexpr (RES) bulk_load(st + tensor_bytes, static_cast<const char *>(a.residual) + next * K * ES - off, bytes, &full[s]);
+        next += gridDim.x;
     };
-    if (t == 0) {
+    if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);
         fence_mbar_init();
     }
+    if (threadIdx.x < 64) part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;   // the CTA may have fewer warps
     __syncthreads();
     griddep_wait();   // nothing was read or written so far
-    if (t == 0)
-        for (int64_t i = 0; i < steps && i < stages; i++) issue(i);
-    float w[E][1];
+    if (threadIdx.x == 0)
+        for (int i = 0; i < steps && i < stages; i++) issue(i);
+    float w[VPT][W];
+    if constexpr (MODE != kNormFactor) {
 #pragma unroll
-    for (int i = 0; i < E; i++)
-        if (t + i * T < K) load_weights<1>(w[i], a.weight, a.wf32, t + i * T);
-    uint32_t m = 0;
+        for (int i = 0; i < VPT; i++) {
+#pragma unroll
+            for (int j = 0; j < W; j++) w[i][j] = 0.0f;
+            if ((t + i * T) * W < K) load_weights<W>(w[i], a.weight, a.wf32, (t + i * T) * W);
+        }
+    }
+    uint32_t m = 0;   // largest |y| of this thread
     int s = 0;
     uint32_t parity = 0;
-    for (int64_t n = 0; n < steps; n++) {
-        const int64_t row = blockIdx.x + n * gridDim.x;
-        const uint8_t *const st = dsm + (int64_t)s * stage_bytes + skew(row);
+    int64_t row = blockIdx.x;
+    for (int n = 0; n < steps; n++, row += gridDim.x) {
+        const uint8_t *const st = dsm + s * stage_bytes + skew(row);
         const bool ok = mbar_wait_bounded(&full[s], parity);
-        Piece<DT, 1> h[E];
-        float sum = 0.0f;
+        Piece<DT, W> h[VPT];
 #pragma unroll
-        for (int i = 0; i < E; i++) {
-            const int k = t + i * T;
+        for (int i = 0; i < VPT; i++) {
+            const int k = (t + i * T) * W;
             h[i].zero();
             if (k < K) {
                 h[i].shared(st, k);
                 if constexpr (RES) {
-                    Piece<DT, 1> r;
-                    r.shared(st + tensor_bytes, k);
-                    const float f[1] = {h[i].at(0) + r.at(0)};
-                    h[i].set(f);
+                    Piece<DT, W> res;
+                    res.shared(st + tensor_bytes, k);
+                    h[i].add(res);
                 }
             }
-            sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
         }
-        sum = warp_sum(sum);
+        const float sum = warp_sum(squares<DT, W, VPT>(h));
         if (lane == 0) part[n & 1][t >> 5] = sum;
-        if (__syncthreads_or(!ok)) {   // the copies in flight land before shared memory goes away
+        if (__syncthreads_or(!ok)) {   // a wait ran out: the copies in flight land before shared memory goes away
             if (t == 0) {
-                for (int64_t j = n; j < steps && j < n + stages; j++) (void)mbar_wait_bounded(&full[j % stages], (uint32_t)((j / stages) & 1));
+                for (int j = n; j < steps && j < n + stages; j++) (void)mbar_wait_bounded(&full[j % stages], (uint32_t)((j / stages) & 1));
                 if (a.status != nullptr) atomicOr(a.status, kStTimeout);
             }
             break;
         }
         if (t == 0 && n + stages < steps) {   // every thread has the stage in its registers
             fence_proxy_async();
-            issue(n + stages);
+            issue(s);
         }
-        const float f = row_factor(warp_sum(lane < (T >> 5) ? part[n & 1][lane] : 0.0f), K, a.eps);
-        if (t == 0) a.rstd[row] = f;
+        float f = part[n & 1][lane & (WIDE ? 31 : 15)];
 #pragma unroll
-        for (int i = 0; i < E; i++) {
-            const int k = t + i * T;
-            if (k < K) {
-                if constexpr (RES) h[i].store(a.h, row * K + k);
-                float y[1] = {h[i].at(0) * f * w[i][0]};
-                norm_put<DT, 1>(a, y, true, row * K, k, m);
+        for (int o = WIDE ? 16 : 8; o > 0; o >>= 1) f += __shfl_xor_sync(0xFFFFFFFFu, f, o);
+        f = row_factor(f, a.inv, a.eps);
+        if (t == 0) a.rstd[row] = f;
+        const int64_t base = row * K;
+        if constexpr (RES) {
+#pragma unroll
+            for (int i = 0; i < VPT; i++)
+                if ((t + i * T) * W < K) h[i].store(a.h, base + (t + i * T) * W);
+        }
+        if constexpr (MODE == kNormCast) {
+            float y[VPT][W];
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                norm_y<DT, W>(y[i], h[i], f, w[i]);
+            }
+            norm_cast<W, VPT>(a, y, a.q_row + base, a.s_row + row * (K / 128), t * W, T * W, lane);
+        } else if constexpr (MODE == kNormStore) {
+#pragma unroll
+            for (int i = 0; i < VPT; i++) {
+                const int k = (t + i * T) * W;
+                float y[W];
+                norm_y<DT, W>(y, h[i], f, w[i]);
+                norm_put<DT, W>(a, y, k < K, base, k, m);
             }
         }
         if (++s == stages) {
@@ -459,7 +496,7 @@ __global__ void __launch_bounds__(512) k_norm_ring(const NormArgs a, int stages,
             parity ^= 1;
         }
     }
-    if (a.amax != nullptr) norm_amax<DT>(a, m);
+    if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
 
 // The gradient.  The rows of dy, h and dh come by bulk copies into a ring of
@@ -711,8 +748,47 @@ template <int DT, int W, int VPT, int MODE> cudaError_t norm_rows(NormArgs a, in
                     dim3((unsigned)grid), dim3(threads), 0, st, a);
 }
 
+template <int DT, int W, bool WIDE, int MODE, bool RES>
+cudaError_t norm_ring_t(const NormArgs &a, int threads, int per_sm, int stages, int stage_bytes, cudaStream_t st)
+{
+    const cudaError_t e = engine_smem_ready<k_norm_ring<DT, W, WIDE, MODE, RES>>(kRingBytes, true);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)per_sm * sm_count();
+    return launch_k(true, k_norm_ring<DT, W, WIDE, MODE, RES>, dim3((unsigned)(a.M < most ? a.M : most)), dim3(threads),
+                    (size_t)stages * stage_bytes, st, a, stages, stage_bytes);
+}
+
+// Whether the ring's kernel takes the call, and its launch: rows of 257 to 16384
+// elements that begin anywhere, or BF16 ones of 2048 on, where there are enough of them to keep every CTA's ring busy
+// (8192 x 4096 BF16 without a residual 20.8 us, one row a CTA 27.3; 16384 x 7168 cast with
+// one 121.6 and 154.8; 8192 x 5001 FP32 57 and 140; but 8192 x 4096 FP32 with a residual
+// 85.1 and 79.7, 8192 x 512 BF16 6.4 and 4.9, 2048 x 4096 cast 12.5 and 11.1).
+template <int DT, int W, int MODE, bool RES> bool norm_ring(const NormArgs &a, cudaStream_t st, cudaError_t &e)
+{
+    constexpr int ES = In<DT>::BYTES;
+    if (a.K <= 256 || a.K > 16384 || (W > 1 && a.K < 2048)) return false;
+    const bool wide = a.K > 8192;
+    const int threads = (int)((a.K + 511) / 512) * 32;
+    const int stage_bytes = (RES ? 2 : 1) * (int)((a.K * ES + 15) / 16 * 16 + (a.K * ES % 16 != 0 ? 16 : 0));
+    const int fit = kRingBytes / (2 * stage_bytes);
+    // With a residual fewer rows at a time are better: 16384 x 7168 stored 142 us at two stages, 159 to 164 at three
+    // and more; 8192 x 4096 cast 38.3 at 512 threads an SM, 40.3 at 1024, without a residual 28 and 25.
+    int per_sm = (wide || !RES ? 1024 : 512) / threads;
+    per_sm = per_sm > 8 ? 8 : per_sm;
+    per_sm = per_sm > fit ? fit : per_sm;
+    if (per_sm == 0 || a.M < (int64_t)(W > 1 ? 8 : 2) * per_sm * sm_count()) return false;
+    const int room = kRingBytes / per_sm / stage_bytes, most = RES && MODE == kNormStore ? 2 : 8, stages = room > most ? most : room;
+    e = wide ? norm_ring_t<DT, W, true, MODE, RES>(a, threads, per_sm, stages, stage_bytes, st)
+             : norm_ring_t<DT, W, false, MODE, RES>(a, threads, per_sm, stages, stage_bytes, st);
+    return true;
+}
+
 template <int DT, int W, int MODE> cudaError_t norm_w(const NormArgs &a, cudaStream_t st)
 {
+    if constexpr (DT == BF16 || W == 1) {
+        cudaError_t e;
+        if (a.residual != nullptr ? norm_ring<DT, W, MODE, true>(a, st, e) : norm_ring<DT, W, MODE, false>(a, st, e)) return e;
+    }
     constexpr int E = W == 1 ? 4 : 8;   // elements of a thread, times 1, 2 or 4
     const int64_t pieces = (a.K + W - 1) / W;
     const int s1 = log2_up((pieces + E / W - 1) / (E / W)), s2 = log2_up((pieces + 2 * E / W - 1) / (2 * E / W)),
@@ -725,34 +801,8 @@ template <int DT, int W, int MODE> cudaError_t norm_w(const NormArgs &a, cudaStr
                     dim3((unsigned)a.M), dim3(1024), 0, st, a);
 }
 
-template <int DT, int E, bool RES> cudaError_t norm_ring_t(const NormArgs &a, int threads, int per_sm, cudaStream_t st)
-{
-    const int bytes = (RES ? 2 : 1) * (int)((a.K * In<DT>::BYTES + 15) / 16 * 16 + 16), fit = kRingBytes / per_sm / bytes;
-    const cudaError_t e = engine_smem_ready<k_norm_ring<DT, E, RES>>(kRingBytes, true);
-    if (e != cudaSuccess) return e;
-    const int stages = fit < 8 ? fit : 8;
-    const int64_t most = (int64_t)per_sm * sm_count();
-    return launch_k(true, k_norm_ring<DT, E, RES>, dim3((unsigned)(a.M < most ? a.M : most)), dim3(threads), (size_t)stages * bytes, st,
-                    a, stages, bytes);
-}
-
-// Odd rows of 256 to 8192 elements, enough of them to keep every CTA's ring busy.
-template <int DT> bool norm_ring(const NormArgs &a, cudaStream_t st, cudaError_t &e)
-{
-    if (a.K <= 256 || a.K > 8192) return false;
-    constexpr int E = 16;
-    const int threads = (int)((a.K + 32 * E - 1) / (32 * E)) * 32, per_sm = 512 / threads < 8 ? 512 / threads : 8;
-    if (a.M < 2 * per_sm * sm_count()) return false;
-    e = a.residual != nullptr ? norm_ring_t<DT, E, true>(a, threads, per_sm, st) : norm_ring_t<DT, E, false>(a, threads, per_sm, st);
-    return true;
-}
-
 template <int DT, int MODE> cudaError_t norm_t(const NormArgs &a, cudaStream_t st)
 {
-    if constexpr (MODE == kNormStore) {
-        cudaError_t e;
-        if (a.K % In<DT>::VEC != 0 && norm_ring<DT>(a, st, e)) return e;
-    }
     if constexpr (MODE != kNormCast) {
         if (a.K % In<DT>::VEC != 0) return norm_w<DT, 1, MODE>(a, st);
     }

@@ -43,15 +43,26 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
     const int64_t tiles_m = M / kTileRowsE, tiles_k = (K + TC - 1) / TC;
 
     griddep_wait();   // the rows' factors and sums are the kernel's ahead
+    float s_ahead[8], w_ahead[VEC];
+    auto fetch = [&](int64_t tile) {
+        if (tile >= tiles_m * tiles_k) return;
+        const int64_t tm = tile / tiles_k, k = (tile - tm * tiles_k) * TC + lane * VEC;
+#pragma unroll
+        for (int j = 0; j < 8; j++) s_ahead[j] = __ldg(rstd + tm * kTileRowsE + 8 * warp + j);
+        col_weights<VEC>(w_ahead, weight, wf32, k, k < K);
+    };
+    fetch(blockIdx.x);
     run_tiles(&tmap, tiles_m, tiles_k, TC, false, status, [&](uint8_t *st, int64_t tm, int64_t tk) {
-        const int64_t mb = tm * kTileRowsE, kb = tk * TC, k = kb + lane * VEC;
+        const int64_t mb = tm * kTileRowsE, kb = tk * TC;
         uint4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = lds16(st + (8 * warp + j) * kRowBytes + lane * 16);
         float s[8], w[VEC];
 #pragma unroll
-        for (int j = 0; j < 8; j++) s[j] = __ldg(rstd + mb + 8 * warp + j);
-        col_weights<VEC>(w, weight, wf32, k, k < K);
+        for (int j = 0; j < 8; j++) s[j] = s_ahead[j];
+#pragma unroll
+        for (int c = 0; c < VEC; c++) w[c] = w_ahead[c];
+        fetch(tm * tiles_k + tk + gridDim.x);   // the next tile's, on their way behind this one
         // y = (h s) w for a pair of a row's elements
         auto y2 = [&](int j, int c, float &y0, float &y1) {
             y0 = elem<DT>(v[j], c);

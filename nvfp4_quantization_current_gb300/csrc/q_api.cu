@@ -545,7 +545,7 @@ q_status norm_add(const void *x, q_dtype in, int64_t M, int64_t K, const void *r
     }
     TRY(need(fn, "y", y, 16));
     if (y == h) return fail(Q_ERR_ARG, "%s: y and h are the same buffer", fn);
-    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, h, y, rstd, amax, nullptr, nullptr, status, M, K, 0};
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, y, rstd, amax, nullptr, nullptr, status, M, K, 0};
     LAUNCH(fn, qk::launch_norm_add(a, (int)in, S(stream)));
     return Q_OK;
 }
@@ -570,7 +570,7 @@ q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const
         TRY(need(fn, "s_colT", s_colT, 4));
         TRY(multiple(fn, "M (with q_colT)", M, 128));
     }
-    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, h, nullptr, rstd, nullptr, q_row, s_row, status, M, K, 0};
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, nullptr, rstd, nullptr, q_row, s_row, status, M, K, 0};
     LAUNCH(fn, qk::launch_norm_cast_rows(a, (int)in, S(stream)));
     if (q_colT != nullptr)
         LAUNCH(fn, qk::launch_norm_cast_cols(residual != nullptr ? h : x, (int)in, M, K, rstd, weight, wt == Q_F32, q_colT, s_colT,

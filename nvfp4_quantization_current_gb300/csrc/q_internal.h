@@ -116,7 +116,7 @@ cudaError_t launch_drop_add(const void *x, int dt, int64_t n, const void *residu
 struct NormArgs {
     const void *x, *residual, *weight;
     bool wf32;
-    float eps;
+    float eps, inv;   // inv = 1 / K
     void *h, *y;
     float *rstd, *amax;
     uint8_t *q_row;
