@@ -787,22 +787,18 @@ def _once(name, *grads):
     return tuple(None if g is None else _OnceMore.apply(g, torch.zeros((), requires_grad=True), name) for g in grads)
 
 
-def _norm_in(name, x, weight, residual):
+def _norm_in(name, x, dev, weight, residual):
     """(dtype, M, K) of x as rows of its last dimension, the operands checked against each other."""
     dt = _DTYPES.get(x.dtype)
-    if dt is None or not x.is_cuda or x.dim() == 0 or not x.is_contiguous():
+    if dt is None or not x.is_cuda or not x.is_contiguous() or x.dim() == 0:
         raise ValueError(f"{name} must be a contiguous CUDA tensor of bfloat16 or float32, of one dimension or more")
-    K = x.shape[-1]
-    if weight.dim() != 1 or weight.shape[0] != K or weight.dtype not in _DTYPES or weight.device != x.device or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of {K} elements on {x.device}")
+    shape = x.shape
+    K = shape[-1]
+    if weight.shape != (K,) or weight.dtype not in _DTYPES or weight.device != dev or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of {K} elements on {dev}")
     if residual is not None:
         _alike("residual", residual, x)
-    return dt, x.numel() // K if K else 0, K
-
-
-def _no_gradient(fn, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise RuntimeError(f"{fn} records no gradient, but one of its tensors requires one")
+    return dt, shape[0] if len(shape) == 2 else x.numel() // K if K else 0, K
 
 
 def _word(name, t, dev):
@@ -810,6 +806,20 @@ def _word(name, t, dev):
     if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
         raise ValueError(f"{name} must be a float32 tensor of one element on {dev}")
     return t.data_ptr()
+
+
+def _sum_into(x, residual, h_out):
+    """The tensor that x + residual goes to (x without a residual), and its address (None)."""
+    if residual is None:
+        if h_out is not None:
+            raise ValueError("h_out without a residual (the sum would be x)")
+        return x, None
+    if h_out is None:
+        h_out = torch.empty_like(x)
+    else:
+        _alike("h_out", h_out, x)
+        _written(h_out)
+    return h_out, h_out.data_ptr()
 
 
 class _NormAdd(torch.autograd.Function):
@@ -846,29 +856,29 @@ def norm_add(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     reports a maximum that is not finite.  ``out`` (for y) and ``h_out`` may be
     x and the residual themselves.  Autograd takes :func:`norm_grad` as the
     backward pass; with ``out`` or ``h_out`` no gradient is recorded."""
-    dt, M, K = _norm_in("x", x, weight, residual)
-    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad):
+    dev = x.device
+    dt, M, K = _norm_in("x", x, dev, weight, residual)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad or
+                                    out is not None and out.requires_grad or h_out is not None and h_out.requires_grad):
         if out is not None or h_out is not None:
             raise RuntimeError("norm_add with out= or h_out= records no gradient, but one of its tensors requires one")
         r = _NormAdd.apply(x, weight, residual, eps, amax, status)
         return r[0], x if residual is None else r[2], r[1]
-    dev = x.device
-    if residual is None and h_out is not None:
-        raise ValueError("h_out without a residual (the sum would be x)")
-    for name, t in (("out", out), ("h_out", h_out)):
-        if t is not None:
-            _no_gradient("norm_add", t)
-            _alike(name, t, x)
-            _written(t)
-    y = torch.empty_like(x) if out is None else out
-    h = None if residual is None else torch.empty_like(x) if h_out is None else h_out
+    if out is None:
+        y = torch.empty_like(x)
+    else:
+        _alike("out", out, x)
+        _written(out)
+        y = out
+    h, hp = _sum_into(x, residual, h_out)
     rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    top = None
     if amax is not None:
+        top = _word("amax", amax, dev)
         _written(amax)
-    _call_on(dev, "norm_add", x.data_ptr(), dt, M, K, _ptr(residual), weight.data_ptr(), _DTYPES[weight.dtype], float(eps), _ptr(h),
-             y.data_ptr(), rstd.data_ptr(), None if amax is None else _word("amax", amax, dev),
-             None if status is None else _status(status, dev), _stream(dev))
-    return y, x if h is None else h, rstd
+    _call_on(dev, "norm_add", x.data_ptr(), dt, M, K, None if hp is None else residual.data_ptr(), weight.data_ptr(), _DTYPES[weight.dtype], eps,
+             hp, y.data_ptr(), rstd.data_ptr(), top, None if status is None else _status(status, dev), _stream(dev))
+    return y, h, rstd
 
 
 def norm_q_blockwise(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None, rowwise=True,
@@ -878,29 +888,26 @@ def norm_q_blockwise(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     result in FP32, which is not stored, for a 2-D x.  ``out`` (1x128 copies of an x
     of this shape) has the directions that it holds written; ``h_out`` may be x or
     the residual.  It records no gradient (``linear.py`` has the backward pass)."""
-    dt, M, K = _norm_in("x", x, weight, residual)
-    _no_gradient("norm_q_blockwise", x, weight, residual, h_out)
+    dev = x.device
+    dt, M, K = _norm_in("x", x, dev, weight, residual)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad or
+                                    h_out is not None and h_out.requires_grad):
+        raise RuntimeError("norm_q_blockwise records no gradient, but one of its tensors requires one")
     if x.dim() != 2:
         raise ValueError("x must be a 2-D tensor")
-    dev = x.device
     if out is None:
-        out = alloc_blockwise(M, K, dev, "1x128", rowwise, colwise)
+        out = alloc_blockwise(M, K, dev, Q_T1x128, rowwise, colwise)
     else:
         _copies("out", out, M, K, dev)
         if colwise and out.q_colT is None:
             raise ValueError("out has no transposed copy")
         _written_copies(out)
-    if h_out is not None:
-        if residual is None:
-            raise ValueError("h_out without a residual (the sum would be x)")
-        _alike("h_out", h_out, x)
-        _written(h_out)
-    h = None if residual is None else torch.empty_like(x) if h_out is None else h_out
+    h, hp = _sum_into(x, residual, h_out)
     rstd = torch.empty((M,), dtype=torch.float32, device=dev)
-    _call_on(dev, "norm_q_blockwise", x.data_ptr(), dt, M, K, _ptr(residual), weight.data_ptr(), _DTYPES[weight.dtype], float(eps),
-             _ptr(h), rstd.data_ptr(), _ptr(out.q_row), _ptr(out.s_row), _ptr(out.q_colT), _ptr(out.s_colT),
+    _call_on(dev, "norm_q_blockwise", x.data_ptr(), dt, M, K, None if hp is None else residual.data_ptr(), weight.data_ptr(),
+             _DTYPES[weight.dtype], eps, hp, rstd.data_ptr(), _ptr(out.q_row), _ptr(out.s_row), _ptr(out.q_colT), _ptr(out.s_colT),
              None if status is None else _status(status, dev), _stream(dev))
-    return out, x if h is None else h, rstd
+    return out, h, rstd
 
 
 def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dh: Optional[torch.Tensor] = None,
@@ -910,9 +917,11 @@ def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: tor
     is used again, added to it, and the weight's gradient in the weight's type
     (None without ``need_dw``).  ``out`` (for dx) may be dy, h or dh; ``status``
     reports a kernel that gave up waiting.  It records no gradient itself."""
-    dt, M, K = _norm_in("dy", dy, weight, None)
-    _no_gradient("norm_grad", dy, h, rstd, weight, dh, out)
     dev = dy.device
+    dt, M, K = _norm_in("dy", dy, dev, weight, None)
+    if torch.is_grad_enabled() and (dy.requires_grad or h.requires_grad or rstd.requires_grad or weight.requires_grad or
+                                    dh is not None and dh.requires_grad or out is not None and out.requires_grad):
+        raise RuntimeError("norm_grad records no gradient, but one of its tensors requires one")
     _alike("h", h, dy)
     if not _is(rstd, torch.float32, dy.shape[:-1], dev):
         raise ValueError(f"rstd must be a contiguous float32 tensor of shape {tuple(dy.shape[:-1])} on {dev}")
@@ -924,8 +933,10 @@ def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: tor
         _alike("out", out, dy)
         _written(out)
         dx = out
-    dw = torch.empty_like(weight) if need_dw else None
-    work = _f32((lib().norm_grad_work(M, K, dt),), dev) if need_dw else None
+    dw = work = None
+    if need_dw:
+        dw = torch.empty_like(weight)
+        work = torch.empty((lib().norm_grad_work(M, K, dt),), dtype=torch.float32, device=dev)
     _call_on(dev, "norm_grad", dy.data_ptr(), dt, M, K, h.data_ptr(), rstd.data_ptr(), weight.data_ptr(), _DTYPES[weight.dtype], _ptr(dh),
              dx.data_ptr(), _ptr(dw), _ptr(work), None if status is None else _status(status, dev), _stream(dev))
     return dx, dw
@@ -940,17 +951,19 @@ _BLK = {"1x16": Q_B1x16, "16x16": Q_B16x16, Q_B1x16: Q_B1x16, Q_B16x16: Q_B16x16
 
 def _operand4(name, q, sb, s, blk, dev):
     """(rows, K) of an NVFP4 operand on dev, its codes and scales checked against each other."""
+    shape = q.shape
+    R, K = (shape[0], shape[1] * 2) if len(shape) == 2 else (0, 0)
+    want = (R, K // 16) if blk == Q_B1x16 else (R // 16, K // 16)
+    if len(shape) == 2 and q.dtype is torch.uint8 and sb.dtype is torch.uint8 and s.dtype is torch.float32 and sb.shape == want and \
+            q.is_cuda and q.is_contiguous() and sb.is_contiguous() and s.numel() == 1 and q.device == dev and sb.device == dev and s.device == dev:
+        return R, K
     if not q.is_cuda or q.device != dev or sb.device != dev or s.device != dev:
         raise ValueError(f"{name}: codes and scales must be CUDA tensors on one device, that of a (the library has no CPU path)")
     if q.dtype != torch.uint8 or sb.dtype != torch.uint8 or s.dtype != torch.float32:
         raise ValueError(f"{name}: codes and block scales must be uint8 and the tensor's scale float32, got {q.dtype}, {sb.dtype} and {s.dtype}")
     if q.dim() != 2 or not (q.is_contiguous() and sb.is_contiguous()):
         raise ValueError(f"{name}: codes must be a contiguous 2-D tensor and block scales contiguous")
-    R, K = q.shape[0], q.shape[1] * 2
-    want = (R, K // 16) if blk == Q_B1x16 else (R // 16, K // 16)
-    if sb.shape != want or s.numel() != 1:
-        raise ValueError(f"{name}: block scales are {tuple(sb.shape)} and the tensor's {tuple(s.shape)}, codes of {R} x {K} need {want} and one")
-    return R, K
+    raise ValueError(f"{name}: block scales are {tuple(sb.shape)} and the tensor's {tuple(s.shape)}, codes of {R} x {K} need {want} and one")
 
 
 def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, sb_b: torch.Tensor, s_b: torch.Tensor,

@@ -379,7 +379,15 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
 
-// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.
+// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.  The first: of lines
+// that L2 may drop first (the gradient's inputs: 8192 x 4096 BF16 46.5 us, 47.0 else; where a sum is cast it is 2 us slower).
+QD void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    uint64_t once;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(once) : "memory");
+}
 QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -530,9 +538,9 @@ __global__ void __launch_bounds__(512) k_norm_grad(const NormGradArgs a, int sta
         uint8_t *const st = dsm + (int64_t)s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], bytes * kTensors);
         const int64_t from = r0 * K * ES - off;
-        bulk_load(st, static_cast<const char *>(a.dy) + from, bytes, &full[s]);
-        bulk_load(st + tensor_bytes, static_cast<const char *>(a.h) + from, bytes, &full[s]);
-        if constexpr (DH) bulk_load(st + 2 * tensor_bytes, static_cast<const char *>(a.dh) + from, bytes, &full[s]);
+        bulk_load_once(st, static_cast<const char *>(a.dy) + from, bytes, &full[s]);
+        bulk_load_once(st + tensor_bytes, static_cast<const char *>(a.h) + from, bytes, &full[s]);
+        if constexpr (DH) bulk_load_once(st + 2 * tensor_bytes, static_cast<const char *>(a.dh) + from, bytes, &full[s]);
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);

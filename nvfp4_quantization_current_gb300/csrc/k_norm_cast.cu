@@ -1,11 +1,13 @@
 // The transposed blockwise copy of the norm's result: 128x1 blocks along M of
 // y = (h s) w in FP32 (k_norm.cu), y itself never stored.
 //
-// On the tile engine: thread (warp w, lane l) holds rows 8w..8w+7 x one 16-byte
-// column chunk of h and multiplies by the rows' factors and the columns'
-// weights as it goes.  Per-warp column maxima meet in shared memory, and the
-// codes are transposed in the consumed stage and written as full 128-byte rows
-// (as in k_blockwise).
+// On the tile engine with two CTAs of 256 threads per SM, tiles of 128 rows x 256
+// bytes: while one waits at a barrier, the other works (one CTA with tiles of 512
+// bytes took 26 us of 8192 x 4096 BF16, its issue slots 40 % in use).  A thread (half
+// a warp over a row's 16-byte chunks) holds 8 rows of a chunk of h and multiplies by
+// the rows' factors and the columns' weights as it goes.  The half warps' column
+// maxima meet in shared memory, and the codes are transposed in the consumed stage
+// and written as full 128-byte rows.
 #include "q_engine.cuh"
 #include "q_internal.h"
 
@@ -30,30 +32,35 @@ template <int N> QD void col_weights(float (&w)[N], const void *weight, bool f32
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K,
-                                                              const float *__restrict__ rstd, const void *__restrict__ weight,
-                                                              bool wf32, uint8_t *__restrict__ q_colT,
-                                                              float *__restrict__ s_colT, int32_t *status)
-{
-    constexpr int VEC = In<DT>::VEC, TC = 32 * VEC, CW = VEC / 4, TPC = kEngThreads / TC;   // threads per column
-    __shared__ __align__(16) float part[kEngWarps][CW][32][4];   // per-warp column maxima, of four columns of each lane in turn
-    __shared__ __align__(16) float calpha[TC];
-    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    const int64_t tiles_m = M / kTileRowsE, tiles_k = (K + TC - 1) / TC;
+struct ColCfg {
+    static constexpr int kRows = 128, kThreads = 256, kStages = 3, kRowBytes = 256;
+    static constexpr int kTileBytes = kRows * kRowBytes, kSmem = kStages * kTileBytes;
+};
 
-    griddep_wait();   // the rows' factors and sums are the kernel's ahead
+template <int DT>
+__global__ void __launch_bounds__(ColCfg::kThreads, 2)
+k_norm_cols(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K, const float *__restrict__ rstd,
+            const void *__restrict__ weight, bool wf32, uint8_t *__restrict__ q_colT, float *__restrict__ s_colT, int32_t *status)
+{
+    constexpr int VEC = In<DT>::VEC, TC = 16 * VEC, CW = VEC / 4, TPC = ColCfg::kThreads / TC;   // TPC: threads per column
+    constexpr int kRows = ColCfg::kRows, kRowBytes = ColCfg::kRowBytes;
+    __shared__ __align__(16) float part[16][CW][16][4];   // half warps' column maxima, of four columns of each chunk in turn
+    __shared__ __align__(16) float calpha[TC];
+    const int t = threadIdx.x, warp = t >> 4, lane = t & 15;   // half warps, and chunks of a row
+    const int64_t tiles_m = M / kRows, tiles_k = (K + TC - 1) / TC;
+
+    griddep_wait();   // the rows' factors and sums are the kernel's ahead, which left the last of them in L2: the walk begins there
     float s_ahead[8], w_ahead[VEC];
     auto fetch = [&](int64_t tile) {
-        if (tile >= tiles_m * tiles_k) return;
+        if (tile < 0) return;
         const int64_t tm = tile / tiles_k, k = (tile - tm * tiles_k) * TC + lane * VEC;
 #pragma unroll
-        for (int j = 0; j < 8; j++) s_ahead[j] = __ldg(rstd + tm * kTileRowsE + 8 * warp + j);
+        for (int j = 0; j < 8; j++) s_ahead[j] = __ldg(rstd + tm * kRows + 8 * warp + j);
         col_weights<VEC>(w_ahead, weight, wf32, k, k < K);
     };
-    fetch(blockIdx.x);
-    run_tiles(&tmap, tiles_m, tiles_k, TC, false, status, [&](uint8_t *st, int64_t tm, int64_t tk) {
-        const int64_t mb = tm * kTileRowsE, kb = tk * TC;
+    fetch(tiles_m * tiles_k - 1 - blockIdx.x);
+    run_tiles<ColCfg>(&tmap, tiles_m, tiles_k, TC, true, status, [&](uint8_t *st, int64_t tm, int64_t tk) {
+        const int64_t mb = tm * kRows, kb = tk * TC;
         uint4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = lds16(st + (8 * warp + j) * kRowBytes + lane * 16);
@@ -62,7 +69,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
         for (int j = 0; j < 8; j++) s[j] = s_ahead[j];
 #pragma unroll
         for (int c = 0; c < VEC; c++) w[c] = w_ahead[c];
-        fetch(tm * tiles_k + tk + gridDim.x);   // the next tile's, on their way behind this one
+        fetch(tm * tiles_k + tk - (int64_t)gridDim.x);   // the next tile's, on their way behind this one
         // y = (h s) w for a pair of a row's elements
         auto y2 = [&](int j, int c, float &y0, float &y1) {
             y0 = elem<DT>(v[j], c);
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
             const int col = t / TPC, sub = t % TPC, l = col / VEC, q = col % VEC;   // lane l's column q
             float b = 0.0f;
 #pragma unroll
-            for (int i = sub; i < kEngWarps; i += TPC) b = fmax_abs(b, part[i][q / 4][l][q % 4]);
+            for (int i = sub; i < 16; i += TPC) b = fmax_abs(b, part[i][q / 4][l][q % 4]);
             const uint32_t bits = group_max<TPC>(__float_as_uint(b) & 0x7FFFFFFFu);
             if (sub == 0) {
                 const float alpha = alpha_from_amax(448.0f, __uint_as_float(bits));
@@ -119,7 +126,15 @@ __global__ void __launch_bounds__(kEngThreads, 1) k_norm_cols(const __grid_const
         }
         park_fp8T<VEC>(st, code, warp, lane);
         __syncthreads();
-        copy_out_fp8T<VEC>(st, q_colT, M, K, mb, kb);
+        // the parked [TC][128] codes as rows of q_colT, 16 bytes of two neighbouring slots at a time (the order that
+        // copy_out_fp8T undoes)
+#pragma unroll
+        for (int it = 0; it < TC * 8 / ColCfg::kThreads; it++) {
+            const int idx = it * ColCfg::kThreads + t, col = idx >> 3, pr = idx & 7, sw = col / VEC;
+            uint4 o = *reinterpret_cast<const uint4 *>(st + col * 128 + ((2 * pr) ^ (sw & ~1)) * 8);
+            if (sw & 1) o = make_uint4(o.z, o.w, o.x, o.y);
+            if (kb + col < K) stg16(q_colT + (kb + col) * M + mb + 16 * pr, o);
+        }
     });
 }
 
@@ -127,15 +142,14 @@ template <int DT>
 cudaError_t cols_t(const void *h, int64_t M, int64_t K, const float *rstd, const void *weight, bool wf32, uint8_t *q_colT,
                    float *s_colT, int32_t *status, cudaStream_t st)
 {
-    constexpr int TC = 32 * In<DT>::VEC;
+    constexpr int TC = 16 * In<DT>::VEC;
     alignas(64) CUtensorMap map;
-    cudaError_t e = make_tile_map(&map, h, DT, M, K);
-    if (e == cudaSuccess) e = engine_smem_ready<k_norm_cols<DT>>();
+    cudaError_t e = make_tile_map(&map, h, DT, M, K, ColCfg::kRows, ColCfg::kRowBytes);
+    if (e == cudaSuccess) e = engine_smem_ready<k_norm_cols<DT>>(ColCfg::kSmem, true);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (M / kTileRowsE) * ((K + TC - 1) / TC);
-    const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
-    return launch_k(true, k_norm_cols<DT>, dim3(grid), dim3(kEngThreads), kEngSmem, st, map, M, K, rstd, weight, wf32, q_colT,
-                    s_colT, status);
+    const int64_t tiles = (M / ColCfg::kRows) * ((K + TC - 1) / TC), most = 2 * sm_count();
+    return launch_k(true, k_norm_cols<DT>, dim3((unsigned)(tiles < most ? tiles : most)), dim3(ColCfg::kThreads), ColCfg::kSmem, st,
+                    map, M, K, rstd, weight, wf32, q_colT, s_colT, status);
 }
 
 }  // namespace

@@ -30,12 +30,12 @@ cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 }
 
 // A 2-D TMA tensor map over a row-major [M, K] input (dt: BF16, F32, or U8
-// for code matrices, K even) whose box is box_rows rows x 512 bytes (the tile
-// engine's stage; box_rows <= 256).  The x coordinate counts elements of 2
+// for code matrices, K even) whose box is box_rows rows x row_bytes bytes (the tile
+// engine's stage; box_rows <= 256, row_bytes a multiple of 16 up to 512).  The x coordinate counts elements of 2
 // bytes (BF16, U8) or 4 bytes (F32).  Fails with cudaErrorNotSupported if the
 // driver entry point is unavailable.
 cudaError_t make_tile_map(void *map /* CUtensorMap, 64-byte aligned */, const void *x, int dt, int64_t M, int64_t K,
-                          int box_rows = 128);
+                          int box_rows = 128, int row_bytes = 512);
 
 // A 2-D TMA tensor map for bulk stores into a row-major byte matrix of
 // `rows` rows of row_bytes bytes (row_bytes a multiple of 16, base 16-byte

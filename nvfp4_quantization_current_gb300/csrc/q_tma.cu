@@ -38,7 +38,7 @@ template <typename... Args> static cudaError_t encode(Args... args)
     return fn(args...) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tile_map(void *map, const void *x, int dt, int64_t M, int64_t K, int box_rows)
+cudaError_t make_tile_map(void *map, const void *x, int dt, int64_t M, int64_t K, int box_rows, int row_bytes)
 {
     // A byte matrix is described as 16-bit elements (K/2 per row, K even):
     // a box edge may not exceed 256 elements, and 512 bytes of U8 would.
@@ -47,7 +47,7 @@ cudaError_t make_tile_map(void *map, const void *x, int dt, int64_t M, int64_t K
                                    : (dt == F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16);
     cuuint64_t dims[2] = {(cuuint64_t)(dt == U8 ? K / 2 : K), (cuuint64_t)M};
     cuuint64_t strides[1] = {(cuuint64_t)(dt == U8 ? K : K * es)};
-    cuuint32_t box[2] = {(cuuint32_t)(512 / es), (cuuint32_t)box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)(row_bytes / es), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1u, 1u};
     return encode(static_cast<CUtensorMap *>(map), ty,
                     2, const_cast<void *>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
