@@ -1,4 +1,6 @@
-"""A linear layer on the blockwise FP8 copies, with dropout and the residual sum behind it:
+"""Linear layers on the library's copies, and the norm ahead of them.
+
+:class:`BlockwiseLinear` works on the blockwise FP8 copies, with dropout and the residual sum behind it:
 
     y = residual + dropout(x W^T)
 
@@ -12,6 +14,17 @@ keeps FP8 copies for the backward pass, no mask and no BF16 activation.
 
 The recipe is the DeepSeek-V3-like one of "Mixed-precision training: fp16 to
 fp8", "Blockwise scaling".
+
+:class:`NormBlockwiseLinear` has the root-mean-square norm and the residual's
+addition ahead of it, y = norm(x + residual) W^T: :func:`norm_q_blockwise` makes
+the copies while it norms, and :func:`norm_grad` takes the input gradient's
+product back through the norm.  :class:`RMSNorm` is the norm by itself.
+
+:class:`NVFP4Linear` works on NVFP4 copies as the recipe of "From BF16 to
+FP8/FP4: low-precision and mixed-precision LLM pretraining", 2.4, has it: 1x16
+blocks for activations and gradients, 16x16 blocks for weights, stochastic
+rounding on gradients, the random Hadamard transform on both inputs of the
+weight gradient, and :func:`matmul_nvfp4` for the three products.
 """
 from __future__ import annotations
 
@@ -19,7 +32,8 @@ from typing import Optional
 
 import torch
 
-from . import BlockwiseTensor, _ready, drop_add, drop_q_blockwise, mm_blockwise, q_blockwise
+from . import (BlockwiseTensor, NVFP4Tensor, _once, _ready, _word, drop_add, drop_q_blockwise, matmul_nvfp4, mm_blockwise, norm_add,
+               norm_grad, norm_q_blockwise, q_blockwise, q_nvfp4, q_nvfp4_recipe, q_nvfp4_rht_colT)
 
 
 def _cast_rows(x, rowwise, colwise, status):
@@ -159,3 +173,201 @@ class BlockwiseLinear(torch.nn.Module):
             copies = self.quantize_weight(colwise=train and x.requires_grad)
         return _BlockwiseLinear.apply(x, self.weight, residual, copies, p, self.seed,
                                       int(offset), self.main_grad, train, self._status_on(x.device))
+
+
+class RMSNorm(torch.nn.Module):
+    """``y = h rsqrt(mean(h^2) + eps) weight`` over the last dimension, h = x or
+    x + residual; with a residual the result is ``(y, h)``, h being the new
+    residual.  x is bfloat16 or float32 with any strides, the residual of its shape
+    and type.  ``amax`` (a one-element float32 tensor) receives max|y|, for
+    :class:`NVFP4Linear` to be given."""
+
+    def __init__(self, features: int, eps: float = 1e-6, device="cuda", dtype=torch.bfloat16):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype))
+        self.eps = float(eps)
+
+    def forward(self, x, residual=None, amax: Optional[torch.Tensor] = None):
+        y, h, _ = norm_add(_ready(x), self.weight, self.eps, None if residual is None else _ready(residual), amax=amax)
+        return y if residual is None else (y, h)
+
+
+def _rows_to(x, step):
+    """x [M, K] with zero rows below it up to a multiple of `step`."""
+    return x if x.shape[0] % step == 0 else torch.nn.functional.pad(x, (0, 0, 0, -x.shape[0] % step))
+
+
+class _NormBlockwiseLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, norm_weight, weight, residual, w, eps, main_grad, train, status):
+        need = [train and n for n in ctx.needs_input_grad[:4]]
+        through, need_w = need[0] or need[1] or need[3], need[2]
+        if through and w.q_colT is None:
+            raise ValueError("copies lacks the transposed copy, which the input gradient reads")
+        if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+            raise ValueError(f"residual must have x's shape {tuple(x.shape)} and type, not {tuple(residual.shape)}, {residual.dtype}")
+        x2, r2 = (None if t is None else _ready(t.reshape(-1, t.shape[-1])) for t in (x, residual))
+        M = x2.shape[0]
+        if need_w and M % 128 != 0:   # zero rows below: their norm is zero and adds nothing to the weight gradient
+            x2, r2 = _rows_to(x2, 128), None if r2 is None else _rows_to(r2, 128)
+        xq, h, rstd = norm_q_blockwise(x2, norm_weight.detach(), eps, r2, rowwise=True, colwise=need_w, status=status)
+        y = mm_blockwise(xq.q_row[:M], xq.s_row[:M], w.q_row, w.s_row, dtype=x.dtype, status=status)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(*((h[:M], rstd[:M], norm_weight, w.q_colT, w.s_colT) if through else (None,) * 5),
+                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
+        ctx.args = (main_grad, weight.dtype, x.shape, residual is not None, status)
+        y = y.view(*x.shape[:-1], weight.shape[0])
+        return (y, h[:M].reshape(x.shape)) if residual is not None else y
+
+    @staticmethod
+    def backward(ctx, dy, dh=None):
+        if dy is None:   # the sum alone was used
+            return (dh, None, None, dh) + (None,) * 5
+        with torch.no_grad():
+            grads = _NormBlockwiseLinear.gradients(ctx, dy, dh)
+        dx, dn, dw = _once("NormBlockwiseLinear", *grads)
+        return (dx, dn, dw, dx if ctx.args[3] else None) + (None,) * 5
+
+    @staticmethod
+    def gradients(ctx, dy, dh):
+        h, rstd, norm_weight, w_q, w_s, x_q, x_s = ctx.saved_tensors
+        main_grad, w_dtype, x_shape, _, status = ctx.args
+        need = ctx.needs_input_grad
+        through, need_w = need[0] or need[1] or need[3], need[2]
+        d = _ready(dy.reshape(-1, dy.shape[-1]))
+        M = d.shape[0]
+        g = _cast_rows(d, through, need_w, status)
+        dx = dn = dw = None
+        if through:
+            dn_in = mm_blockwise(g.q_row, g.s_row, w_q, w_s, dtype=dy.dtype, status=status)
+            dx, dn = norm_grad(dn_in, h, rstd, norm_weight, None if dh is None else _ready(dh.reshape(-1, dh.shape[-1])), need_dw=need[1],
+                               out=dn_in, status=status)
+            dx = dx.view(x_shape)
+        if need_w:
+            dw = mm_blockwise(g.q_colT, g.s_colT, x_q, x_s, tile_b="1x128", dtype=w_dtype, out=main_grad,
+                              accumulate=main_grad is not None, status=status)
+        return dx, dn, None if main_grad is not None else dw
+
+
+class NormBlockwiseLinear(BlockwiseLinear):
+    """``y = norm(x + residual) W^T`` on blockwise FP8 copies, the norm that of
+    :class:`RMSNorm` with the parameter ``norm_weight``; with a residual the result is
+    ``(y, h)``, h = x + residual being the new residual.  x and the residual are
+    bfloat16 or float32, of one type and shape, with any strides.  ``main_grad``,
+    ``copies`` and ``status`` are those of :class:`BlockwiseLinear`; there is no second
+    derivative: one that is asked for raises."""
+
+    def __init__(self, in_features: int, out_features: int, eps: float = 1e-6, device="cuda", dtype=torch.bfloat16):
+        super().__init__(in_features, out_features, device=device, dtype=dtype)
+        if not eps > 0:   # rows of zeros, padding among them, have no norm without it
+            raise ValueError("eps must be positive")
+        self.norm_weight = torch.nn.Parameter(torch.ones(in_features, device=device, dtype=dtype))
+        self.eps = float(eps)
+
+    def forward(self, x, residual=None, copies: Optional[BlockwiseTensor] = None):
+        train = torch.is_grad_enabled()
+        if copies is None:
+            through = x.requires_grad or self.norm_weight.requires_grad or residual is not None and residual.requires_grad
+            copies = self.quantize_weight(colwise=train and through)
+        return _NormBlockwiseLinear.apply(x, self.norm_weight, self.weight, residual, copies, self.eps, self.main_grad, train,
+                                          self._status_on(x.device))
+
+
+class _NVFP4Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, w, sign_mask, seed, offset, main_grad, train, status, amax):
+        need_x, need_w = (train and n for n in ctx.needs_input_grad[:2])
+        if need_x and w.q_colT is None:
+            raise ValueError("copies lacks the transposed copy, which the input gradient reads")
+        x2 = _ready(x.reshape(-1, x.shape[-1]))
+        M = x2.shape[0]
+        col = None
+        if need_w:   # the product over tokens takes 32 of them at a time: zero rows below add nothing
+            row, col = q_nvfp4_recipe(_rows_to(x2, 32), sign_mask, status=status)
+        else:
+            if amax is not None:
+                _word("amax", amax, x.device)
+            row = q_nvfp4(_rows_to(x2, 16), amax=amax, status=status)
+        y = matmul_nvfp4(row.q_row[:M], row.sb_row[:M], row.s_global, w.q_row, w.sb_row, w.s_global, dtype=x.dtype, status=status)
+        ctx.save_for_backward(*((w.q_colT, w.sb_colT, w.s_global) if need_x else (None,) * 3),
+                              *((col.q_colT, col.sb_colT, col.s_global) if need_w else (None,) * 3))
+        ctx.args = (sign_mask, seed, offset, main_grad, weight.dtype, x.shape, status)
+        return y.view(*x.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    def backward(ctx, dy):
+        with torch.no_grad():
+            grads = _NVFP4Linear.gradients(ctx, dy)
+        return _once("NVFP4Linear", *grads) + (None,) * 8
+
+    @staticmethod
+    def gradients(ctx, dy):
+        w, x = ctx.saved_tensors[:3], ctx.saved_tensors[3:]
+        sign_mask, seed, offset, main_grad, w_dtype, x_shape, status = ctx.args
+        need_x, need_w = ctx.needs_input_grad[:2]
+        d = _ready(dy.reshape(-1, dy.shape[-1]))
+        M = d.shape[0]
+        dx = dw = row = col = None
+        if need_x and need_w:
+            row, col = q_nvfp4_recipe(_rows_to(d, 32), sign_mask, "sr", seed, offset, status=status)
+        elif need_x:
+            row = q_nvfp4(_rows_to(d, 16), "1x16", "sr", seed, offset, status=status)
+        elif need_w:
+            col = q_nvfp4_rht_colT(_rows_to(d, 32), sign_mask, "sr", seed, offset, status=status)
+        if need_x:
+            dx = matmul_nvfp4(row.q_row[:M], row.sb_row[:M], row.s_global, *w, dtype=dy.dtype, status=status).view(x_shape)
+        if need_w:
+            dw = matmul_nvfp4(col.q_colT, col.sb_colT, col.s_global, *x, blk_b="1x16", dtype=w_dtype, out=main_grad,
+                              accumulate=main_grad is not None, status=status)
+        return dx, None if main_grad is not None else dw
+
+
+class NVFP4Linear(torch.nn.Module):
+    """``y = x W^T`` on NVFP4 copies.
+
+    ``in_features`` and ``out_features`` are multiples of 32; x is bfloat16 or float32
+    with any number of rows and any strides.  ``main_grad`` (FP32, the weight's shape),
+    ``copies`` (of :meth:`quantize_weight`) and ``status`` are as in
+    :class:`BlockwiseLinear`.  ``amax`` (a one-element float32 tensor holding max|x|, as
+    :class:`RMSNorm` gives it) saves a read of x where no weight gradient is wanted;
+    with one, both of the recipe's maxima take a single read in any case.
+
+    Gradients are rounded stochastically.  The numbers follow from the layer's ``seed``
+    and the call's ``offset`` (in counters of 16 elements), which are drawn from
+    torch's CPU generator where they are not given; a call with gradients that is
+    captured into a CUDA graph has to be given its offset (every replay draws what it
+    was captured with).  ``sign_mask`` is that of the Hadamard transform of both inputs
+    of the weight gradient.  There is no second derivative: one that is asked for
+    raises."""
+
+    def __init__(self, in_features: int, out_features: int, seed: Optional[int] = None, sign_mask: int = 0xB4E1, device="cuda",
+                 dtype=torch.bfloat16):
+        super().__init__()
+        if in_features % 32 or out_features % 32:
+            raise ValueError("in_features and out_features must be multiples of 32")
+        if not 0 <= sign_mask <= 0xFFFF:
+            raise ValueError("sign_mask must have 16 bits")
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, device=device, dtype=dtype))
+        torch.nn.init.normal_(self.weight, std=0.02)
+        self.seed = int(seed) if seed is not None else _drawn()
+        self.sign_mask = int(sign_mask)
+        self.main_grad: Optional[torch.Tensor] = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    _status_on = BlockwiseLinear._status_on
+
+    def quantize_weight(self, colwise=True) -> NVFP4Tensor:
+        """The weight's 16x16 copies (``colwise``: also the transposed one, for the input gradient)."""
+        return q_nvfp4(self.weight.detach(), "16x16", rowwise=True, colwise=colwise, status=self._status_on(self.weight.device))
+
+    def forward(self, x, offset: Optional[int] = None, copies: Optional[NVFP4Tensor] = None, amax: Optional[torch.Tensor] = None):
+        train = torch.is_grad_enabled()
+        if offset is None:
+            draws = train and (x.requires_grad or self.weight.requires_grad)
+            if draws and x.is_cuda and torch.cuda.is_current_stream_capturing():
+                raise ValueError("a captured call with gradients needs its offset: a drawn one would be every replay's")
+            offset = _drawn() if draws else 0
+        if copies is None:
+            copies = self.quantize_weight(colwise=train and x.requires_grad)
+        return _NVFP4Linear.apply(x, self.weight, copies, self.sign_mask, self.seed, int(offset), self.main_grad, train,
+                                  self._status_on(x.device), amax)
