@@ -11,8 +11,8 @@
 // Warp 0 of each CTA loads its operand tiles, all of whose bytes count on the
 // leader's barriers; the leader's warp 1 issues the copies of scales to tensor
 // memory and the MMAs.  Warps 2 to 7 fetch scales: two each for P's 128 rows and
-// the halves of Q's 256 (every CTA needs all of Q's), two blocks at a time in turn,
-// each row's 16 bytes of a block by one lane, and put them into the stage's place.
+// the halves of Q's 256 (every CTA needs all of Q's), four blocks at a time (handed over two
+// at a time, which made room for one stage more, 8192 x 14336 x 4096 took 188 us for 154).
 // The eight warps 8-15 read 32 rows x 128 columns each when a tile is done.
 #pragma once
 
@@ -23,7 +23,6 @@ namespace qk {
 
 constexpr int kPair4EpiWarps = 8, kPair4ScaleWarps = 6;
 constexpr int kPair4Threads = 32 * (2 + kPair4ScaleWarps + kPair4EpiWarps);
-constexpr int kPair4Stages = 4;
 constexpr int kPair4OperandBytes = 2 * 128 * 128;
 constexpr int kPair4Unit = 4, kPair4Slots = 2;   // blocks whose scales are handed over together (ScaleUnit), and places for them
 constexpr int kPair4Second = 208;           // first column of the second buffer; the scales' columns begin at 464
@@ -32,15 +31,20 @@ constexpr int kPair4Scales = kPair4Second + 256;
 // the kernel is launched with.
 constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
 
-struct Pair4Smem {
-    uint8_t stage[kPair4Stages][kPair4OperandBytes];
-    uint8_t staging[kPair4EpiWarps][4096];
+// Operand stages are what shared memory goes to first: memory's queues are full, a stage's copies take some 2000 cycles and
+// its MMAs 512 (8192 x 4096 x 14336 179 us at three stages, 146 at four, 142 at five).  A BF16 C is stored from registers
+// and needs no staging to speak of; an FP32 C goes through staging as bulk stores and adds (adds from registers took 224
+// us of 14336 x 4096 x 8192, bulk ones 174).
+template <int OUT> struct Pair4Smem {
+    static constexpr int kStages = OUT == F32 ? 4 : 5, kStaging = OUT == F32 ? 4096 : 1024;
+    uint8_t stage[kStages][kPair4OperandBytes];
+    uint8_t staging[kPair4EpiWarps][kStaging];
     uint8_t scales[kPair4Slots][kPair4Unit][3 * kScaleAtom];   // P's rows, and Q's in halves
-    uint64_t full[kPair4Stages], empty[kPair4Stages], sc_full[kPair4Slots], sc_empty[kPair4Slots], acc_full[2], acc_free, drained;
+    uint64_t full[kStages], empty[kStages], sc_full[kPair4Slots], sc_empty[kPair4Slots], acc_full[2], acc_free, drained;
     uint32_t tmem_base;
     int abort_flag;
 };
-static_assert(sizeof(Pair4Smem) <= 232448, "shared memory of a CTA");
+static_assert(sizeof(Pair4Smem<F32>) <= 232448 && sizeof(Pair4Smem<BF16>) <= 232448, "shared memory of a CTA");
 
 // Tile t of the walk, in units of 256 x 256: groups of `group` tile rows, each
 // walked column by column, so that the tiles in flight share their operands in
@@ -58,17 +62,17 @@ QD void pair4_tile(int t, int tiles_p, int tiles_q, int group, int &p, int &q)
     q = r / height;
 }
 
-// The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  A unit's loads are issued
-// behind the fence of the unit ahead, which would wait for them: among the operands'
+// The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  Loads are issued
+// behind the fence of the hand-over ahead, which would wait for them: among the operands'
 // copies, which keep memory's queues full, a load takes some 4000 cycles.
-template <bool WHOLE>
-QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int first, int pairs, int tiles_p, int tiles_q, int rank,
+template <bool WHOLE, class Smem>
+QD void put_scales4(Smem &sm, const Mm4Args &a, int atom, int part, int first, int pairs, int tiles_p, int tiles_q, int rank,
                     int lane, volatile int *stop)
 {
     const Mm4Scales &g = atom == 0 ? a.p : a.q;
     const int kb_n = (int)a.store.kblocks, tiles = tiles_p * tiles_q;
     const uint32_t bar = cluster_addr(smem_u32(&sm.sc_full[0]), 0);
-    // places in the walk: of the unit that is loaded next, and of the one that is handed over
+    // places in the walk: of the four blocks that are loaded next, and of those that are handed over
     struct Place {
         int t, kb;
         int64_t row0;
@@ -86,8 +90,8 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
             if (at.t < tiles) settle(at);
         }
     };
-    // Two units' loads on their way, where registers allow.
-    constexpr uint32_t kSets = WHOLE ? 2 : 1;
+    // Two loads of four blocks on their way, where registers allow.
+    constexpr int kSets = WHOLE ? 2 : 1;
     ScaleUnit<WHOLE> held[kSets];
     if (first >= tiles) return;
     Place next = {first, 0, 0};
@@ -99,7 +103,7 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
         advance(next);
     };
 #pragma unroll
-    for (uint32_t i = 0; i < kSets; i++) load(held[i]);
+    for (int i = 0; i < kSets; i++) load(held[i]);
     for (uint32_t use = 0; now.t < tiles; use++) {
 #pragma unroll
         for (uint32_t slot = 0; slot < kPair4Slots; slot++) {
@@ -120,14 +124,65 @@ QD void put_scales4(Pair4Smem &sm, const Mm4Args &a, int atom, int part, int fir
     }
 }
 
-template <int OUT, bool WHOLE>
+// One lane's row of 64 sums to a BF16 C that is overwritten, columns col on, as vectors of 32 bytes (16 where C's rows lie
+// on 16-byte boundaries only; 8 columns lie in C or outside together).
+QD void store_row64(const MmArgs &g, const uint64_t (&acc)[32], int64_t row, int64_t col, bool wide)
+{
+    if (row >= g.rows_p) return;
+    uint16_t *const c = static_cast<uint16_t *>(g.c) + row * g.ldc + col;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float a, b;
+            unpack2(acc[8 * i + j], a, b);
+            w[j] = bf16_pair(a, b);
+        }
+        const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
+        if (wide && col + 16 * i + 16 <= g.rows_q) {
+            stg32(c + 16 * i, lo, hi);
+        } else {
+            if (col + 16 * i < g.rows_q) stg16(c + 16 * i, lo);
+            if (col + 16 * i + 8 < g.rows_q) stg16(c + 16 * i + 8, hi);
+        }
+    }
+}
+
+// A warp's 32 rows x 64 sums to a BF16 C of any pitch, or added to one, 8 columns at a time through 1 KiB of staging.
+QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
+{
+#pragma unroll
+    for (int p = 0; p < 8; p++) {
+        // chunk i of row r at place i ^ (r / 4 % 2): a quarter of a warp's 16-byte accesses lie on all banks
+        ulonglong2 *const to = reinterpret_cast<ulonglong2 *>(staging) + 2 * lane;
+        const int odd = (lane >> 2) & 1;
+        to[odd] = make_ulonglong2(acc[4 * p], acc[4 * p + 1]);
+        to[odd ^ 1] = make_ulonglong2(acc[4 * p + 2], acc[4 * p + 3]);
+        __syncwarp();
+        const int64_t col = col0 + 8 * p + (lane & 7);
+#pragma unroll
+        for (int it = 0; it < 8; it++) {
+            const int r = 4 * it + (lane >> 3), chunk = ((lane >> 2) & 1) ^ ((r >> 2) & 1);
+            if (row0 + r < g.rows_p && col < g.rows_q)
+                put_one<BF16>(static_cast<uint16_t *>(g.c) + (row0 + r) * g.ldc + col, staging[8 * r + 4 * chunk + (lane & 3)], g.accumulate);
+        }
+        __syncwarp();
+    }
+}
+
+// ANY: C's rows are no multiple of 16 bytes, or a BF16 C is added to.  (A kernel of its own: the code for it, though not
+// reached, took 161 us of 8192 x 14336 x 4096 where the kernel without it takes 154.)
+template <int OUT, bool WHOLE, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair4Threads, 1)
 k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
            const __grid_constant__ CUtensorMap map_c, const Mm4Args a)
 {
     const MmArgs &g = a.store;
+    using Smem = Pair4Smem<OUT>;
+    constexpr int kStages = Smem::kStages;
     extern __shared__ __align__(1024) uint8_t dsm[];
-    Pair4Smem &sm = *reinterpret_cast<Pair4Smem *>(dsm);
+    Smem &sm = *reinterpret_cast<Smem *>(dsm);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -137,7 +192,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     volatile int *const stop = &sm.abort_flag;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPair4Stages; s++) {
+        for (int s = 0; s < kStages; s++) {
             mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
         }
@@ -173,7 +228,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                 pair4_tile(t, tiles_p, tiles_q, a.group, tp, tq);
                 const int p0 = tp * 256 + 128 * rank, q0 = tq * 256 + 128 * rank;
                 for (int kb = 0; kb < kb_n; kb++) {
-                    if (issued >= kPair4Stages && !mm_wait(&sm.empty[s], use, stop, g.status)) {
+                    if (issued >= kStages && !mm_wait(&sm.empty[s], use, stop, g.status)) {
                         ok = false;
                         break;
                     }
@@ -183,7 +238,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                     tma_load_tile_pair(st, &map_p, kb * 128, p0, bar);
                     tma_load_tile_pair(st + 128 * 128, &map_q, kb * 128, q0, bar);
                     issued++;
-                    if (++s == kPair4Stages) {
+                    if (++s == kStages) {
                         s = 0;
                         use ^= 1;
                     }
@@ -191,12 +246,12 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             }
             // every stage is released before this CTA may leave: the leader's commits
             // arrive here
-            for (uint32_t j = issued > kPair4Stages ? issued - kPair4Stages : 0; ok && j < issued; j++)
-                ok = mm_wait(&sm.empty[j % kPair4Stages], (j / kPair4Stages) & 1, stop, g.status);
+            for (uint32_t j = issued > kStages ? issued - kStages : 0; ok && j < issued; j++)
+                ok = mm_wait(&sm.empty[j % kStages], (j / kStages) & 1, stop, g.status);
             if (!ok) {   // copies in flight land before shared memory goes away
                 if (rank == 0) {
-                    for (uint32_t j = issued > kPair4Stages ? issued - kPair4Stages : 0; j < issued; j++)
-                        (void)mbar_wait_bounded(&sm.full[j % kPair4Stages], (j / kPair4Stages) & 1);
+                    for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; j++)
+                        (void)mbar_wait_bounded(&sm.full[j % kStages], (j / kStages) & 1);
                 } else {   // counted on the leader's barriers: far longer than any copy takes
                     const unsigned long long t0 = globaltimer();
                     while (globaltimer() - t0 < 10000000ull) {}
@@ -239,7 +294,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                         }
                         __syncwarp();
                         if (kb % kPair4Unit == kPair4Unit - 1 || kb + 1 == kb_n) unit++;
-                        if (++s == kPair4Stages) {
+                        if (++s == kStages) {
                             s = 0;
                             par ^= 1;
                         }
@@ -260,6 +315,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         const uint32_t to_leader = cluster_addr(smem_u32(&sm.acc_free), 0);
         const float fp = __ldg(a.s_p), fq = __ldg(a.s_q);
         const uint64_t sp = pack2(__float_as_uint(fp), __float_as_uint(fp)), sq = pack2(__float_as_uint(fq), __float_as_uint(fq));
+        const bool wide = ((reinterpret_cast<uintptr_t>(g.c) | (uintptr_t)(2 * g.ldc)) & 31) == 0;   // of a BF16 C
         uint32_t tile = 0;
         for (int t = first; t < tiles && !__any_sync(0xFFFFFFFFu, *stop); t += pairs, tile++) {
             int tp, tq;
@@ -280,9 +336,12 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                 uint64_t acc[32];
 #pragma unroll
                 for (int j = 0; j < 32; j++) acc[j] = fmul2(fmul2(pack2(r[2 * j], r[2 * j + 1]), sp), sq);
-                if (!__any_sync(0xFFFFFFFFu, *stop))
-                    mm_store_tile<OUT, true, 1, 64>(g, &map_c, sm.staging[warp - 2 - kPair4ScaleWarps], acc,
-                                                    (int64_t)tp * 256 + 128 * (int)rank + quad * 32, (int64_t)tq * 256 + half * 128 + h * 64, lane);
+                if (__any_sync(0xFFFFFFFFu, *stop)) return;
+                const int64_t row = (int64_t)tp * 256 + 128 * (int)rank + quad * 32, col = (int64_t)tq * 256 + half * 128 + h * 64;
+                uint8_t *const staging = sm.staging[warp - 2 - kPair4ScaleWarps];
+                if constexpr (OUT == BF16 && ANY) store_any64(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
+                else if constexpr (OUT == BF16) store_row64(g, acc, row + lane, col, wide);
+                else mm_store_tile<OUT, true, 1, 64>(g, &map_c, staging, acc, row, col, lane);
             };
             part(half, true);
             part(1 - half, false);

@@ -48,12 +48,12 @@ cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int6
 
 // The registers that the pair kernel's epilogue takes over have to be there at
 // its launch: it would wait for them forever.
-template <int OUT, bool WHOLE> cudaError_t pair4_registers_ready()
+template <int OUT, bool WHOLE, bool ANY> cudaError_t pair4_registers_ready()
 {
     static std::atomic<bool> ready{false};
     if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, WHOLE>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, WHOLE, ANY>);
     if (e != cudaSuccess) return e;
     if (a.numRegs * kPair4Threads < 32 * (kPair4EpiWarps * kPair4EpiRegs + (2 + kPair4ScaleWarps) * kPair4Regs)) return cudaErrorInvalidConfiguration;
     ready.store(true, std::memory_order_relaxed);
@@ -61,29 +61,34 @@ template <int OUT, bool WHOLE> cudaError_t pair4_registers_ready()
 }
 
 // Tiles of 256 x 256 on CTA pairs.
-template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
+template <int OUT, bool WHOLE, bool ANY> cudaError_t mm4_pair_t(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q, map_c = {};
     MmArgs &g = a.store;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K / 2, 128);
     if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, 128);
-    const bool bulk = g.ldc % (OUT == F32 ? 4 : 8) == 0 && (OUT == F32 || !g.accumulate);
-    g.store = !bulk ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
-    if (e == cudaSuccess && bulk) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, WHOLE>>(sizeof(Pair4Smem));
-    if (e == cudaSuccess) e = pair4_registers_ready<OUT, WHOLE>();
+    g.store = ANY || OUT == BF16 ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
+    if (e == cudaSuccess && !ANY && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, WHOLE, ANY>>(sizeof(Pair4Smem<OUT>));
+    if (e == cudaSuccess) e = pair4_registers_ready<OUT, WHOLE, ANY>();
     if (e != cudaSuccess) return e;
     const int64_t tiles_p = (g.rows_p + 255) / 256, tiles_q = (g.rows_q + 255) / 256, tiles = tiles_p * tiles_q, pairs = sm_count() / 2;
     a.group = tiles_q < tiles_p && tiles_q <= 32 ? 2 : tiles_p < 32 ? (int)tiles_p : 32;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_k(true, k_mm4_pair<OUT, WHOLE>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
-                    sizeof(Pair4Smem), st, map_p, map_q, map_c, a);
+    return launch_k(true, k_mm4_pair<OUT, WHOLE, ANY>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
+                    sizeof(Pair4Smem<OUT>), st, map_p, map_q, map_c, a);
 }
 
 Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K) { return {at, K / 16, (int)rows, blk ? 4 : 0}; }
 
 // Every row of scales begins on a 16-byte boundary.
 bool whole_rows(const Mm4Scales &s) { return ((reinterpret_cast<uintptr_t>(s.at) | (uintptr_t)s.pitch) & 15) == 0; }
+
+template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, cudaStream_t st)
+{
+    const bool any = a.store.ldc % (OUT == F32 ? 4 : 8) != 0 || (OUT == BF16 && a.store.accumulate);
+    return any ? mm4_pair_t<OUT, WHOLE, true>(p, q, a, K, st) : mm4_pair_t<OUT, WHOLE, false>(p, q, a, K, st);
+}
 
 // CTAs that clusters of `split` keep resident, one per SM (see the blockwise product's).
 int cluster_ctas4(int split)
