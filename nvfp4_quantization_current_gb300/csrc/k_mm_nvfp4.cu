@@ -122,7 +122,7 @@ int cluster_ctas4(int split)
 // The estimate's terms (us) are a fit to 1160 calls of every plan that 170 shapes
 // allow (1 to 4096 tokens, weights from 512 x 256 to 18432 x 18432, K of every
 // multiple of 32, weights in either blocks; GB300, graphs of calls); its choices take
-// 0.6% more time than the best plan on the average and 10% at most.  A call has a
+// 0.5% more time than the best plan on the average and 11% at most.  A call has a
 // fixed part, a cluster adds its sum, a CTA takes `block` for each 256 elements of K
 // (`odd` times as long where scale rows begin anywhere), two CTAs of an SM `share`
 // times one's time, and a CTA that comes after another a start of its own.  Some of
@@ -139,15 +139,15 @@ Mm4Plan mm4_plan(int64_t M, int64_t N, int64_t kblocks, bool whole, int sms)
         double fixed, block, share, odd, split[3], start;
         int resident;
     };
-    static constexpr Width kWidths[] = {{16, 3.57, 0.274, 1.504, 1.203, {0.57, 0.57, 0.69}, 2.88, 2},
-                                        {32, 4.72, 0.296, 1.498, 1.113, {0.06, 0.0, 0.32}, 3.96, 2},
-                                        {64, 6.25, 0.312, 1.609, 1.166, {0.0, 0.0, 0.21}, 5.76, 2},
-                                        {128, 6.96, 0.327, 1.0, 1.187, {0.0, 0.0, 0.0}, 6.89, 1},
-                                        {192, 8.78, 0.357, 1.0, 1.298, {0.0, 0.0, 0.0}, 9.36, 1}};
+    static constexpr Width kWidths[] = {{16, 3.62, 0.269, 1.473, 1.207, {0.56, 0.62, 0.67}, 2.92, 2},
+                                        {32, 4.71, 0.290, 1.477, 1.137, {0.09, 0.0, 0.31}, 3.95, 2},
+                                        {64, 6.22, 0.316, 1.589, 1.152, {0.0, 0.0, 0.04}, 5.77, 2},
+                                        {128, 6.97, 0.323, 1.0, 1.192, {0.0, 0.0, 0.0}, 6.87, 1},
+                                        {192, 8.73, 0.358, 1.0, 1.272, {0.0, 0.0, 0.0}, 9.31, 1}};
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
     const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
     Mm4Plan best = {0, 1};
-    double cost = 3.55 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * 0.363 * (whole ? 1.0 : 1.316) + 1.445 * (whole ? 1.0 : 1.718));
+    double cost = 1.99 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * 0.339 * (whole ? 1.0 : 1.393) + 2.43 * (whole ? 1.0 : 1.438));
     for (const Width &w : kWidths) {
         const int64_t tz = (M + w.bn - 1) / w.bn;
         if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;

@@ -1,143 +1,22 @@
-// The root-mean-square norm ahead of a linear layer, with the residual's addition, and its gradient.
+// The root-mean-square norm ahead of a linear layer, with the residual's addition.
 //
 //   h = x + residual (rounded to its type once; h = x without a residual)
 //   s = 1 / sqrt(mean(h^2) + eps) per row,   y = (h s) w
-//   dx = s (g - v mean(g v)) + dh,  g = dy w,  v = h s,      dw = sum over rows of dy v
 //
 // The sums run in FP32 in an order fixed by the shape.  y is either stored
 // (norm_add) or cast in registers to the rowwise 1x128 E4M3 copy
-// (norm_q_blockwise; k_norm_cast.cu makes both copies).
-#include "q_engine.cuh"
-#include "q_internal.h"
+// (norm_q_blockwise; k_norm_cast.cu makes the transposed one from h and s).  All of it
+// is bound by memory, and a row is read once: it stays in registers between its sum
+// and what is made of it.  Measured on a GB300, in graphs of calls: 8192 x 4096 BF16
+// with a residual 42.4 us (268 MB at 6.3 TB/s, a copy's rate being 6.8), without one
+// 20.8, in FP32 79.6; its rowwise copy 38.9 with a residual, 26.0 without (301 warp
+// instructions for 512 elements: issue slots 70 % in use); 16 rows 2.0, of which the
+// launch is most.
+#include "q_norm.cuh"
 
 namespace qk {
 
 namespace {
-
-// W consecutive elements in one access: 16 bytes, or one element where rows do
-// not start on 16-byte boundaries.
-template <int DT, int W> struct Piece {
-    static constexpr int kBytes = W * In<DT>::BYTES;
-    static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
-    uint32_t w[kWords];
-    QD void load(const void *p, int64_t i)
-    {
-        const char *const at = static_cast<const char *>(p) + i * In<DT>::BYTES;
-        if constexpr (kBytes == 16) {
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(at));
-        } else if constexpr (kBytes == 4) {
-            w[0] = *reinterpret_cast<const uint32_t *>(at);
-        } else {
-            w[0] = *reinterpret_cast<const uint16_t *>(at);
-        }
-    }
-    QD void shared(const uint8_t *p, int i)
-    {
-        const uint8_t *const at = p + i * In<DT>::BYTES;
-        if constexpr (kBytes == 16) {
-            const uint4 v = lds16(at);
-            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-        } else if constexpr (kBytes == 4) {
-            w[0] = *reinterpret_cast<const uint32_t *>(at);
-        } else {
-            w[0] = *reinterpret_cast<const uint16_t *>(at);
-        }
-    }
-    QD void store(void *p, int64_t i) const
-    {
-        char *const at = static_cast<char *>(p) + i * In<DT>::BYTES;
-        if constexpr (kBytes == 16) stg16(at, make_uint4(w[0], w[1], w[2], w[3]));
-        else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t *>(at) = w[0];
-        else *reinterpret_cast<uint16_t *>(at) = (uint16_t)w[0];
-    }
-    QD void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < kWords; i++) w[i] = 0u;
-    }
-    QD float at(int j) const
-    {
-        if constexpr (DT == F32) return __uint_as_float(w[j]);
-        else if constexpr (W == 1) return __uint_as_float(w[0] << 16);
-        else return __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
-    }
-    // Elements 2j and 2j + 1 as two packed FP32 values.
-    QD uint64_t pair(int j) const
-    {
-        static_assert(W % 2 == 0, "pairs");
-        if constexpr (DT == F32) return pack2(w[2 * j], w[2 * j + 1]);
-        else return pack2(w[j] << 16, w[j] & 0xFFFF0000u);
-    }
-    QD void set_pair(int j, uint64_t v)
-    {
-        float a, b;
-        unpack2(v, a, b);
-        if constexpr (DT == F32) w[2 * j] = __float_as_uint(a), w[2 * j + 1] = __float_as_uint(b);
-        else w[j] = bf16_pair(a, b);
-    }
-    QD void add(const Piece &p)
-    {
-        if constexpr (W > 1) {
-#pragma unroll
-            for (int j = 0; j < W / 2; j++) set_pair(j, fadd2(pair(j), p.pair(j)));
-        } else {
-            const float f[1] = {at(0) + p.at(0)};
-            set(f);
-        }
-    }
-    QD void set(const float (&f)[W])
-    {
-        if constexpr (DT == F32) {
-#pragma unroll
-            for (int j = 0; j < W; j++) w[j] = __float_as_uint(f[j]);
-        } else if constexpr (W == 1) {
-            w[0] = bf16_bits(f[0]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; j += 2) w[j / 2] = bf16_pair(f[j], f[j + 1]);
-        }
-    }
-};
-
-// W weights from element k on, whichever type they have (k a multiple of W, the weights 16-byte aligned).
-template <int W> QD void load_weights(float (&f)[W], const void *w, bool f32, int64_t k)
-{
-    if (f32) {
-        const float *p = static_cast<const float *>(w) + k;
-        if constexpr (W % 4 == 0) {
-#pragma unroll
-            for (int j = 0; j < W; j += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(p + j));
-                f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; j++) f[j] = __ldg(p + j);
-        }
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(w) + k;
-        if constexpr (W == 8) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-#pragma unroll
-            for (int j = 0; j < 8; j++) f[j] = elem<BF16>(v, j);
-        } else if constexpr (W == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-            f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
-            f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; j++) f[j] = __uint_as_float((uint32_t)__ldg(p + j) << 16);
-        }
-    }
-}
-
-QD float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
 
 // The sum of squares of a thread's pieces.
 template <int DT, int W, int N> QD float squares(const Piece<DT, W> (&h)[N])
@@ -157,19 +36,6 @@ template <int DT, int W, int N> QD float squares(const Piece<DT, W> (&h)[N])
         for (int i = 0; i < N; i++) sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
     }
     return sum;
-}
-
-// Sum over the 2^gshift consecutive threads (gshift >= 5) that share a row, to
-// all of them; part: a word per warp, used by no other call that is in flight.
-// Every thread of the CTA calls it.
-QD float row_sum(float v, float *part, int gshift)
-{
-    v = warp_sum(v);
-    if (gshift == 5) return v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = 1 << (gshift - 5);
-    if (lane == 0) part[warp] = v;
-    __syncthreads();
-    return warp_sum(lane < n ? part[(warp & ~(n - 1)) + lane] : 0.0f);
 }
 
 // 1 / sqrt(sum / K + eps): the approximate root's reciprocal (two units in the last place) after one step of Newton's
@@ -379,21 +245,6 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
 
-// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.  The first: of lines
-// that L2 may drop first (the gradient's inputs: 8192 x 4096 BF16 46.5 us, 47.0 else; where a sum is cast it is 2 us slower).
-QD void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    uint64_t once;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(once) : "memory");
-}
-QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-}
-
 // Many rows.  They come by bulk copies into a ring of shared memory, so that
 // memory stays busy while rows are summed and written: a step is one row, 16 elements
 // per thread in pieces of W (WIDE: rows longer than 512 threads' are).  Rows that begin between 16-byte boundaries are copied with
@@ -507,237 +358,9 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 512, RES || WIDE ? 1 : 2) k_norm
     if (MODE == kNormStore && a.amax != nullptr) norm_amax<DT>(a, m);
 }
 
-// The gradient.  The rows of dy, h and dh come by bulk copies into a ring of
-// shared memory, so that memory stays busy while rows are summed: a step is R rows,
-// each over all threads of the CTA, or 8 R short ones, R for a warp (where E is 8), E
-// elements per thread in pieces of W.  A thread keeps its columns over all steps, and with them its part of
-// dw in registers, which it leaves as one row of `work`.  Rows that begin between
-// 16-byte boundaries are copied with the bytes around them (a 16-byte piece that holds
-// one of the row's bytes is the allocation's) and read an element at a time.
-template <int DT, int W, int E, int R, bool DH>
-__global__ void __launch_bounds__(512) k_norm_grad(const NormGradArgs a, int stages, int stage_bytes)
-{
-    constexpr bool kWarpRows = E == 8;
-    constexpr int VPT = E / W, kMostStages = 8, ES = In<DT>::BYTES, kTensors = DH ? 3 : 2;
-    extern __shared__ __align__(128) uint8_t dsm[];
-    __shared__ float part[2][R][16];
-    __shared__ __align__(8) uint64_t full[kMostStages];
-    const int lane = threadIdx.x & 31, rows = kWarpRows ? 8 * R : R;
-    const int T = kWarpRows ? 32 : blockDim.x, t = kWarpRows ? lane : threadIdx.x, mine = kWarpRows ? (threadIdx.x >> 5) * R : 0;   // the first row
-    const int K = (int)a.K, tensor_bytes = stage_bytes / kTensors;
-    const int64_t steps_all = (a.M + rows - 1) / rows;
-    const int64_t steps = steps_all > blockIdx.x ? (steps_all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    // step i of this CTA: rows from row0(i) on, whose bytes begin `skew` into their copies
-    auto row0 = [&](int64_t i) { return ((int64_t)blockIdx.x + i * gridDim.x) * rows; };
-    auto skew = [&](int64_t row) { return W > 1 ? 0 : (int)((row * K * ES) & 15); };
-    auto issue = [&](int64_t i) {
-        const int64_t r0 = row0(i), n = a.M - r0 < rows ? a.M - r0 : rows;
-        const int off = skew(r0);
-        const uint32_t bytes = (uint32_t)(off + n * K * ES + 15) & ~15u;
-        const int s = (int)(i % stages);
-        uint8_t *const st = dsm + (int64_t)s * stage_bytes;
-        mbar_arrive_expect_tx(&full[s], bytes * kTensors);
-        const int64_t from = r0 * K * ES - off;
-        bulk_load_once(st, static_cast<const char *>(a.dy) + from, bytes, &full[s]);
-        bulk_load_once(st + tensor_bytes, static_cast<const char *>(a.h) + from, bytes, &full[s]);
-        if constexpr (DH) bulk_load_once(st + 2 * tensor_bytes, static_cast<const char *>(a.dh) + from, bytes, &full[s]);
-    };
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
-    griddep_wait();   // nothing was read or written so far
-    if (threadIdx.x == 0)
-        for (int64_t i = 0; i < steps && i < stages; i++) issue(i);
-    // The weights too, where registers allow; else they are loaded (from L1) where they are used.
-    constexpr bool kHeld = E <= 16;
-    float w[kHeld ? VPT : 1][W], dw[VPT][W];
-#pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int k = (t + i * T) * W;
-#pragma unroll
-        for (int j = 0; j < W; j++) w[kHeld ? i : 0][j] = dw[i][j] = 0.0f;
-        if (kHeld && k < K) load_weights<W>(w[kHeld ? i : 0], a.weight, a.wf32, k);
-    }
-    const float inv = __fdiv_rn(1.0f, (float)K);
-    int s = 0;
-    uint32_t parity = 0;
-    for (int64_t n = 0; n < steps; n++) {
-        const int64_t r0 = row0(n) + mine;
-        float f[R];
-#pragma unroll
-        for (int r = 0; r < R; r++) f[r] = r0 + r < a.M ? __ldg(a.rstd + r0 + r) : 0.0f;
-        const uint8_t *const st = dsm + (int64_t)s * stage_bytes + skew(row0(n)) + (int64_t)mine * K * ES;
-        const bool ok = mbar_wait_bounded(&full[s], parity);
-        Piece<DT, W> h[R][VPT], dy[R][VPT], dh[DH ? R : 1][DH ? VPT : 1];
-        float c[R];
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            const uint8_t *const at = st + r * K * ES;
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPT; i++) {
-                const int k = (t + i * T) * W;
-                h[r][i].zero();
-                dy[r][i].zero();
-                if (r0 + r < a.M && k < K) {
-                    dy[r][i].shared(at, k);
-                    h[r][i].shared(at + tensor_bytes, k);
-                    if constexpr (DH) dh[r][i].shared(at + 2 * tensor_bytes, k);
-                    if (!kHeld) load_weights<W>(w[0], a.weight, a.wf32, k);
-                }
-#pragma unroll
-                for (int j = 0; j < W; j++) {
-                    const float v = h[r][i].at(j) * f[r], d = dy[r][i].at(j);
-                    dw[i][j] = __fmaf_rn(d, v, dw[i][j]);
-                    sum = __fmaf_rn(d * w[kHeld ? i : 0][j], v, sum);
-                }
-            }
-            c[r] = sum;
-        }
-        // the rows' sums, and word that a wait ran out (no thread waits for another step then)
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            c[r] = warp_sum(c[r]);
-            if (!kWarpRows && lane == 0) part[n & 1][r][threadIdx.x >> 5] = c[r];
-        }
-        const bool stop = __syncthreads_or(!ok);
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-            if (!kWarpRows) c[r] = warp_sum(lane < (int)(blockDim.x >> 5) ? part[n & 1][r][lane] : 0.0f);
-            c[r] *= inv;
-        }
-        if (stop) {   // the copies in flight land before shared memory goes away
-            if (threadIdx.x == 0) {
-                for (int64_t j = n; j < steps && j < n + stages; j++) (void)mbar_wait_bounded(&full[j % stages], (uint32_t)((j / stages) & 1));
-                if (a.status != nullptr) atomicOr(a.status, kStTimeout);
-            }
-            break;
-        }
-        if (threadIdx.x == 0 && n + stages < steps) {   // every thread has the stage in its registers
-            fence_proxy_async();
-            issue(n + stages);
-        }
-#pragma unroll
-        for (int r = 0; r < R; r++) {
-#pragma unroll
-            for (int i = 0; i < VPT; i++) {
-                const int k = (t + i * T) * W;
-                if (r0 + r >= a.M || k >= K) continue;
-                float o[W];
-                if (!kHeld) load_weights<W>(w[0], a.weight, a.wf32, k);
-#pragma unroll
-                for (int j = 0; j < W; j++) {
-                    const float v = h[r][i].at(j) * f[r], e = __fmaf_rn(-v, c[r], dy[r][i].at(j) * w[kHeld ? i : 0][j]);
-                    o[j] = DH ? __fmaf_rn(e, f[r], dh[DH ? r : 0][DH ? i : 0].at(j)) : e * f[r];
-                }
-                Piece<DT, W> out;
-                out.set(o);
-                out.store(a.dx, (r0 + r) * K + k);
-            }
-        }
-        if (++s == stages) {
-            s = 0;
-            parity ^= 1;
-        }
-    }
-    if (a.work == nullptr) return;
-    // one row of `work`: the CTA's only part, or the sum of eight, which meet where the rows were
-    float *const to = !kWarpRows ? a.work + (int64_t)blockIdx.x * K : reinterpret_cast<float *>(dsm) + (threadIdx.x >> 5) * K;
-    if (kWarpRows) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < VPT; i++) {
-        const int k = (t + i * T) * W;
-        if (k < K) {
-            if constexpr (W % 4 == 0) {
-#pragma unroll
-                for (int j = 0; j < W; j += 4) *reinterpret_cast<float4 *>(to + k + j) = make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < W; j++) to[k + j] = dw[i][j];
-            }
-        }
-    }
-    if (kWarpRows) {
-        __syncthreads();
-        for (int k = threadIdx.x; k < K; k += blockDim.x) {
-            float sum = reinterpret_cast<const float *>(dsm)[k];
-            for (int r = 1; r < 8; r++) sum += reinterpret_cast<const float *>(dsm)[r * K + k];
-            a.work[(int64_t)blockIdx.x * K + k] = sum;
-        }
-    }
-}
-
-// Longer rows: a CTA's part of dw is kept in its row of `work`.
-template <int DT, int W, bool DH>
-__global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a)
-{
-    __shared__ float part[2][32];
-    float *const mine = a.work == nullptr ? nullptr : a.work + (int64_t)blockIdx.x * a.K;
-    griddep_wait();   // nothing was read or written so far
-    int flip = 0;
-    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, flip ^= 1) {
-        const int64_t base = row * a.K;
-        const float s = a.rstd[row];
-        float sum = 0.0f;
-        for (int64_t k = threadIdx.x * W; k < a.K; k += 1024 * W) {
-            Piece<DT, W> h, dy;
-            float w[W];
-            dy.load(a.dy, base + k);
-            h.load(a.h, base + k);
-            load_weights<W>(w, a.weight, a.wf32, k);
-#pragma unroll
-            for (int j = 0; j < W; j++) sum = __fmaf_rn(dy.at(j) * w[j], h.at(j) * s, sum);
-        }
-        const float c = __fdiv_rn(row_sum(sum, part[flip], 10), (float)a.K);
-        for (int64_t k = threadIdx.x * W; k < a.K; k += 1024 * W) {
-            Piece<DT, W> h, dy, dh, out;
-            float w[W], f[W];
-            dy.load(a.dy, base + k);
-            h.load(a.h, base + k);
-            if constexpr (DH) dh.load(a.dh, base + k);
-            load_weights<W>(w, a.weight, a.wf32, k);
-#pragma unroll
-            for (int j = 0; j < W; j++) {
-                const float v = h.at(j) * s, e = __fmaf_rn(-v, c, dy.at(j) * w[j]);
-                f[j] = DH ? __fmaf_rn(e, s, dh.at(j)) : e * s;
-                if (mine != nullptr) mine[k + j] = __fmaf_rn(dy.at(j), v, row == blockIdx.x ? 0.0f : mine[k + j]);
-            }
-            out.set(f);
-            out.store(a.dx, base + k);
-        }
-    }
-}
-
-// dw: the rows of `work`, added in the same order every time: 64 walks of every 64th row, then the walks.
-__global__ void __launch_bounds__(1024) k_norm_dw(const float *work, int64_t parts, int64_t K, void *dw, bool f32)
-{
-    __shared__ float sums[64][17];
-    const int c = threadIdx.x & 15, walk = threadIdx.x >> 4, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t k = (int64_t)blockIdx.x * 16 + c;
-    griddep_wait();
-    float sum = 0.0f;
-    if (k < K) {
-#pragma unroll 8
-        for (int64_t p = walk; p < parts; p += 64) sum += work[p * K + k];
-    }
-    sums[walk][c] = sum;
-    __syncthreads();
-    if (warp >= 16) return;
-    sum = warp_sum(sums[lane][warp] + sums[lane + 32][warp]);   // the walks of column `warp`
-    const int64_t at = (int64_t)blockIdx.x * 16 + warp;
-    if (lane == 0 && at < K) {
-        if (f32) static_cast<float *>(dw)[at] = sum;
-        else static_cast<uint16_t *>(dw)[at] = (uint16_t)bf16_bits(sum);
-    }
-}
-
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-
-constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM's CTAs for rows on their way
 
 int log2_up(int64_t n)
 {
@@ -817,71 +440,6 @@ template <int DT, int MODE> cudaError_t norm_t(const NormArgs &a, cudaStream_t s
     return norm_w<DT, In<DT>::VEC, MODE>(a, st);
 }
 
-// How a gradient's rows are laid out: rows of a step, elements of a thread (0: the loop over long rows), threads, CTAs,
-// and the ring.  Two rows a step share a reduction (8192 x 4096 BF16 without dh 41.8 us
-// at one, 37.8 at two), unless they spill (with dh 46.4 and 52.3, and dw's 3 in each);
-// 16 elements a thread beat 8 on twice the threads (46.8 and 56.7).
-struct GradPlan {
-    int rows, elements, threads, ctas, stages, stage_bytes;
-};
-GradPlan grad_plan(int64_t M, int64_t K, int dt, bool dh)
-{
-    const int es = dt == BF16 ? 2 : 4, tensors = dh ? 3 : 2;
-    GradPlan p = {1, 0, 1024, 0, 0, 0};
-    // The shared memory of an SM holds the rings of all CTAs, two steps in each at least.
-    auto copy_bytes = [&](int rows) { return (rows * K * es + 15) / 16 * 16 + (K * es % 16 != 0 ? 16 : 0); };   // and what lies around the rows
-    int per_sm = 1;
-    if (K <= 256) {
-        p.rows = 32;
-        p.elements = 8;
-        p.threads = 256;
-        per_sm = 2;
-    } else if (K <= 16384 && 2 * tensors * copy_bytes(1) <= kRingBytes) {
-        p.elements = K <= 8192 ? 16 : 32;
-        p.threads = (int)((K + 32 * p.elements - 1) / (32 * p.elements)) * 32;
-        p.rows = p.elements == 16 && !dh && K * es % 16 == 0 && 4 * tensors * copy_bytes(2) <= kRingBytes ? 2 : 1;
-        per_sm = 512 / p.threads < 8 ? 512 / p.threads : 8;
-    }
-    if (p.elements != 0) {
-        p.stage_bytes = tensors * (int)copy_bytes(p.rows);
-        const int fits = kRingBytes / (2 * p.stage_bytes);
-        per_sm = per_sm > fits ? fits : per_sm;
-        p.stages = kRingBytes / per_sm / p.stage_bytes;
-        if (p.stages > 8) p.stages = 8;
-    }
-    const int64_t most = (int64_t)per_sm * 152, need = (M + p.rows - 1) / p.rows;
-    p.ctas = (int)(need < most ? need : most);
-    return p;
-}
-
-template <int DT, int W, int E, int R, bool DH> cudaError_t grad_rows(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
-{
-    const cudaError_t e = engine_smem_ready<k_norm_grad<DT, W, E, R, DH>>(kRingBytes, true);
-    if (e != cudaSuccess) return e;
-    return launch_k(true, k_norm_grad<DT, W, E, R, DH>, dim3(p.ctas), dim3(p.threads), (size_t)p.stages * p.stage_bytes, st, a,
-                    p.stages, p.stage_bytes);
-}
-
-template <int DT, int W, bool DH> cudaError_t grad_w(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
-{
-    switch (p.elements) {
-    case 8: return grad_rows<DT, W, 8, 4, DH>(a, p, st);
-    case 16:
-        if constexpr (!DH && W > 1)
-            if (p.rows == 2) return grad_rows<DT, W, 16, 2, DH>(a, p, st);
-        return grad_rows<DT, W, 16, 1, DH>(a, p, st);
-    case 32: return grad_rows<DT, W, 32, 1, DH>(a, p, st);
-    default: return launch_k(true, k_norm_grad_long<DT, W, DH>, dim3(p.ctas), dim3(p.threads), 0, st, a);
-    }
-}
-
-template <int DT> cudaError_t grad_t(const NormGradArgs &a, const GradPlan &p, cudaStream_t st)
-{
-    constexpr int VEC = In<DT>::VEC;
-    if (a.K % VEC != 0) return a.dh != nullptr ? grad_w<DT, 1, true>(a, p, st) : grad_w<DT, 1, false>(a, p, st);
-    return a.dh != nullptr ? grad_w<DT, VEC, true>(a, p, st) : grad_w<DT, VEC, false>(a, p, st);
-}
-
 }  // namespace
 
 cudaError_t launch_norm_add(const NormArgs &a, int dt, cudaStream_t st)
@@ -897,23 +455,6 @@ cudaError_t launch_norm_cast_rows(const NormArgs &a, int dt, cudaStream_t st)
 {
     if (a.q_row == nullptr) return dt == BF16 ? norm_t<BF16, kNormFactor>(a, st) : norm_t<F32, kNormFactor>(a, st);
     return dt == BF16 ? norm_t<BF16, kNormCast>(a, st) : norm_t<F32, kNormCast>(a, st);
-}
-
-int64_t norm_grad_rows(int64_t M, int64_t K, int dt)
-{
-    // enough with dh and without it
-    const GradPlan p = grad_plan(M, K, dt, false), q = grad_plan(M, K, dt, true);
-    return p.ctas > q.ctas ? p.ctas : q.ctas;
-}
-
-cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st)
-{
-    const GradPlan p = grad_plan(a.M, a.K, dt, a.dh != nullptr);
-    if (dw == nullptr) a.work = nullptr;
-    const cudaError_t e = dt == BF16 ? grad_t<BF16>(a, p, st) : grad_t<F32>(a, p, st);
-    if (e != cudaSuccess || dw == nullptr) return e;
-    return launch_k(true, k_norm_dw, dim3((unsigned)((a.K + 15) / 16)), dim3(1024), 0, st, (const float *)a.work,
-                    (int64_t)p.ctas, a.K, dw, a.wf32);
 }
 
 }  // namespace qk
