@@ -259,34 +259,6 @@ QD void mul2(float &a, float &b, float s0, float s1)
         : "+f"(a), "+f"(b) : "f"(s0), "f"(s1));
 }
 
-// Two FP32 values in a 64-bit register, and packed FP32 arithmetic on them
-// (each half rounded as the scalar instruction rounds it).
-QD uint64_t pack2(uint32_t a, uint32_t b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-QD void unpack2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-QD uint64_t fmul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-QD uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-QD uint64_t fadd2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Butterfly on two column pairs: (a, b) -> (a + b, a - b) for (a0, b0) and
 // (a1, b1) together (one packed FP32x2 add and one sub, each rounded once).
 QD void bfly2(float &a0, float &a1, float &b0, float &b1)

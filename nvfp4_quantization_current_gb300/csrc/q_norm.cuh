@@ -4,6 +4,7 @@
 
 #include "q_engine.cuh"
 #include "q_internal.h"
+#include "q_packed.cuh"
 
 namespace qk {
 

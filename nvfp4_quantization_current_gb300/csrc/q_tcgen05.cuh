@@ -3,6 +3,7 @@
 #pragma once
 
 #include "q_engine.cuh"
+#include "q_packed.cuh"
 
 namespace qk {
 
