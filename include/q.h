@@ -505,8 +505,10 @@ q_status matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, q
  *   rstd [M] FP32 (written);  eps >= 0, finite.
  *   h is written where there is a residual, and has to be NULL without one.
  *   amax  NULL, or one float: max|y| over the tensor as it is stored, what
- *   q_amax(y) gives and Q_AMAX_GIVEN takes.  *status (may be NULL): Q_ST_NONFINITE
- *   where that maximum is inf or NaN; without amax nothing is reported.
+ *   q_amax(y) gives and Q_AMAX_GIVEN takes.
+ *   *status (may be NULL): Q_ST_NONFINITE where that maximum is inf or NaN (without
+ *   amax it is not looked for), Q_ST_TIMEOUT where a wait for the rows' copies ran
+ *   out (2 s; the outputs are not whole then).
  * A row whose squares leave FP32's range has rstd 0, a row of zeros with
  * eps = 0 rstd inf.  NaN and inf stay in their rows.
  * h may be x or residual themselves, and y the other one, or x where there is

@@ -164,7 +164,9 @@ def _out(dtype):
 
 
 # The kernels write through a pointer: this is what autograd's check of the tensors that it saved goes by.
-_written = torch.autograd.graph.increment_version
+# (Inference tensors have no counter.)
+def _written(t):
+    torch.autograd.graph.increment_version([u for u in t if not u.is_inference()] if isinstance(t, list) else [] if t.is_inference() else t)
 
 
 def _written_copies(c):

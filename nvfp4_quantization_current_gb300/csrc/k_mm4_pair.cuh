@@ -300,7 +300,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                         }
                     }
                 }
-                if (!ok && elect_one()) {   // aborted: MMAs in flight end before their memory goes away
+                if (__any_sync(0xFFFFFFFFu, !ok || *stop) && elect_one()) {   // aborted: MMAs in flight end before their memory goes away
                     mma_commit_pair(&sm.drained);
                     (void)mbar_wait_bounded(&sm.drained, 0);
                 }
@@ -313,7 +313,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         regs_more<kPair4EpiRegs>();
         const int quad = warp & 3, half = (warp - 2 - kPair4ScaleWarps) >> 2;   // 32 tensor memory lanes, 128 columns
         const uint32_t to_leader = cluster_addr(smem_u32(&sm.acc_free), 0);
-        const float fp = __ldg(a.s_p), fq = __ldg(a.s_q);
+        const float fp = load_float(a.s_p), fq = load_float(a.s_q);
         const uint64_t sp = pack2(__float_as_uint(fp), __float_as_uint(fp)), sq = pack2(__float_as_uint(fq), __float_as_uint(fq));
         const bool wide = ((reinterpret_cast<uintptr_t>(g.c) | (uintptr_t)(2 * g.ldc)) & 31) == 0;   // of a BF16 C
         uint32_t tile = 0;

@@ -156,9 +156,9 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
             }
             __syncwarp();
         }
-        if (!ok && elect_one()) {   // aborted: the MMAs in flight end before their memory goes away
-            mma_commit(&sm.drained);
-            (void)mbar_wait_bounded(&sm.drained, 0);
+        if (elect_one()) {   // the MMAs in flight end before their memory goes away, whoever gave up
+            if (!ok) mma_commit(&sm.drained);
+            (void)mbar_wait_bounded(ok ? &sm.done : &sm.drained, 0);
         }
         __syncwarp();
     } else {
@@ -203,7 +203,7 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
     if (warp < kEpiWarps && !gave_up) {
         // a warp takes two columns at a time, four rows per lane
         using T = typename OutT<OUT>::T;
-        const float s_p = __ldg(a.s_p), s_q = __ldg(a.s_q);
+        const float s_p = load_float(a.s_p), s_q = load_float(a.s_q);
         const int64_t row = (int64_t)p0 + 4 * lane;
         const bool vec = (g.ldc & 3) == 0 && row + 4 <= g.rows_p && !g.accumulate;
         const int j1 = BN * (rank + 1) / split;

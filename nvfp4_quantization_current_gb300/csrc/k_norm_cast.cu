@@ -9,6 +9,7 @@
 // maxima meet in shared memory, and the codes are transposed in the consumed stage
 // and written as full 128-byte rows.
 #include "q_engine.cuh"
+#include "q_global.cuh"
 #include "q_internal.h"
 
 namespace qk {
@@ -22,9 +23,10 @@ template <int N> QD void col_weights(float (&w)[N], const void *weight, bool f32
     for (int c = 0; c < N; c += 4) {
         float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (in && f32) {
-            f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(weight) + k + c));
+            const uint4 v = load_16(static_cast<const float *>(weight) + k + c);
+            f = make_float4(elem<F32>(v, 0), elem<F32>(v, 1), elem<F32>(v, 2), elem<F32>(v, 3));
         } else if (in) {
-            const uint2 b = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(weight) + k + c));
+            const uint2 b = load_8(static_cast<const uint16_t *>(weight) + k + c);
             f = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
                             __uint_as_float(b.y & 0xFFFF0000u));
         }
@@ -55,7 +57,7 @@ k_norm_cols(const __grid_constant__ CUtensorMap tmap, int64_t M, int64_t K, cons
         if (tile < 0) return;
         const int64_t tm = tile / tiles_k, k = (tile - tm * tiles_k) * TC + lane * VEC;
 #pragma unroll
-        for (int j = 0; j < 8; j++) s_ahead[j] = __ldg(rstd + tm * kRows + 8 * warp + j);
+        for (int j = 0; j < 8; j++) s_ahead[j] = load_float(rstd + tm * kRows + 8 * warp + j);
         col_weights<VEC>(w_ahead, weight, wf32, k, k < K);
     };
     fetch(tiles_m * tiles_k - 1 - blockIdx.x);

@@ -601,7 +601,7 @@ q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void 
     if (dh != nullptr) TRY(need(fn, "dh", dh, 16));
     TRY(need(fn, "dx", dx, 16));
     if (dw != nullptr) TRY(need(fn, "work", work, 16));
-    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, status, M, K};
+    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, status, M, K, false};
     LAUNCH(fn, qk::launch_norm_grad(a, (int)in, dw, S(stream)));
     return Q_OK;
 }

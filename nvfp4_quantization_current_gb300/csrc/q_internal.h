@@ -141,6 +141,7 @@ struct NormGradArgs {
     float *work;
     int32_t *status;
     int64_t M, K;
+    bool once;   // set by the launcher: the inputs are read once
 };
 int64_t norm_grad_rows(int64_t M, int64_t K, int dt);   // rows of K floats in `work`
 cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st);

@@ -2,6 +2,7 @@
 // block scales from memory to where the tensor core copies them from.
 #pragma once
 
+#include "q_global.cuh"
 #include "q_mm.cuh"
 
 namespace qk {
@@ -52,7 +53,7 @@ template <bool WHOLE> struct ScaleUnit {
         const uint8_t *const begin = g.at + (row >> g.shift) * g.pitch;
         const uintptr_t p = (reinterpret_cast<uintptr_t>(begin + (int64_t)kb * 16) & ~(uintptr_t)15) + 16 * n;
         if (row >= g.rows || p >= reinterpret_cast<uintptr_t>(begin + g.pitch)) return make_uint4(0u, 0u, 0u, 0u);
-        return __ldg(reinterpret_cast<const uint4 *>(p));
+        return load_16(reinterpret_cast<const void *>(p));
     }
     template <int N> QD void load(const Mm4Scales &g, int64_t row0, int kb, int lane)
     {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "q_engine.cuh"
+#include "q_global.cuh"
 #include "q_internal.h"
 #include "q_packed.cuh"
 
@@ -102,26 +103,27 @@ template <int W> QD void load_weights(float (&f)[W], const void *w, bool f32, in
         if constexpr (W % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < W; j += 4) {
-                const float4 v = __ldg(reinterpret_cast<const float4 *>(p + j));
-                f[j] = v.x, f[j + 1] = v.y, f[j + 2] = v.z, f[j + 3] = v.w;
+                const uint4 v = load_16(p + j);
+#pragma unroll
+                for (int i = 0; i < 4; i++) f[j + i] = elem<F32>(v, i);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < W; j++) f[j] = __ldg(p + j);
+            for (int j = 0; j < W; j++) f[j] = load_float(p + j);
         }
     } else {
         const uint16_t *p = static_cast<const uint16_t *>(w) + k;
         if constexpr (W == 8) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint4 v = load_16(p);
 #pragma unroll
             for (int j = 0; j < 8; j++) f[j] = elem<BF16>(v, j);
         } else if constexpr (W == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+            const uint2 v = load_8(p);
             f[0] = __uint_as_float(v.x << 16), f[1] = __uint_as_float(v.x & 0xFFFF0000u);
             f[2] = __uint_as_float(v.y << 16), f[3] = __uint_as_float(v.y & 0xFFFF0000u);
         } else {
 #pragma unroll
-            for (int j = 0; j < W; j++) f[j] = __uint_as_float((uint32_t)__ldg(p + j) << 16);
+            for (int j = 0; j < W; j++) f[j] = load_bf16(p + j);
         }
     }
 }
@@ -146,19 +148,24 @@ QD float row_sum(float v, float *part, int gshift)
     return warp_sum(lane < n ? part[(warp & ~(n - 1)) + lane] : 0.0f);
 }
 
-// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.  The first: of lines
-// that L2 may drop first (the gradient's inputs: 8192 x 4096 BF16 46.5 us, 47.0 else; where a sum is cast it is 2 us slower).
-QD void bulk_load_once(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    uint64_t once;
-    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
-                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(once) : "memory");
-}
+// A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.
 QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+// The same with a policy of what L2 keeps: of lines that it may drop first, or as usual.
+QD uint64_t l2_policy(bool drop_first)
+{
+    uint64_t first, usual;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first));
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(usual));
+    return drop_first ? first : usual;
+}
+QD void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy) : "memory");
 }
 
 constexpr int kRingBytes = 200 * 1024;   // shared memory of an SM's CTAs for rows on their way

@@ -96,6 +96,28 @@ def test_norm_many_rows(M, K, dtype, residual):
     check_norm(M, K, dtype, F32, residual, eps=0.5)
 
 
+# rows of every layout the rings take, and one more row than their CTAs share evenly
+MANY = [(5000, 2048), (2500, 4104), (4870, 4096), (2440, 8192), (1220, 14336), (1300, 16384), (3050, 513), (2000, 8191), (700, 10001), (400, 16383)]
+
+
+@pytest.mark.parametrize("M,K", MANY)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_rings(M, K, dtype, residual):
+    check_norm(M, K, dtype, F32, residual, amax=residual)
+    check_norm(M, K, dtype, dtype, residual, amax=not residual)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("K", [2048, 2056, 1111])
+def test_norm_rings_in_place(residual, K):
+    x, w, r = make(5000, K, BF16, BF16, residual, 13)
+    y, h, rstd = Q.norm_add(x, w, residual=r)
+    a, b = x.clone(), None if r is None else r.clone()
+    got = Q.norm_add(a, w, residual=b, out=b if residual else a, h_out=a if residual else None)
+    assert torch.equal(got[0], y) and torch.equal(got[2], rstd) and (not residual or torch.equal(got[1], h))
+
+
 def test_norm_in_place():
     x, w, r = make(37, 512, BF16, BF16, True, 1)
     y, h, rstd = Q.norm_add(x, w, residual=r)
@@ -188,7 +210,14 @@ def test_norm_cast_rows(M, K, dtype, wt, residual):
     check_cast(M, K, dtype, wt, residual, True, False)
 
 
-@pytest.mark.parametrize("M,K", [(128, 128), (256, 640), (1152, 384), (384, 8064), (128, 16512), (2944, 1152), (128, 33024)])
+@pytest.mark.parametrize("M,K", [(5000, 2048), (2500, 4096), (1300, 14336), (2440, 8192)])
+@pytest.mark.parametrize("dtype,wt", [(BF16, BF16), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_cast_rings(M, K, dtype, wt, residual):
+    check_cast(M, K, dtype, wt, residual, True, False)
+
+
+@pytest.mark.parametrize("M,K", [(128, 128), (256, 640), (1152, 384), (384, 8064), (128, 16512), (2944, 1152), (128, 33024), (2560, 4096), (4992, 2048)])
 @pytest.mark.parametrize("dtype,wt", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
 @pytest.mark.parametrize("residual,rowwise", [(False, True), (True, True), (True, False)])
 def test_norm_cast_both(M, K, dtype, wt, residual, rowwise):
@@ -259,7 +288,8 @@ def test_grad_row_lengths(K, dtype, wt):
         check_grad(M, K, dtype, wt, dh)
 
 
-@pytest.mark.parametrize("M,K", [(8192, 64), (3001, 1111), (1000, 4096), (2500, 7168), (700, 33), (400, 16392), (5000, 4097)])
+@pytest.mark.parametrize("M,K", [(8192, 64), (3001, 1111), (1000, 4096), (2500, 7168), (700, 33), (400, 16392), (5000, 4097), (700, 14336), (305, 16384), (5000, 256),
+                                 (20000, 7), (3000, 300), (1500, 8200)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("dh", [False, True])
 def test_grad_many_rows(M, K, dtype, dh):
@@ -365,6 +395,15 @@ def test_offsets_past_32_bits():
     assert torch.equal(t.q_row[rows], small.q_row) and torch.equal(t.s_row[rows], small.s_row)
     last = Q.norm_q_blockwise(x[299776:299904], w, colwise=True)[0]
     assert torch.equal(t.q_colT[:, 299776:], last.q_colT) and torch.equal(t.s_colT[:, -1:], last.s_colT)
+
+
+def test_inference_mode():
+    x, w, r = make(9, 256, BF16, BF16, True, 14)
+    want = Q.norm_add(x, w, residual=r)
+    with torch.inference_mode():
+        y, h, top = torch.empty_like(x), torch.empty_like(x), torch.zeros(1, device="cuda")
+        got = Q.norm_add(x, w, residual=r, out=y, h_out=h, amax=top)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_first_call_of_a_host_thread():
