@@ -39,6 +39,15 @@ Operators on the blockwise copies:
 * :func:`drop_q_blockwise` -- the blockwise copies of a dropped gradient in
   one read.
 
+The product of the NVFP4 copies, and the norm ahead of a layer:
+
+* :func:`matmul_nvfp4` -- the block-scaled FP4 matrix product of the NVFP4
+  recipe's forward, input-gradient and weight-gradient passes;
+* :func:`norm_add` -- the RMS norm with the residual's addition, and the
+  largest magnitude of its result for a cast that follows;
+* :func:`norm_q_blockwise` -- the same with its result as blockwise copies;
+* :func:`norm_grad` -- the norm's gradient.
+
 ``linear.py`` puts them together as a linear layer.
 """
 from __future__ import annotations

@@ -14,6 +14,18 @@
 // the halves of Q's 256 (every CTA needs all of Q's), four blocks at a time (handed over two
 // at a time, which made room for one stage more, 8192 x 14336 x 4096 took 188 us for 154).
 // The eight warps 8-15 read 32 rows x 128 columns each when a tile is done.
+//
+// Measured on a GB300, in graphs of calls: 8192 x 14336 x 4096 to BF16 152 to 155 us
+// (6.2 to 6.3 PFLOP/s), 8192 x 4096 x 14336 141 to 143 (6.8), 16384 x 18432 x 7168
+// 618 to 660 (6.6 to 7.0), 14336 x 4096 x 8192 added to FP32 174 to 176 (5.5).  A tile
+// of 8192 x 14336 x 4096 takes the MMA warp 12346 cycles, of which it waits 3180 for
+// operands, 1070 for scales and 730 for the sums' place; at the nominal rate its MMAs
+// take 8192.  The tensor pipe is active 61 (FP32) to 67 % (BF16) of the time.
+// Called for seconds on end, 8192 x 14336 x 4096 takes 167 us: 1.35 kW, the power
+// cap active, 1.80 GHz.  The scales' way: loaded and handed over stage by stage 260
+// us, units of four blocks in slots of their own 212, without release at cluster
+// scope (which waited for the loads) 171; copies of four bytes straight to their
+// places 560.
 #pragma once
 
 #include "q_internal.h"

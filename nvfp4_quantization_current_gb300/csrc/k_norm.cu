@@ -9,9 +9,9 @@
 // is bound by memory, and a row is read once: it stays in registers between its sum
 // and what is made of it.  Measured on a GB300, in graphs of calls: 8192 x 4096 BF16
 // with a residual 42.4 us (268 MB at 6.3 TB/s, a copy's rate being 6.8), without one
-// 20.8, in FP32 79.6; its rowwise copy 38.9 with a residual, 26.0 without (301 warp
-// instructions for 512 elements: issue slots 70 % in use); 16 rows 2.0, of which the
-// launch is most.
+// 20.4 to 20.8, in FP32 79.9; its rowwise copy 39 with a residual, 25.9 without (with one,
+// 334 warp instructions for 512 elements: issue slots 54 % in use, DRAM 71 %, at 16384 x
+// 4096); 16 rows 2.0 to 2.1.
 #include "q_norm.cuh"
 
 namespace qk {

@@ -2,8 +2,9 @@
 // y = (h s) w in FP32 (k_norm.cu), y itself never stored.
 //
 // On the tile engine with two CTAs of 256 threads per SM, tiles of 128 rows x 256
-// bytes: while one waits at a barrier, the other works (one CTA with tiles of 512
-// bytes took 26 us of 8192 x 4096 BF16, its issue slots 40 % in use).  A thread (half
+// bytes: while one waits at a barrier, the other works (its issue slots are 49 % in use
+// at 16384 x 4096).  Both copies of 8192 x 4096 BF16 with a residual take 58.6 to 59.6
+// us, 39.3 of them for the rows alone; walked from the first tile on, 62.1.  A thread (half
 // a warp over a row's 16-byte chunks) holds 8 rows of a chunk of h and multiplies by
 // the rows' factors and the columns' weights as it goes.  The half warps' column
 // maxima meet in shared memory, and the codes are transposed in the consumed stage

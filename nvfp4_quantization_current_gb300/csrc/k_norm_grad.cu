@@ -4,8 +4,8 @@
 // The sums run in FP32 in an order fixed by the shape.  Bound by memory: dy, h and dh
 // are read and dx written once, and a CTA's part of dw is a row of scratch that a
 // second, small kernel adds up.  Measured on a GB300, in graphs of calls: 8192 x 4096
-// BF16 with dh 46.5 us (268 MB at 5.8 TB/s; 41.4 without dw, whose kernel waits for
-// the last CTA and then for its own loads), without dh 37.2, 3001 x 1111 FP32 11.4 (7.8
+// BF16 with dh 46.5 to 47.3 us (268 MB at 5.7 to 5.8 TB/s; 41.3 without dw, whose kernel
+// waits for the last CTA), without dh 37.2, 3001 x 1111 FP32 11.4 to 13.5 (8.0
 // without dw).  One row per CTA at a time, loaded where it is used, took 66.6 and 36.7.
 #include "q_norm.cuh"
 
