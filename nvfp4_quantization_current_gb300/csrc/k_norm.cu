@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 512, RES || WIDE ? 1 : 2) k_norm
         for (int s = 0; s < stages; s++) mbar_init(&full[s], 1);
         fence_mbar_init();
     }
-    if (threadIdx.x < 64) part[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;   // the CTA may have fewer warps
+    for (int i = threadIdx.x; i < 64; i += blockDim.x) part[i >> 5][i & 31] = 0.0f;   // the CTA may have fewer warps, one even
     __syncthreads();
     griddep_wait();   // nothing was read or written so far
     if (threadIdx.x == 0)

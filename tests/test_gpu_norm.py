@@ -108,6 +108,20 @@ def test_norm_rings(M, K, dtype, residual):
     check_norm(M, K, dtype, dtype, residual, amax=not residual)
 
 
+@pytest.mark.parametrize("K", [257, 301, 385, 509, 511])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_rings_of_one_warp(K, dtype, residual):
+    # behind rows of many warps, whose parts of large sums lie in shared memory
+    x, w, r = make(3000, 8191, dtype, dtype, residual, 3)
+    big = x * 1000
+    for M in (2432, 5001):
+        Q.norm_add(big, w, residual=r)
+        check_norm(M, K, dtype, dtype, residual, amax=False)
+        Q.norm_add(big, w, residual=r)
+        check_norm(M, K, dtype, F32, residual)
+
+
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("K", [2048, 2056, 1111])
 def test_norm_rings_in_place(residual, K):
