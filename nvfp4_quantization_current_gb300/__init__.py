@@ -865,7 +865,8 @@ def norm_add(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     ``amax`` (a one-element float32 tensor) receives max|y|, for
     :func:`q_nvfp4` or :func:`q_current_scaling` to be given; ``status`` then
     reports a maximum that is not finite.  ``out`` (for y) and ``h_out`` may be
-    x and the residual themselves.  Autograd takes :func:`norm_grad` as the
+    x and the residual themselves (without a residual ``out=x`` leaves y in what is
+    returned as h, which :func:`norm_grad` then has no use for).  Autograd takes :func:`norm_grad` as the
     backward pass; with ``out`` or ``h_out`` no gradient is recorded."""
     dev = x.device
     dt, M, K = _norm_in("x", x, dev, weight, residual)

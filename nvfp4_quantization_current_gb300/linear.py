@@ -25,6 +25,9 @@ FP8/FP4: low-precision and mixed-precision LLM pretraining", 2.4, has it: 1x16
 blocks for activations and gradients, 16x16 blocks for weights, stochastic
 rounding on gradients, the random Hadamard transform on both inputs of the
 weight gradient, and :func:`matmul_nvfp4` for the three products.
+
+A backward pass may be captured into a CUDA graph if no eager graph of the same
+parameters or inputs is alive then: let go of earlier results and losses first.
 """
 from __future__ import annotations
 
