@@ -1,6 +1,7 @@
 // The NVFP4 product for results of many tiles.
 //
-// A pair of CTAs (a cluster of two) owns a 256 x 256 tile of C and walks the
+// A pair of CTAs (a cluster of two) owns a 256 x BN tile of C, BN 256 or, where such tiles would be too few for
+// the machine, 128 (the rest here is about 256; two buffers of 128 columns do not overlap), and walks the
 // tiles persistently; one MMA spans both, each CTA holding its own 128 rows of P
 // and half of Q's 256 (as in k_mm_pair.cuh).  The tensor core applies the block
 // scales, so a tile's whole sum is formed in tensor memory: 256 columns, and the
@@ -35,10 +36,7 @@ namespace qk {
 
 constexpr int kPair4EpiWarps = 8, kPair4ScaleWarps = 6;
 constexpr int kPair4Threads = 32 * (2 + kPair4ScaleWarps + kPair4EpiWarps);
-constexpr int kPair4OperandBytes = 2 * 128 * 128;
 constexpr int kPair4Unit = 4, kPair4Slots = 2;   // blocks whose scales are handed over together (ScaleUnit), and places for them
-constexpr int kPair4Second = 208;           // first column of the second buffer; the scales' columns begin at 464
-constexpr int kPair4Scales = kPair4Second + 256;
 // Registers per thread of the epilogue's and the other warps; their sum is what
 // the kernel is launched with.
 constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
@@ -47,18 +45,22 @@ constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
 // its MMAs 512 (8192 x 4096 x 14336 179 us at three stages, 146 at four, 142 at five).  A BF16 C is stored from registers
 // and needs no staging to speak of; an FP32 C goes through staging as bulk stores and adds (adds from registers took 224
 // us of 14336 x 4096 x 8192, bulk ones 174).
-template <int OUT> struct Pair4Smem {
-    static constexpr int kStages = OUT == F32 ? 4 : 5, kStaging = OUT == F32 ? 4096 : 1024;
-    uint8_t stage[kStages][kPair4OperandBytes];
+template <int OUT, int BN> struct Pair4Smem {
+    static constexpr int kStages = BN == 128 ? (OUT == F32 ? 6 : 7) : OUT == F32 ? 4 : 5, kStaging = OUT == F32 ? 4096 : 1024;
+    static constexpr int kAtomsQ = BN / 128, kOperandBytes = (128 + BN / 2) * 128, kScaleBytes = (1 + kAtomsQ) * kScaleAtom;
+    static constexpr int kSecond = BN == 128 ? 128 : 208, kScales = kSecond + BN;   // first tensor memory columns of the second buffer, and of the scales
+    static_assert(kScales + 16 * (1 + kAtomsQ) <= 512, "tensor memory");
+    uint8_t stage[kStages][kOperandBytes];
     uint8_t staging[kPair4EpiWarps][kStaging];
-    uint8_t scales[kPair4Slots][kPair4Unit][3 * kScaleAtom];   // P's rows, and Q's in halves
+    uint8_t scales[kPair4Slots][kPair4Unit][kScaleBytes];   // P's rows, and Q's in 128s
     uint64_t full[kStages], empty[kStages], sc_full[kPair4Slots], sc_empty[kPair4Slots], acc_full[2], acc_free, drained;
     uint32_t tmem_base;
     int abort_flag;
 };
-static_assert(sizeof(Pair4Smem<F32>) <= 232448 && sizeof(Pair4Smem<BF16>) <= 232448, "shared memory of a CTA");
+static_assert(sizeof(Pair4Smem<F32, 256>) <= 232448 && sizeof(Pair4Smem<BF16, 256>) <= 232448 && sizeof(Pair4Smem<F32, 128>) <= 232448 &&
+              sizeof(Pair4Smem<BF16, 128>) <= 232448, "shared memory of a CTA");
 
-// Tile t of the walk, in units of 256 x 256: groups of `group` tile rows, each
+// Tile t of the walk, in units of 256 x BN: groups of `group` tile rows, each
 // walked column by column, so that the tiles in flight share their operands in
 // L2.  The launcher says how many: where there are few tile rows, all of them, up
 // to 32, where there are few columns, two (power is what these calls run into, and
@@ -77,7 +79,7 @@ QD void pair4_tile(int t, int tiles_p, int tiles_q, int group, int &p, int &q)
 // The scales of 64 rows (half `part` of an atom) for all tiles of a CTA's walk, one warp.  Loads are issued
 // behind the fence of the hand-over ahead, which would wait for them: among the operands'
 // copies, which keep memory's queues full, a load takes some 4000 cycles.
-template <bool WHOLE, class Smem>
+template <bool WHOLE, int BN, class Smem>
 QD void put_scales4(Smem &sm, const Mm4Args &a, int atom, int part, int first, int pairs, int tiles_p, int tiles_q, int rank,
                     int lane, volatile int *stop)
 {
@@ -92,7 +94,7 @@ QD void put_scales4(Smem &sm, const Mm4Args &a, int atom, int part, int first, i
     auto settle = [&](Place &at) {
         int tp, tq;
         pair4_tile(at.t, tiles_p, tiles_q, a.group, tp, tq);
-        at.row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * 256 + 128 * (atom - 1)) + 16 * part;
+        at.row0 = (atom == 0 ? (int64_t)tp * 256 + 128 * rank : (int64_t)tq * BN + 128 * (atom - 1)) + 16 * part;
     };
     auto advance = [&](Place &at) {
         at.kb += kPair4Unit;
@@ -183,23 +185,23 @@ QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], 
     }
 }
 
-// ANY: C's rows are no multiple of 16 bytes, or a BF16 C is added to.  (A kernel of its own: the code for it, though not
+// ANY (at BN 256): C's rows are no multiple of 16 bytes, or a BF16 C is added to.  (A kernel of its own: the code for it, though not
 // reached, took 161 us of 8192 x 14336 x 4096 where the kernel without it takes 154.)
-template <int OUT, bool WHOLE, bool ANY>
+template <int OUT, int BN, bool WHOLE, bool ANY>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair4Threads, 1)
 k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
            const __grid_constant__ CUtensorMap map_c, const Mm4Args a)
 {
     const MmArgs &g = a.store;
-    using Smem = Pair4Smem<OUT>;
-    constexpr int kStages = Smem::kStages;
+    using Smem = Pair4Smem<OUT, BN>;
+    constexpr int kStages = Smem::kStages, kAtomsQ = Smem::kAtomsQ;
     extern __shared__ __align__(1024) uint8_t dsm[];
     Smem &sm = *reinterpret_cast<Smem *>(dsm);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int kb_n = (int)g.kblocks;
-    const int tiles_p = (int)((g.rows_p + 255) / 256), tiles_q = (int)((g.rows_q + 255) / 256);
+    const int tiles_p = (int)((g.rows_p + 255) / 256), tiles_q = (int)((g.rows_q + BN - 1) / BN);
     const int tiles = tiles_p * tiles_q, pairs = gridDim.x / 2, first = blockIdx.x / 2;
     volatile int *const stop = &sm.abort_flag;
 
@@ -209,7 +211,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             mbar_init(&sm.empty[s], 1);
         }
         for (int s = 0; s < kPair4Slots; s++) {
-            mbar_init(&sm.sc_full[s], 2 * kPair4ScaleWarps);
+            mbar_init(&sm.sc_full[s], 2 * 2 * (1 + kAtomsQ));
             mbar_init(&sm.sc_empty[s], 1);
         }
         for (int b = 0; b < 2; b++) mbar_init(&sm.acc_full[b], 1);
@@ -238,14 +240,14 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             for (int t = first; t < tiles && ok; t += pairs) {
                 int tp, tq;
                 pair4_tile(t, tiles_p, tiles_q, a.group, tp, tq);
-                const int p0 = tp * 256 + 128 * rank, q0 = tq * 256 + 128 * rank;
+                const int p0 = tp * 256 + 128 * rank, q0 = tq * BN + BN / 2 * rank;
                 for (int kb = 0; kb < kb_n; kb++) {
                     if (issued >= kStages && !mm_wait(&sm.empty[s], use, stop, g.status)) {
                         ok = false;
                         break;
                     }
                     uint8_t *st = sm.stage[s];
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kPair4OperandBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * Smem::kOperandBytes);
                     const uint32_t bar = cluster_addr(smem_u32(&sm.full[s]), 0);
                     tma_load_tile_pair(st, &map_p, kb * 128, p0, bar);
                     tma_load_tile_pair(st + 128 * 128, &map_q, kb * 128, q0, bar);
@@ -273,12 +275,12 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             if (rank == 0) {
                 const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * 128);
                 const uint64_t src0 = smem_desc_scales(sm.scales[0][0]);
-                const uint32_t sp = tmem + kPair4Scales, sq = sp + 16;
+                const uint32_t sp = tmem + Smem::kScales, sq = sp + 16;
                 bool ok = true;
                 int s = 0;
                 uint32_t par = 0, tile = 0, unit = 0;
                 for (int t = first; t < tiles && ok; t += pairs, tile++) {
-                    const uint32_t d = tmem + (tile & 1) * kPair4Second;
+                    const uint32_t d = tmem + (tile & 1) * Smem::kSecond;
                     // the columns that this tile shares with the one before have been read
                     if (tile > 0) ok = mm_wait(&sm.acc_free, (tile - 1) & 1, stop, g.status);
                     for (int kb = 0; kb < kb_n; kb++) {
@@ -289,17 +291,17 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                         if (!ok) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t at = (uint64_t)(s * (kPair4OperandBytes >> 4));
-                            const uint64_t src = src0 + (uint64_t)((slot * kPair4Unit + kb % kPair4Unit) * (3 * kScaleAtom >> 4));
+                            const uint64_t at = (uint64_t)(s * (Smem::kOperandBytes >> 4));
+                            const uint64_t src = src0 + (uint64_t)((slot * kPair4Unit + kb % kPair4Unit) * (Smem::kScaleBytes >> 4));
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 scales_to_tmem_pair(sp + 4 * k, src + 32 * k);
 #pragma unroll
-                                for (int j = 0; j < 2; j++) scales_to_tmem_pair(sq + 8 * k + 4 * j, src + 128 * (1 + j) + 32 * k);
+                                for (int j = 0; j < kAtomsQ; j++) scales_to_tmem_pair(sq + 4 * (k * kAtomsQ + j), src + 128 * (1 + j) + 32 * k);
                             }
 #pragma unroll
                             for (int k = 0; k < 4; k++)
-                                mma_f4_pair(d, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e2m1(256, 256), sp + 4 * k, sq + 8 * k, kb > 0 || k > 0);
+                                mma_f4_pair(d, a0 + at + 2 * k, b0 + at + 2 * k, idesc_e2m1(256, BN), sp + 4 * k, sq + 4 * kAtomsQ * k, kb > 0 || k > 0);
                             mma_commit_pair(&sm.empty[s]);
                             if (kb % kPair4Unit == kPair4Unit - 1 || kb + 1 == kb_n) mma_commit_pair(&sm.sc_empty[slot]);
                             if (kb + 1 == kb_n) mma_commit_pair(&sm.acc_full[tile & 1]);
@@ -319,11 +321,11 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             }
         } else if (warp >= 2) {
             const int w = warp - 2, atom = w >> 1;
-            put_scales4<WHOLE>(sm, a, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
+            if (atom <= kAtomsQ) put_scales4<WHOLE, BN>(sm, a, atom, w & 1, first, pairs, tiles_p, tiles_q, (int)rank, lane, stop);
         }
     } else {
         regs_more<kPair4EpiRegs>();
-        const int quad = warp & 3, half = (warp - 2 - kPair4ScaleWarps) >> 2;   // 32 tensor memory lanes, 128 columns
+        const int quad = warp & 3, half = (warp - 2 - kPair4ScaleWarps) >> 2;   // 32 tensor memory lanes, half the columns
         const uint32_t to_leader = cluster_addr(smem_u32(&sm.acc_free), 0);
         const float fp = load_float(a.s_p), fq = load_float(a.s_q);
         const uint64_t sp = pack2(__float_as_uint(fp), __float_as_uint(fp)), sq = pack2(__float_as_uint(fq), __float_as_uint(fq));
@@ -335,8 +337,8 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             mm_wait(&sm.acc_full[tile & 1], (tile >> 1) & 1, stop, g.status);
             __syncwarp();
             tc_fence_after();
-            const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + (tile & 1) * kPair4Second + half * 128;
-            // The columns shared with the next tile are the last 48 of the second half, then
+            const uint32_t addr = tmem + ((uint32_t)(quad * 32) << 16) + (tile & 1) * Smem::kSecond + half * (BN / 2);
+            // (BN 256) The columns shared with the next tile are the last 48 of the second half, then
             // the first 48 of the first: each half begins at its end of the tile.
             auto part = [&](int h, bool shared) {
                 uint32_t r[64];
@@ -349,14 +351,18 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
 #pragma unroll
                 for (int j = 0; j < 32; j++) acc[j] = fmul2(fmul2(pack2(r[2 * j], r[2 * j + 1]), sp), sq);
                 if (__any_sync(0xFFFFFFFFu, *stop)) return;
-                const int64_t row = (int64_t)tp * 256 + 128 * (int)rank + quad * 32, col = (int64_t)tq * 256 + half * 128 + h * 64;
+                const int64_t row = (int64_t)tp * 256 + 128 * (int)rank + quad * 32, col = (int64_t)tq * BN + half * (BN / 2) + h * 64;
                 uint8_t *const staging = sm.staging[warp - 2 - kPair4ScaleWarps];
                 if constexpr (OUT == BF16 && ANY) store_any64(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
                 else if constexpr (OUT == BF16) store_row64(g, acc, row + lane, col, wide);
                 else mm_store_tile<OUT, true, 1, 64>(g, &map_c, staging, acc, row, col, lane);
             };
-            part(half, true);
-            part(1 - half, false);
+            if constexpr (BN == 256) {
+                part(half, true);
+                part(1 - half, false);
+            } else {
+                part(0, true);
+            }
         }
         if (lane == 0) bulk_wait_all();
     }

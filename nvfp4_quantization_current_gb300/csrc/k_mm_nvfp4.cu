@@ -48,35 +48,35 @@ cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int6
 
 // The registers that the pair kernel's epilogue takes over have to be there at
 // its launch: it would wait for them forever.
-template <int OUT, bool WHOLE, bool ANY> cudaError_t pair4_registers_ready()
+template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t pair4_registers_ready()
 {
     static std::atomic<bool> ready{false};
     if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, WHOLE, ANY>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, BN, WHOLE, ANY>);
     if (e != cudaSuccess) return e;
     if (a.numRegs * kPair4Threads < 32 * (kPair4EpiWarps * kPair4EpiRegs + (2 + kPair4ScaleWarps) * kPair4Regs)) return cudaErrorInvalidConfiguration;
     ready.store(true, std::memory_order_relaxed);
     return cudaSuccess;
 }
 
-// Tiles of 256 x 256 on CTA pairs.
-template <int OUT, bool WHOLE, bool ANY> cudaError_t mm4_pair_t(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
+// Tiles of 256 x BN on CTA pairs.
+template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t mm4_pair_t(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q, map_c = {};
     MmArgs &g = a.store;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K / 2, 128);
-    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, 128);
+    if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, BN / 2);
     g.store = ANY || OUT == BF16 ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
     if (e == cudaSuccess && !ANY && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, WHOLE, ANY>>(sizeof(Pair4Smem<OUT>));
-    if (e == cudaSuccess) e = pair4_registers_ready<OUT, WHOLE, ANY>();
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, BN, WHOLE, ANY>>(sizeof(Pair4Smem<OUT, BN>));
+    if (e == cudaSuccess) e = pair4_registers_ready<OUT, BN, WHOLE, ANY>();
     if (e != cudaSuccess) return e;
-    const int64_t tiles_p = (g.rows_p + 255) / 256, tiles_q = (g.rows_q + 255) / 256, tiles = tiles_p * tiles_q, pairs = sm_count() / 2;
+    const int64_t tiles_p = (g.rows_p + 255) / 256, tiles_q = (g.rows_q + BN - 1) / BN, tiles = tiles_p * tiles_q, pairs = sm_count() / 2;
     a.group = tiles_q < tiles_p && tiles_q <= 32 ? 2 : tiles_p < 32 ? (int)tiles_p : 32;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_k(true, k_mm4_pair<OUT, WHOLE, ANY>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
-                    sizeof(Pair4Smem<OUT>), st, map_p, map_q, map_c, a);
+    return launch_k(true, k_mm4_pair<OUT, BN, WHOLE, ANY>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
+                    sizeof(Pair4Smem<OUT, BN>), st, map_p, map_q, map_c, a);
 }
 
 Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K) { return {at, K / 16, (int)rows, blk ? 4 : 0}; }
@@ -84,10 +84,10 @@ Mm4Scales scales_of(const uint8_t *at, int blk, int64_t rows, int64_t K) { retur
 // Every row of scales begins on a 16-byte boundary.
 bool whole_rows(const Mm4Scales &s) { return ((reinterpret_cast<uintptr_t>(s.at) | (uintptr_t)s.pitch) & 15) == 0; }
 
-template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, cudaStream_t st)
+template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, int bn, bool any, cudaStream_t st)
 {
-    const bool any = a.store.ldc % (OUT == F32 ? 4 : 8) != 0 || (OUT == BF16 && a.store.accumulate);
-    return any ? mm4_pair_t<OUT, WHOLE, true>(p, q, a, K, st) : mm4_pair_t<OUT, WHOLE, false>(p, q, a, K, st);
+    if (any) return mm4_pair_t<OUT, 256, WHOLE, true>(p, q, a, K, st);
+    return bn == 128 ? mm4_pair_t<OUT, 128, WHOLE, false>(p, q, a, K, st) : mm4_pair_t<OUT, 256, WHOLE, false>(p, q, a, K, st);
 }
 
 // CTAs that clusters of `split` keep resident, one per SM (see the blockwise product's).
@@ -119,20 +119,22 @@ int cluster_ctas4(int split)
 }
 
 // Which kernel, and how wide and how deep a split: the least estimated time.
-// The estimate's terms (us) are a fit to 1160 calls of every plan that 170 shapes
-// allow (1 to 4096 tokens, weights from 512 x 256 to 18432 x 18432, K of every
-// multiple of 32, weights in either blocks; GB300, graphs of calls); its choices take
-// 0.5% more time than the best plan on the average and 11% at most.  A call has a
-// fixed part, a cluster adds its sum, a CTA takes `block` for each 256 elements of K
+// The estimate's terms (us) are fits to calls of every plan that a shape
+// allows, those of the split kernel to 170 shapes (1 to 4096 tokens, weights from 512 x
+// 256 to 18432 x 18432, K of every multiple of 32, weights in either blocks), those of the pair kernel to
+// 240 (GB300, graphs of calls, 1919 of them); its choices take 0.8% more time than the best plan of these on
+// the average and 14% at most.  A call has a fixed part, a cluster adds its sum, a CTA takes `block` for each 256 elements of K
 // (`odd` times as long where scale rows begin anywhere), two CTAs of an SM `share`
-// times one's time, and a CTA that comes after another a start of its own.  Some of
+// times one's time, and a CTA that comes after another a start of its own; a pair takes `tile` for a tile's end.  Some of
 // what it is drawn from: one token with 4096 x 4096 weights 4.9 us at a split of four,
-// 7.8 without, 9.7 on the pair kernel; 333 tokens 10.8 there, 11.3 at 192 wide and two
-// deep, 12.4 at 128; 64 tokens with 4096 x 14336 10.6 at 64 and four, 25.5 on the pair.
+// 7.8 without, 9.7 on the pair kernel; 64 tokens with 4096 x 14336 10.6 at 64 and four, 25.5 on the
+// pair.  Tiles of 256 x 128 are for results that tiles of 256 x 256 are too few for, the best plan of 36 shapes, by 9% on
+// the average: 333 tokens with 4096 x 4096 10.0 us, 10.9 in 256s, 11.1 at 192 wide and
+// two deep; 380 with 2304 x 1280 5.8, 6.8 and 6.9; but 768 with 4096 x 4096, two rounds of them, 15.1 and 11.4.
 struct Mm4Plan {
-    int bn, split;   // bn 0: the pair kernel
+    int bn, split;   // split 0: the pair kernel
 };
-Mm4Plan mm4_plan(int64_t M, int64_t N, int64_t kblocks, bool whole, int sms)
+Mm4Plan mm4_plan(int64_t M, int64_t N, int64_t kblocks, bool whole, bool any, int sms)
 {
     struct Width {
         int bn;
@@ -144,10 +146,23 @@ Mm4Plan mm4_plan(int64_t M, int64_t N, int64_t kblocks, bool whole, int sms)
                                         {64, 6.22, 0.316, 1.589, 1.152, {0.0, 0.0, 0.04}, 5.77, 2},
                                         {128, 6.97, 0.323, 1.0, 1.192, {0.0, 0.0, 0.0}, 6.87, 1},
                                         {192, 8.73, 0.358, 1.0, 1.272, {0.0, 0.0, 0.0}, 9.31, 1}};
+    struct Pair {
+        int bn;
+        double fixed, block, tile, odd, odd_tile;
+    };
+    static constexpr Pair kPairs[] = {{256, 2.856, 0.361, 1.663, 1.352, 1.438}, {128, 2.843, 0.323, 0.995, 1.383, 1.986}};
     const int64_t ty = (N + 127) / 128, pairs = sms / 2;
-    const int64_t pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
-    Mm4Plan best = {0, 1};
-    double cost = 1.99 + (double)((pair_tiles + pairs - 1) / pairs) * ((double)kblocks * 0.339 * (whole ? 1.0 : 1.393) + 2.43 * (whole ? 1.0 : 1.438));
+    Mm4Plan best = {256, 0};
+    double cost = 0.0;
+    for (const Pair &p : kPairs) {
+        if (p.bn == 128 && any) continue;   // that kernel has no such form
+        const int64_t tiles = ((M + 255) / 256) * ((N + p.bn - 1) / p.bn);
+        const double c = p.fixed + (double)((tiles + pairs - 1) / pairs) * ((double)kblocks * p.block * (whole ? 1.0 : p.odd) + p.tile * (whole ? 1.0 : p.odd_tile));
+        if (p.bn == 256 || c < cost) {
+            cost = c;
+            best.bn = p.bn;
+        }
+    }
     for (const Width &w : kWidths) {
         const int64_t tz = (M + w.bn - 1) / w.bn;
         if ((w.bn > 16 && M <= w.bn / 2) || ty > 65535 || tz > 65535) continue;
@@ -172,9 +187,10 @@ cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t 
 {
     const int64_t M = g.store.rows_p, N = g.store.rows_q;
     const bool whole = whole_rows(g.p) && whole_rows(g.q);
-    const Mm4Plan plan = mm4_plan(M, N, g.store.kblocks, whole, sm_count());
+    const bool any = g.store.ldc % (OUT == F32 ? 4 : 8) != 0 || (OUT == BF16 && g.store.accumulate);
+    const Mm4Plan plan = mm4_plan(M, N, g.store.kblocks, whole, any, sm_count());
     const int split = plan.split;
-    if (plan.bn == 0) return whole ? mm4_pair<OUT, true>(a, b, g, K, st) : mm4_pair<OUT, false>(a, b, g, K, st);
+    if (split == 0) return whole ? mm4_pair<OUT, true>(a, b, g, K, plan.bn, any, st) : mm4_pair<OUT, false>(a, b, g, K, plan.bn, any, st);
     Mm4Args w = g;   // the weights on the lanes
     w.p = g.q;
     w.q = g.p;

@@ -131,6 +131,19 @@ def test_plans(M, N, K, bb, dtype, accumulate):
     check(M, N, K, "1x16", bb, dtype, accumulate, seed=M, lossless=True)
 
 
+# results whose tiles of 256 x 256 are too few for the machine, and take tiles of 256 x 128: ends inside them, one and two
+# rounds, broken blocks of K, block scales at any address, columns of either CTA missing
+NARROW = [(333, 4096, 2048, "16x16"), (257, 2816, 1280, "1x16"), (300, 2784, 768, "16x16"), (1769, 640, 512, "16x16"), (161, 2224, 1024, "16x16"),
+          (380, 2312, 1280, "1x16"), (242, 4520, 256, "1x16"), (500, 4040, 1184, "1x16"), (2000, 600, 3584, "1x16"), (1790, 840, 288, "1x16")]
+
+
+@pytest.mark.parametrize("M,N,K,bb", NARROW)
+@pytest.mark.parametrize("dtype,accumulate", [(BF16, False), (F32, False), (F32, True), (BF16, True)])
+def test_narrow_tiles(M, N, K, bb, dtype, accumulate):
+    check(M, N, K, "1x16", bb, dtype, accumulate, seed=M + K, lossless=True)
+    check(M, N, K, "1x16", bb, dtype, accumulate, seed=M)
+
+
 def test_random_shapes():
     rng = np.random.default_rng(5)
     for i in range(60):
