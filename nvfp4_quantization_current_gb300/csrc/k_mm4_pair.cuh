@@ -46,7 +46,7 @@ constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
 // and needs no staging to speak of; an FP32 C goes through staging as bulk stores and adds (adds from registers took 224
 // us of 14336 x 4096 x 8192, bulk ones 174).
 template <int OUT, int BN> struct Pair4Smem {
-    static constexpr int kStages = BN == 128 ? (OUT == F32 ? 6 : 7) : OUT == F32 ? 4 : 5, kStaging = OUT == F32 ? 4096 : 1024;
+    static constexpr int kBufs = BN == 128 ? 2 : 1, kStages = BN == 256 ? 5 : OUT == F32 ? 6 : 7, kStaging = OUT == F32 ? 2048 * kBufs : 1024;
     static constexpr int kAtomsQ = BN / 128, kOperandBytes = (128 + BN / 2) * 128, kScaleBytes = (1 + kAtomsQ) * kScaleAtom;
     static constexpr int kSecond = BN == 128 ? 128 : 208, kScales = kSecond + BN;   // first tensor memory columns of the second buffer, and of the scales
     static_assert(kScales + 16 * (1 + kAtomsQ) <= 512, "tensor memory");
@@ -182,6 +182,46 @@ QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], 
                 put_one<BF16>(static_cast<uint16_t *>(g.c) + (row0 + r) * g.ldc + col, staging[8 * r + 4 * chunk + (lane & 3)], g.accumulate);
         }
         __syncwarp();
+    }
+}
+
+// A warp's 32 rows x 64 sums to an FP32 C, in pieces of 16 rows x 128 bytes through BUFS (one or two) times 2 KiB of staging, where 16-byte chunk i of
+// row r is at place i ^ (r % 8), the 128-byte swizzle of the bulk stores.  (Direct: by the warp's lanes, a C of any pitch.)
+template <int BUFS> QD void store_f32_64(const MmArgs &g, const CUtensorMap *map_c, uint8_t *const staging0, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
+{
+    const bool bulk = g.store != kStoreDirect;
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+        const int64_t row = row0 + 16 * (p & 1), col = col0 + 32 * (p >> 1);
+        uint8_t *const staging = staging0 + (p & (BUFS - 1)) * 2048;
+        if (bulk && lane == 0) {   // the last piece that was here has left it
+            if constexpr (BUFS == 2) bulk_wait_read_but1();
+            else bulk_wait_read_all();
+        }
+        __syncwarp();
+        if ((lane >> 4) == (p & 1)) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                *reinterpret_cast<ulonglong2 *>(staging + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                    make_ulonglong2(acc[(p >> 1) * 16 + 2 * i], acc[(p >> 1) * 16 + 2 * i + 1]);
+        }
+        if (bulk) {
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (row < g.rows_p && col < g.rows_q) {
+                    if (g.store == kStoreBulkAdd) bulk_add_tile(map_c, staging, (int)col, (int)row);
+                    else tma_store_tile(map_c, staging, (int)col, (int)row);
+                }
+                bulk_commit();   // an empty group too: the waits count them
+            }
+        } else {
+            __syncwarp();
+            for (int r = 0; r < 16 && row + r < g.rows_p; r++)
+                if (col + lane < g.rows_q)
+                    put_one<F32>(static_cast<float *>(g.c) + (row + r) * g.ldc + col + lane,
+                                 *reinterpret_cast<const float *>(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4), g.accumulate);
+        }
     }
 }
 
@@ -355,7 +395,7 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                 uint8_t *const staging = sm.staging[warp - 2 - kPair4ScaleWarps];
                 if constexpr (OUT == BF16 && ANY) store_any64(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
                 else if constexpr (OUT == BF16) store_row64(g, acc, row + lane, col, wide);
-                else mm_store_tile<OUT, true, 1, 64>(g, &map_c, staging, acc, row, col, lane);
+                else store_f32_64<Smem::kBufs>(g, &map_c, staging, acc, row, col, lane);
             };
             if constexpr (BN == 256) {
                 part(half, true);

@@ -68,7 +68,7 @@ template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t mm4_pair_t(const ui
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K / 2, 128);
     if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, BN / 2);
     g.store = ANY || OUT == BF16 ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
-    if (e == cudaSuccess && !ANY && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q);
+    if (e == cudaSuccess && !ANY && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q, 16);
     if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, BN, WHOLE, ANY>>(sizeof(Pair4Smem<OUT, BN>));
     if (e == cudaSuccess) e = pair4_registers_ready<OUT, BN, WHOLE, ANY>();
     if (e != cudaSuccess) return e;

@@ -50,9 +50,9 @@ cudaError_t make_operand_map(void *map /* CUtensorMap, 64-byte aligned */, const
                              int box_rows);
 
 // A 2-D TMA tensor map for stores into a row-major BF16 / F32 matrix
-// [rows, cols] (row bytes a multiple of 16, base 16-byte aligned), box 32 rows
+// [rows, cols] (row bytes a multiple of 16, base 16-byte aligned), box box_rows
 // x 128 bytes read from shared memory in the 128-byte swizzle.
-cudaError_t make_result_map(void *map /* CUtensorMap, 64-byte aligned */, void *c, int dt, int64_t rows, int64_t cols);
+cudaError_t make_result_map(void *map /* CUtensorMap, 64-byte aligned */, void *c, int dt, int64_t rows, int64_t cols, int box_rows = 32);
 
 // current scaling
 cudaError_t launch_amax(const void *x, int dt, int64_t n, float *amax, int32_t *status, cudaStream_t st);

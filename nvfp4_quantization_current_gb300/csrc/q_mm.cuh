@@ -80,8 +80,8 @@ QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)
                  ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
-// One warp's sums, 32 rows (from row0) x COLS columns (from col0), to C in
-// pieces of 32 rows x 128 bytes through its BUFS (one or two) 4 KiB staging buffers: the
+// One warp's sums, 32 rows (from row0) x 128 columns (from col0), to C in
+// pieces of 32 rows x 128 bytes through its two 4 KiB staging buffers: the
 // 16-byte chunk i of row r at place i ^ (r % 8), which is the 128-byte swizzle
 // of the bulk store and keeps the lanes' accesses off each other's banks.
 // Rows and columns outside C are cut off by the store.  C's whose rows are no
@@ -92,20 +92,17 @@ QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)
 // ROWS: thread t holds row t, acc[j] columns 2j and 2j + 1.  Otherwise
 // acc[16c + 8h + 2i + k] is row 16h + 8k + t / 4, columns 32c + 8i + 2 (t % 4)
 // and the next (tmem_ld_rows16).
-template <int OUT, bool ROWS, int BUFS = 2, int COLS = 128>
-QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *staging, const uint64_t (&acc)[COLS / 2], int64_t row0,
+template <int OUT, bool ROWS>
+QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *staging, const uint64_t (&acc)[64], int64_t row0,
                       int64_t col0, int lane)
 {
     using T = typename OutT<OUT>::T;
     const bool bulk = g.store != kStoreDirect;
     auto place = [&](uint8_t *buf, int r, int i) { return buf + r * 128 + ((i ^ (r & 7)) << 4); };
-    auto claim = [&](int piece) {   // the piece before the last one (with one buffer: the last) has left this buffer
-        if (bulk && lane == 0) {
-            if constexpr (BUFS == 2) bulk_wait_read_but1();
-            else bulk_wait_read_all();
-        }
+    auto claim = [&](int piece) {   // the piece before the last one has left this buffer
+        if (bulk && lane == 0) bulk_wait_read_but1();
         __syncwarp();
-        return staging + (piece & (BUFS - 1)) * 4096;
+        return staging + (piece & 1) * 4096;
     };
     auto send = [&](const uint8_t *buf, int64_t col) {
         fence_proxy_async();
@@ -120,7 +117,7 @@ QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *stagin
     };
     if (OUT == BF16 && bulk) {
 #pragma unroll
-        for (int p = 0; p < COLS / 64; p++) {
+        for (int p = 0; p < 2; p++) {
             uint8_t *buf = claim(p);
             if constexpr (ROWS) {
 #pragma unroll
@@ -148,7 +145,7 @@ QD void mm_store_tile(const MmArgs &g, const CUtensorMap *map_c, uint8_t *stagin
         return;
     }
 #pragma unroll
-    for (int p = 0; p < COLS / 32; p++) {
+    for (int p = 0; p < 4; p++) {
         uint8_t *buf = claim(p);
         if constexpr (ROWS) {
 #pragma unroll

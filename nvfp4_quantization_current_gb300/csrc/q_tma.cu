@@ -76,12 +76,12 @@ cudaError_t make_operand_map(void *map, const void *codes, int64_t rows, int64_t
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-cudaError_t make_result_map(void *map, void *c, int dt, int64_t rows, int64_t cols)
+cudaError_t make_result_map(void *map, void *c, int dt, int64_t rows, int64_t cols, int box_rows)
 {
     const int es = dt == F32 ? 4 : 2;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)(cols * es)};
-    cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32u};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1u, 1u};
     return encode(static_cast<CUtensorMap *>(map), dt == F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   2, c, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
