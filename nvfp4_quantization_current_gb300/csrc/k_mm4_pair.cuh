@@ -18,10 +18,10 @@
 //
 // Measured on a GB300, in graphs of calls: 8192 x 14336 x 4096 to BF16 152 to 155 us
 // (6.2 to 6.3 PFLOP/s), 8192 x 4096 x 14336 141 to 143 (6.8), 16384 x 18432 x 7168
-// 618 to 660 (6.6 to 7.0), 14336 x 4096 x 8192 added to FP32 174 to 176 (5.5).  A tile
+// 618 to 660 (6.6 to 7.0), 14336 x 4096 x 8192 added to FP32 161 to 166 (5.8 to 6.0).  A tile
 // of 8192 x 14336 x 4096 takes the MMA warp 12346 cycles, of which it waits 3180 for
 // operands, 1070 for scales and 730 for the sums' place; at the nominal rate its MMAs
-// take 8192.  The tensor pipe is active 61 (FP32) to 67 % (BF16) of the time.
+// take 8192.  The tensor pipe is active 67 % of the time (BF16, 4864 x 4096 x 8192).
 // Called for seconds on end, 8192 x 14336 x 4096 takes 167 us: 1.35 kW, the power
 // cap active, 1.80 GHz.  The scales' way: loaded and handed over stage by stage 260
 // us, units of four blocks in slots of their own 212, without release at cluster
@@ -44,7 +44,8 @@ constexpr int kPair4EpiRegs = 152, kPair4Regs = 104;
 // Operand stages are what shared memory goes to first: memory's queues are full, a stage's copies take some 2000 cycles and
 // its MMAs 512 (8192 x 4096 x 14336 179 us at three stages, 146 at four, 142 at five).  A BF16 C is stored from registers
 // and needs no staging to speak of; an FP32 C goes through staging as bulk stores and adds (adds from registers took 224
-// us of 14336 x 4096 x 8192, bulk ones 174).
+// us of 14336 x 4096 x 8192, bulk ones 174, both at four stages; with half the staging, pieces of 16 rows, and five 162, but K =
+// 2048 103 for 101).  At BN 128 there is room for two pieces: 333 x 4096 x 4096 10.4 us, 11.3 with one.
 template <int OUT, int BN> struct Pair4Smem {
     static constexpr int kBufs = BN == 128 ? 2 : 1, kStages = BN == 256 ? 5 : OUT == F32 ? 6 : 7, kStaging = OUT == F32 ? 2048 * kBufs : 1024;
     static constexpr int kAtomsQ = BN / 128, kOperandBytes = (128 + BN / 2) * 128, kScaleBytes = (1 + kAtomsQ) * kScaleAtom;
@@ -138,12 +139,17 @@ QD void put_scales4(Smem &sm, const Mm4Args &a, int atom, int part, int first, i
     }
 }
 
-// One lane's row of 64 sums to a BF16 C that is overwritten, columns col on, as vectors of 32 bytes (16 where C's rows lie
+// One lane's row of 64 sums to a BF16 C (ADD: added to one), columns col on, as vectors of 32 bytes (16 where C's rows lie
 // on 16-byte boundaries only; 8 columns lie in C or outside together).
-QD void store_row64(const MmArgs &g, const uint64_t (&acc)[32], int64_t row, int64_t col, bool wide)
+template <bool ADD> QD void store_row64(const MmArgs &g, const uint64_t (&acc)[32], int64_t row, int64_t col, bool wide)
 {
     if (row >= g.rows_p) return;
     uint16_t *const c = static_cast<uint16_t *>(g.c) + row * g.ldc + col;
+    uint4 was[ADD ? 8 : 1];   // what is added to, all of it before the first store
+    if constexpr (ADD) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) was[i] = col + 8 * i < g.rows_q ? load_16(c + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         uint32_t w[8];
@@ -151,6 +157,12 @@ QD void store_row64(const MmArgs &g, const uint64_t (&acc)[32], int64_t row, int
         for (int j = 0; j < 8; j++) {
             float a, b;
             unpack2(acc[8 * i + j], a, b);
+            if constexpr (ADD) {
+                const uint4 &v = was[2 * i + j / 4];
+                const uint32_t two = j % 4 == 0 ? v.x : j % 4 == 1 ? v.y : j % 4 == 2 ? v.z : v.w;
+                a += __uint_as_float(two << 16);
+                b += __uint_as_float(two & 0xFFFF0000u);
+            }
             w[j] = bf16_pair(a, b);
         }
         const uint4 lo = make_uint4(w[0], w[1], w[2], w[3]), hi = make_uint4(w[4], w[5], w[6], w[7]);
@@ -163,8 +175,8 @@ QD void store_row64(const MmArgs &g, const uint64_t (&acc)[32], int64_t row, int
     }
 }
 
-// A warp's 32 rows x 64 sums to a BF16 C of any pitch, or added to one, 8 columns at a time through 1 KiB of staging.
-QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
+// A warp's 32 rows x 64 sums to a BF16 C of any pitch (ADD: added to one), 8 columns at a time through 1 KiB of staging.
+template <bool ADD> QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
 {
 #pragma unroll
     for (int p = 0; p < 8; p++) {
@@ -175,26 +187,34 @@ QD void store_any64(const MmArgs &g, float *staging, const uint64_t (&acc)[32], 
         to[odd ^ 1] = make_ulonglong2(acc[4 * p + 2], acc[4 * p + 3]);
         __syncwarp();
         const int64_t col = col0 + 8 * p + (lane & 7);
+        float was[ADD ? 8 : 1];   // what is added to, all of it before the first store
+        if constexpr (ADD) {
+#pragma unroll
+            for (int it = 0; it < 8; it++) {
+                const int64_t row = row0 + 4 * it + (lane >> 3);
+                was[it] = row < g.rows_p && col < g.rows_q ? load_bf16(static_cast<const uint16_t *>(g.c) + row * g.ldc + col) : 0.0f;
+            }
+        }
 #pragma unroll
         for (int it = 0; it < 8; it++) {
             const int r = 4 * it + (lane >> 3), chunk = ((lane >> 2) & 1) ^ ((r >> 2) & 1);
-            if (row0 + r < g.rows_p && col < g.rows_q)
-                put_one<BF16>(static_cast<uint16_t *>(g.c) + (row0 + r) * g.ldc + col, staging[8 * r + 4 * chunk + (lane & 3)], g.accumulate);
+            float v = staging[8 * r + 4 * chunk + (lane & 3)];
+            if constexpr (ADD) v += was[it];
+            if (row0 + r < g.rows_p && col < g.rows_q) static_cast<uint16_t *>(g.c)[(row0 + r) * g.ldc + col] = (uint16_t)bf16_bits(v);
         }
         __syncwarp();
     }
 }
 
 // A warp's 32 rows x 64 sums to an FP32 C, in pieces of 16 rows x 128 bytes through BUFS (one or two) times 2 KiB of staging, where 16-byte chunk i of
-// row r is at place i ^ (r % 8), the 128-byte swizzle of the bulk stores.  (Direct: by the warp's lanes, a C of any pitch.)
-template <int BUFS> QD void store_f32_64(const MmArgs &g, const CUtensorMap *map_c, uint8_t *const staging0, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
+// row r is at place i ^ (r % 8), the 128-byte swizzle of the bulk stores.  (DIRECT: by the warp's lanes, a C of any pitch.)
+template <int BUFS, bool DIRECT> QD void store_f32_64(const MmArgs &g, const CUtensorMap *map_c, uint8_t *const staging0, const uint64_t (&acc)[32], int64_t row0, int64_t col0, int lane)
 {
-    const bool bulk = g.store != kStoreDirect;
 #pragma unroll
     for (int p = 0; p < 4; p++) {
         const int64_t row = row0 + 16 * (p & 1), col = col0 + 32 * (p >> 1);
         uint8_t *const staging = staging0 + (p & (BUFS - 1)) * 2048;
-        if (bulk && lane == 0) {   // the last piece that was here has left it
+        if (!DIRECT && lane == 0) {   // the last piece that was here has left it
             if constexpr (BUFS == 2) bulk_wait_read_but1();
             else bulk_wait_read_all();
         }
@@ -205,7 +225,7 @@ template <int BUFS> QD void store_f32_64(const MmArgs &g, const CUtensorMap *map
                 *reinterpret_cast<ulonglong2 *>(staging + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
                     make_ulonglong2(acc[(p >> 1) * 16 + 2 * i], acc[(p >> 1) * 16 + 2 * i + 1]);
         }
-        if (bulk) {
+        if constexpr (!DIRECT) {
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -217,17 +237,27 @@ template <int BUFS> QD void store_f32_64(const MmArgs &g, const CUtensorMap *map
             }
         } else {
             __syncwarp();
-            for (int r = 0; r < 16 && row + r < g.rows_p; r++)
-                if (col + lane < g.rows_q)
-                    put_one<F32>(static_cast<float *>(g.c) + (row + r) * g.ldc + col + lane,
-                                 *reinterpret_cast<const float *>(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4), g.accumulate);
+            float *const c = static_cast<float *>(g.c) + row * g.ldc + col + lane;
+            const int rows = col + lane >= g.rows_q || row >= g.rows_p ? 0 : g.rows_p - row < 16 ? (int)(g.rows_p - row) : 16;
+            float was[16];   // what is added to, all of it before the first store
+#pragma unroll
+            for (int r = 0; r < 16; r++) was[r] = g.accumulate && r < rows ? load_float(c + r * g.ldc) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                const float v = *reinterpret_cast<const float *>(staging + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+                if (r < rows) c[r * g.ldc] = g.accumulate ? was[r] + v : v;
+            }
         }
     }
 }
 
-// ANY (at BN 256): C's rows are no multiple of 16 bytes, or a BF16 C is added to.  (A kernel of its own: the code for it, though not
-// reached, took 161 us of 8192 x 14336 x 4096 where the kernel without it takes 154.)
-template <int OUT, int BN, bool WHOLE, bool ANY>
+// What C is like: its rows are multiples of 16 bytes, and a BF16 one is overwritten; or (at BN 256) rows of any pitch; or a BF16
+// C that is added to.  (Kernels of their own: the code for the others, though not reached, took 161 us of 8192 x 14336 x 4096
+// where the kernel without it takes 154, and 49.6 us of 4096 x 4095 x 4096 for 47.6.  4096 x 4095 x 4096 added to: FP32 65 us, BF16
+// 122, a BF16 C of 4096 columns 49.)
+enum { kPlainC = 0, kAnyC = 1, kAddC = 2 };
+
+template <int OUT, int BN, bool WHOLE, int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPair4Threads, 1)
 k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
            const __grid_constant__ CUtensorMap map_c, const Mm4Args a)
@@ -393,9 +423,12 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                 if (__any_sync(0xFFFFFFFFu, *stop)) return;
                 const int64_t row = (int64_t)tp * 256 + 128 * (int)rank + quad * 32, col = (int64_t)tq * BN + half * (BN / 2) + h * 64;
                 uint8_t *const staging = sm.staging[warp - 2 - kPair4ScaleWarps];
-                if constexpr (OUT == BF16 && ANY) store_any64(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
-                else if constexpr (OUT == BF16) store_row64(g, acc, row + lane, col, wide);
-                else store_f32_64<Smem::kBufs>(g, &map_c, staging, acc, row, col, lane);
+                if constexpr (OUT == BF16 && KIND == kAddC) {
+                    if (g.ldc % 8 == 0) store_row64<true>(g, acc, row + lane, col, wide);
+                    else store_any64<true>(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
+                } else if constexpr (OUT == BF16 && KIND == kAnyC) store_any64<false>(g, reinterpret_cast<float *>(staging), acc, row, col, lane);
+                else if constexpr (OUT == BF16) store_row64<false>(g, acc, row + lane, col, wide);
+                else store_f32_64<Smem::kBufs, KIND == kAnyC>(g, &map_c, staging, acc, row, col, lane);
             };
             if constexpr (BN == 256) {
                 part(half, true);

@@ -48,12 +48,12 @@ cudaError_t mm4_split(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int6
 
 // The registers that the pair kernel's epilogue takes over have to be there at
 // its launch: it would wait for them forever.
-template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t pair4_registers_ready()
+template <int OUT, int BN, bool WHOLE, int KIND> cudaError_t pair4_registers_ready()
 {
     static std::atomic<bool> ready{false};
     if (ready.load(std::memory_order_relaxed)) return cudaSuccess;
     cudaFuncAttributes a;
-    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, BN, WHOLE, ANY>);
+    const cudaError_t e = cudaFuncGetAttributes(&a, k_mm4_pair<OUT, BN, WHOLE, KIND>);
     if (e != cudaSuccess) return e;
     if (a.numRegs * kPair4Threads < 32 * (kPair4EpiWarps * kPair4EpiRegs + (2 + kPair4ScaleWarps) * kPair4Regs)) return cudaErrorInvalidConfiguration;
     ready.store(true, std::memory_order_relaxed);
@@ -61,21 +61,21 @@ template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t pair4_registers_rea
 }
 
 // Tiles of 256 x BN on CTA pairs.
-template <int OUT, int BN, bool WHOLE, bool ANY> cudaError_t mm4_pair_t(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
+template <int OUT, int BN, bool WHOLE, int KIND> cudaError_t mm4_pair_t(const uint8_t *p, const uint8_t *q, Mm4Args a, int64_t K, cudaStream_t st)
 {
     alignas(64) CUtensorMap map_p, map_q, map_c = {};
     MmArgs &g = a.store;
     cudaError_t e = make_operand_map(&map_p, p, g.rows_p, K / 2, 128);
     if (e == cudaSuccess) e = make_operand_map(&map_q, q, g.rows_q, K / 2, BN / 2);
-    g.store = ANY || OUT == BF16 ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
-    if (e == cudaSuccess && !ANY && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q, 16);
-    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, BN, WHOLE, ANY>>(sizeof(Pair4Smem<OUT, BN>));
-    if (e == cudaSuccess) e = pair4_registers_ready<OUT, BN, WHOLE, ANY>();
+    g.store = KIND == kAnyC || OUT == BF16 ? kStoreDirect : g.accumulate ? kStoreBulkAdd : kStoreBulk;
+    if (e == cudaSuccess && KIND == kPlainC && OUT == F32) e = make_result_map(&map_c, g.c, OUT, g.rows_p, g.rows_q, 16);
+    if (e == cudaSuccess) e = engine_smem_ready<k_mm4_pair<OUT, BN, WHOLE, KIND>>(sizeof(Pair4Smem<OUT, BN>));
+    if (e == cudaSuccess) e = pair4_registers_ready<OUT, BN, WHOLE, KIND>();
     if (e != cudaSuccess) return e;
     const int64_t tiles_p = (g.rows_p + 255) / 256, tiles_q = (g.rows_q + BN - 1) / BN, tiles = tiles_p * tiles_q, pairs = sm_count() / 2;
     a.group = tiles_q < tiles_p && tiles_q <= 32 ? 2 : tiles_p < 32 ? (int)tiles_p : 32;
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_k(true, k_mm4_pair<OUT, BN, WHOLE, ANY>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
+    return launch_k(true, k_mm4_pair<OUT, BN, WHOLE, KIND>, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPair4Threads),
                     sizeof(Pair4Smem<OUT, BN>), st, map_p, map_q, map_c, a);
 }
 
@@ -86,8 +86,10 @@ bool whole_rows(const Mm4Scales &s) { return ((reinterpret_cast<uintptr_t>(s.at)
 
 template <int OUT, bool WHOLE> cudaError_t mm4_pair(const uint8_t *p, const uint8_t *q, const Mm4Args &a, int64_t K, int bn, bool any, cudaStream_t st)
 {
-    if (any) return mm4_pair_t<OUT, 256, WHOLE, true>(p, q, a, K, st);
-    return bn == 128 ? mm4_pair_t<OUT, 128, WHOLE, false>(p, q, a, K, st) : mm4_pair_t<OUT, 256, WHOLE, false>(p, q, a, K, st);
+    if constexpr (OUT == BF16)
+        if (a.store.accumulate) return mm4_pair_t<OUT, 256, WHOLE, kAddC>(p, q, a, K, st);
+    if (any) return mm4_pair_t<OUT, 256, WHOLE, kAnyC>(p, q, a, K, st);
+    return bn == 128 ? mm4_pair_t<OUT, 128, WHOLE, kPlainC>(p, q, a, K, st) : mm4_pair_t<OUT, 256, WHOLE, kPlainC>(p, q, a, K, st);
 }
 
 // CTAs that clusters of `split` keep resident, one per SM (see the blockwise product's).
