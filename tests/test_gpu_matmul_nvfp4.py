@@ -144,6 +144,15 @@ def test_narrow_tiles(M, N, K, bb, dtype, accumulate):
     check(M, N, K, "1x16", bb, dtype, accumulate, seed=M)
 
 
+# rows of C of 32, 16, 8, 4 and 2 bytes' pitch, added to and overwritten by the pair kernel
+@pytest.mark.parametrize("N", [2304, 2312, 2308, 2310, 2311])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_pitches(N, dtype, accumulate):
+    check(2601, N, 512, "1x16", "1x16", dtype, accumulate, seed=N, lossless=True)
+    check(2601, N, 512, "1x16", "1x16", dtype, accumulate, seed=N)
+
+
 def test_random_shapes():
     rng = np.random.default_rng(5)
     for i in range(60):
