@@ -779,10 +779,11 @@ def _call_on(dev, name, *args):
             _call(name, *args)
 
 
-class _OnceMore(torch.autograd.Function):
-    """A gradient as it is, whose own derivative raises (`start` begins a graph where g has none)."""
+class _Once(torch.autograd.Function):
+    """A gradient as it is, whose own derivative raises.  `via`: what the gradient follows from, so that a graph of the
+    backward pass leads through here on every way to the call's inputs; one that went past would lose its part without a word."""
     @staticmethod
-    def forward(ctx, g, start, name):
+    def forward(ctx, name, g, *via):
         ctx.name = name
         return g.view_as(g)
 
@@ -791,11 +792,11 @@ class _OnceMore(torch.autograd.Function):
         raise RuntimeError(f"{ctx.name} has no second derivative")
 
 
-def _once(name, *grads):
-    """Gradients that autograd computed without their graph; under create_graph they raise where one is asked for."""
+def _once(name, grads, *via):
+    """Gradients that autograd computed without their graph; under create_graph their derivatives by anything behind `via` raise."""
     if not torch.is_grad_enabled():
         return grads
-    return tuple(None if g is None else _OnceMore.apply(g, torch.zeros((), requires_grad=True), name) for g in grads)
+    return tuple(None if g is None else _Once.apply(name, g, *via) for g in grads)
 
 
 def _norm_in(name, x, dev, weight, residual):
@@ -850,7 +851,7 @@ class _NormAdd(torch.autograd.Function):
             return dh, None, dh if need[2] else None, None, None, None
         with torch.no_grad():
             dx, dw = norm_grad(_ready(dy), h, rstd, weight, None if dh is None else _ready(dh), need_dw=need[1])
-        dx, dw = _once("norm_add", dx, dw)
+        dx, dw = _once("norm_add", (dx, dw), dy, dh, h, weight)
         return dx, dw, dx if need[2] else None, None, None, None
 
 

@@ -52,16 +52,10 @@ def _cast_rows(x, rowwise, colwise, status):
     return t
 
 
-class _Once(torch.autograd.Function):
-    """A gradient as it is.  Its own derivative, which the FP8 casts do not have, raises: a graph of the
-    backward pass that ended here would lose that part without a word (`start` begins one where dy has none)."""
-    @staticmethod
-    def forward(ctx, g, dy, start):
-        return g.view_as(g)
-
-    @staticmethod
-    def backward(ctx, _):
-        raise RuntimeError("BlockwiseLinear has no second derivative")
+def _link(wanted):
+    """An output of a layer's function without elements, kept for its backward pass (None where there is none): it leads to
+    all of the function's inputs, which themselves are not kept, for :func:`_once` to stand on the way to them."""
+    return torch.empty(0) if wanted else None
 
 
 class _BlockwiseLinear(torch.autograd.Function):
@@ -78,22 +72,24 @@ class _BlockwiseLinear(torch.autograd.Function):
         y = mm_blockwise(xq.q_row, xq.s_row, w.q_row, w.s_row, dtype=x.dtype, status=status)
         if p > 0 or residual is not None:
             drop_add(y, p, seed, offset, None if residual is None else _ready(residual.reshape(y.shape)), out=y)
+        link = _link(need_x or need_w)
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(*((w.q_colT, w.s_colT) if need_x else (None, None)),
-                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
+                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)), link)
         ctx.args = (p, seed, offset, main_grad, weight.dtype, x.shape, None if residual is None else residual.shape, status)
-        return y.view(out_shape)
+        return y.view(out_shape), link
 
     @staticmethod
-    def backward(ctx, dy):
+    def backward(ctx, dy, _):
+        *saved, link = ctx.saved_tensors   # once: a checkpoint unpacks each a single time
         with torch.no_grad():
-            dx, dw = _BlockwiseLinear.gradients(ctx, dy)
-        if torch.is_grad_enabled():   # create_graph
-            dx, dw = (None if g is None else _Once.apply(g, dy, torch.zeros((), requires_grad=True)) for g in (dx, dw))
+            grads = _BlockwiseLinear.gradients(ctx, dy, saved)
+        dx, dw = _once("BlockwiseLinear", grads, dy, link)
         return (dx, dw, None if ctx.args[6] is None else dy.reshape(ctx.args[6])) + (None,) * 7
 
     @staticmethod
-    def gradients(ctx, dy):
-        w_q, w_s, x_q, x_s = ctx.saved_tensors
+    def gradients(ctx, dy, saved):
+        w_q, w_s, x_q, x_s = saved
         p, seed, offset, main_grad, w_dtype, x_shape, _, status = ctx.args
         need_x, need_w = ctx.needs_input_grad[:2]
         if not (need_x or need_w):
@@ -175,7 +171,7 @@ class BlockwiseLinear(torch.nn.Module):
         if copies is None:
             copies = self.quantize_weight(colwise=train and x.requires_grad)
         return _BlockwiseLinear.apply(x, self.weight, residual, copies, p, self.seed,
-                                      int(offset), self.main_grad, train, self._status_on(x.device))
+                                      int(offset), self.main_grad, train, self._status_on(x.device))[0]
 
 
 class RMSNorm(torch.nn.Module):
@@ -216,24 +212,26 @@ class _NormBlockwiseLinear(torch.autograd.Function):
         xq, h, rstd = norm_q_blockwise(x2, norm_weight.detach(), eps, r2, rowwise=True, colwise=need_w, status=status)
         y = mm_blockwise(xq.q_row[:M], xq.s_row[:M], w.q_row, w.s_row, dtype=x.dtype, status=status)
         ctx.set_materialize_grads(False)
+        link = _link(through or need_w)
         ctx.save_for_backward(*((h[:M], rstd[:M], norm_weight, w.q_colT, w.s_colT) if through else (None,) * 5),
-                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)))
+                              *((xq.q_colT, xq.s_colT) if need_w else (None, None)), link)
         ctx.args = (main_grad, weight.dtype, x.shape, residual is not None, status)
         y = y.view(*x.shape[:-1], weight.shape[0])
-        return (y, h[:M].reshape(x.shape)) if residual is not None else y
+        return (y, link, h[:M].reshape(x.shape)) if residual is not None else (y, link)
 
     @staticmethod
-    def backward(ctx, dy, dh=None):
+    def backward(ctx, dy, _, dh=None):
         if dy is None:   # the sum alone was used
             return (dh, None, None, dh) + (None,) * 5
+        *saved, link = ctx.saved_tensors   # once: a checkpoint unpacks each a single time
         with torch.no_grad():
-            grads = _NormBlockwiseLinear.gradients(ctx, dy, dh)
-        dx, dn, dw = _once("NormBlockwiseLinear", *grads)
+            grads = _NormBlockwiseLinear.gradients(ctx, dy, dh, saved)
+        dx, dn, dw = _once("NormBlockwiseLinear", grads, dy, dh, link)
         return (dx, dn, dw, dx if ctx.args[3] else None) + (None,) * 5
 
     @staticmethod
-    def gradients(ctx, dy, dh):
-        h, rstd, norm_weight, w_q, w_s, x_q, x_s = ctx.saved_tensors
+    def gradients(ctx, dy, dh, saved):
+        h, rstd, norm_weight, w_q, w_s, x_q, x_s = saved
         main_grad, w_dtype, x_shape, _, status = ctx.args
         need = ctx.needs_input_grad
         through, need_w = need[0] or need[1] or need[3], need[2]
@@ -272,8 +270,9 @@ class NormBlockwiseLinear(BlockwiseLinear):
         if copies is None:
             through = x.requires_grad or self.norm_weight.requires_grad or residual is not None and residual.requires_grad
             copies = self.quantize_weight(colwise=train and through)
-        return _NormBlockwiseLinear.apply(x, self.norm_weight, self.weight, residual, copies, self.eps, self.main_grad, train,
-                                          self._status_on(x.device))
+        y, _, *h = _NormBlockwiseLinear.apply(x, self.norm_weight, self.weight, residual, copies, self.eps, self.main_grad, train,
+                                              self._status_on(x.device))
+        return (y, *h) if h else y
 
 
 class _NVFP4Linear(torch.autograd.Function):
@@ -292,20 +291,23 @@ class _NVFP4Linear(torch.autograd.Function):
                 _word("amax", amax, x.device)
             row = q_nvfp4(_rows_to(x2, 16), amax=amax, status=status)
         y = matmul_nvfp4(row.q_row[:M], row.sb_row[:M], row.s_global, w.q_row, w.sb_row, w.s_global, dtype=x.dtype, status=status)
+        link = _link(need_x or need_w)
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(*((w.q_colT, w.sb_colT, w.s_global) if need_x else (None,) * 3),
-                              *((col.q_colT, col.sb_colT, col.s_global) if need_w else (None,) * 3))
+                              *((col.q_colT, col.sb_colT, col.s_global) if need_w else (None,) * 3), link)
         ctx.args = (sign_mask, seed, offset, main_grad, weight.dtype, x.shape, status)
-        return y.view(*x.shape[:-1], weight.shape[0])
+        return y.view(*x.shape[:-1], weight.shape[0]), link
 
     @staticmethod
-    def backward(ctx, dy):
+    def backward(ctx, dy, _):
+        *saved, link = ctx.saved_tensors   # once: a checkpoint unpacks each a single time
         with torch.no_grad():
-            grads = _NVFP4Linear.gradients(ctx, dy)
-        return _once("NVFP4Linear", *grads) + (None,) * 8
+            grads = _NVFP4Linear.gradients(ctx, dy, saved)
+        return _once("NVFP4Linear", grads, dy, link) + (None,) * 8
 
     @staticmethod
-    def gradients(ctx, dy):
-        w, x = ctx.saved_tensors[:3], ctx.saved_tensors[3:]
+    def gradients(ctx, dy, saved):
+        w, x = saved[:3], saved[3:]
         sign_mask, seed, offset, main_grad, w_dtype, x_shape, status = ctx.args
         need_x, need_w = ctx.needs_input_grad[:2]
         d = _ready(dy.reshape(-1, dy.shape[-1]))
@@ -373,4 +375,4 @@ class NVFP4Linear(torch.nn.Module):
         if copies is None:
             copies = self.quantize_weight(colwise=train and x.requires_grad)
         return _NVFP4Linear.apply(x, self.weight, copies, self.sign_mask, self.seed, int(offset), self.main_grad, train,
-                                  self._status_on(x.device), amax)
+                                  self._status_on(x.device), amax)[0]
