@@ -480,7 +480,8 @@ q_status drop_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, doubl
  * FP32; s_a and s_b multiply the sum one after the other, in FP32.  The result
  * does not depend on timing, and a row's result does not depend on the values
  * of other rows.  How K is split goes by M, N and K, so the same row may round
- * otherwise in a call of another M.
+ * otherwise in a call of another M; it goes by `out`, accumulate, whether every
+ * row of scales begins on a 16-byte boundary and the device's SMs as well.
  * Shapes: K % 32 == 0, M % 16 == 0 (N % 16 == 0) for a 16x16 operand; M, N, K
  * < 2^31.  M == 0 or N == 0 does nothing; K == 0 is a sum over nothing: c is
  * set to zero, or left as it is when accumulating.
@@ -500,7 +501,8 @@ q_status matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, q
  *   residual is NULL);  rstd = 1 / sqrt(mean(h^2) + eps);  y = (h rstd) w
  * The norm is that of h as it is kept, so that norm_grad, which is given h and
  * rstd, works with the numbers of the forward pass.  Sums are FP32, in an
- * order that K alone decides; y is rounded once.
+ * order that K and `in` decide: a row's h, rstd and y are the same bits in a call
+ * of any M, with the residual or with h given.  y is rounded once.
  *   x, residual, h, y  [M, K] of dtype `in`;  weight [K] of dtype wt;
  *   rstd [M] FP32 (written);  eps >= 0, finite.
  *   h is written where there is a residual, and has to be NULL without one.
@@ -537,7 +539,8 @@ q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const
  *   dx = rstd (g - v mean(g v)) + dh     dw = sum over the rows of dy v
  * dx is the gradient of x and of residual alike; dh (or NULL) is the gradient
  * of h from where h is used again (the residual stream).  Sums are FP32, in an
- * order that M and K decide; dx and dw are rounded once.
+ * order that K, `in` and whether there is dh decide, dw's by M as well; dx and dw
+ * are rounded once.
  *   dy, h, dh, dx [M, K] of dtype `in`;  weight, dw [K] of dtype wt.
  *   dw may be NULL.  Otherwise work is scratch of norm_grad_work(M, K, in)
  *   floats, whose contents before and after do not matter; calls that may run

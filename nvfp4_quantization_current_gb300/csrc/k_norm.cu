@@ -3,7 +3,8 @@
 //   h = x + residual (rounded to its type once; h = x without a residual)
 //   s = 1 / sqrt(mean(h^2) + eps) per row,   y = (h s) w
 //
-// The sums run in FP32 in an order fixed by the shape.  y is either stored
+// The sums run in FP32 in an order that the row's length and type fix, so that a row's
+// result is the same in every call.  y is either stored
 // (norm_add) or cast in registers to the rowwise 1x128 E4M3 copy
 // (norm_q_blockwise; k_norm_cast.cu makes the transposed one from h and s).  All of it
 // is bound by memory, and a row is read once: it stays in registers between its sum
@@ -18,22 +19,26 @@ namespace qk {
 
 namespace {
 
-// The sum of squares of a thread's pieces.
+// The sum of squares of a thread's pieces.  Of 16 single elements, which two threads may share (k_norm_rows), the
+// even and the odd ones are summed apart first.
 template <int DT, int W, int N> QD float squares(const Piece<DT, W> (&h)[N])
 {
-    float sum = 0.0f;
+    float sum = 0.0f, odd = 0.0f;
     if constexpr (W > 1) {
         uint64_t two = 0;
 #pragma unroll
         for (int i = 0; i < N; i++)
 #pragma unroll
             for (int j = 0; j < W / 2; j++) two = ffma2(h[i].pair(j), h[i].pair(j), two);
-        float odd;
         unpack2(two, sum, odd);
         sum += odd;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i++) sum = __fmaf_rn(h[i].at(0), h[i].at(0), sum);
+        for (int i = 0; i < N; i++) {
+            float &to = N == 16 && i % 2 ? odd : sum;
+            to = __fmaf_rn(h[i].at(0), h[i].at(0), to);
+        }
+        if (N == 16) sum += odd;
     }
     return sum;
 }
@@ -132,14 +137,18 @@ template <int DT> QD void norm_amax(const NormArgs &a, uint32_t m)
     cta_max_to(m, reinterpret_cast<uint32_t *>(a.amax), a.status);
 }
 
-// A row to 2^gshift threads, the element pieces t, t + 2^gshift, ... of it in
-// each thread's registers: read once, whatever is made of it.
+// A row to T threads (whole warps), the element pieces t, t + T, ... of it in
+// each thread's registers: read once, whatever is made of it.  Of rows of up to 8192
+// single elements a thread takes eight (16 take 5.2 us of 16 x 1111 BF16, eight 3.2), threads t and t + T / 2 what a
+// thread of the ring takes.
 template <int DT, int W, int VPT, int MODE, bool RES>
 __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
 {
-    __shared__ float part[32];
-    const int g = 1 << a.gshift, t = threadIdx.x & (g - 1), lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> a.gshift) + (threadIdx.x >> a.gshift);
+    constexpr bool kHalves = W == 1 && VPT == 8;
+    __shared__ float part[32], upper[kHalves ? 512 : 1];
+    // this thread's row of the CTA's: its warp by the warps of a row (of 32 at most, so that 16 bits of the quotient do)
+    const int T = a.row_threads, mine = (int)((threadIdx.x >> 5) * a.per_warps >> 16), t = threadIdx.x - mine * T, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * a.cta_rows + mine;
     const bool live = row < a.M;
     const int K = (int)a.K;
     const int64_t base = row * a.K;
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
         Piece<DT, W> r[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; i++) {
-            const int k = (t + i * g) * W;
+            const int k = (t + i * T) * W;
             h[i].zero();
             if (RES) r[i].zero();
             if (live && k < K) {
@@ -162,33 +171,47 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
         if constexpr (kAhead) {
 #pragma unroll
             for (int i = 0; i < VPT; i++) {
-                const int k = (t + i * g) * W;
+                const int k = (t + i * T) * W;
                 if (k < K) load_weights<W>(w[i], a.weight, a.wf32, k);
             }
         }
         if constexpr (RES) {
 #pragma unroll
             for (int i = 0; i < VPT; i++) {
-                const int k = (t + i * g) * W;
+                const int k = (t + i * T) * W;
                 h[i].add(r[i]);
                 if (live && k < K) h[i].store(a.h, base + k);
             }
         }
     }
-    const float s = row_factor(row_sum(squares<DT, W, VPT>(h), part, a.gshift), a.inv, a.eps);
+    float sum = squares<DT, W, VPT>(h);
+    if constexpr (kHalves) {
+        const int half = T >> 1, at = mine * half + t;
+        if (t >= half) upper[at - half] = sum;
+        __syncthreads();
+        if (t < half) {
+            sum = warp_sum(sum + upper[at]);
+            if (lane == 0) part[threadIdx.x >> 5] = sum;
+        }
+        __syncthreads();
+        sum = warp_sum(lane < half >> 5 ? part[mine * (T >> 5) + lane] : 0.0f);
+    } else {
+        sum = row_sum(sum, part, mine * (T >> 5), T >> 5);
+    }
+    const float s = row_factor(sum, a.inv, a.eps);
     if (live && t == 0) a.rstd[row] = s;
     if constexpr (MODE == kNormFactor) return;
     if constexpr (MODE == kNormCast && kAhead) {
         float y[VPT][W];
 #pragma unroll
         for (int i = 0; i < VPT; i++) norm_y<DT, W>(y[i], h[i], s, w[i]);
-        if (live) norm_cast<W, VPT>(a, y, a.q_row + base, a.s_row + row * (K / 128), t * W, g * W, lane);   // a warp's rows are live together
+        if (live) norm_cast<W, VPT>(a, y, a.q_row + base, a.s_row + row * (K / 128), t * W, T * W, lane);   // a warp's rows are live together
         return;
     }
     uint32_t m = 0;   // largest |y| of this thread
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
-        const int k = (t + i * g) * W;
+        const int k = (t + i * T) * W;
         const bool in = live && k < K;
         if (!kAhead && in) load_weights<W>(w[0], a.weight, a.wf32, k);
         float y[1][W];
@@ -223,7 +246,7 @@ __global__ void __launch_bounds__(1024) k_norm_long(const NormArgs a)
 #pragma unroll
         for (int j = 0; j < W; j++) sum = __fmaf_rn(h.at(j), h.at(j), sum);
     }
-    const float s = row_factor(row_sum(sum, part, 10), a.inv, a.eps);
+    const float s = row_factor(row_sum(sum, part, 0, 32), a.inv, a.eps);
     if (threadIdx.x == 0) a.rstd[blockIdx.x] = s;
     if constexpr (MODE == kNormFactor) return;
     const void *const from = RES ? a.h : a.x;
@@ -362,18 +385,16 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 512, RES || WIDE ? 1 : 2) k_norm
 // launches
 // ---------------------------------------------------------------------------
 
-int log2_up(int64_t n)
-{
-    int s = 0;
-    while (((int64_t)1 << s) < n) s++;
-    return s;
-}
+// Threads of a row whose threads take E elements each.
+int row_threads(int64_t K, int E) { return (int)((K + 32 * E - 1) / (32 * E)) * 32; }
 
-template <int DT, int W, int VPT, int MODE> cudaError_t norm_rows(NormArgs a, int gshift, cudaStream_t st)
+template <int DT, int W, int VPT, int MODE> cudaError_t norm_rows(NormArgs a, cudaStream_t st)
 {
-    a.gshift = gshift;
-    const int threads = gshift < 8 ? 256 : 1 << gshift, rows = threads >> gshift;
-    const int64_t grid = (a.M + rows - 1) / rows;
+    a.row_threads = W == 1 && VPT == 8 ? 2 * row_threads(a.K, 16) : row_threads(a.K, VPT * W);
+    a.cta_rows = a.row_threads < 256 ? 256 / a.row_threads : 1;
+    a.per_warps = 65536u / (a.row_threads / 32) + 1;
+    const int threads = a.cta_rows * a.row_threads;
+    const int64_t grid = (a.M + a.cta_rows - 1) / a.cta_rows;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     return launch_k(true, a.residual != nullptr ? k_norm_rows<DT, W, VPT, MODE, true> : k_norm_rows<DT, W, VPT, MODE, false>,
                     dim3((unsigned)grid), dim3(threads), 0, st, a);
@@ -399,7 +420,7 @@ template <int DT, int W, int MODE, bool RES> bool norm_ring(const NormArgs &a, c
     constexpr int ES = In<DT>::BYTES;
     if (a.K <= 256 || a.K > 16384 || (W > 1 && a.K < 2048)) return false;
     const bool wide = a.K > 8192;
-    const int threads = (int)((a.K + 511) / 512) * 32;
+    const int threads = row_threads(a.K, 16);
     const int stage_bytes = (RES ? 2 : 1) * (int)((a.K * ES + 15) / 16 * 16 + (a.K * ES % 16 != 0 ? 16 : 0));
     const int fit = kRingBytes / (2 * stage_bytes);
     // With a residual fewer rows at a time are better: 16384 x 7168 stored 142 us at two stages, 159 to 164 at three
@@ -420,13 +441,15 @@ template <int DT, int W, int MODE> cudaError_t norm_w(const NormArgs &a, cudaStr
         cudaError_t e;
         if (a.residual != nullptr ? norm_ring<DT, W, MODE, true>(a, st, e) : norm_ring<DT, W, MODE, false>(a, st, e)) return e;
     }
-    constexpr int E = W == 1 ? 4 : 8;   // elements of a thread, times 1, 2 or 4
-    const int64_t pieces = (a.K + W - 1) / W;
-    const int s1 = log2_up((pieces + E / W - 1) / (E / W)), s2 = log2_up((pieces + 2 * E / W - 1) / (2 * E / W)),
-              s4 = log2_up((pieces + 4 * E / W - 1) / (4 * E / W));
-    if (s1 <= 5) return norm_rows<DT, W, E / W, MODE>(a, 5, st);
-    if (s2 <= 10) return norm_rows<DT, W, 2 * E / W, MODE>(a, s2 < 5 ? 5 : s2, st);
-    if (s4 <= 10) return norm_rows<DT, W, 4 * E / W, MODE>(a, s4, st);
+    // Elements of a thread.  Rows that the ring may take are laid out as there, so that the order of a row's sum, and with it
+    // every bit of the result, is the same in a call of few rows and in one of many.
+    constexpr int E = W == 1 ? 4 : 8;
+    if (a.K <= 32 * E) return norm_rows<DT, W, E / W, MODE>(a, st);
+    if constexpr (W == 1)
+        if (a.K <= 8192) return norm_rows<DT, 1, 8, MODE>(a, st);
+    if (a.K <= 16384) return norm_rows<DT, W, 16 / W, MODE>(a, st);
+    if constexpr (W > 1)
+        if (a.K <= 32768) return norm_rows<DT, W, 32 / W, MODE>(a, st);
     if (a.M > INT32_MAX) return cudaErrorInvalidValue;
     return launch_k(true, a.residual != nullptr ? k_norm_long<DT, W, MODE, true> : k_norm_long<DT, W, MODE, false>,
                     dim3((unsigned)a.M), dim3(1024), 0, st, a);

@@ -1,7 +1,7 @@
 // The gradient of the norm ahead of a linear layer (k_norm.cu), per row with
 // v = h s and g = dy w
 //   dx = s (g - v mean(g v)) + dh,      dw = sum over rows of dy v
-// The sums run in FP32 in an order fixed by the shape.  Bound by memory: dy, h and dh
+// The sums run in FP32 in an order that the shape, the type and whether there is dh fix.  Bound by memory: dy, h and dh
 // are read and dx written once, and a CTA's part of dw is a row of scratch that a
 // second, small kernel adds up.  Measured on a GB300, in graphs of calls: 8192 x 4096
 // BF16 with dh 46.5 to 47.3 us (268 MB at 5.7 to 5.8 TB/s; 41.3 without dw, whose kernel
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(1024) k_norm_grad_long(const NormGradArgs a)
 #pragma unroll
             for (int j = 0; j < W; j++) sum = __fmaf_rn(dy.at(j) * w[j], h.at(j) * s, sum);
         }
-        const float c = __fdiv_rn(row_sum(sum, part[flip], 10), (float)a.K);
+        const float c = __fdiv_rn(row_sum(sum, part[flip], 0, 32), (float)a.K);
         for (int64_t k = threadIdx.x * W; k < a.K; k += 1024 * W) {
             Piece<DT, W> h, dy, dh, out;
             float w[W], f[W];

@@ -123,7 +123,8 @@ struct NormArgs {
     float *s_row;
     int32_t *status;
     int64_t M, K;
-    int gshift;   // set by the launcher
+    int row_threads, cta_rows;   // set by the launcher, as the next
+    uint32_t per_warps;
 };
 cudaError_t launch_norm_add(const NormArgs &a, int dt, cudaStream_t st);
 // h and rstd, and the rowwise copy where q_row is given

@@ -135,17 +135,17 @@ QD float warp_sum(float v)
     return v;
 }
 
-// Sum over the 2^gshift consecutive threads (gshift >= 5) that share a row, to
-// all of them; part: a word per warp, used by no other call that is in flight.
+// Sum over the n consecutive warps from `first` on that share a row, to all of
+// their threads; part: a word per warp, used by no other call that is in flight.
 // Every thread of the CTA calls it.
-QD float row_sum(float v, float *part, int gshift)
+QD float row_sum(float v, float *part, int first, int n)
 {
     v = warp_sum(v);
-    if (gshift == 5) return v;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = 1 << (gshift - 5);
-    if (lane == 0) part[warp] = v;
+    if (n == 1) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
-    return warp_sum(lane < n ? part[(warp & ~(n - 1)) + lane] : 0.0f);
+    return warp_sum(lane < n ? part[first + lane] : 0.0f);
 }
 
 // A copy of whole 16-byte pieces into this CTA's shared memory, counted on `bar`.
