@@ -419,7 +419,9 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
 /*
  * Diagnostic of that failure path (a library check): in the calling thread's
  * next mm_blockwise or matmul_nvfp4 that launches a kernel, every cluster takes a
- * wait for run out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it.
+ * wait for run out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it;
+ * on = 2 takes the first wait of the warp that issues the MMAs, with its operands' copies
+ * in flight, any other value waits from the call's start on.
  */
 q_status selftest_mm_give_up(int on);
 

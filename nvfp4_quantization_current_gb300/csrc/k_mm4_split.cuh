@@ -97,7 +97,7 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
         }
         mbar_init(&sm.done, 1);
         mbar_init(&sm.drained, 1);
-        sm.abort_flag = g.give_up && rank == 0;
+        sm.abort_flag = g.give_up == 1 && rank == 0;
         fence_mbar_init();
     }
     if (warp == kEpiWarps && elect_one()) {
@@ -128,13 +128,15 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
                 tma_load_tile(sm.stage[s], &map_p, (kb0 + kb) * 128, p0, &sm.full[s]);
                 tma_load_tile(sm.stage[s] + 128 * 128, &map_q, (kb0 + kb) * 128, q0, &sm.full[s]);
             }
-            if (kb < kb_n)   // aborted: the copies in flight land before shared memory goes away
-                for (int j = kb > kStages ? kb - kStages : 0; j < kb; j++)
-                    (void)mbar_wait_bounded(&sm.full[j % kStages], (j / kStages) & 1);
+            // All that was issued lands before shared memory is put to other use or goes away, whoever gave up: where
+            // the MMAs' warp did, copies that nobody reads may be in flight.
+            for (int j = kb > kStages ? kb - kStages : 0; j < kb; j++)
+                (void)mbar_wait_bounded(&sm.full[j % kStages], (j / kStages) & 1);
         }
     } else if (warp == kEpiWarps + 1) {
-        bool ok = true;
-        for (int kb = 0; kb < kb_n; kb++) {
+        bool ok = g.give_up != 2 || rank != 0;
+        if (!ok) *stop = 1;   // the test's wait that runs out
+        for (int kb = 0; ok && kb < kb_n; kb++) {
             const int s = kb % kStages, slot = (kb >> 2) & 1;
             ok = mm_wait(&sm.full[s], (kb / kStages) & 1, stop, g.status);
             if ((kb & 3) == 0) ok = ok && mm_wait(&sm.sc_full[slot], (kb >> 3) & 1, stop, g.status);

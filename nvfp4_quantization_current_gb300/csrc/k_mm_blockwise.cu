@@ -214,7 +214,7 @@ cudaError_t mm_t(const uint8_t *a, const uint8_t *b, const MmArgs &g, cudaStream
 
 cudaError_t launch_mm_blockwise(const uint8_t *a, const float *s_a, int tile_a, const uint8_t *b, const float *s_b, int tile_b,
                                 int64_t M, int64_t N, int64_t K, void *c, int out, bool accumulate, int32_t *status,
-                                bool give_up, cudaStream_t st)
+                                int give_up, cudaStream_t st)
 {
     MmArgs g = {s_a, s_b, M, N, K / kMmBlock, tile_a ? 7 : 0, tile_b ? 7 : 0, c, N, status, accumulate, kStoreDirect, give_up};
     return out == BF16 ? mm_t<BF16>(a, b, g, st) : mm_t<F32>(a, b, g, st);

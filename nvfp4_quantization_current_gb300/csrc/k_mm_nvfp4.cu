@@ -213,7 +213,7 @@ cudaError_t mm4_t(const uint8_t *a, const uint8_t *b, const Mm4Args &g, int64_t 
 
 cudaError_t launch_matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, int blk_a, const uint8_t *b,
                                 const uint8_t *sb_b, const float *s_b, int blk_b, int64_t M, int64_t N, int64_t K, void *c, int out,
-                                bool accumulate, int32_t *status, bool give_up, cudaStream_t st)
+                                bool accumulate, int32_t *status, int give_up, cudaStream_t st)
 {
     Mm4Args g = {};
     g.store = {nullptr, nullptr, M, N, (K + kMm4Block - 1) / kMm4Block, 0, 0, c, N, status, accumulate, kStoreDirect, give_up};

@@ -75,8 +75,8 @@ q_status check_out(const char *fn, q_dtype out)
 // enqueued (the error path of every entry point, exercised without a GPU).
 thread_local int g_inject_launch_failures = 0;
 
-// Whether a wait of this thread's next product gives up (selftest_mm_give_up).
-thread_local bool g_inject_mm_give_up = false;
+// Which wait of this thread's next product gives up (selftest_mm_give_up).
+thread_local int g_inject_mm_give_up = 0;
 
 #define LAUNCH(where, expr)                                                \
     do {                                                                   \
@@ -422,8 +422,8 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
     TRY(need(fn, "s_a", s_a, 4));
     TRY(need(fn, "b", b, 16));
     TRY(need(fn, "s_b", s_b, 4));
-    const bool give_up = g_inject_mm_give_up;
-    g_inject_mm_give_up = false;
+    const int give_up = g_inject_mm_give_up;
+    g_inject_mm_give_up = 0;
     LAUNCH(fn, qk::launch_mm_blockwise(a, s_a, (int)tile_a, b, s_b, (int)tile_b, M, N, K, c, (int)out, accumulate != 0, status,
                                        give_up, S(stream)));
     return Q_OK;
@@ -501,8 +501,8 @@ q_status matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, q
     TRY(need(fn, "b", b, 16));
     TRY(need(fn, "sb_b", sb_b, 1));
     TRY(need(fn, "s_b", s_b, 4));
-    const bool give_up = g_inject_mm_give_up;
-    g_inject_mm_give_up = false;
+    const int give_up = g_inject_mm_give_up;
+    g_inject_mm_give_up = 0;
     LAUNCH(fn, qk::launch_matmul_nvfp4(a, sb_a, s_a, (int)blk_a, b, sb_b, s_b, (int)blk_b, M, N, K, c, (int)out, accumulate != 0,
                                        status, give_up, S(stream)));
     return Q_OK;
@@ -615,7 +615,7 @@ q_status q_selftest_inject_launch_error(int n)
 
 q_status selftest_mm_give_up(int on)
 {
-    g_inject_mm_give_up = on != 0;
+    g_inject_mm_give_up = on == 0 || on == 2 ? on : 1;
     return Q_OK;
 }
 

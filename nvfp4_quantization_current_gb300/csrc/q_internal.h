@@ -148,17 +148,17 @@ int64_t norm_grad_rows(int64_t M, int64_t K, int dt);   // rows of K floats in `
 cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st);
 
 // block-scaled FP8 product: c [M, N] (+)= a [M, K] b [N, K]^T with the tiles'
-// scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0; give_up: a wait of
-// every cluster counts as run out
+// scales (tile: 0 = 1x128, 1 = 128x128), M, N, K > 0; give_up: as in
+// MmArgs, of every cluster
 cudaError_t launch_mm_blockwise(const uint8_t *a, const float *s_a, int tile_a, const uint8_t *b, const float *s_b, int tile_b,
                                 int64_t M, int64_t N, int64_t K, void *c, int out, bool accumulate, int32_t *status,
-                                bool give_up, cudaStream_t st);
+                                int give_up, cudaStream_t st);
 
 // NVFP4 product: c [M, N] (+)= a [M, K] b [N, K]^T with block scales (blk: 0 = 1x16,
 // 1 = 16x16) and the tensors' scales, M, N, K > 0; give_up as above
 cudaError_t launch_matmul_nvfp4(const uint8_t *a, const uint8_t *sb_a, const float *s_a, int blk_a, const uint8_t *b,
                                 const uint8_t *sb_b, const float *s_b, int blk_b, int64_t M, int64_t N, int64_t K, void *c, int out,
-                                bool accumulate, int32_t *status, bool give_up, cudaStream_t st);
+                                bool accumulate, int32_t *status, int give_up, cudaStream_t st);
 
 // NVFP4 (the amax is already in *amax)
 cudaError_t launch_nvfp4(const void *x, int dt, int64_t M, int64_t K, int blk, int rnd, uint64_t seed,

@@ -21,7 +21,7 @@ struct MmArgs {
     int32_t *status;
     bool accumulate;
     int store;
-    bool give_up;               // every cluster takes a wait for run out: the split kernel's first CTA, both of a pair (a test)
+    int give_up;                // of every cluster, for a test (the split kernel's first CTA, a pair): 1 a wait has run out, 2 the MMAs' first one does
 };
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the
