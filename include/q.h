@@ -421,7 +421,8 @@ q_status mm_blockwise(const uint8_t *a, const float *s_a, q_tile tile_a, const u
  * next mm_blockwise or matmul_nvfp4 that launches a kernel, every cluster takes a
  * wait for run out.  *status gets Q_ST_TIMEOUT and C is left as it is.  on = 0 clears it;
  * on = 2 takes the first wait of the warp that issues the MMAs, with its operands' copies
- * in flight, any other value waits from the call's start on.
+ * in flight, on = 3 and 4 those behind the loads of a CTA pair's first or second CTA, which
+ * never begin, any other value waits from the call's start on.
  */
 q_status selftest_mm_give_up(int on);
 

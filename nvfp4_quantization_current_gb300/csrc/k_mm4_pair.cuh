@@ -56,7 +56,7 @@ template <int OUT, int BN> struct Pair4Smem {
     uint8_t scales[kPair4Slots][kPair4Unit][kScaleBytes];   // P's rows, and Q's in 128s
     uint64_t full[kStages], empty[kStages], sc_full[kPair4Slots], sc_empty[kPair4Slots], acc_full[2], acc_free, drained;
     uint32_t tmem_base;
-    int abort_flag;
+    int abort_flag, issued, landed;
 };
 static_assert(sizeof(Pair4Smem<F32, 256>) <= 232448 && sizeof(Pair4Smem<BF16, 256>) <= 232448 && sizeof(Pair4Smem<F32, 128>) <= 232448 &&
               sizeof(Pair4Smem<BF16, 128>) <= 232448, "shared memory of a CTA");
@@ -287,7 +287,8 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
         for (int b = 0; b < 2; b++) mbar_init(&sm.acc_full[b], 1);
         mbar_init(&sm.acc_free, 2 * kPair4EpiWarps);
         mbar_init(&sm.drained, 1);
-        sm.abort_flag = g.give_up;
+        sm.abort_flag = g.give_up == 1;
+        sm.issued = sm.landed = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc_pair<512>(&sm.tmem_base);
@@ -303,7 +304,8 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
     if (warp < 2 + kPair4ScaleWarps) {
         regs_fewer<kPair4Regs>();
         if (warp == 0 && elect_one()) {
-            bool ok = true;
+            bool ok = g.give_up < 3 || (int)rank != g.give_up - 3;
+            if (!ok) *stop = 1;   // the test's loads that do not begin
             uint32_t issued = 0;
             int s = 0;
             uint32_t use = 1;   // parity of the release that the stage's next use waits for
@@ -332,21 +334,14 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             // arrive here
             for (uint32_t j = issued > kStages ? issued - kStages : 0; ok && j < issued; j++)
                 ok = mm_wait(&sm.empty[j % kStages], (j / kStages) & 1, stop, g.status);
-            if (!ok) {   // copies in flight land before shared memory goes away
-                if (rank == 0) {
-                    for (uint32_t j = issued > kStages ? issued - kStages : 0; j < issued; j++)
-                        (void)mbar_wait_bounded(&sm.full[j % kStages], (j / kStages) & 1);
-                } else {   // counted on the leader's barriers: far longer than any copy takes
-                    const unsigned long long t0 = globaltimer();
-                    while (globaltimer() - t0 < 10000000ull) {}
-                }
-            }
+            pair_loads_end<kStages>(ok, sm.full, issued, Smem::kOperandBytes, &sm.issued, &sm.landed, &sm.abort_flag, rank);
         } else if (warp == 1) {
             if (rank == 0) {
                 const uint64_t a0 = smem_desc_k128(sm.stage[0]), b0 = smem_desc_k128(sm.stage[0] + 128 * 128);
                 const uint64_t src0 = smem_desc_scales(sm.scales[0][0]);
                 const uint32_t sp = tmem + Smem::kScales, sq = sp + 16;
-                bool ok = true;
+                bool ok = g.give_up != 2;
+                if (!ok) *stop = 1;   // the test's wait that runs out
                 int s = 0;
                 uint32_t par = 0, tile = 0, unit = 0;
                 for (int t = first; t < tiles && ok; t += pairs, tile++) {

@@ -97,7 +97,7 @@ k_mm4_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ C
         }
         mbar_init(&sm.done, 1);
         mbar_init(&sm.drained, 1);
-        sm.abort_flag = g.give_up == 1 && rank == 0;
+        sm.abort_flag = g.give_up != 0 && g.give_up != 2 && rank == 0;
         fence_mbar_init();
     }
     if (warp == kEpiWarps && elect_one()) {

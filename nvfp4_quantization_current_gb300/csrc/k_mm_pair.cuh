@@ -88,7 +88,7 @@ struct PairSmem {
     uint64_t full[kPairStages], empty[kPairStages], acc_full[2], peer_free[2], drained[2];
     uint64_t sc_full[kPairScaleSlots], sc_empty[kPairScaleSlots];
     uint32_t tmem_base;
-    int abort_flag, left[2];   // left: the buffer's MMA warp waits no more
+    int abort_flag, issued, landed, left[2];   // left: the buffer's MMA warp waits no more
 };
 static_assert(sizeof(PairSmem) <= 232448, "shared memory of a CTA");
 
@@ -195,7 +195,8 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             mbar_init(&sm.sc_full[s], 32);
             mbar_init(&sm.sc_empty[s], 1);
         }
-        sm.abort_flag = g.give_up;
+        sm.abort_flag = g.give_up == 1;
+        sm.issued = sm.landed = 0;
         sm.left[0] = sm.left[1] = 0;
         fence_mbar_init();
     }
@@ -212,7 +213,8 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
     if (warp < 4) {
         regs_fewer<kPairRegs>();
         if (warp == 0 && elect_one()) {
-            bool ok = true;
+            bool ok = g.give_up < 3 || (int)rank != g.give_up - 3;
+            if (!ok) *stop = 1;   // the test's loads that do not begin
             uint32_t issued = 0;
             int s = 0;
             uint32_t use = 1;   // parity of the release that the stage's next use waits for
@@ -241,15 +243,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
             // arrive here
             for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; ok && j < issued; j++)
                 ok = mm_wait(&sm.empty[j % kPairStages], (j / kPairStages) & 1, stop, g.status);
-            if (!ok) {   // copies in flight land before shared memory goes away
-                if (rank == 0) {
-                    for (uint32_t j = issued > kPairStages ? issued - kPairStages : 0; j < issued; j++)
-                        (void)mbar_wait_bounded(&sm.full[j % kPairStages], (j / kPairStages) & 1);
-                } else {   // counted on the leader's barriers: far longer than any copy takes
-                    const unsigned long long t0 = globaltimer();
-                    while (globaltimer() - t0 < 10000000ull) {}
-                }
-            }
+            pair_loads_end<kPairStages>(ok, sm.full, issued, kPairStageBytes, &sm.issued, &sm.landed, &sm.abort_flag, rank);
         } else if (warp < 3 && warp > 0) {
             // One warp per accumulator buffer: every other block.
             const int buf = warp - 1;
@@ -262,6 +256,7 @@ k_mm_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUt
                 group_r += groups;
             }
             uint32_t par = 0, freed = 0;
+            if (g.give_up == 2 && rank == 0) *stop = 1;   // the test's wait that runs out
             for (uint32_t n = buf; n < blocks + 2; n += 2) {
                 if (rank == 0) {
                     if (n >= blocks) break;

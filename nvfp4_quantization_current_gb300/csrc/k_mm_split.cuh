@@ -57,12 +57,6 @@ QD float4 ld_cluster4(uint32_t addr)
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
-QD int ld_cluster1(uint32_t addr)
-{
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
 // Whether a CTA of the cluster gave up.
 QD bool cluster_gave_up(const int *abort_flag, int split)
 {
@@ -99,7 +93,7 @@ k_mm_split(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             mbar_init(&sm.acc_empty[b], kEpiWarps);
         }
         mbar_init(&sm.drained, 1);
-        sm.abort_flag = g.give_up == 1 && rank == 0;
+        sm.abort_flag = g.give_up != 0 && g.give_up != 2 && rank == 0;
         fence_mbar_init();
     }
     if (warp == kEpiWarps && elect_one()) {

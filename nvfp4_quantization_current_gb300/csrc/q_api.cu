@@ -615,7 +615,7 @@ q_status q_selftest_inject_launch_error(int n)
 
 q_status selftest_mm_give_up(int on)
 {
-    g_inject_mm_give_up = on == 0 || on == 2 ? on : 1;
+    g_inject_mm_give_up = on >= 0 && on <= 4 ? on : 1;
     return Q_OK;
 }
 

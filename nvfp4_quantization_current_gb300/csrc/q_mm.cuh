@@ -21,7 +21,9 @@ struct MmArgs {
     int32_t *status;
     bool accumulate;
     int store;
-    int give_up;                // of every cluster, for a test (the split kernel's first CTA, a pair): 1 a wait has run out, 2 the MMAs' first one does
+    // For a test, of every cluster: 1 a wait has run out (in the split kernel's first CTA, in both of a pair), 2 the MMAs'
+    // first one does, 3 and 4 the loads of a pair's first or second CTA never begin (the split kernel: as 1).
+    int give_up;
 };
 
 // Waits for a phase of `bar`; false when the CTA's abort flag is up or the
@@ -72,6 +74,38 @@ template <int OUT> QD void put_one(typename OutT<OUT>::T *p, float v, bool accum
     } else {
         *p = (uint16_t)bf16_bits(accumulate ? __uint_as_float((uint32_t)*p << 16) + v : v);
     }
+}
+
+// The end of the loads of a pair's CTA (one thread), `n` stages of `part` bytes; ok: every one of them has been read.  If not,
+// the copies in flight land here, before shared memory goes away.  Those of both CTAs count on the leader's barriers, so
+// the leader waits for them (bounded), and its peer for the leader's word.  Uses of a stage that one CTA has issued and
+// the other has not would never complete: the leader leaves out what is missing.  (Neither can be more than STAGES ahead.)
+// Where the MMAs end early, the loads of both CTAs do: each waits for its stages' releases.  `issued`, `landed`: words of
+// shared memory, zero so far.
+template <int STAGES>
+QD void pair_loads_end(bool ok, uint64_t *full, uint32_t n, uint32_t part, int *issued, int *landed, int *abort_flag, uint32_t rank)
+{
+    *static_cast<volatile int *>(issued) = (int)n + 1;
+    const int other = (int)rank ^ 1;
+    if (!ok) {
+        st_cluster1(cluster_addr(smem_u32(abort_flag), other), 1);   // the peer need not wait its time out
+        const unsigned long long t0 = globaltimer();
+        if (rank == 0) {
+            uint32_t peer;
+            while ((peer = (uint32_t)ld_cluster1(cluster_addr(smem_u32(issued), other))) == 0 && globaltimer() - t0 < 2 * kWaitNs) {}
+            peer = peer == 0 ? n : peer - 1;
+            const uint32_t most = n > peer ? n : peer;
+            for (uint32_t j = most > STAGES ? most - STAGES : 0; j < most; j++) {
+                uint64_t *const bar = &full[j % STAGES];
+                if (j >= n) mbar_arrive_expect_tx(bar, part);
+                if (j >= peer) mbar_complete_tx(bar, part);
+                (void)mbar_wait_bounded(bar, (j / STAGES) & 1);
+            }
+        } else {
+            while (*static_cast<volatile int *>(landed) == 0 && globaltimer() - t0 < (STAGES + 3) * kWaitNs) {}
+        }
+    }
+    if (rank == 0) st_cluster1(cluster_addr(smem_u32(landed), other), 1);
 }
 
 QD void bulk_add_tile(const CUtensorMap *map, const void *src, int x, int y)

@@ -147,6 +147,14 @@ QD uint32_t cluster_addr(uint32_t addr, int rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// A word of the cluster's shared memory, which another CTA may write or read meanwhile.
+QD int ld_cluster1(uint32_t addr)
+{
+    int v;
+    asm volatile("ld.relaxed.cluster.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+QD void st_cluster1(uint32_t addr, int v) { asm volatile("st.relaxed.cluster.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 // Arrival on a barrier of the cluster.  No data in generic memory is handed
 // over with it (only tensor memory that has been read, which the tcgen05
 // fences order), so it and the waits for it stay at CTA scope: an acquire at
@@ -183,6 +191,11 @@ QD void tma_load_tile_pair(void *dst, const CUtensorMap *map, int x, int y, uint
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// Bytes that `bar` awaits and that will not come.
+QD void mbar_complete_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // mma_f8 over the pair: the descriptors give offsets that hold in both CTAs.
 QD void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
