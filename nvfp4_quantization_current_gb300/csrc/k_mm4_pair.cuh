@@ -24,9 +24,8 @@
 // take 8192.  The tensor pipe is active 67 % of the time (BF16, 4864 x 4096 x 8192).
 // Called for seconds on end, 8192 x 14336 x 4096 takes 167 us: 1.35 kW, the power
 // cap active, 1.80 GHz.  The scales' way: loaded and handed over stage by stage 260
-// us, units of four blocks in slots of their own 212, without release at cluster
-// scope (which waited for the loads) 171; copies of four bytes straight to their
-// places 560.
+// us, units of four blocks in slots of their own 212, without a release that waited
+// for the loads 171; copies of four bytes straight to their places 560.
 #pragma once
 
 #include "q_internal.h"
@@ -128,11 +127,9 @@ QD void put_scales4(Smem &sm, const Mm4Args &a, int atom, int part, int first, i
             held[slot % kSets].template put<4>(g, now.row0, now.kb, sm.scales[slot][lane >> 3] + atom * kScaleAtom, 16 * part + (lane & 7), lane);
             fence_proxy_async();
             __syncwarp();
-            // What is handed over is read by this SM's own tensor core, whichever CTA's thread
-            // asks for it: the fence has put it there, and the arrival needs no release to the
-            // cluster, which waited for the loads on their way as well (8192 x 14336 x 4096 213
-            // us with it, 171 without).
-            if (lane == 0) mbar_arrive_cluster(bar + 8 * slot);
+            // The copies that the leader's thread asks for read both CTAs' scales.  (8192 x 14336 x 4096 153 us; 167
+            // where a release of all memory comes by way of a warp without loads, 213 from here.)
+            if (lane == 0) mbar_arrive_shared_cluster(bar + 8 * slot);
             advance(now);
             load(held[slot % kSets]);
         }
@@ -350,8 +347,9 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
                     if (tile > 0) ok = mm_wait(&sm.acc_free, (tile - 1) & 1, stop, g.status);
                     for (int kb = 0; kb < kb_n; kb++) {
                         const uint32_t slot = unit % kPair4Slots;
+                        // (scales first: the fence behind them runs while operands are on their way)
+                        if (kb % kPair4Unit == 0) ok = ok && mm_wait<true>(&sm.sc_full[slot], (unit / kPair4Slots) & 1, stop, g.status);
                         ok = ok && mm_wait(&sm.full[s], par, stop, g.status);
-                        if (kb % kPair4Unit == 0) ok = ok && mm_wait(&sm.sc_full[slot], (unit / kPair4Slots) & 1, stop, g.status);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         tc_fence_after();

@@ -30,11 +30,15 @@ struct MmArgs {
 // wait ran out (which raises it and reports the timeout).  The hardware wakes
 // the warp: polling sees the phase some 130 cycles sooner, but the polls' power
 // costs the large products 2 to 3%.
-QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+// SHARED: for what other CTAs of the cluster have put into their shared memory (mbar_arrive_shared_cluster).
+template <bool SHARED = false> QD bool mm_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
     unsigned long long t0 = 0;
     for (uint32_t n = 1;; n++) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (SHARED ? mbar_try_wait_relaxed_cluster(bar, parity) : mbar_try_wait(bar, parity)) {
+            if constexpr (SHARED) shared_acquire_cluster();
+            return true;
+        }
         if (n % 1024 == 0) {   // the timer and the flag are off the way of the waits that are served
             if (*abort_flag) return false;
             const unsigned long long now = globaltimer();

@@ -163,6 +163,15 @@ QD void mbar_arrive_cluster(uint32_t addr)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// Arrival that hands over what this thread, and those whose word it has, wrote to their CTA's shared memory, to a
+// thread of the cluster that waits and fences in turn.  The fences leave memory elsewhere alone: a release of
+// everything waits for loads on their way as well, behind copies that keep memory's queues full.
+QD void mbar_arrive_shared_cluster(uint32_t addr)
+{
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+                 "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+QD void shared_acquire_cluster() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 
 // Ahead of a kernel's loads: its tensor map, and a tile into L2 (coherent: a
 // later write reaches it there).
