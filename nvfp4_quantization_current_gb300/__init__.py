@@ -838,6 +838,7 @@ class _NormAdd(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps, amax, status):
         y, h, rstd = norm_add(x, weight, eps, residual, amax=amax, status=status)
+        ctx.status = status
         ctx.set_materialize_grads(False)
         ctx.mark_non_differentiable(rstd)
         ctx.save_for_backward(h, rstd, weight)
@@ -850,7 +851,7 @@ class _NormAdd(torch.autograd.Function):
         if dy is None:   # the sum alone was used
             return dh, None, dh if need[2] else None, None, None, None
         with torch.no_grad():
-            dx, dw = norm_grad(_ready(dy), h, rstd, weight, None if dh is None else _ready(dh), need_dw=need[1])
+            dx, dw = norm_grad(_ready(dy), h, rstd, weight, None if dh is None else _ready(dh), need_dw=need[1], status=ctx.status)
         dx, dw = _once("norm_add", (dx, dw), dy, dh, h, weight)
         return dx, dw, dx if need[2] else None, None, None, None
 
@@ -865,7 +866,7 @@ def norm_add(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
 
     ``amax`` (a one-element float32 tensor) receives max|y|, for
     :func:`q_nvfp4` or :func:`q_current_scaling` to be given; ``status`` then
-    reports a maximum that is not finite.  ``out`` (for y) and ``h_out`` may be
+    reports a maximum that is not finite, and in any case a kernel that gave up waiting, in the backward pass too.  ``out`` (for y) and ``h_out`` may be
     x and the residual themselves (without a residual ``out=x`` leaves y in what is
     returned as h, which :func:`norm_grad` then has no use for).  Autograd takes :func:`norm_grad` as the
     backward pass; with ``out`` or ``h_out`` no gradient is recorded."""

@@ -179,15 +179,21 @@ class RMSNorm(torch.nn.Module):
     x + residual; with a residual the result is ``(y, h)``, h being the new
     residual.  x is bfloat16 or float32 with any strides, the residual of its shape
     and type.  ``amax`` (a one-element float32 tensor) receives max|y|, for
-    :class:`NVFP4Linear` to be given."""
+    :class:`NVFP4Linear` to be given.  ``status`` is as in :class:`BlockwiseLinear`:
+    ``Q_ST_TIMEOUT`` where a kernel of either pass gave up waiting, and with ``amax``
+    ``Q_ST_NONFINITE`` where that maximum is not finite."""
 
     def __init__(self, features: int, eps: float = 1e-6, device="cuda", dtype=torch.bfloat16):
         super().__init__()
         self.weight = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype))
         self.eps = float(eps)
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    _status_on = BlockwiseLinear._status_on
 
     def forward(self, x, residual=None, amax: Optional[torch.Tensor] = None):
-        y, h, _ = norm_add(_ready(x), self.weight, self.eps, None if residual is None else _ready(residual), amax=amax)
+        y, h, _ = norm_add(_ready(x), self.weight, self.eps, None if residual is None else _ready(residual), amax=amax,
+                           status=self._status_on(x.device))
         return y if residual is None else (y, h)
 
 
