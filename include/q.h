@@ -558,6 +558,14 @@ q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void 
                    const void *dh, void *dx, void *dw, float *work, int32_t *status, q_stream_t stream);
 int64_t norm_grad_work(int64_t M, int64_t K, q_dtype in);
 
+/*
+ * Diagnostic of these calls' waits (a library check): in the calling thread's next
+ * norm_add, norm_q_blockwise or norm_grad that launches a kernel, the first wait of
+ * every CTA for rows' copies counts as run out, where the call has such waits (rows
+ * that go straight to registers have none).  on = 0 clears it.
+ */
+q_status selftest_norm_give_up(int on);
+
 #ifdef __cplusplus
 }
 #endif

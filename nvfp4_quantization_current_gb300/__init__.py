@@ -90,6 +90,7 @@ SIGNATURES = {
     "q_selftest_wait_timeout": (_I, [_P, _U64, _P]),
     "q_selftest_inject_launch_error": (_I, [_I]),
     "selftest_mm_give_up": (_I, [_I]),
+    "selftest_norm_give_up": (_I, [_I]),
     "q_mxfp8_requant_col": (_I, [_P, _P, _I64, _I64, _I, _P, _P, _P, _P]),
     "q_blockwise": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P, _P, _P, _P]),
     "q_blockwise_mx": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P, _P, _P, _P]),

@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 512, RES || WIDE ? 1 : 2) k_norm
     int64_t row = blockIdx.x;
     for (int n = 0; n < steps; n++, row += gridDim.x) {
         const uint8_t *const st = dsm + s * stage_bytes + skew(row);
-        const bool ok = mbar_wait_bounded(&full[s], parity);
+        const bool ok = !a.give_up && mbar_wait_bounded(&full[s], parity);
         Piece<DT, W> h[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; i++) {

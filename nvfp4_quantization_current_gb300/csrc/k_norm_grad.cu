@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(512) k_norm_grad(const NormGradArgs a, int sta
 #pragma unroll
         for (int r = 0; r < R; r++) f[r] = r0 + r < a.M ? load_float(a.rstd + r0 + r) : 0.0f;
         const uint8_t *const st = dsm + (int64_t)s * stage_bytes + skew(row0(n)) + (int64_t)mine * K * ES;
-        const bool ok = mbar_wait_bounded(&full[s], parity);
+        const bool ok = !a.give_up && mbar_wait_bounded(&full[s], parity);
         Piece<DT, W> h[R][VPT], dy[R][VPT], dh[DH ? R : 1][DH ? VPT : 1];
         float c[R];
 #pragma unroll

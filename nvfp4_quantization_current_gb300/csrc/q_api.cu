@@ -77,6 +77,14 @@ thread_local int g_inject_launch_failures = 0;
 
 // Which wait of this thread's next product gives up (selftest_mm_give_up).
 thread_local int g_inject_mm_give_up = 0;
+// Whether this thread's next norm or gradient of one does (selftest_norm_give_up).
+thread_local bool g_inject_norm_give_up = false;
+bool norm_gives_up()
+{
+    const bool on = g_inject_norm_give_up;
+    g_inject_norm_give_up = false;
+    return on;
+}
 
 #define LAUNCH(where, expr)                                                \
     do {                                                                   \
@@ -545,7 +553,7 @@ q_status norm_add(const void *x, q_dtype in, int64_t M, int64_t K, const void *r
     }
     TRY(need(fn, "y", y, 16));
     if (y == h) return fail(Q_ERR_ARG, "%s: y and h are the same buffer", fn);
-    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, y, rstd, amax, nullptr, nullptr, status, M, K, 0};
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, y, rstd, amax, nullptr, nullptr, status, M, K, 0, 0, 0, norm_gives_up()};
     LAUNCH(fn, qk::launch_norm_add(a, (int)in, S(stream)));
     return Q_OK;
 }
@@ -570,7 +578,7 @@ q_status norm_q_blockwise(const void *x, q_dtype in, int64_t M, int64_t K, const
         TRY(need(fn, "s_colT", s_colT, 4));
         TRY(multiple(fn, "M (with q_colT)", M, 128));
     }
-    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, nullptr, rstd, nullptr, q_row, s_row, status, M, K, 0};
+    qk::NormArgs a = {x, residual, weight, wt == Q_F32, eps, (float)(1.0 / (double)K), h, nullptr, rstd, nullptr, q_row, s_row, status, M, K, 0, 0, 0, norm_gives_up()};
     LAUNCH(fn, qk::launch_norm_cast_rows(a, (int)in, S(stream)));
     if (q_colT != nullptr)
         LAUNCH(fn, qk::launch_norm_cast_cols(residual != nullptr ? h : x, (int)in, M, K, rstd, weight, wt == Q_F32, q_colT, s_colT,
@@ -601,7 +609,7 @@ q_status norm_grad(const void *dy, q_dtype in, int64_t M, int64_t K, const void 
     if (dh != nullptr) TRY(need(fn, "dh", dh, 16));
     TRY(need(fn, "dx", dx, 16));
     if (dw != nullptr) TRY(need(fn, "work", work, 16));
-    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, status, M, K, false};
+    qk::NormGradArgs a = {dy, h, dh, weight, wt == Q_F32, rstd, dx, work, status, M, K, false, norm_gives_up()};
     LAUNCH(fn, qk::launch_norm_grad(a, (int)in, dw, S(stream)));
     return Q_OK;
 }
@@ -616,6 +624,12 @@ q_status q_selftest_inject_launch_error(int n)
 q_status selftest_mm_give_up(int on)
 {
     g_inject_mm_give_up = on >= 0 && on <= 4 ? on : 1;
+    return Q_OK;
+}
+
+q_status selftest_norm_give_up(int on)
+{
+    g_inject_norm_give_up = on != 0;
     return Q_OK;
 }
 

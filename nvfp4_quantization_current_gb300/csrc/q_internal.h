@@ -125,6 +125,7 @@ struct NormArgs {
     int64_t M, K;
     int row_threads, cta_rows;   // set by the launcher, as the next
     uint32_t per_warps;
+    bool give_up;   // the rings' first wait counts as run out (a test)
 };
 cudaError_t launch_norm_add(const NormArgs &a, int dt, cudaStream_t st);
 // h and rstd, and the rowwise copy where q_row is given
@@ -143,6 +144,7 @@ struct NormGradArgs {
     int32_t *status;
     int64_t M, K;
     bool once;   // set by the launcher: the inputs are read once
+    bool give_up;   // as above
 };
 int64_t norm_grad_rows(int64_t M, int64_t K, int dt);   // rows of K floats in `work`
 cudaError_t launch_norm_grad(NormGradArgs a, int dt, void *dw, cudaStream_t st);
