@@ -58,6 +58,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libq.so")
@@ -171,6 +172,12 @@ def _fmt(fmt):
 
 def _out(dtype):
     return {torch.float32: Q_F32, torch.bfloat16: Q_BF16}[dtype]
+
+
+def _tangents(*tensors):
+    """Whether a tensor carries a forward-mode derivative, which the library's calls would drop (no level of it being the usual case)."""
+    return forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled() and \
+        any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 # The kernels write through a pointer: this is what autograd's check of the tensors that it saved goes by.
@@ -662,7 +669,8 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
             if s.device != q.device:
                 raise ValueError(f"{name}: scales are on {s.device}, codes on {q.device}")
         raise ValueError(f"a is on {dev}, b on {b.device}")
-    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled() or \
+            _tangents(s_a, s_b, out):
         raise RuntimeError("mm_blockwise records no gradient, but its scales or out require one")
     if out is None:
         if accumulate:
@@ -732,7 +740,7 @@ def drop_add(x: torch.Tensor, p: float, seed: int, offset: int = 0, residual: Op
     if residual is not None:
         _alike("residual", residual, x)
     if (x.requires_grad or residual is not None and residual.requires_grad or out is not None and out.requires_grad) \
-            and torch.is_grad_enabled():
+            and torch.is_grad_enabled() or _tangents(x, residual, out):
         if out is not None:
             raise RuntimeError("drop_add with out= records no gradient, but one of its tensors requires one")
         return _DropAdd.apply(x, residual, p, seed, offset)
@@ -874,7 +882,8 @@ def norm_add(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     dev = x.device
     dt, M, K = _norm_in("x", x, dev, weight, residual)
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad or
-                                    out is not None and out.requires_grad or h_out is not None and h_out.requires_grad):
+                                    out is not None and out.requires_grad or h_out is not None and h_out.requires_grad) or \
+            _tangents(x, weight, residual, out, h_out):
         if out is not None or h_out is not None:
             raise RuntimeError("norm_add with out= or h_out= records no gradient, but one of its tensors requires one")
         r = _NormAdd.apply(x, weight, residual, eps, amax, status)
@@ -906,7 +915,7 @@ def norm_q_blockwise(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, r
     dev = x.device
     dt, M, K = _norm_in("x", x, dev, weight, residual)
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or residual is not None and residual.requires_grad or
-                                    h_out is not None and h_out.requires_grad):
+                                    h_out is not None and h_out.requires_grad) or _tangents(x, weight, residual, h_out):
         raise RuntimeError("norm_q_blockwise records no gradient, but one of its tensors requires one")
     if x.dim() != 2:
         raise ValueError("x must be a 2-D tensor")
@@ -935,7 +944,8 @@ def norm_grad(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: tor
     dev = dy.device
     dt, M, K = _norm_in("dy", dy, dev, weight, None)
     if torch.is_grad_enabled() and (dy.requires_grad or h.requires_grad or rstd.requires_grad or weight.requires_grad or
-                                    dh is not None and dh.requires_grad or out is not None and out.requires_grad):
+                                    dh is not None and dh.requires_grad or out is not None and out.requires_grad) or \
+            _tangents(dy, h, rstd, weight, dh, out):
         raise RuntimeError("norm_grad records no gradient, but one of its tensors requires one")
     _alike("h", h, dy)
     if not _is(rstd, torch.float32, dy.shape[:-1], dev):
@@ -1001,7 +1011,8 @@ def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torc
     N, Kb = _operand4("b", b, sb_b, s_b, bb, dev)
     if K != Kb:
         raise ValueError(f"a has K = {K}, b has K = {Kb}")
-    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+    if (s_a.requires_grad or s_b.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled() or \
+            _tangents(s_a, s_b, out):
         raise RuntimeError("matmul_nvfp4 records no gradient, but its scales or out require one")
     if out is None:
         if accumulate:
