@@ -118,8 +118,8 @@ class BlockwiseLinear(torch.nn.Module):
 
     ``in_features`` and ``out_features`` are multiples of 128; x is bfloat16 or
     float32 with any number of rows and any strides, the residual alike and of
-    x's type.  With ``main_grad`` set (FP32, the weight's shape) the weight
-    gradient is added to it and ``weight.grad`` stays unset.  ``copies`` takes the
+    x's type; the weight may lie on any address.  With ``main_grad`` set (FP32, the
+    weight's shape, on a 16-byte boundary) the weight gradient is added to it and ``weight.grad`` stays unset.  ``copies`` takes the
     result of :meth:`quantize_weight`, made once for the micro-batches of a step,
     or once for serving.  There is no second derivative: one that is asked for
     raises.
@@ -158,7 +158,7 @@ class BlockwiseLinear(torch.nn.Module):
 
     def quantize_weight(self, colwise=True) -> BlockwiseTensor:
         """The weight's 128x128 copies (``colwise``: also the transposed one, for the input gradient)."""
-        return q_blockwise(self.weight.detach(), "128x128", rowwise=True, colwise=colwise,
+        return q_blockwise(_ready(self.weight.detach()), "128x128", rowwise=True, colwise=colwise,
                            status=self._status_on(self.weight.device))
 
     def forward(self, x, residual=None, offset: Optional[int] = None, copies: Optional[BlockwiseTensor] = None):
@@ -192,7 +192,7 @@ class RMSNorm(torch.nn.Module):
     _status_on = BlockwiseLinear._status_on
 
     def forward(self, x, residual=None, amax: Optional[torch.Tensor] = None):
-        y, h, _ = norm_add(_ready(x), self.weight, self.eps, None if residual is None else _ready(residual), amax=amax,
+        y, h, _ = norm_add(_ready(x), _ready(self.weight), self.eps, None if residual is None else _ready(residual), amax=amax,
                            status=self._status_on(x.device))
         return y if residual is None else (y, h)
 
@@ -215,7 +215,7 @@ class _NormBlockwiseLinear(torch.autograd.Function):
         M = x2.shape[0]
         if need_w and M % 128 != 0:   # zero rows below: their norm is zero and adds nothing to the weight gradient
             x2, r2 = _rows_to(x2, 128), None if r2 is None else _rows_to(r2, 128)
-        xq, h, rstd = norm_q_blockwise(x2, norm_weight.detach(), eps, r2, rowwise=True, colwise=need_w, status=status)
+        xq, h, rstd = norm_q_blockwise(x2, _ready(norm_weight.detach()), eps, r2, rowwise=True, colwise=need_w, status=status)
         y = mm_blockwise(xq.q_row[:M], xq.s_row[:M], w.q_row, w.s_row, dtype=x.dtype, status=status)
         ctx.set_materialize_grads(False)
         link = _link(through or need_w)
@@ -247,7 +247,7 @@ class _NormBlockwiseLinear(torch.autograd.Function):
         dx = dn = dw = None
         if through:
             dn_in = mm_blockwise(g.q_row, g.s_row, w_q, w_s, dtype=dy.dtype, status=status)
-            dx, dn = norm_grad(dn_in, h, rstd, norm_weight, None if dh is None else _ready(dh.reshape(-1, dh.shape[-1])), need_dw=need[1],
+            dx, dn = norm_grad(dn_in, h, rstd, _ready(norm_weight), None if dh is None else _ready(dh.reshape(-1, dh.shape[-1])), need_dw=need[1],
                                out=dn_in, status=status)
             dx = dx.view(x_shape)
         if need_w:
@@ -369,7 +369,7 @@ class NVFP4Linear(torch.nn.Module):
 
     def quantize_weight(self, colwise=True) -> NVFP4Tensor:
         """The weight's 16x16 copies (``colwise``: also the transposed one, for the input gradient)."""
-        return q_nvfp4(self.weight.detach(), "16x16", rowwise=True, colwise=colwise, status=self._status_on(self.weight.device))
+        return q_nvfp4(_ready(self.weight.detach()), "16x16", rowwise=True, colwise=colwise, status=self._status_on(self.weight.device))
 
     def forward(self, x, offset: Optional[int] = None, copies: Optional[NVFP4Tensor] = None, amax: Optional[torch.Tensor] = None):
         train = torch.is_grad_enabled()
