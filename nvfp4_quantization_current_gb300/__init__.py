@@ -658,7 +658,9 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     upward; sums in FP32, results independent of timing.  It records no gradient:
     scales or an ``out`` that require one are refused (``linear.py`` has the
     backward pass)."""
-    ta, tb = _TILE[tile_a], _TILE[tile_b]
+    ta, tb = _TILE.get(tile_a), _TILE.get(tile_b)
+    if ta is None or tb is None:
+        raise ValueError(f"tile_a and tile_b must be 1x128 or 128x128, not {tile_a} and {tile_b}")
     M, K = _operand("a", a, s_a, ta)
     N, Kb = _operand("b", b, s_b, tb)
     if K != Kb:
@@ -675,9 +677,11 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype} is not bfloat16 or float32")
         out = torch.empty((M, N), dtype=dtype, device=dev)
-    elif out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
-        raise ValueError(f"out must be a contiguous {M} x {N} tensor on {dev}")
+    elif out.shape != (M, N) or out.dtype not in _DTYPES or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be a contiguous {M} x {N} tensor of bfloat16 or float32 on {dev}")
     else:
         _written(out)
     _call("mm_blockwise", a.data_ptr(), s_a.data_ptr(), ta, b.data_ptr(), s_b.data_ptr(), tb, M, N, K, out.data_ptr(),
@@ -1005,7 +1009,9 @@ def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torc
     float32; ``accumulate`` adds to ``out``.  One token upward; sums in FP32, results
     independent of timing.  It records no gradient: scales or an ``out`` that require
     one are refused (``linear.py`` has the backward pass)."""
-    ba, bb = _BLK[blk_a], _BLK[blk_b]
+    ba, bb = _BLK.get(blk_a), _BLK.get(blk_b)
+    if ba is None or bb is None:
+        raise ValueError(f"blk_a and blk_b must be 1x16 or 16x16, not {blk_a} and {blk_b}")
     dev = a.device
     M, K = _operand4("a", a, sb_a, s_a, ba, dev)
     N, Kb = _operand4("b", b, sb_b, s_b, bb, dev)
@@ -1017,6 +1023,8 @@ def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torc
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype} is not bfloat16 or float32")
         out = torch.empty((M, N), dtype=dtype, device=dev)
     elif out.shape != (M, N) or out.dtype not in _DTYPES or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"out must be a contiguous {M} x {N} tensor of bfloat16 or float32 on {dev}")
