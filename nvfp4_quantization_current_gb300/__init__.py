@@ -658,9 +658,7 @@ def mm_blockwise(a: torch.Tensor, s_a: torch.Tensor, b: torch.Tensor, s_b: torch
     upward; sums in FP32, results independent of timing.  It records no gradient:
     scales or an ``out`` that require one are refused (``linear.py`` has the
     backward pass)."""
-    ta, tb = _TILE.get(tile_a), _TILE.get(tile_b)
-    if ta is None or tb is None:
-        raise ValueError(f"tile_a and tile_b must be 1x128 or 128x128, not {tile_a} and {tile_b}")
+    ta, tb = _TILE[tile_a], _TILE[tile_b]
     M, K = _operand("a", a, s_a, ta)
     N, Kb = _operand("b", b, s_b, tb)
     if K != Kb:
@@ -1009,9 +1007,7 @@ def matmul_nvfp4(a: torch.Tensor, sb_a: torch.Tensor, s_a: torch.Tensor, b: torc
     float32; ``accumulate`` adds to ``out``.  One token upward; sums in FP32, results
     independent of timing.  It records no gradient: scales or an ``out`` that require
     one are refused (``linear.py`` has the backward pass)."""
-    ba, bb = _BLK.get(blk_a), _BLK.get(blk_b)
-    if ba is None or bb is None:
-        raise ValueError(f"blk_a and blk_b must be 1x16 or 16x16, not {blk_a} and {blk_b}")
+    ba, bb = _BLK[blk_a], _BLK[blk_b]
     dev = a.device
     M, K = _operand4("a", a, sb_a, s_a, ba, dev)
     N, Kb = _operand4("b", b, sb_b, s_b, bb, dev)
