@@ -26,17 +26,6 @@ struct Mm4Args {
     int group;                // of the pair kernel's tile order
 };
 
-// Bytes s to s + 15 of the 32 that two vectors hold.
-QD uint4 bytes_from(const uint4 &a, const uint4 &b, int s)
-{
-    const bool two = s & 8, one = s & 4;
-    const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w, w4 = two ? b.z : b.x,
-                   w5 = two ? b.w : b.y;
-    const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
-    const int r = 8 * (s & 3);
-    return make_uint4(__funnelshift_r(v0, v1, r), __funnelshift_r(v1, v2, r), __funnelshift_r(v2, v3, r), __funnelshift_r(v3, v4, r));
-}
-
 // The scales of up to 64 rows and four blocks on their way through a warp's registers: lane l has block l / 8 of the
 // rows l % 8 + 8 i + 32 j (j < N).  Four lanes take 64 bytes of a scale row, so that a
 // load touches 8 lines, and a lane's four rows of one i share a source line of the
