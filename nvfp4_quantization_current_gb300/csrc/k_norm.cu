@@ -10,9 +10,9 @@
 // is bound by memory, and a row is read once: it stays in registers between its sum
 // and what is made of it.  Measured on a GB300, in graphs of calls: 8192 x 4096 BF16
 // with a residual 42.4 us (268 MB at 6.3 TB/s, a copy's rate being 6.8), without one
-// 20.4 to 20.8, in FP32 79.9; its rowwise copy 39 with a residual, 25.9 without (with one,
-// 334 warp instructions for 512 elements: issue slots 54 % in use, DRAM 71 %, at 16384 x
-// 4096); 16 rows 2.0 to 2.1.
+// 20.4 to 20.8, in FP32 78.6 to 79.9; its rowwise copy 39 with a residual, 26.2 without (with one,
+// 338 warp instructions for 512 elements: issue slots 54 % in use, DRAM 72 %, at 16384 x
+// 4096); 16 rows 1.9 to 2.2.
 #include "q_norm.cuh"
 
 namespace qk {
@@ -147,8 +147,10 @@ __global__ void __launch_bounds__(1024) k_norm_rows(const NormArgs a)
     constexpr bool kHalves = W == 1 && VPT == 8;
     __shared__ float part[32], upper[kHalves ? 512 : 1];
     // this thread's row of the CTA's: its warp by the warps of a row (of 32 at most, so that 16 bits of the quotient do)
-    const int T = a.row_threads, mine = (int)((threadIdx.x >> 5) * a.per_warps >> 16), t = threadIdx.x - mine * T, lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * a.cta_rows + mine;
+    constexpr bool kWhole = VPT * W == 32;   // the longest rows: all threads of the largest CTA (numbers that are known spare registers)
+    const int T = kWhole ? 1024 : a.row_threads, mine = kWhole ? 0 : (int)((threadIdx.x >> 5) * a.per_warps >> 16);
+    const int t = threadIdx.x - mine * T, lane = threadIdx.x & 31;
+    const int64_t row = kWhole ? blockIdx.x : (int64_t)blockIdx.x * a.cta_rows + mine;
     const bool live = row < a.M;
     const int K = (int)a.K;
     const int64_t base = row * a.K;
@@ -390,7 +392,7 @@ int row_threads(int64_t K, int E) { return (int)((K + 32 * E - 1) / (32 * E)) * 
 
 template <int DT, int W, int VPT, int MODE> cudaError_t norm_rows(NormArgs a, cudaStream_t st)
 {
-    a.row_threads = W == 1 && VPT == 8 ? 2 * row_threads(a.K, 16) : row_threads(a.K, VPT * W);
+    a.row_threads = W == 1 && VPT == 8 ? 2 * row_threads(a.K, 16) : VPT * W == 32 ? 1024 : row_threads(a.K, VPT * W);
     a.cta_rows = a.row_threads < 256 ? 256 / a.row_threads : 1;
     a.per_warps = 65536u / (a.row_threads / 32) + 1;
     const int threads = a.cta_rows * a.row_threads;
@@ -412,9 +414,10 @@ cudaError_t norm_ring_t(const NormArgs &a, int threads, int per_sm, int stages, 
 
 // Whether the ring's kernel takes the call, and its launch: rows of 257 to 16384
 // elements that begin anywhere, or BF16 ones of 2048 on, where there are enough of them to keep every CTA's ring busy
-// (8192 x 4096 BF16 without a residual 20.8 us, one row a CTA 27.3; 16384 x 7168 cast with
-// one 121.6 and 154.8; 8192 x 5001 FP32 57 and 140; but 8192 x 4096 FP32 with a residual
-// 85.1 and 79.7, 8192 x 512 BF16 6.4 and 4.9, 2048 x 4096 cast 12.5 and 11.1).
+// (8192 x 4096 BF16 without a residual 20.6 us, one row a CTA 26.5; 16384 x 7168 cast with
+// one 122 and 151; 8192 x 5001 FP32 57 and 127; but 8192 x 4096 FP32 with a residual
+// 85.0 and 78.6, 8192 x 512 BF16 5.9 and 3.4, 2048 x 4096 cast 12.5 and 11.1; and the other way by
+// little, 8192 x 4096 BF16 stored with a residual 42.9 and 41.6, 16384 x 7168 142.5 and 148.6).
 template <int DT, int W, int MODE, bool RES> bool norm_ring(const NormArgs &a, cudaStream_t st, cudaError_t &e)
 {
     constexpr int ES = In<DT>::BYTES;
