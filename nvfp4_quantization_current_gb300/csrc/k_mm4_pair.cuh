@@ -12,18 +12,19 @@
 // Warp 0 of each CTA loads its operand tiles, all of whose bytes count on the
 // leader's barriers; the leader's warp 1 issues the copies of scales to tensor
 // memory and the MMAs.  Warps 2 to 7 fetch scales: two each for P's 128 rows and
-// the halves of Q's 256 (every CTA needs all of Q's), four blocks at a time (handed over two
+// the halves of Q's 256 (every CTA needs all of Q's; at 128 the last two have none), four blocks at a time (handed over two
 // at a time, which made room for one stage more, 8192 x 14336 x 4096 took 188 us for 154).
 // The eight warps 8-15 read 32 rows x 128 columns each when a tile is done.
 //
 // Measured on a GB300, in graphs of calls: 8192 x 14336 x 4096 to BF16 152 to 155 us
-// (6.2 to 6.3 PFLOP/s), 8192 x 4096 x 14336 141 to 143 (6.8), 16384 x 18432 x 7168
-// 618 to 660 (6.6 to 7.0), 14336 x 4096 x 8192 added to FP32 161 to 166 (5.8 to 6.0).  A tile
-// of 8192 x 14336 x 4096 takes the MMA warp 12346 cycles, of which it waits 3180 for
-// operands, 1070 for scales and 730 for the sums' place; at the nominal rate its MMAs
-// take 8192.  The tensor pipe is active 67 % of the time (BF16, 4864 x 4096 x 8192).
-// Called for seconds on end, 8192 x 14336 x 4096 takes 167 us: 1.35 kW, the power
-// cap active, 1.80 GHz.  The scales' way: loaded and handed over stage by stage 260
+// (6.2 to 6.3 PFLOP/s), 8192 x 4096 x 14336 138 to 141 (6.8 to 7.0), 16384 x 18432 x 7168
+// 615 to 660 (6.6 to 7.0), 14336 x 4096 x 8192 added to FP32 163 to 166 (5.8 to 5.9).  A tile
+// of 8192 x 14336 x 4096 takes the MMA warp 12170 cycles, of which it waits 1690 for
+// scales, then 1620 for operands (of 12346 cycles 3180 for operands and then 1070 for scales, where it waited for
+// operands first: each hides part of the other) and 740 for the sums' place; at the nominal rate its MMAs
+// take 8192.  The tensor pipe is active 69 % of the time (BF16, 4864 x 4096 x 8192).
+// Called for seconds on end, 8192 x 14336 x 4096 takes 168 us: 1.35 kW, the power
+// cap active, 1.78 GHz.  The scales' way: loaded and handed over stage by stage 260
 // us, units of four blocks in slots of their own 212, without a release that waited
 // for the loads 171; copies of four bytes straight to their places 560.
 #pragma once

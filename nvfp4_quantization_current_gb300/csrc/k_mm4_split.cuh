@@ -13,7 +13,7 @@
 //
 // Measured on a GB300, in graphs of calls: one token with 4096 x 4096 weights 4.6 us,
 // 16 tokens with 14336 x 4096 7.5 us (4.0 TB/s), one with 18432 x 7168 13.4 to 13.9 us
-// (66.6 MB at 4.8 to 5.0 TB/s), 64 with 4096 x 14336 10.2 to 10.6 us.
+// (66.6 MB at 4.8 to 5.0 TB/s), 64 with 4096 x 14336 10.0 to 10.6 us.
 #pragma once
 
 #include "k_mm_split.cuh"

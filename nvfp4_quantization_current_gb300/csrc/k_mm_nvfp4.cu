@@ -128,11 +128,11 @@ int cluster_ctas4(int split)
 // the average and 14% at most.  A call has a fixed part, a cluster adds its sum, a CTA takes `block` for each 256 elements of K
 // (`odd` times as long where scale rows begin anywhere), two CTAs of an SM `share`
 // times one's time, and a CTA that comes after another a start of its own; a pair takes `tile` for a tile's end.  Some of
-// what it is drawn from: one token with 4096 x 4096 weights 4.9 us at a split of four,
-// 7.8 without, 9.7 on the pair kernel; 64 tokens with 4096 x 14336 10.6 at 64 and four, 25.5 on the
+// what it is drawn from: one token with 4096 x 4096 weights 4.6 us at a split of four,
+// 7.6 without, 8.6 on the pair kernel; 64 tokens with 4096 x 14336 10.0 at 64 and four, 21.4 on the
 // pair.  Tiles of 256 x 128 are for results that tiles of 256 x 256 are too few for, the best plan of 36 shapes, by 9% on
-// the average: 333 tokens with 4096 x 4096 10.0 us, 10.9 in 256s, 11.1 at 192 wide and
-// two deep; 380 with 2304 x 1280 5.8, 6.8 and 6.9; but 768 with 4096 x 4096, two rounds of them, 15.1 and 11.4.
+// the average: 333 tokens with 4096 x 4096 9.6 us, 10.4 in 256s, 10.8 at 192 wide and
+// two deep; 380 with 2304 x 1280 5.7, 6.6 and 8.4; but 768 with 4096 x 4096, two rounds of them, 14.4 and 11.0.
 struct Mm4Plan {
     int bn, split;   // split 0: the pair kernel
 };
