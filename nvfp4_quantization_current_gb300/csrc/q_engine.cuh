@@ -97,17 +97,6 @@ QD bool mbar_try_wait(uint64_t *bar, uint32_t parity)
     return done != 0;
 }
 
-// The phase alone, whichever CTA of the cluster completed it: a fence behind it says what else is seen.
-QD bool mbar_try_wait_relaxed_cluster(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    return done != 0;
-}
-
 QD unsigned long long globaltimer()
 {
     unsigned long long t;

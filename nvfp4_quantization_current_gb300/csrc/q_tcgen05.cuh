@@ -171,6 +171,16 @@ QD void mbar_arrive_shared_cluster(uint32_t addr)
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
                  "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// The phase alone, whichever CTA of the cluster completed it: a fence behind it says what else is seen.
+QD bool mbar_try_wait_relaxed_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
 QD void shared_acquire_cluster() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 
 // Ahead of a kernel's loads: its tensor map, and a tile into L2 (coherent: a
