@@ -332,6 +332,10 @@ k_mm4_pair(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CU
             // arrive here
             for (uint32_t j = issued > kStages ? issued - kStages : 0; ok && j < issued; j++)
                 ok = mm_wait(&sm.empty[j % kStages], (j / kStages) & 1, stop, g.status);
+            // and every slot of scales, whose last releases nobody else waits for
+            const uint32_t units = ok ? issued / (uint32_t)kb_n * (uint32_t)((kb_n + kPair4Unit - 1) / kPair4Unit) : 0u;
+            for (uint32_t u = units > kPair4Slots ? units - kPair4Slots : 0; ok && u < units; u++)
+                ok = mm_wait(&sm.sc_empty[u % kPair4Slots], (u / kPair4Slots) & 1, stop, g.status);
             pair_loads_end<kStages>(ok, sm.full, issued, Smem::kOperandBytes, &sm.issued, &sm.landed, &sm.abort_flag, rank);
         } else if (warp == 1) {
             if (rank == 0) {
